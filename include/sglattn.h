@@ -68,7 +68,7 @@ enum {
     SGL_ERR_WORKSPACE = -7    /* workspace missing, misaligned or too small */
 };
 
-enum { SGL_DTYPE_F32 = 0, SGL_DTYPE_BF16 = 1, SGL_DTYPE_BF16_FP8KV = 2 };
+enum { SGL_DTYPE_F32 = 0, SGL_DTYPE_BF16 = 1, SGL_DTYPE_BF16_FP8KV = 2, SGL_DTYPE_BF16_FP4KV = 3 };
 /* SGL_DTYPE_BF16_FP8KV: Q and O bf16, the K and V pools FP8 E4M3 bytes
  * (decode and extend); K = k_scale * pool value, V = v_scale * pool value
  * (per-tensor scales in sgl_attn_params).  sgl_extend_attn_kvwrite takes
@@ -76,7 +76,22 @@ enum { SGL_DTYPE_F32 = 0, SGL_DTYPE_BF16 = 1, SGL_DTYPE_BF16_FP8KV = 2 };
  * k_new / k_scale and v_new / v_scale (saturating at +-448, NaN kept).  The
  * query enters the tensor cores as f16: a query element outside the f16
  * range sets SGL_ERR_BOUNDS for sgl_check.  ["SGLang 深度拆解" (the FP8 KV
- * cache halves the KV bytes); CS349D lecture-16 notes §4 (FP8 KV cache)] */
+ * cache halves the KV bytes); CS349D lecture-16 notes §4 (FP8 KV cache)]
+ *
+ * SGL_DTYPE_BF16_FP4KV: Q and O bf16, the K and V pools in 4 bits: E2M1 codes
+ * (0, 0.5, 1, 1.5, 2, 3, 4, 6 and their negatives) with one E4M3 scale for 16
+ * consecutive elements of a head; K = k_scale * sf * code value, likewise V
+ * (scales finite and > 0).  A pool is uint8 [num_slots, row], row =
+ * sgl_fp4_row_bytes(Hkv, d), base 16-byte aligned.  A row holds its token's
+ * heads in blocks of four (the last block may hold fewer): first the block's
+ * codes, d / 2 bytes per head, element 2i in the low half of byte i; then the
+ * block's scales, d / 16 bytes per head; the row is padded to a multiple of 16
+ * bytes (the padding is neither read nor written).  Rows are written by
+ * sgl_kv_append and sgl_extend_attn_kvwrite: per 16 values sf = the E4M3 value
+ * nearest to max|x| / (6 * scale) (at most 448; NaN where a value is NaN), the
+ * codes those of x / (sf * scale), both to nearest even, saturating at 6; all
+ * codes are zeros where sf is 0.  The query enters the tensor cores as f16,
+ * as with SGL_DTYPE_BF16_FP8KV. */
 
 /* Name of a status code (static string). */
 const char* sgl_status_string(int status);
@@ -522,6 +537,110 @@ int sgl_extend_attn_kvwrite(const void* q_new, const void* k_new, const void* v_
                             const int32_t* req_to_token, int64_t ld, const int32_t* prefix_lens,
                             const int32_t* extend_lens, const sgl_attn_params* params, void* o, float* lse,
                             void* workspace, size_t ws_bytes, sgl_stream_t stream);
+
+/* ======================================================================== */
+/* Rotary positions and the append to the cache                             */
+/* ======================================================================== */
+
+/* Bytes of one row of a 4-bit pool (SGL_DTYPE_BF16_FP4KV); head_dim 64 or 128. */
+int sgl_fp4_row_bytes(int32_t num_kv_heads, int32_t head_dim, int64_t* bytes);
+
+/* Which elements of a head's rotated part form pair j: (j, j + rot_dim / 2), or (2j, 2j + 1). */
+enum { SGL_ROPE_HALF = 0, SGL_ROPE_PAIRS = 1 };
+/* Radians per position of pair j, with f_j = theta^(-2j / rot_dim):
+ *   NONE    f_j
+ *   LINEAR  f_j / factor (positions interpolated)
+ *   NTK     f_j with theta * factor^(rot_dim / (rot_dim - 2)) for theta
+ *   YARN    f_j / factor * w + f_j * (1 - w), w rising linearly in j from 0 at
+ *           the pair that makes `high` turns over original_positions (rounded
+ *           down, at least 0) to 1 at the pair that makes `low` turns (rounded
+ *           up, at most rot_dim - 1)
+ *   BANDED  f_j / factor * (1 - w) + f_j * w, w = (turns - low) / (high - low)
+ *           clamped to [0, 1], turns = original_positions * f_j / (2 pi) */
+enum { SGL_ROPE_SCALE_NONE = 0, SGL_ROPE_SCALE_LINEAR = 1, SGL_ROPE_SCALE_NTK = 2, SGL_ROPE_SCALE_YARN = 3,
+       SGL_ROPE_SCALE_BANDED = 4 };
+enum { SGL_ROPE_MAX_DIM = 256 };
+
+typedef struct {
+    int32_t head_dim;            /* multiple of 16, at most 1024 */
+    int32_t rot_dim;             /* rotated elements of a head: multiple of 16, at most 256; the half
+                                    layout takes 16 and multiples of 32 */
+    int32_t rot_offset;          /* first rotated element: multiple of 16 */
+    int32_t layout;              /* SGL_ROPE_HALF or SGL_ROPE_PAIRS */
+    int32_t scaling;             /* SGL_ROPE_SCALE_* */
+    double theta;                /* > 1 */
+    double factor;               /* >= 1 (not NONE) */
+    int64_t original_positions;  /* > 0 (YARN, BANDED) */
+    double low, high;            /* 0 < low < high, in turns (YARN, BANDED) */
+    double attention_factor;     /* multiplies cos and sin; 0: 1, or with YARN 0.1 ln(factor) + 1 */
+} sgl_rope_params;
+
+typedef struct sgl_rope_table sgl_rope_table;
+
+/* The frequencies of a rotation (a host object; calls copy what they need
+ * from it, so it may be destroyed once they have returned, and serves any
+ * number of threads and devices). */
+int sgl_rope_create(const sgl_rope_params* params, sgl_rope_table** out);
+void sgl_rope_destroy(sgl_rope_table* rope);
+
+/* Rotary positions of query and key rows.
+ *   q, k         device [n_rows, heads, head_dim] (dtype SGL_DTYPE_F32 or
+ *                SGL_DTYPE_BF16): heads contiguous, rows `stride` elements
+ *                apart (e.g. columns of a fused projection); either may have
+ *                0 heads
+ *   positions    device int32 [n_rows], any value up to 2^31 - 1; a row at a
+ *                negative position is left as it is in the outputs
+ *   q_out, k_out rows as q and k (the part of a head that is not rotated is
+ *                copied); may be q and k themselves (same stride), and must
+ *                not overlap them in any other way
+ * Pointers and row strides are multiples of 16 bytes.  The products are fp32,
+ * rounded once; angles are exact to fp32 at every position. */
+int sgl_rope(const sgl_rope_table* rope, int32_t dtype, const void* q, int64_t q_stride, int32_t num_q_heads,
+             const void* k, int64_t k_stride, int32_t num_k_heads, const int32_t* positions, int64_t n_rows, void* q_out,
+             int64_t q_out_stride, void* k_out, int64_t k_out_stride, sgl_stream_t stream);
+
+/* New keys and values into the paged pools, keys and queries rotated on the way.
+ *   rope         rotation of q and k (head_dim must match), or NULL: none
+ *   params       dtype, batch, heads, head_dim, num_slots, k_scale, v_scale
+ *                (the other fields are not used)
+ *   q            device [n_rows, Hq, d], rows q_stride elements apart, or
+ *                NULL with q_out NULL; rotated into q_out (rows q_out_stride
+ *                apart; may be q itself, and must not overlap it otherwise)
+ *   k_new, v_new device [n_rows, Hkv, d] (fp32 with SGL_DTYPE_F32, else
+ *                bf16), rows k_stride / v_stride elements apart
+ *   req_to_token device int32 [B, ld]
+ *   lens, extend_lens  device int32 [B].  extend_lens given (chunked prefill):
+ *                rows ordered by request, row i of request r at position
+ *                lens[r] + i, i < extend_lens[r]; rows past the last request's
+ *                are not touched (a padded batch).  extend_lens NULL (decode):
+ *                row r is request r's newest token, at position lens[r] - 1
+ *                (n_rows <= B); a request with lens[r] = 0 is left alone
+ *   k_pool, v_pool  the pools of params->dtype; the row of position p of
+ *                request r is req_to_token[r, p].  The rows of one call must
+ *                name distinct slots.
+ * The rotated key is rounded to the new rows' type, then stored as that type
+ * or as FP8 / 4-bit codes (the values that a rotation followed by a separate
+ * store gives).  A slot outside the pool is not written and sets bit 0 of the
+ * workspace's error word, a position outside the table bit 1 (the row is left
+ * out); sgl_check reports both.  workspace: device, 256-byte aligned, its
+ * first 256 bytes (a decode plan's workspace serves).  Can be captured.
+ * ["SGLang 深度解读" "5. Attention 层": the new tokens' K/V are stored into
+ * token_to_kv_pool at their req_to_token slots before attention] */
+int sgl_kv_append(const sgl_rope_table* rope, const sgl_attn_params* params, const void* q, int64_t q_stride,
+                  const void* k_new, int64_t k_stride, const void* v_new, int64_t v_stride, void* k_pool, void* v_pool,
+                  const int32_t* req_to_token, int64_t ld, const int32_t* lens, const int32_t* extend_lens,
+                  int64_t n_rows, void* q_out, int64_t q_out_stride, void* workspace, size_t ws_bytes,
+                  sgl_stream_t stream);
+
+/* The same for an MLA pool: kv_new device bf16 [n_rows, 576] (the latent,
+ * then the position part), q [n_rows, Hq, 576]; rope with head_dim 576
+ * (normally rot_dim 64 at rot_offset 512).
+ * [CS349D lecture-16 notes §5.1: one stored row of a latent and a position
+ * part per token] */
+int sgl_mla_kv_append(const sgl_rope_table* rope, const sgl_mla_params* params, const void* q, int64_t q_stride,
+                      const void* kv_new, int64_t kv_stride, void* kv_pool, const int32_t* req_to_token, int64_t ld,
+                      const int32_t* lens, const int32_t* extend_lens, int64_t n_rows, void* q_out,
+                      int64_t q_out_stride, void* workspace, size_t ws_bytes, sgl_stream_t stream);
 
 /* Wait for `stream`, read the workspace's error word and clear it.
  * SGL_OK, or SGL_ERR_BOUNDS if a kernel skipped an out-of-range slot or a

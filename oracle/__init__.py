@@ -22,6 +22,8 @@ attention  decode / extend attention as naive softmax over gathered slots,
 kvbytes    the KV-bytes-per-token formulas (GQA and MLA) used for the roofline.
 fp8        E4M3 decoding and dequantised views of FP8 pools.
 sched      the round-based cache-aware scheduling simulation.
+fp4        the 4-bit KV format: codes, scales, packed pool rows.
+rope       rotary positions and their frequency scalings.
 mla        MLA decode attention in the latent space (one stored row per
            token, read as key and, its latent prefix, as value).
 
@@ -30,4 +32,4 @@ pages or the mathematics fix (brute force, closed forms, worked examples,
 library special cases).
 """
 
-from . import tree, groups, attention, kvbytes, fp8, sched, mla  # noqa: F401
+from . import tree, groups, attention, kvbytes, fp8, fp4, rope, sched, mla  # noqa: F401

@@ -22,6 +22,7 @@ SGL_OK = 0
 SGL_DTYPE_F32 = 0
 SGL_DTYPE_BF16 = 1
 SGL_DTYPE_BF16_FP8KV = 2
+SGL_DTYPE_BF16_FP4KV = 3
 
 
 class SglError(RuntimeError):
@@ -86,6 +87,17 @@ class SglSimStats(ctypes.Structure):
                 ("evicted_tokens", ctypes.c_int64)]
 
 
+class SglRopeParams(ctypes.Structure):
+    _fields_ = [("head_dim", ctypes.c_int32), ("rot_dim", ctypes.c_int32), ("rot_offset", ctypes.c_int32),
+                ("layout", ctypes.c_int32), ("scaling", ctypes.c_int32), ("theta", ctypes.c_double),
+                ("factor", ctypes.c_double), ("original_positions", ctypes.c_int64), ("low", ctypes.c_double),
+                ("high", ctypes.c_double), ("attention_factor", ctypes.c_double)]
+
+
+SGL_ROPE_HALF, SGL_ROPE_PAIRS = 0, 1
+(SGL_ROPE_SCALE_NONE, SGL_ROPE_SCALE_LINEAR, SGL_ROPE_SCALE_NTK, SGL_ROPE_SCALE_YARN,
+ SGL_ROPE_SCALE_BANDED) = range(5)
+
 SGL_SCHED_FCFS, SGL_SCHED_LPM = 0, 1
 SGL_INSERT_AT_PREFILL, SGL_INSERT_AT_FINISH = 0, 1
 
@@ -139,6 +151,17 @@ _SIGS = {
     "sgl_mla_decode_plan": (ctypes.c_int, [ctypes.POINTER(SglMlaParams), _I32P, ctypes.POINTER(SglPrefixGroups),
                                            ctypes.POINTER(_P), ctypes.POINTER(ctypes.c_size_t)]),
     "sgl_mla_decode_attn": (ctypes.c_int, [_P, _P, _P, ctypes.c_int64, _P, _P, _P, _P, _P, ctypes.c_size_t, _P]),
+    "sgl_fp4_row_bytes": (ctypes.c_int, [ctypes.c_int32, ctypes.c_int32, _I64P]),
+    "sgl_rope_create": (ctypes.c_int, [ctypes.POINTER(SglRopeParams), ctypes.POINTER(_P)]),
+    "sgl_rope_destroy": (None, [_P]),
+    "sgl_rope": (ctypes.c_int, [_P, ctypes.c_int32, _P, ctypes.c_int64, ctypes.c_int32, _P, ctypes.c_int64,
+                                ctypes.c_int32, _P, ctypes.c_int64, _P, ctypes.c_int64, _P, ctypes.c_int64, _P]),
+    "sgl_kv_append": (ctypes.c_int, [_P, ctypes.POINTER(SglAttnParams), _P, ctypes.c_int64, _P, ctypes.c_int64, _P,
+                                     ctypes.c_int64, _P, _P, _P, ctypes.c_int64, _P, _P, ctypes.c_int64, _P,
+                                     ctypes.c_int64, _P, ctypes.c_size_t, _P]),
+    "sgl_mla_kv_append": (ctypes.c_int, [_P, ctypes.POINTER(SglMlaParams), _P, ctypes.c_int64, _P, ctypes.c_int64, _P,
+                                         _P, ctypes.c_int64, _P, _P, ctypes.c_int64, _P, ctypes.c_int64, _P,
+                                         ctypes.c_size_t, _P]),
 }
 
 _LIB = None
@@ -617,3 +640,129 @@ def sgl_decode_attn_noalloc(q, k_pool, v_pool, req_to_token, seq_lens, plan, o, 
                                        _dev(req_to_token, "req_to_token"), req_to_token.shape[1],
                                        _dev(seq_lens, "seq_lens"), plan.handle, _dev(o, "o"), _dev(lse, "lse"),
                                        _stream(stream)), "sgl_decode_attn_noalloc")
+
+
+# ------------------------------------- rotary positions, append to the cache
+def sgl_fp4_row_bytes(num_kv_heads, head_dim):
+    """Bytes of one row of a 4-bit pool (uint8 [num_slots, row bytes])."""
+    b = ctypes.c_int64()
+    _ok(_lib().sgl_fp4_row_bytes(num_kv_heads, head_dim, ctypes.byref(b)), "sgl_fp4_row_bytes")
+    return b.value
+
+
+class Rope:
+    """Owns an sgl_rope_table handle; head_dim and rot_dim as given."""
+
+    def __init__(self, handle, head_dim, rot_dim):
+        self.handle = handle
+        self.head_dim = head_dim
+        self.rot_dim = rot_dim
+
+    def __del__(self):
+        if self.handle and _LIB is not None:
+            _LIB.sgl_rope_destroy(self.handle)
+            self.handle = None
+
+
+def sgl_rope_create(head_dim, rot_dim=0, rot_offset=0, layout=SGL_ROPE_HALF, scaling=SGL_ROPE_SCALE_NONE, theta=10000.0,
+                    factor=1.0, original_positions=0, low=0.0, high=0.0, attention_factor=0.0):
+    """The frequencies of a rotation (rot_dim 0: the whole head from rot_offset on)."""
+    p = SglRopeParams(head_dim, rot_dim or head_dim - rot_offset, rot_offset, layout, scaling, theta, factor,
+                      original_positions, low, high, attention_factor)
+    h = _P()
+    _ok(_lib().sgl_rope_create(ctypes.byref(p), ctypes.byref(h)), "sgl_rope_create")
+    return Rope(h, p.head_dim, p.rot_dim)
+
+
+def _rows(t, what, heads=None, dim=None, dtype=None, n=None):
+    """A CUDA tensor [rows, heads, dim] whose heads are contiguous in each row: (address, row stride)."""
+    import torch
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError("%s must be a CUDA tensor" % what)
+    if t.dim() != 3 or (heads is not None and t.shape[1] != heads) or (dim is not None and t.shape[2] != dim):
+        raise ValueError("%s must have shape [rows, %s, %s]" % (what, "heads" if heads is None else heads, dim))
+    if n is not None and t.shape[0] != n:
+        raise ValueError("%s must have %d rows" % (what, n))
+    if dtype is not None and t.dtype != dtype:
+        raise TypeError("%s must be %s" % (what, dtype))
+    if (t.shape[2] > 1 and t.stride(2) != 1) or (t.shape[1] > 1 and t.stride(1) != t.shape[2]):
+        raise ValueError("%s must hold each row's heads contiguously" % what)
+    return t.data_ptr(), (t.stride(0) if t.shape[0] > 1 else t.shape[1] * t.shape[2])
+
+
+def _ints(t, what, shape):
+    import torch
+    p = _dev(t, what)
+    if t.dtype != torch.int32 or tuple(t.shape) != shape:
+        raise ValueError("%s must be int32 of shape %s" % (what, shape))
+    return p
+
+
+def sgl_rope(rope, q, k, positions, q_out=None, k_out=None, stream=None):
+    """Rotary positions of q [N, Hq, head_dim] and k [N, Hk, head_dim] (either may be None; rows may be strided, as
+    columns of a fused projection are) into q_out and k_out (None: in place).  positions: int32 [N]."""
+    import torch
+    some = q if q is not None else k
+    if some is None:
+        raise ValueError("q or k must be given")
+    n, dt = some.shape[0], some.dtype
+    if dt not in (torch.float32, torch.bfloat16):
+        raise TypeError("q and k must be float32 or bfloat16")
+    args = []
+    for x, out, what in ((q, q_out, "q"), (k, k_out, "k")):
+        if x is None:
+            args.append((None, 0, 0, None, 0))
+            continue
+        p, st = _rows(x, what, None, rope.head_dim, dt, n)
+        po, so = _rows(x if out is None else out, what + "_out", x.shape[1], rope.head_dim, dt, n)
+        args.append((p, st, x.shape[1], po, so))
+    (pq, sq, hq, pqo, sqo), (pk, sk, hk, pko, sko) = args
+    _ok(_lib().sgl_rope(rope.handle, SGL_DTYPE_F32 if dt == torch.float32 else SGL_DTYPE_BF16, pq, sq, hq, pk, sk, hk,
+                        _ints(positions, "positions", (n,)), n, pqo, sqo, pko, sko, _stream(stream)), "sgl_rope")
+
+
+def sgl_kv_append(rope, params, q, k_new, v_new, k_pool, v_pool, req_to_token, lens, extend_lens, q_out, workspace,
+                  stream=None):
+    """New keys and values [N, Hkv, d] into the paged pools, keys and queries rotated on the way (rope None: not
+    rotated; q and q_out None: keys and values only).  extend_lens given: N = the sum of extend_lens (or more, in a
+    padded batch) rows ordered by request, row i of request r at position lens[r] + i; None: row r is request r's
+    newest token, at position lens[r] - 1."""
+    import torch
+    dt = torch.float32 if params.dtype == SGL_DTYPE_F32 else torch.bfloat16
+    n, hkv, d = k_new.shape[0], params.num_kv_heads, params.head_dim
+    pk, sk = _rows(k_new, "k_new", hkv, d, dt)
+    pv, sv = _rows(v_new, "v_new", hkv, d, dt, n)
+    pq = pqo = None
+    sq = sqo = 0
+    if q is not None:
+        pq, sq = _rows(q, "q", params.num_qo_heads, d, dt, n)
+    if q_out is not None:
+        pqo, sqo = _rows(q_out, "q_out", params.num_qo_heads, d, dt, n)
+    B = (params.batch,)
+    _ok(_lib().sgl_kv_append(None if rope is None else rope.handle, ctypes.byref(params), pq, sq, pk, sk, pv, sv,
+                             _dev(k_pool, "k_pool"), _dev(v_pool, "v_pool"), _dev(req_to_token, "req_to_token"),
+                             req_to_token.shape[1], _ints(lens, "lens", B),
+                             None if extend_lens is None else _ints(extend_lens, "extend_lens", B), n, pqo, sqo,
+                             _dev(workspace, "workspace"), workspace.numel() * workspace.element_size(),
+                             _stream(stream)), "sgl_kv_append")
+
+
+def sgl_mla_kv_append(rope, params, q, kv_new, kv_pool, req_to_token, lens, extend_lens, q_out, workspace, stream=None):
+    """sgl_kv_append for an MLA pool: kv_new [N, 576] (latent, then position part), q [N, Hq, 576], bf16."""
+    import torch
+    dt, d = torch.bfloat16, params.latent_dim + params.rope_dim
+    n = kv_new.shape[0]
+    pk, sk = _rows(kv_new.unsqueeze(1) if kv_new.dim() == 2 else kv_new, "kv_new", 1, d, dt)
+    pq = pqo = None
+    sq = sqo = 0
+    if q is not None:
+        pq, sq = _rows(q, "q", params.num_qo_heads, d, dt, n)
+    if q_out is not None:
+        pqo, sqo = _rows(q_out, "q_out", params.num_qo_heads, d, dt, n)
+    B = (params.batch,)
+    _ok(_lib().sgl_mla_kv_append(None if rope is None else rope.handle, ctypes.byref(params), pq, sq, pk, sk,
+                                 _dev(kv_pool, "kv_pool"), _dev(req_to_token, "req_to_token"), req_to_token.shape[1],
+                                 _ints(lens, "lens", B),
+                                 None if extend_lens is None else _ints(extend_lens, "extend_lens", B), n, pqo, sqo,
+                                 _dev(workspace, "workspace"), workspace.numel() * workspace.element_size(),
+                                 _stream(stream)), "sgl_mla_kv_append")

@@ -428,6 +428,7 @@ static int extend_impl(const void* q_new, const void* k_new, const void* v_new, 
                        float* lse, void* workspace, size_t ws_bytes, sgl_stream_t stream) {
     int st = sgl::check_params(params);
     if (st) return st;
+    if (params->dtype == SGL_DTYPE_BF16_FP4KV) return SGL_ERR_UNSUPPORTED;
     const int32_t B = params->batch;
     if (B > 0 && (!params->host_extend_lens || !params->host_prefix_lens || !prefix_lens || !extend_lens))
         return SGL_ERR_INVALID_ARG;

@@ -48,9 +48,13 @@ int check_params(const sgl_attn_params* p) {
     if (!p) return SGL_ERR_INVALID_ARG;
     if (p->batch < 0 || p->num_qo_heads <= 0 || p->num_kv_heads <= 0 || p->num_slots < 0 || p->page_size < 1)
         return SGL_ERR_INVALID_ARG;
-    if (p->dtype != SGL_DTYPE_F32 && p->dtype != SGL_DTYPE_BF16 && p->dtype != SGL_DTYPE_BF16_FP8KV)
+    if (p->dtype != SGL_DTYPE_F32 && p->dtype != SGL_DTYPE_BF16 && p->dtype != SGL_DTYPE_BF16_FP8KV &&
+        p->dtype != SGL_DTYPE_BF16_FP4KV)
         return SGL_ERR_UNSUPPORTED;
     if (p->dtype == SGL_DTYPE_BF16_FP8KV && !(p->k_scale > 0.f && p->v_scale > 0.f)) return SGL_ERR_INVALID_ARG;
+    if (p->dtype == SGL_DTYPE_BF16_FP4KV && !(p->k_scale > 0.f && p->v_scale > 0.f && std::isfinite(p->k_scale) &&
+                                              std::isfinite(p->v_scale)))
+        return SGL_ERR_INVALID_ARG;
     if (p->head_dim != 64 && p->head_dim != 128) return SGL_ERR_UNSUPPORTED;
     if (p->num_qo_heads % p->num_kv_heads) return SGL_ERR_UNSUPPORTED;
     int G = p->num_qo_heads / p->num_kv_heads;
@@ -104,6 +108,7 @@ int sgl_decode_plan(const sgl_attn_params* p, const int32_t* seq_lens, const sgl
                     sgl_plan** plan_out, size_t* workspace_bytes) {
     int st = sgl::check_params(p);
     if (st) return st;
+    if (p->dtype == SGL_DTYPE_BF16_FP4KV) return SGL_ERR_UNSUPPORTED;
     if (!g || !plan_out || !workspace_bytes) return SGL_ERR_INVALID_ARG;
     const int32_t B = p->batch;
     if (B > 0 && !seq_lens) return SGL_ERR_INVALID_ARG;
@@ -380,6 +385,7 @@ int sgl_plan_info(const sgl_plan* plan, sgl_plan_info_t* out) {
 int sgl_extend_workspace_bytes(const sgl_attn_params* p, size_t* bytes) {
     int st = sgl::check_params(p);
     if (st) return st;
+    if (p->dtype == SGL_DTYPE_BF16_FP4KV) return SGL_ERR_UNSUPPORTED;
     if (!bytes) return SGL_ERR_INVALID_ARG;
     *bytes = sgl::kWsAlign;   // the error word
     return SGL_OK;

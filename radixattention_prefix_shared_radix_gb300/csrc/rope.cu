@@ -1,0 +1,650 @@
+// Rotary positions, and the append of new keys and values to the paged pools
+// with the rotation on the way.
+//
+// Rotation: with angle t = p f_j for position p and pair j, each pair (a, b)
+// of a head becomes (a cos t - b sin t, b cos t + a sin t), computed in fp32
+// and rounded once.  Pair j is elements (j, j + rot/2) (half layout) or
+// (2j, 2j + 1) (pairs layout) of the head's rotated part.
+//
+// Angles: a table of cosines and sines would have to be read (512 bytes per
+// token of a 128-wide head, and a table as long as the longest context), and
+// p f_j in fp32 is off by p 2^-24 radians, which is wrong beyond a few
+// thousand positions.  Instead a frequency is a 64-bit fixed-point fraction
+// of a turn: p times it, modulo 2^64, is the fraction of a turn that the
+// angle stands at, off by p 2^-65 turns at most, with one integer product
+// and no range reduction.  The nearest quarter turn is split off before the
+// conversion to fp32, so that the fp32 angle is at most an eighth of a turn.
+//
+// Work: a CTA takes T tokens (and, for a few tokens, a slice of their
+// heads).  One warp per token finds its request, position and slot; then all
+// threads compute the tokens' sines and cosines into shared memory, once for
+// all heads; then each thread takes units of 16 elements -- two 16-byte (32
+// for fp32) pieces that the rotation pairs up -- from the new rows to the
+// outputs.  The first unit's loads are issued before the positions are
+// known.  Memory-bound: rows are read and written once.
+//
+// ["SGLang 深度解读" (luoboask.github.io) section "5. Attention 层": the new
+// tokens' K/V are stored into token_to_kv_pool at their req_to_token slots
+// before attention; CS349D lecture-16 notes §5.1: the position part of an
+// MLA row is rotated, its latent part is not]
+
+#include <algorithm>
+#include <cmath>
+#include <cstring>
+#include <new>
+
+#include "common.h"
+#include "fp4.cuh"
+
+// Frequencies of the rotated pairs (host object).
+struct sgl_rope_table {
+    sgl_rope_params p;
+    float amplitude;                 // multiplies cos and sin
+    uint64_t turn[SGL_ROPE_MAX_DIM / 2];   // 2^64 / (2 pi) radians per position, rounded
+};
+
+namespace {
+
+using namespace sgldev;
+
+constexpr int kThreads = 256;
+constexpr int kMaxT = 4;             // tokens per CTA
+constexpr int kMaxHalf = SGL_ROPE_MAX_DIM / 2;
+
+enum { kPoolNone = 0, kPoolSame = 1, kPoolE4m3 = 2, kPoolFp4 = 3 };
+
+struct RopeArgs {
+    // rows [n_rows, heads, d], a row every `stride` elements
+    const void *q, *k, *v;
+    int64_t qs, ks, vs;
+    void *qo, *ko;                   // rotated rows (ko: without pools)
+    int64_t qos, kos;
+    uint8_t *kp, *vp;                // pools
+    const int32_t* positions;        // rotation only
+    const int32_t* r2t;
+    int64_t ld;
+    const int32_t *lens, *ext;       // ext null: one token per request at lens[r] - 1
+    uint32_t* err;
+    int64_t n_rows, num_slots;
+    int B, Hq, Hk, Hv, d;
+    int rot, off;                    // rotated part [off, off + rot) of a head (rot 0: none)
+    int pairs;                       // layout
+    int T, units, slice;             // tokens per CTA, units per token, units per CTA and token
+    int row_bytes;                   // bytes of a pool row
+    bool copy_q;                     // q_out is not q: the part that is not rotated is copied
+    float k_scale, v_scale, amplitude;
+    uint64_t turn[kMaxHalf];
+};
+
+// request and index within it of new row n: the first r with
+// ext[0] + .. + ext[r] > n.  One warp, 128 requests per round of loads.
+__device__ __forceinline__ bool find_request(const int32_t* ext, int B, int64_t n, int lane, int* req, int* idx) {
+    int64_t acc = 0;
+    for (int b = 0; b < B; b += 128) {
+        int e[4];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+            const int r = b + 32 * c + lane;
+            e[c] = r < B ? max(__ldg(ext + r), 0) : 0;
+        }
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+            int64_t s = e[c];
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int64_t y = __shfl_up_sync(0xffffffffu, s, o);
+                if (lane >= o) s += y;
+            }
+            const uint32_t hit = __ballot_sync(0xffffffffu, acc + s > n);
+            if (hit) {
+                const int l = __ffs(hit) - 1;
+                *req = b + 32 * c + l;
+                *idx = (int)(n - acc - __shfl_sync(0xffffffffu, s - e[c], l));
+                return true;
+            }
+            acc += __shfl_sync(0xffffffffu, s, 31);
+        }
+    }
+    return false;
+}
+
+// cos and sin of the angle `ph` / 2^64 turns
+__device__ __forceinline__ float2 cos_sin_turn(uint64_t ph) {
+    const uint32_t quarter = (uint32_t)((ph + (1ull << 61)) >> 62);
+    const int64_t rest = (int64_t)(ph - ((uint64_t)quarter << 62));     // [-1/8, 1/8) turn
+    // half turns = rest / 2^63; 32 of its bits (an angle below 2^-34 turns is
+    // below the last bit of the products it enters)
+    float s, c;
+    sincospif((float)(int32_t)(rest >> 30) * 0x1p-33f, &s, &c);
+    float2 r = (quarter & 1u) ? make_float2(-s, c) : make_float2(c, s);
+    if (quarter & 2u) r = make_float2(-r.x, -r.y);
+    return r;
+}
+
+// eight consecutive elements as loaded
+template <typename T>
+struct Eight;
+template <>
+struct Eight<bf16> {
+    uint4 w;
+    __device__ __forceinline__ void load(const void* base, int64_t at) {
+        w = *reinterpret_cast<const uint4*>(static_cast<const bf16*>(base) + at);
+    }
+    __device__ __forceinline__ void put(bf16* dst) const { *reinterpret_cast<uint4*>(dst) = w; }
+    __device__ __forceinline__ void set(const float* x) {
+        w = make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7]));
+    }
+    __device__ __forceinline__ void get(float* x) const {
+        const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            x[2 * i] = __uint_as_float(u[i] << 16);
+            x[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+        }
+    }
+};
+template <>
+struct Eight<float> {
+    float4 a, b;
+    __device__ __forceinline__ void load(const void* base, int64_t at) {
+        const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(base) + at);
+        a = p[0];
+        b = p[1];
+    }
+    __device__ __forceinline__ void put(float* dst) const {
+        reinterpret_cast<float4*>(dst)[0] = a;
+        reinterpret_cast<float4*>(dst)[1] = b;
+    }
+    __device__ __forceinline__ void set(const float* x) {
+        a = make_float4(x[0], x[1], x[2], x[3]);
+        b = make_float4(x[4], x[5], x[6], x[7]);
+    }
+    __device__ __forceinline__ void get(float* x) const {
+        x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
+        x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+    }
+};
+// a unit of 16 elements of one head of one token
+struct Unit {
+    int part;        // 0: q, 1: k, 2: v
+    int h;           // head
+    int e0, e1;      // its two runs of eight elements within the head
+    int fr;          // first frequency, or -1: not rotated
+};
+__device__ __forceinline__ Unit unit_of(const RopeArgs& a, int u) {
+    const int uph = a.d >> 4;
+    int hh = u / uph;
+    const int c = u - hh * uph;
+    Unit x;
+    x.part = 0;
+    if (hh >= a.Hq) {
+        hh -= a.Hq;
+        x.part = 1;
+        if (hh >= a.Hk) {
+            hh -= a.Hk;
+            x.part = 2;
+        }
+    }
+    x.h = hh;
+    const int rc = c - (a.off >> 4);
+    x.e0 = 16 * c;
+    x.e1 = x.e0 + 8;
+    x.fr = -1;
+    if (x.part < 2 && rc >= 0 && rc < (a.rot >> 4)) {
+        x.fr = 8 * rc;
+        if (!a.pairs) {
+            x.e0 = a.off + 8 * rc;
+            x.e1 = x.e0 + (a.rot >> 1);
+        }
+    }
+    return x;
+}
+
+// largest magnitude of eight bf16 values as a pair of 16-bit patterns
+// (patterns order like magnitudes, NaN above infinity)
+__device__ __forceinline__ uint32_t amax8(uint4 w) {
+    const uint32_t m = 0x7fff7fffu;
+    return __vmaxu2(__vmaxu2(w.x & m, w.y & m), __vmaxu2(w.z & m, w.w & m));
+}
+
+template <typename T, int POOL>
+__global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ RopeArgs a) {
+    __shared__ __align__(16) float2 cs[kMaxT][kMaxHalf];
+    __shared__ int s_pos[kMaxT], s_slot[kMaxT];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int64_t n0 = (int64_t)blockIdx.x * a.T;
+    const int u0 = blockIdx.y * a.slice;                       // this CTA's units of each token
+    const int nu = min(a.slice, a.units - u0);
+    const int total = a.T * nu;
+    grid_dep_wait();      // launched as a programmatic dependent: inputs may come from the kernel before
+    grid_dep_launch();
+    auto row_ptr = [&](const Unit& x, int64_t n, int64_t* at) -> const void* {
+        *at = n * (x.part == 0 ? a.qs : x.part == 1 ? a.ks : a.vs) + (int64_t)x.h * a.d;
+        return x.part == 0 ? a.q : x.part == 1 ? a.k : a.v;
+    };
+    // the first unit's elements, in flight while the positions are looked up
+    Eight<T> x0, x1;
+    Unit un{};
+    int tok = 0;
+    auto fetch = [&](int i) {
+        tok = i / nu;
+        if (i >= total || n0 + tok >= a.n_rows) {
+            tok = -1;
+            return;
+        }
+        un = unit_of(a, u0 + i - tok * nu);
+        int64_t at;
+        const void* p = row_ptr(un, n0 + tok, &at);
+        x0.load(p, at + un.e0);
+        x1.load(p, at + un.e1);
+    };
+    fetch(tid);
+    // position and slot of each token: -1 where there is nothing to do
+    if (warp < a.T) {
+        const int64_t n = n0 + warp;
+        int pos = -1, slot = -1;
+        if (n < a.n_rows) {
+            if constexpr (POOL == kPoolNone) {
+                pos = __ldg(a.positions + n);
+            } else {
+                int r = (int)n, i = 0;
+                bool ok = true;
+                if (a.ext)
+                    ok = find_request(a.ext, a.B, n, lane, &r, &i);
+                if (ok) {
+                    const int64_t p = a.ext ? (int64_t)__ldg(a.lens + r) + i : (int64_t)__ldg(a.lens + r) - 1;
+                    // no context (decode): nothing to append; past the table: an error
+                    if (p >= a.ld || (p < 0 && a.ext)) {
+                        if (lane == 0) atomicOr(a.err, 2u);
+                    } else if (p >= 0) {
+                        pos = (int)p;
+                        slot = __ldg(a.r2t + (int64_t)r * a.ld + p);
+                        if (slot < 0 || slot >= a.num_slots) {
+                            if (lane == 0) atomicOr(a.err, 1u);
+                            slot = -1;
+                        }
+                    }
+                }
+            }
+        }
+        if (lane == 0) {
+            s_pos[warp] = pos;
+            s_slot[warp] = slot;
+        }
+    }
+    __syncthreads();
+    const int half = a.rot >> 1;
+    for (int i = tid; i < a.T * half; i += kThreads) {
+        const int t = i / half, j = i - t * half;
+        const int p = s_pos[t];
+        if (p >= 0) {
+            const float2 v = cos_sin_turn((uint64_t)(uint32_t)p * a.turn[j]);
+            cs[t][j] = make_float2(v.x * a.amplitude, v.y * a.amplitude);
+        }
+    }
+    __syncthreads();
+    // (whole warps go round: 4-bit blocks are finished across lanes)
+    for (int i0 = warp * 32; i0 < total; i0 += kThreads) {
+        const int t = tok;
+        const Unit x = un;
+        const bool live = t >= 0 && s_pos[t < 0 ? 0 : t] >= 0;
+        const int slot = live ? s_slot[t] : -1;
+        Eight<T> r0 = x0, r1 = x1;      // (what is not rotated keeps its bits)
+        fetch(i0 + kThreads + lane);
+        if (live && x.fr >= 0) {
+            float y[16];
+            r0.get(y);
+            r1.get(y + 8);
+            // (written out, so that every instantiation rounds alike)
+            const float4* c4 = reinterpret_cast<const float4*>(&cs[t][x.fr]);
+            float c[8], s[8];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float4 v = c4[j];
+                c[2 * j] = v.x;
+                s[2 * j] = v.y;
+                c[2 * j + 1] = v.z;
+                s[2 * j + 1] = v.w;
+            }
+            if (a.pairs) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const float p = y[2 * j], q = y[2 * j + 1];
+                    y[2 * j] = __fmaf_rn(p, c[j], -__fmul_rn(q, s[j]));
+                    y[2 * j + 1] = __fmaf_rn(q, c[j], __fmul_rn(p, s[j]));
+                }
+            } else {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const float p = y[j], q = y[j + 8];
+                    y[j] = __fmaf_rn(p, c[j], -__fmul_rn(q, s[j]));
+                    y[j + 8] = __fmaf_rn(q, c[j], __fmul_rn(p, s[j]));
+                }
+            }
+            r0.set(y);
+            r1.set(y + 8);
+        }
+        const int64_t n = n0 + t;
+        if (x.part == 0 || POOL == kPoolNone) {
+            if (live && (x.fr >= 0 || a.copy_q)) {
+                T* dst = x.part == 0 ? static_cast<T*>(a.qo) + n * a.qos : static_cast<T*>(a.ko) + n * a.kos;
+                dst += (int64_t)x.h * a.d;
+                r0.put(dst + x.e0);
+                r1.put(dst + x.e1);
+            }
+        }
+        if constexpr (POOL == kPoolSame) {
+            if (x.part > 0 && slot >= 0) {
+                T* dst = reinterpret_cast<T*>((x.part == 1 ? a.kp : a.vp) + (int64_t)slot * a.row_bytes) + x.h * a.d;
+                r0.put(dst + x.e0);
+                r1.put(dst + x.e1);
+            }
+        } else if constexpr (POOL == kPoolE4m3 || POOL == kPoolFp4) {
+            // quantised pools hold codes of the rows' bf16 values, as an
+            // unfused rotation would have left them
+            const float scale = x.part == 1 ? a.k_scale : a.v_scale;
+            uint8_t* row = (x.part == 1 ? a.kp : a.vp) + (int64_t)max(slot, 0) * a.row_bytes;
+            float z[16];
+            r0.get(z);
+            r1.get(z + 8);
+            if constexpr (POOL == kPoolE4m3) {
+                if (x.part > 0 && slot >= 0) {
+#pragma unroll
+                    for (int b = 0; b < 2; ++b) {
+                        uint32_t c[4];
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            uint16_t h;
+                            const float lo = __fdiv_rn(z[8 * b + 2 * j], scale), hi = __fdiv_rn(z[8 * b + 2 * j + 1], scale);
+                            asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(h) : "f"(hi), "f"(lo));
+                            c[j] = h;
+                        }
+                        *reinterpret_cast<uint2*>(row + x.h * a.d + (b ? x.e1 : x.e0)) =
+                            make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
+                    }
+                }
+            } else {
+                // The scale of each run's block of 16.  The runs are the two
+                // halves of one block (one amax), or, rotated in the half
+                // layout, half of one block each, whose other halves the
+                // neighbouring unit holds.
+                uint32_t m0 = amax8(r0.w), m1 = amax8(r1.w);
+                const bool split = x.fr >= 0 && !a.pairs && a.rot > 16;
+                const int other = split ? ((x.fr & 8) ? lane - 1 : lane + 1) : lane;
+                const uint32_t o0 = __shfl_sync(0xffffffffu, m0, other & 31), o1 = __shfl_sync(0xffffffffu, m1, other & 31);
+                m0 = __vmaxu2(m0, split ? o0 : m1);
+                m1 = split ? __vmaxu2(m1, o1) : m0;
+                if (x.part > 0 && slot >= 0) {
+                    const int co = fp4_code_off(x.h, a.d), so = fp4_scale_off(x.h, x.part == 1 ? a.Hk : a.Hv, a.d);
+#pragma unroll
+                    for (int b = 0; b < 2; ++b) {
+                        const uint32_t m = b ? m1 : m0;
+                        const float amax = __uint_as_float(max(m & 0xffffu, m >> 16) << 16);
+                        const uint32_t sf = e4m3_of(__fdiv_rn(amax, 6.f * scale));
+                        const float f = e4m3_value(sf) * scale;
+                        float c[8];
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) c[j] = f > 0.f ? __fdiv_rn(z[8 * b + j], f) : z[8 * b + j] * 0.f;
+                        const int e = b ? x.e1 : x.e0;
+                        *reinterpret_cast<uint32_t*>(row + co + e / 2) = e2m1x8_of(c);
+                        if ((e & 8) == 0) row[so + e / 16] = (uint8_t)sf;
+                    }
+                }
+            }
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Host side
+// ---------------------------------------------------------------------------
+int cuda_status(cudaError_t e) {
+    if (e == cudaSuccess) return SGL_OK;
+    sgl::set_cuda_error(static_cast<int>(e));
+    return SGL_ERR_CUDA;
+}
+bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+// rows of `heads` heads, `stride` elements apart, of es bytes each
+bool rows_ok(const void* p, int64_t stride, int heads, int d, int es) {
+    return p && aligned16(p) && stride >= (int64_t)heads * d && stride * es % 16 == 0;
+}
+
+template <typename T, int POOL>
+int launch(RopeArgs& a, cudaStream_t s) {
+    if (a.n_rows == 0 || a.units == 0) return SGL_OK;
+    // Tokens per CTA and slices of a token's heads: four tokens share a CTA
+    // once that leaves every SM its eight CTAs; below one CTA per SM a
+    // token's heads are spread over several (of at least 64 units each).
+    constexpr int kSms = 152;
+    a.T = a.n_rows >= (int64_t)kMaxT * kSms * 4 ? kMaxT : 1;
+    int slices = 1;
+    if (a.n_rows < kSms) slices = (int)std::min<int64_t>((kSms + a.n_rows - 1) / a.n_rows, (a.units + 63) / 64);
+    a.slice = ((a.units + slices - 1) / slices + 31) / 32 * 32;
+    slices = (a.units + a.slice - 1) / a.slice;
+    const int64_t ctas = (a.n_rows + a.T - 1) / a.T;
+    if (ctas > INT32_MAX) return SGL_ERR_UNSUPPORTED;
+    cudaLaunchAttribute pdl[1];
+    pdl[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    pdl[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)ctas, (unsigned)slices);
+    cfg.blockDim = dim3(kThreads);
+    cfg.stream = s;
+    cfg.attrs = pdl;
+    cfg.numAttrs = 1;
+    return cuda_status(cudaLaunchKernelEx(&cfg, rope_kernel<T, POOL>, a));
+}
+
+void set_table(RopeArgs& a, const sgl_rope_table* t) {
+    if (!t) return;
+    a.rot = t->p.rot_dim;
+    a.off = t->p.rot_offset;
+    a.pairs = t->p.layout == SGL_ROPE_PAIRS;
+    a.amplitude = t->amplitude;
+    std::memcpy(a.turn, t->turn, sizeof(uint64_t) * (size_t)(t->p.rot_dim / 2));
+}
+
+// the arguments that both appends share, checked
+int append_rows(RopeArgs& a, const sgl_rope_table* rope, int es, int64_t n_rows, const int32_t* req_to_token, int64_t ld,
+                const int32_t* lens, const int32_t* extend_lens, int32_t batch, const void* q, int64_t q_stride,
+                void* q_out, int64_t q_out_stride, int Hq, int d, void* workspace, size_t ws_bytes) {
+    if (n_rows < 0 || ld < 0 || (rope && rope->p.head_dim != d)) return SGL_ERR_INVALID_ARG;
+    if (!extend_lens && n_rows > batch) return SGL_ERR_INVALID_ARG;
+    if (!workspace || (reinterpret_cast<uintptr_t>(workspace) % sgl::kWsAlign) != 0 || ws_bytes < sgl::kWsAlign)
+        return SGL_ERR_WORKSPACE;
+    if (n_rows > 0 && (!req_to_token || !lens)) return SGL_ERR_INVALID_ARG;
+    if (!q != !q_out) return SGL_ERR_INVALID_ARG;
+    if (n_rows > 0 && q && !(rows_ok(q, q_stride, Hq, d, es) && rows_ok(q_out, q_out_stride, Hq, d, es)))
+        return SGL_ERR_INVALID_ARG;
+    if (q && q == q_out && q_stride != q_out_stride) return SGL_ERR_INVALID_ARG;
+    set_table(a, rope);
+    a.q = q;
+    a.qs = q_stride;
+    a.qo = q_out;
+    a.qos = q_out_stride;
+    a.Hq = q ? Hq : 0;
+    a.copy_q = q != q_out;
+    a.r2t = req_to_token;
+    a.ld = ld;
+    a.lens = lens;
+    a.ext = extend_lens;
+    a.B = batch;
+    a.err = static_cast<uint32_t*>(workspace);
+    a.n_rows = n_rows;
+    a.d = d;
+    return SGL_OK;
+}
+
+}  // namespace
+
+namespace sgl {
+int check_params(const sgl_attn_params* p);
+}
+
+extern "C" {
+
+int sgl_fp4_row_bytes(int32_t num_kv_heads, int32_t head_dim, int64_t* bytes) {
+    if (!bytes || num_kv_heads <= 0) return SGL_ERR_INVALID_ARG;
+    if ((head_dim != 64 && head_dim != 128) || num_kv_heads > (1 << 16)) return SGL_ERR_UNSUPPORTED;
+    *bytes = fp4_row_bytes(num_kv_heads, head_dim);
+    return SGL_OK;
+}
+
+int sgl_rope_create(const sgl_rope_params* p, sgl_rope_table** out) {
+    if (!p || !out) return SGL_ERR_INVALID_ARG;
+    const int n = p->rot_dim;
+    if (p->head_dim <= 0 || n <= 0 || p->rot_offset < 0 || (int64_t)p->rot_offset + n > p->head_dim)
+        return SGL_ERR_INVALID_ARG;
+    if (!(p->theta > 1.0) || !std::isfinite(p->theta) || !(p->attention_factor >= 0.0) ||
+        !std::isfinite(p->attention_factor))
+        return SGL_ERR_INVALID_ARG;
+    if (p->layout != SGL_ROPE_HALF && p->layout != SGL_ROPE_PAIRS) return SGL_ERR_UNSUPPORTED;
+    if (p->head_dim % 16 || p->head_dim > 1024 || n % 16 || n > SGL_ROPE_MAX_DIM || p->rot_offset % 16)
+        return SGL_ERR_UNSUPPORTED;
+    if (p->layout == SGL_ROPE_HALF && n != 16 && n % 32) return SGL_ERR_UNSUPPORTED;
+    const int kind = p->scaling;
+    if (kind < SGL_ROPE_SCALE_NONE || kind > SGL_ROPE_SCALE_BANDED) return SGL_ERR_UNSUPPORTED;
+    const double by = p->factor;
+    if (kind != SGL_ROPE_SCALE_NONE && !(by >= 1.0 && std::isfinite(by))) return SGL_ERR_INVALID_ARG;
+    const bool bands = kind == SGL_ROPE_SCALE_YARN || kind == SGL_ROPE_SCALE_BANDED;
+    if (bands && !(p->original_positions > 0 && p->low > 0.0 && p->high > p->low && std::isfinite(p->high)))
+        return SGL_ERR_INVALID_ARG;
+    auto* t = new (std::nothrow) sgl_rope_table();
+    if (!t) return SGL_ERR_INVALID_ARG;
+    t->p = *p;
+    const double two_pi = 6.283185307179586476925286766559;
+    const double orig = (double)p->original_positions;
+    double theta = p->theta;
+    if (kind == SGL_ROPE_SCALE_NTK) theta *= std::pow(by, (double)n / (n - 2));
+    double lo = 0.0, hi = 1.0;
+    if (kind == SGL_ROPE_SCALE_YARN) {
+        // the pair index at which a pair makes `turns` turns over the original positions
+        auto index = [&](double turns) { return n * std::log(orig / (turns * two_pi)) / (2.0 * std::log(p->theta)); };
+        lo = std::fmax(std::floor(index(p->high)), 0.0);
+        hi = std::fmin(std::ceil(index(p->low)), n - 1.0);
+        if (hi <= lo) hi = lo + 0.001;
+    }
+    for (int j = 0; j < n / 2; ++j) {
+        double f = std::pow(theta, -2.0 * j / n);
+        if (kind == SGL_ROPE_SCALE_LINEAR) {
+            f /= by;
+        } else if (kind == SGL_ROPE_SCALE_YARN) {
+            const double w = std::fmin(std::fmax((j - lo) / (hi - lo), 0.0), 1.0);
+            f = f / by * w + f * (1.0 - w);
+        } else if (kind == SGL_ROPE_SCALE_BANDED) {
+            const double w = std::fmin(std::fmax((orig * f / two_pi - p->low) / (p->high - p->low), 0.0), 1.0);
+            f = f / by * (1.0 - w) + f * w;
+        }
+        // f < 1 radian, so the fraction of a turn is below 1/6
+        t->turn[j] = (uint64_t)std::nearbyint(std::ldexp(f / two_pi, 64));
+    }
+    double amp = p->attention_factor;
+    if (amp == 0.0) amp = kind == SGL_ROPE_SCALE_YARN ? 0.1 * std::log(by) + 1.0 : 1.0;
+    t->amplitude = (float)amp;
+    *out = t;
+    return SGL_OK;
+}
+
+void sgl_rope_destroy(sgl_rope_table* t) { delete t; }
+
+int sgl_rope(const sgl_rope_table* rope, int32_t dtype, const void* q, int64_t q_stride, int32_t num_q_heads,
+             const void* k, int64_t k_stride, int32_t num_k_heads, const int32_t* positions, int64_t n_rows, void* q_out,
+             int64_t q_out_stride, void* k_out, int64_t k_out_stride, sgl_stream_t stream) {
+    if (!rope || n_rows < 0 || num_q_heads < 0 || num_k_heads < 0) return SGL_ERR_INVALID_ARG;
+    if (dtype != SGL_DTYPE_F32 && dtype != SGL_DTYPE_BF16) return SGL_ERR_UNSUPPORTED;
+    if (n_rows == 0) return SGL_OK;
+    const int d = rope->p.head_dim, es = dtype == SGL_DTYPE_F32 ? 4 : 2;
+    if ((int64_t)num_q_heads + num_k_heads > INT32_MAX / 1024) return SGL_ERR_UNSUPPORTED;
+    if (!positions) return SGL_ERR_INVALID_ARG;
+    if (num_q_heads > 0 && !(rows_ok(q, q_stride, num_q_heads, d, es) && rows_ok(q_out, q_out_stride, num_q_heads, d, es)))
+        return SGL_ERR_INVALID_ARG;
+    if (num_k_heads > 0 && !(rows_ok(k, k_stride, num_k_heads, d, es) && rows_ok(k_out, k_out_stride, num_k_heads, d, es)))
+        return SGL_ERR_INVALID_ARG;
+    // in place: the same rows
+    if (num_q_heads > 0 && q == q_out && q_stride != q_out_stride) return SGL_ERR_INVALID_ARG;
+    if (num_k_heads > 0 && k == k_out && k_stride != k_out_stride) return SGL_ERR_INVALID_ARG;
+    RopeArgs a{};
+    set_table(a, rope);
+    a.q = q;
+    a.k = k;
+    a.qs = q_stride;
+    a.ks = k_stride;
+    a.qo = q_out;
+    a.ko = k_out;
+    a.qos = q_out_stride;
+    a.kos = k_out_stride;
+    a.positions = positions;
+    a.n_rows = n_rows;
+    a.Hq = num_q_heads;
+    a.Hk = num_k_heads;
+    a.d = d;
+    a.units = (num_q_heads + num_k_heads) * (d / 16);
+    a.copy_q = (num_q_heads > 0 && q != q_out) || (num_k_heads > 0 && k != k_out);
+    auto s = reinterpret_cast<cudaStream_t>(stream);
+    return es == 4 ? launch<float, kPoolNone>(a, s) : launch<bf16, kPoolNone>(a, s);
+}
+
+int sgl_kv_append(const sgl_rope_table* rope, const sgl_attn_params* params, const void* q, int64_t q_stride,
+                  const void* k_new, int64_t k_stride, const void* v_new, int64_t v_stride, void* k_pool, void* v_pool,
+                  const int32_t* req_to_token, int64_t ld, const int32_t* lens, const int32_t* extend_lens,
+                  int64_t n_rows, void* q_out, int64_t q_out_stride, void* workspace, size_t ws_bytes,
+                  sgl_stream_t stream) {
+    const int st = sgl::check_params(params);
+    if (st) return st;
+    const int d = params->head_dim, Hkv = params->num_kv_heads, es = params->dtype == SGL_DTYPE_F32 ? 4 : 2;
+    if ((int64_t)params->num_qo_heads + 2 * (int64_t)Hkv > INT32_MAX / 1024) return SGL_ERR_UNSUPPORTED;
+    RopeArgs a{};
+    if (const int e = append_rows(a, rope, es, n_rows, req_to_token, ld, lens, extend_lens, params->batch, q, q_stride,
+                                  q_out, q_out_stride, params->num_qo_heads, d, workspace, ws_bytes))
+        return e;
+    if (n_rows == 0) return SGL_OK;
+    if (!rows_ok(k_new, k_stride, Hkv, d, es) || !rows_ok(v_new, v_stride, Hkv, d, es)) return SGL_ERR_INVALID_ARG;
+    if (!k_pool || !v_pool || !aligned16(k_pool) || !aligned16(v_pool)) return SGL_ERR_INVALID_ARG;
+    a.k = k_new;
+    a.v = v_new;
+    a.ks = k_stride;
+    a.vs = v_stride;
+    a.kp = static_cast<uint8_t*>(k_pool);
+    a.vp = static_cast<uint8_t*>(v_pool);
+    a.num_slots = params->num_slots;
+    a.Hk = a.Hv = Hkv;
+    a.units = (a.Hq + 2 * Hkv) * (d / 16);
+    a.k_scale = params->k_scale;
+    a.v_scale = params->v_scale;
+    auto s = reinterpret_cast<cudaStream_t>(stream);
+    switch (params->dtype) {
+        case SGL_DTYPE_F32: a.row_bytes = Hkv * d * 4; return launch<float, kPoolSame>(a, s);
+        case SGL_DTYPE_BF16: a.row_bytes = Hkv * d * 2; return launch<bf16, kPoolSame>(a, s);
+        case SGL_DTYPE_BF16_FP8KV: a.row_bytes = Hkv * d; return launch<bf16, kPoolE4m3>(a, s);
+        default: a.row_bytes = fp4_row_bytes(Hkv, d); return launch<bf16, kPoolFp4>(a, s);
+    }
+}
+
+int sgl_mla_kv_append(const sgl_rope_table* rope, const sgl_mla_params* params, const void* q, int64_t q_stride,
+                      const void* kv_new, int64_t kv_stride, void* kv_pool, const int32_t* req_to_token, int64_t ld,
+                      const int32_t* lens, const int32_t* extend_lens, int64_t n_rows, void* q_out,
+                      int64_t q_out_stride, void* workspace, size_t ws_bytes, sgl_stream_t stream) {
+    if (!params || params->batch < 0 || params->num_slots < 0 || params->page_size < 1) return SGL_ERR_INVALID_ARG;
+    const int H = params->num_qo_heads, d = 576;
+    if (params->latent_dim != 512 || params->rope_dim != 64 || (H != 16 && H != 32 && H != 64 && H != 128) ||
+        params->num_slots > INT32_MAX)
+        return SGL_ERR_UNSUPPORTED;
+    RopeArgs a{};
+    if (const int e = append_rows(a, rope, 2, n_rows, req_to_token, ld, lens, extend_lens, params->batch, q, q_stride,
+                                  q_out, q_out_stride, H, d, workspace, ws_bytes))
+        return e;
+    if (n_rows == 0) return SGL_OK;
+    if (!rows_ok(kv_new, kv_stride, 1, d, 2) || !kv_pool || !aligned16(kv_pool)) return SGL_ERR_INVALID_ARG;
+    a.k = kv_new;
+    a.ks = kv_stride;
+    a.kp = static_cast<uint8_t*>(kv_pool);
+    a.num_slots = params->num_slots;
+    a.Hk = 1;
+    a.Hv = 0;
+    a.units = (a.Hq + 1) * (d / 16);
+    a.row_bytes = d * 2;
+    return launch<bf16, kPoolSame>(a, reinterpret_cast<cudaStream_t>(stream));
+}
+
+}  // extern "C"
