@@ -38,7 +38,11 @@ template <int D, bool F8>
 int launch_decode_fused(const sgl_plan* plan, const void* q, const void* kp, const void* vp, const int32_t* r2t,
                         int64_t ld, const int32_t* seq_lens, void* o, float* lse, unsigned char* ws, float scale_log2,
                         cudaStream_t s);
-template <int D, bool F8>
+template <int D>
+int launch_decode_fp4(const sgl_plan* plan, const void* q, const void* kp, const void* vp, const int32_t* r2t, int64_t ld,
+                      const int32_t* seq_lens, void* o, float* lse, unsigned char* ws, float scale_log2, cudaStream_t s);
+// KV: what the pools hold (0 bf16, 1 E4M3, 2 4-bit rows)
+template <int D, int KV>
 int launch_extend_tc(const void* q, const void* kp, const void* vp, const void* kn, const void* vn, void* kw, void* vw,
                      const int32_t* r2t, int64_t ld, const int32_t* pre, const int32_t* ext, int B, int64_t n_rows,
                      int64_t tiles, void* o, float* lse, uint32_t* err, int Hq, int Hkv, int64_t num_slots,
@@ -314,6 +318,10 @@ int launch_decode(const sgl_plan* plan, const void* q, const void* kp, const voi
     const sgl_attn_params& p = plan->params;
     const float sl2 = scale_log2_of(&p);
     if (p.batch == 0) return SGL_OK;
+    if (p.dtype == SGL_DTYPE_BF16_FP4KV) {
+        const int e = sgl::launch_decode_fp4<D>(plan, q, kp, vp, r2t, ld, seq_lens, o, lse, ws, sl2, s);
+        return e ? cuda_status(static_cast<cudaError_t>(e)) : SGL_OK;
+    }
     if (p.dtype == SGL_DTYPE_BF16 || p.dtype == SGL_DTYPE_BF16_FP8KV) {
         const int e = p.dtype == SGL_DTYPE_BF16
                           ? sgl::launch_decode_fused<D, false>(plan, q, kp, vp, r2t, ld, seq_lens, o, lse, ws, sl2, s)
@@ -351,7 +359,7 @@ int launch_extend(const sgl_attn_params* p, const void* q, const void* kp, const
         tiles += ((p->host_extend_lens[r] + tq - 1) / tq + 1) / 2;   // CTAs: pairs of query tiles
     }
     if (total_rows == 0) return SGL_OK;
-    if (p->dtype == SGL_DTYPE_BF16 || p->dtype == SGL_DTYPE_BF16_FP8KV) {
+    if (p->dtype != SGL_DTYPE_F32) {
         if (tiles > INT32_MAX) return SGL_ERR_UNSUPPORTED;
         if (p->dtype == SGL_DTYPE_BF16_FP8KV && kn) {
             // FP8 pools: the new rows are quantised into the pool first, and
@@ -364,12 +372,26 @@ int launch_extend(const sgl_attn_params* p, const void* q, const void* kp, const
             kn = vn = nullptr;
             kw = vw = nullptr;
         }
-        const int e = p->dtype == SGL_DTYPE_BF16_FP8KV
-                          ? sgl::launch_extend_tc<D, true>(q, kp, vp, kn, vn, kw, vw, r2t, ld, pre, ext, B, total_rows,
-                                                           tiles, o, lse, err, Hq, Hkv, p->num_slots, sl2, p->k_scale,
-                                                           p->v_scale, s)
-                          : sgl::launch_extend_tc<D, false>(q, kp, vp, kn, vn, kw, vw, r2t, ld, pre, ext, B, total_rows,
-                                                            tiles, o, lse, err, Hq, Hkv, p->num_slots, sl2, 1.f, 1.f, s);
+        if (p->dtype == SGL_DTYPE_BF16_FP4KV && kn) {
+            // 4-bit pools: likewise (the rows of the append, not rotated)
+            const int64_t row = (int64_t)Hkv * D;
+            if (const int st = sgl_kv_append(nullptr, p, nullptr, 0, kn, row, vn, row, kw, vw, r2t, ld, pre, ext,
+                                             total_rows, nullptr, 0, err, sgl::kWsAlign,
+                                             reinterpret_cast<sgl_stream_t>(s)))
+                return st;
+            kn = vn = nullptr;
+            kw = vw = nullptr;
+        }
+        int e;
+        if (p->dtype == SGL_DTYPE_BF16)
+            e = sgl::launch_extend_tc<D, 0>(q, kp, vp, kn, vn, kw, vw, r2t, ld, pre, ext, B, total_rows, tiles, o, lse,
+                                            err, Hq, Hkv, p->num_slots, sl2, 1.f, 1.f, s);
+        else if (p->dtype == SGL_DTYPE_BF16_FP8KV)
+            e = sgl::launch_extend_tc<D, 1>(q, kp, vp, kn, vn, kw, vw, r2t, ld, pre, ext, B, total_rows, tiles, o, lse,
+                                            err, Hq, Hkv, p->num_slots, sl2, p->k_scale, p->v_scale, s);
+        else
+            e = sgl::launch_extend_tc<D, 2>(q, kp, vp, kn, vn, kw, vw, r2t, ld, pre, ext, B, total_rows, tiles, o, lse,
+                                            err, Hq, Hkv, p->num_slots, sl2, p->k_scale, p->v_scale, s);
         if (e) return cuda_status(static_cast<cudaError_t>(e));
     } else {
         if (kn) {
@@ -428,7 +450,6 @@ static int extend_impl(const void* q_new, const void* k_new, const void* v_new, 
                        float* lse, void* workspace, size_t ws_bytes, sgl_stream_t stream) {
     int st = sgl::check_params(params);
     if (st) return st;
-    if (params->dtype == SGL_DTYPE_BF16_FP4KV) return SGL_ERR_UNSUPPORTED;
     const int32_t B = params->batch;
     if (B > 0 && (!params->host_extend_lens || !params->host_prefix_lens || !prefix_lens || !extend_lens))
         return SGL_ERR_INVALID_ARG;

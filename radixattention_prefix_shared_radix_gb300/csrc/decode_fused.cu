@@ -69,8 +69,8 @@
 // all are written, when HBM is idle and each merge is a few short round
 // trips.
 
+#include "decode_stream.cuh"
 #include "merge.cuh"
-#include "tc_tile.cuh"
 
 namespace sgl {
 namespace {
@@ -80,8 +80,7 @@ using namespace tc;
 
 constexpr int kHB = kDecHeadBlock;                       // consumer warps = KV heads of a piece (at most)
 constexpr int kNP = 16;                                  // KV positions per step
-constexpr int kSQ = 8;                                   // slot ring entries (lookups ahead of the copies)
-constexpr int kSlotEntry = 128;                          // 16 slots + step and piece fields (see below)
+using Ent = SlotEntry<kNP>;
 constexpr int kLookup = 2;                               // the lookup warp
 constexpr int kFirstProducer = 3;
 constexpr int kProducers = 4;                            // each issues 8 of a stage's 32 row copies
@@ -89,7 +88,6 @@ constexpr int kFirstConsumer = kFirstProducer + kProducers;
 constexpr int kFusedThreads = 32 * (kFirstConsumer + kHB);
 static_assert(DecCfg<128>::kThreads == kFusedThreads && DecCfg<64>::kThreads == kFusedThreads,
               "the tile roles take the whole CTA");
-static_assert((kSQ & (kSQ - 1)) == 0, "slot ring");
 static_assert((2 * kNP) % kProducers == 0 && 2 * kNP / kProducers <= 32, "row copies per producer warp");
 
 template <int D, bool F8 = false>
@@ -98,7 +96,7 @@ struct FusedLayout {
     static constexpr int ES = F8 ? 1 : 2;                // bytes per pool element
     static constexpr int PITCH = kHB * D * ES + 16;      // one token's K (or V) row of a head block, padded
     static constexpr int STAGE = 2 * kNP * PITCH;        // K rows, then V rows
-    static constexpr int SLOTW = kSQ * kSlotEntry;
+    static constexpr int SLOTW = kSQ * Ent::kBytes;
     static constexpr int DESC = 64;                      // stage descriptor bytes
     static constexpr int FIXED = 1024 + SLOTW + 8 * DESC + 64 + (2 * 8 + 2 * kSQ) * 8 + 1024;
     static constexpr int NSF0 = (232448 - FIXED) / STAGE;
@@ -124,172 +122,10 @@ struct FusedLayout {
     static_assert(TL::KEEP <= OFF_RING, "the ring clears the tile roles' kept area");
 };
 
-struct FusedArgs {
-    TcArgs t;
-    const int32_t* wptr;   // [n_ctas + 1] wide items of each CTA
-    const DecItem* narrow; // narrow pieces, longest first
-    int n_narrow;
-    int n_init;            // pieces assigned at launch: streaming CTA w starts on piece w
-    int n_tile_ctas;       // CTAs 0 .. n_tile_ctas-1 run the wide items first
-    uint32_t* sched;       // [2] next piece to hand out, producers finished (restored at the end)
-};
-
-__device__ __forceinline__ uint32_t movtrans(uint32_t x) {
-    uint32_t y;
-    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;\n" : "=r"(y) : "r"(x));
-    return y;
-}
-
-// D[16x8] += A[16x16] * B[16x8], f16 inputs, fp32 accumulate.
-__device__ __forceinline__ void mma16816_f16(float* c, const uint32_t* a, uint32_t b0, uint32_t b1) {
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
-        "{%0,%1,%2,%3};\n"
-        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-
-__device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel) {
-    uint32_t d;
-    asm("prmt.b32 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(sel));
-    return d;
-}
-__device__ __forceinline__ void lds128(uint32_t addr, uint32_t* w) {
-    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];\n" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(addr));
-}
-__device__ __forceinline__ void lds64(uint32_t addr, uint32_t* w) {
-    asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];\n" : "=r"(w[0]), "=r"(w[1]) : "r"(addr));
-}
-
-// stage descriptor flags
-constexpr int kFirst = 1;   // first step of its piece: the descriptor carries the piece's fields
-constexpr int kEnd = 4;     // no more pieces: the consumers stop
-
-// slot-ring entry (one looked-up step): 16 slots, then
-constexpr int kEntKvh = 64, kEntP0 = 68, kEntFlags = 72, kEntCm = 76, kEntPb = 80, kEntNh = 84, kEntNm = 88;
-constexpr int kEntMem = 96;   // kDecPieceMembers ints: the piece's member requests (first step only)
-static_assert(kEntMem + 4 * kDecPieceMembers <= kSlotEntry, "a slot entry holds a piece's members");
 // stage descriptor (a piece's first step also carries the piece's first KV
 // head and member requests, from which the consumers load their query rows)
 constexpr int kDescP0 = 0, kDescFlags = 4, kDescCm = 8, kDescPb = 12, kDescRows = 16, kDescNh = 20, kDescKvh = 24;
 constexpr int kDescMem = 32;   // kDecPieceMembers ints
-
-// ---------------------------------------------------------------------------
-// Lookup warp (one per CTA)
-// ---------------------------------------------------------------------------
-// Walks this CTA's pieces (its launch piece, whose record and members were
-// loaded before the dependency wait, then pieces taken from the run-time
-// counter) and fills the slot ring up to kSQ steps ahead of the producers:
-// per step the 16 slots (4-byte cp.async from req_to_token; positions past
-// the piece's end marked), the step's first KV head, position and flags,
-// and for a piece's first step its partial base, clamped end, head and
-// member counts and member requests.  Each entry's barrier (SLOTFULL)
-// completes when the lanes' cp.async have landed and lane 0 has written the
-// fields; the producers free it (SLOTFREE).  An entry with no KV head ends
-// the stream.  Global loads (the counter, records, seq_lens) stall only this
-// warp, which runs ahead of the copies.
-template <int D, bool F8>
-__device__ __noinline__ void stream_lookup(const FusedArgs& f, int gw, uint32_t lrec, uint32_t sring,
-                                           uint32_t sfull, uint32_t sfree, int lane) {
-    constexpr int32_t kPastEnd = INT32_MIN;
-    const int32_t* const r2t = f.t.r2t;
-    const int32_t* const members = f.t.members;
-    const int32_t* const seq_lens = f.t.seq_lens;
-    const int64_t ld = f.t.ld;
-    uint32_t* const err = f.t.err;
-    const DecItem* const pieces = f.narrow;
-    const int n_narrow = f.n_narrow;
-    uint32_t* const sched = f.sched;
-    const bool launch = gw >= 0 && gw < f.n_init;
-    bool timed_out = false;
-    int nlook = 0;
-    // one ring entry: wait for it to be free, fill it, arm its barrier.  A
-    // piece's first entry also records its end clamped to seq_len (len, whose
-    // load is only waited for once the slot lookups are issued)
-    auto entry = [&](int kvh, int row, int p0, int e, int flags, int len, int pb, int nh, int nm, int mem) {
-        const int ent = nlook & (kSQ - 1);
-        const uint32_t eb = sring + ent * kSlotEntry;
-        if (!timed_out && !mbar_wait(sfree + 8 * ent, ((nlook / kSQ) & 1) ^ 1)) {
-            atomicOr(err, 4u);
-            timed_out = true;
-        }
-        if (timed_out) return;
-        if (lane < kNP) {
-            const int p = p0 + lane;
-            if (kvh >= 0 && p < e)
-                cp_async4(eb + lane * 4, r2t + (int64_t)row * ld + p);
-            else
-                st_shared_s32(eb + lane * 4, kPastEnd);
-        }
-        if (lane == 0) {
-            st_shared_s32(eb + kEntKvh, kvh);
-            st_shared_s32(eb + kEntP0, p0);
-            st_shared_s32(eb + kEntFlags, flags);
-            if (flags & kFirst) {
-                int cm = e;
-                if (e > len) {   // planned beyond seq_len: mask the excess, flag it
-                    atomicOr(err, 2u);
-                    cm = len > p0 ? len : p0;
-                }
-                st_shared_s32(eb + kEntCm, cm);
-                st_shared_s32(eb + kEntPb, pb);
-                st_shared_s32(eb + kEntNh, nh);
-                st_shared_s32(eb + kEntNm, nm);
-            }
-        }
-        if ((flags & kFirst) && lane < kDecPieceMembers) st_shared_s32(eb + kEntMem + 4 * lane, mem);
-        cp_async_arrive_noinc(sfull + 8 * ent);   // each lane, once its lookups have landed
-        __syncwarp();
-        if (lane == 0) mbar_arrive(sfull + 8 * ent);   // the fields
-        ++nlook;
-    };
-    bool first_piece = true;
-    for (;;) {
-        int row, b, e, kvh, mb, nm, pb, nh, mem;
-        if (first_piece && launch) {
-            row = ld_shared_s32(lrec); b = ld_shared_s32(lrec + 4); e = ld_shared_s32(lrec + 8);
-            kvh = ld_shared_s32(lrec + 12); mb = ld_shared_s32(lrec + 16); nm = ld_shared_s32(lrec + 20);
-            pb = ld_shared_s32(lrec + 24); nh = ld_shared_s32(lrec + 28);
-            mem = lane < kDecPieceMembers ? ld_shared_s32(lrec + 32 + 4 * lane) : 0;
-        } else {
-            int taken = 0;
-            if (lane == 0) taken = (int)atomicAdd(sched, 1u);
-            taken = __shfl_sync(0xffffffffu, taken, 0);
-            if (taken >= n_narrow) break;
-            const int4* rp = reinterpret_cast<const int4*>(pieces + taken);
-            const int4 x = __ldg(rp), y = __ldg(rp + 1);
-            row = x.x; b = x.y; e = x.z; kvh = x.w;
-            mb = y.x; nm = y.y; pb = y.z; nh = y.w;
-            mem = lane < nm ? __ldg(members + mb + lane) : 0;
-        }
-        first_piece = false;
-        int len = __ldg(seq_lens + row);
-        if (e == kDecToSeqEnd) {
-            // a request's trailing piece runs to its length now (within its
-            // row of the table; a length below the piece's start is an error)
-            if (len > ld || len < b) {
-                if (lane == 0) atomicOr(err, 2u);
-                len = len > ld ? (int)ld : b;
-            }
-            e = len;
-        }
-        // at least one step, so that an empty piece still writes its
-        // (empty) partial rows for the merge
-        for (int sp = b; sp < e || sp == b; sp += kNP)
-            entry(kvh, row, sp, e, sp == b ? kFirst : 0, len, pb, nh, nm, mem);
-    }
-    entry(-1, 0, 0, 0, 0, 0, 0, 0, 0, 0);   // the end of the stream
-    cp_async_wait<0>();
-    // The last lookup warp to finish restores the counter for the next call
-    // (every CTA has taken its last number by then).
-    if (lane == 0) {
-        if (atomicAdd(sched + 1, 1u) + 1 == gridDim.x) {
-            sched[0] = (uint32_t)f.n_init;
-            sched[1] = 0u;
-            __threadfence();
-        }
-    }
-}
 
 // ---------------------------------------------------------------------------
 // Producer warp p of kProducers
@@ -312,7 +148,6 @@ __device__ __noinline__ void stream_producer(const FusedArgs& f, int pw, uint32_
     using Lay = FusedLayout<D, F8>;
     constexpr int NS = Lay::NSF;
     constexpr int ES = Lay::ES;
-    constexpr int32_t kPastEnd = INT32_MIN;
     constexpr int RPW = 2 * kNP / kProducers;   // rows per producer warp and step
     // argument fields in registers: every asm below clobbers memory
     const uint8_t* const kp = reinterpret_cast<const uint8_t*>(f.t.kp);
@@ -337,14 +172,14 @@ __device__ __noinline__ void stream_producer(const FusedArgs& f, int pw, uint32_
     int last_arrived = -1; // last step that arrived on a FULL barrier (armed, or the end marker)
     for (int r = 0; !timed_out; ++r) {
         const int ent = r & (kSQ - 1);
-        const uint32_t eb = sring + ent * kSlotEntry;
+        const uint32_t eb = sring + ent * Ent::kBytes;
         if (!mbar_wait(sfull + 8 * ent, (uint32_t)(r / kSQ) & 1u)) {
             atomicOr(err, 4u);
             timed_out = true;
             break;
         }
-        const int kvh = ld_shared_s32(eb + kEntKvh);
-        const int flags = ld_shared_s32(eb + kEntFlags);
+        const int kvh = ld_shared_s32(eb + Ent::kKvh);
+        const int flags = ld_shared_s32(eb + Ent::kFlags);
         const int st = r % NS;
         if (!mbar_wait(empty + 8 * st, ((r / NS) & 1) ^ 1)) {
             atomicOr(err, 4u);
@@ -365,7 +200,7 @@ __device__ __noinline__ void stream_producer(const FusedArgs& f, int pw, uint32_
             break;
         }
         const bool first = (flags & kFirst) != 0;
-        if (first) cur_nh = ld_shared_s32(eb + kEntNh);
+        if (first) cur_nh = ld_shared_s32(eb + Ent::kNh);
         const uint32_t rowb = (uint32_t)(cur_nh * D * ES);
         int32_t sl = mine ? ld_shared_s32(eb + tok * 4) : kPastEnd;
         bool ok = mine && sl != kPastEnd;
@@ -390,18 +225,18 @@ __device__ __noinline__ void stream_producer(const FusedArgs& f, int pw, uint32_
         }
         const uint32_t bytes = (uint32_t)__popc(vmask) * rowb;
         if (lead && lane == 0) {
-            st_shared_s32(db + kDescP0, ld_shared_s32(eb + kEntP0));
+            st_shared_s32(db + kDescP0, ld_shared_s32(eb + Ent::kP0));
             st_shared_s32(db + kDescFlags, flags);
             if (first) {
-                st_shared_s32(db + kDescCm, ld_shared_s32(eb + kEntCm));
-                st_shared_s32(db + kDescPb, ld_shared_s32(eb + kEntPb));
-                st_shared_s32(db + kDescRows, ld_shared_s32(eb + kEntNm) * G);
+                st_shared_s32(db + kDescCm, ld_shared_s32(eb + Ent::kCm));
+                st_shared_s32(db + kDescPb, ld_shared_s32(eb + Ent::kPb));
+                st_shared_s32(db + kDescRows, ld_shared_s32(eb + Ent::kNm) * G);
                 st_shared_s32(db + kDescNh, cur_nh);
                 st_shared_s32(db + kDescKvh, kvh);
             }
         }
         if (lead && first && lane < kDecPieceMembers)
-            st_shared_s32(db + kDescMem + 4 * lane, ld_shared_s32(eb + kEntMem + 4 * lane));
+            st_shared_s32(db + kDescMem + 4 * lane, ld_shared_s32(eb + Ent::kMem + 4 * lane));
         __syncwarp();
         if (lane == 0) mbar_expect_tx(fb, bytes);   // the arrival, plus the bytes the copies complete
         __syncwarp();
@@ -663,26 +498,6 @@ __device__ __noinline__ void stream_consumer(const FusedArgs& f, int c, uint32_t
     if (have && active) finish_item();
 }
 
-// ---------------------------------------------------------------------------
-// Tile roles: the CTA's wide items
-// ---------------------------------------------------------------------------
-__device__ __forceinline__ void dec_tile_info(const TcArgs& a, int w, int* info) {
-    const DecItem it = a.items[w];
-    int e = it.kv_end;
-    const int len = __ldg(a.seq_lens + it.rep_row);
-    if (e > len) {
-        atomicOr(a.err, 2u);
-        e = len;
-    }
-    info[0] = it.rep_row;
-    info[1] = it.kv_begin;
-    info[2] = e > it.kv_begin ? e : it.kv_begin;
-    info[3] = it.kvh;
-    info[4] = it.n_mem * a.G;
-    info[5] = it.mem_begin;
-    info[6] = it.partial_base;
-}
-
 template <int D, bool F8>
 __global__ void __maxnreg__(128) decode_fused_kernel(const __grid_constant__ FusedArgs f,
                                                      const __grid_constant__ CUtensorMap tmk,
@@ -769,7 +584,7 @@ __global__ void __maxnreg__(128) decode_fused_kernel(const __grid_constant__ Fus
     const uint32_t desc = smem_u32(sm + Lay::OFF_DESC);
     const uint32_t sring = smem_u32(sm + Lay::OFF_SLOT);
     if (warp == kLookup) {
-        stream_lookup<D, F8>(f, gw, lrec, sring, slfull, slfree, lane);
+        stream_lookup<kNP>(f, gw, lrec, sring, slfull, slfree, lane);
     } else if (warp >= kFirstProducer && warp < kFirstConsumer) {
         stream_producer<D, F8>(f, warp - kFirstProducer, ring, sring, desc, sfull, sempty, slfull,
                                slfree, lane);

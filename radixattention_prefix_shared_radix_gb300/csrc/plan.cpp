@@ -108,7 +108,6 @@ int sgl_decode_plan(const sgl_attn_params* p, const int32_t* seq_lens, const sgl
                     sgl_plan** plan_out, size_t* workspace_bytes) {
     int st = sgl::check_params(p);
     if (st) return st;
-    if (p->dtype == SGL_DTYPE_BF16_FP4KV) return SGL_ERR_UNSUPPORTED;
     if (!g || !plan_out || !workspace_bytes) return SGL_ERR_INVALID_ARG;
     const int32_t B = p->batch;
     if (B > 0 && !seq_lens) return SGL_ERR_INVALID_ARG;
@@ -130,8 +129,10 @@ int sgl_decode_plan(const sgl_attn_params* p, const int32_t* seq_lens, const sgl
     // CTA): up to 8 heads with one consumer warp each when a head has at
     // most 8 query rows, else up to 4 heads with two consumer warps each;
     // the fp32 kernel runs one item per CTA and takes one head per item.
+    // (The 4-bit streams give a head one warp for up to 16 rows.)
     auto head_block = [&](int32_t nmem) -> int32_t {
         if (p->dtype == SGL_DTYPE_F32) return 1;
+        if (p->dtype == SGL_DTYPE_BF16_FP4KV) return std::min<int32_t>(Hkv, sgl::kDecHeadBlock);
         return std::min<int32_t>(Hkv, nmem * G <= 8 ? sgl::kDecHeadBlock : sgl::kDecHeadBlock / 2);
     };
     struct Unit {   // narrow work: one member block of a segment for a block of KV heads
@@ -232,7 +233,7 @@ int sgl_decode_plan(const sgl_attn_params* p, const int32_t* seq_lens, const sgl
     // Narrow units are cut into pieces of at most Pmax positions (about half
     // an even share of a stream, so that the run-time counter can balance
     // the tail; a cut makes one more partial to merge), no
-    // piece shorter than one 16-position step unless its unit is, ordered
+    // piece shorter than one step (16 positions; 32 of a 4-bit pool) unless its unit is, ordered
     // longest first.  Each streaming CTA starts on its own piece; the rest
     // (and all work of tile CTAs' streams, once their tiles are done) are
     // handed out at run time from a counter, so SMs that stream faster take
@@ -240,14 +241,15 @@ int sgl_decode_plan(const sgl_attn_params* p, const int32_t* seq_lens, const sgl
     const int64_t n_cons = n_ctas - n_tile_ctas;
     // (in position-heads, so that a piece of a 4-head block is as long in
     // bytes as one of an 8-head block)
+    const int64_t step = p->dtype == SGL_DTYPE_BF16_FP4KV ? 32 : 16;   // positions per streaming step
     const int64_t Pph = (int64_t)std::ceil((double)units_n / (double)std::max<int64_t>(1, 2 * n_cons));
     std::vector<std::pair<int32_t, sgl::DecItem>> cut;   // (planned length, piece)
     for (const Unit& u : units) {
         int64_t Pmax = (Pph + u.nh - 1) / u.nh;
-        Pmax = std::min<int64_t>(2048, std::max<int64_t>(32, (Pmax + 15) / 16 * 16));
+        Pmax = std::min<int64_t>(2048, std::max<int64_t>(32, (Pmax + step - 1) / step * step));
         for (int64_t pos = u.b; pos < u.e || (pos == u.b && u.tail);) {
             int64_t take = std::min<int64_t>(u.e - pos, Pmax);
-            if (u.e - pos - take < 16) take = u.e - pos;   // no tail piece under one step
+            if (u.e - pos - take < step) take = u.e - pos;   // no tail piece under one step
             const bool last = pos + take == u.e;
             cut.push_back({(int32_t)take,
                            {u.rep_row, (int32_t)pos, last && u.tail ? sgl::kDecToSeqEnd : (int32_t)(pos + take), u.kvh,
@@ -385,7 +387,6 @@ int sgl_plan_info(const sgl_plan* plan, sgl_plan_info_t* out) {
 int sgl_extend_workspace_bytes(const sgl_attn_params* p, size_t* bytes) {
     int st = sgl::check_params(p);
     if (st) return st;
-    if (p->dtype == SGL_DTYPE_BF16_FP4KV) return SGL_ERR_UNSUPPORTED;
     if (!bytes) return SGL_ERR_INVALID_ARG;
     *bytes = sgl::kWsAlign;   // the error word
     return SGL_OK;

@@ -30,10 +30,10 @@ using namespace tc;
 // two query tiles, 128-position blocks (S MMAs of N = 128: an M = 128
 // tcgen05 MMA costs about the same time for N = 64 as for N = 128), one score
 // buffer each, 2 K/V stages (4 for d = 64), a gather team of 6 warps.  With
-// an FP8 pool (codes staged by the gather team and converted to f16) one
+// an FP8 or 4-bit pool (codes staged by the gather team and converted to f16) one
 // stage for d = 128, whose staging area takes the second stage's room.
-template <int D, bool F8 = false>
-using ExtCfg = TcCfg<D, false, 2, (F8 && D == 128) ? 1 : 2 * (128 / D), 6, 128, 1, F8>;
+template <int D, int KV>
+using ExtCfg = TcCfg<D, false, 2, (KV != kKvBf16 && D == 128) ? 1 : 2 * (128 / D), 6, 128, 1, KV>;
 
 // Query tile pair (blockIdx.x, blockIdx.y) of the extend batch; false if empty.
 __device__ bool extend_tile_info(const TcArgs& a, int* info) {
@@ -78,11 +78,11 @@ __device__ bool extend_tile_info(const TcArgs& a, int* info) {
     return true;
 }
 
-template <int D, bool F8>
-__global__ void __launch_bounds__(ExtCfg<D, F8>::kThreads, 1)
+template <int D, int KV>
+__global__ void __launch_bounds__(ExtCfg<D, KV>::kThreads, 1)
     extend_tc_kernel(const TcArgs a, const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv,
                      const __grid_constant__ CUtensorMap tnk, const __grid_constant__ CUtensorMap tnv) {
-    using C = ExtCfg<D, F8>;
+    using C = ExtCfg<D, KV>;
     using Lay = typename C::Lay;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t* sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
@@ -116,16 +116,18 @@ __global__ void __launch_bounds__(ExtCfg<D, F8>::kThreads, 1)
     }
 }
 
-template <int D, bool F8>
+template <int D, int KV>
 constexpr int extend_smem() {
-    return ExtCfg<D, F8>::Lay::END + 1024;   // + alignment slack
+    return ExtCfg<D, KV>::Lay::END + 1024;   // + alignment slack
 }
-static_assert(extend_smem<128, false>() <= 232448 && extend_smem<64, false>() <= 232448 &&
-                  extend_smem<128, true>() <= 232448 && extend_smem<64, true>() <= 232448,
-              "shared memory per CTA");
-static_assert(extend_smem<128, false>() > 116 * 1024 && extend_smem<64, false>() > 116 * 1024 &&
-                  extend_smem<128, true>() > 116 * 1024 && extend_smem<64, true>() > 116 * 1024,
-              "one CTA per SM: each allocates all 512 TMEM columns");
+template <int D, int KV>
+constexpr bool extend_smem_ok() {
+    // within an SM's, and too much for two CTAs: each allocates all 512 TMEM columns
+    return extend_smem<D, KV>() <= 232448 && extend_smem<D, KV>() > 116 * 1024;
+}
+static_assert(extend_smem_ok<128, kKvBf16>() && extend_smem_ok<64, kKvBf16>() && extend_smem_ok<128, kKvE4m3>() &&
+                  extend_smem_ok<64, kKvE4m3>() && extend_smem_ok<128, kKvFp4>() && extend_smem_ok<64, kKvFp4>(),
+              "shared memory per CTA: one CTA per SM");
 
 }  // namespace
 
@@ -158,6 +160,21 @@ int encode_rows_map(const void* base, int64_t rows, int D, CUtensorMap* m, int b
     return r == CUDA_SUCCESS ? 0 : (int)cudaErrorInvalidValue;
 }
 
+int encode_bytes_map(const void* base, int64_t rows, int row_bytes, int box_bytes, CUtensorMap* m) {
+    const PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
+    if (!enc) return (int)cudaErrorNotSupported;
+    if (rows <= 0 || rows > (int64_t)INT32_MAX || box_bytes <= 0 || box_bytes > 1024 || box_bytes > row_bytes)
+        return (int)cudaErrorInvalidValue;
+    const cuuint64_t gdim[2] = {(cuuint64_t)row_bytes / 4, (cuuint64_t)rows};
+    const cuuint64_t gstride[1] = {(cuuint64_t)row_bytes};
+    const cuuint32_t box[2] = {(cuuint32_t)box_bytes / 4, 1};
+    const cuuint32_t estride[2] = {1, 1};
+    const CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_INT32, 2, const_cast<void*>(base), gdim, gstride, box, estride,
+                           CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+                           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? 0 : (int)cudaErrorInvalidValue;
+}
+
 int encode_pool_maps(const void* kp, const void* vp, int64_t num_slots, int Hkv, int D, CUtensorMap* mk,
                      CUtensorMap* mv) {
     struct Cache {
@@ -186,19 +203,19 @@ int encode_pool_maps(const void* kp, const void* vp, int64_t num_slots, int Hkv,
 }  // namespace tc
 
 // Extend over all requests: grid (pairs of query tiles of 128/G new tokens, KV heads).
-template <int D, bool F8>
+template <int D, int KV>
 int launch_extend_tc(const void* q, const void* kp, const void* vp, const void* kn, const void* vn, void* kw, void* vw,
                      const int32_t* r2t, int64_t ld, const int32_t* pre, const int32_t* ext, int B, int64_t n_rows,
                      int64_t ctas, void* o, float* lse,
                      uint32_t* err, int Hq, int Hkv, int64_t num_slots, float scale_log2, float k_scale, float v_scale,
                      cudaStream_t s) {
-    static const int attr = (int)cudaFuncSetAttribute(extend_tc_kernel<D, F8>,
-                                                      cudaFuncAttributeMaxDynamicSharedMemorySize, extend_smem<D, F8>());
+    static const int attr = (int)cudaFuncSetAttribute(extend_tc_kernel<D, KV>,
+                                                      cudaFuncAttributeMaxDynamicSharedMemorySize, extend_smem<D, KV>());
     if (attr) return attr;
-    // the pools' TMA views (an FP8 pool's codes are copied with cp.async:
-    // its maps stay zero and unused)
+    // the pools' TMA views (FP8 and 4-bit pools are copied with cp.async:
+    // their maps stay zero and unused)
     CUtensorMap mk{}, mv{}, nk{}, nv{};
-    if (!F8)
+    if (KV == kKvBf16)
         if (const int e = tc::encode_pool_maps(kp, vp, num_slots, Hkv, D, &mk, &mv)) return e;
     if (kn) {
         if (const int e = tc::encode_rows_map(kn, n_rows * Hkv, D, &nk)) return e;
@@ -228,26 +245,23 @@ int launch_extend_tc(const void* q, const void* kp, const void* vp, const void* 
     a.scale_log2 = scale_log2;
     a.k_scale = k_scale;
     a.v_scale = v_scale;
-    extend_tc_kernel<D, F8><<<dim3((unsigned)ctas, (unsigned)Hkv), ExtCfg<D, F8>::kThreads, extend_smem<D, F8>(), s>>>(
+    a.row_bytes = KV == kKvFp4 ? fp4_row_bytes(Hkv, D) : 0;
+    extend_tc_kernel<D, KV><<<dim3((unsigned)ctas, (unsigned)Hkv), ExtCfg<D, KV>::kThreads, extend_smem<D, KV>(), s>>>(
         a, mk, mv, nk, nv);
     return (int)cudaGetLastError();
 }
 
-template int launch_extend_tc<64, false>(const void*, const void*, const void*, const void*, const void*, void*,
-                                         void*, const int32_t*, int64_t, const int32_t*, const int32_t*, int,
-                                         int64_t, int64_t, void*, float*, uint32_t*, int, int, int64_t, float,
-                                         float, float, cudaStream_t);
-template int launch_extend_tc<64, true>(const void*, const void*, const void*, const void*, const void*, void*,
-                                         void*, const int32_t*, int64_t, const int32_t*, const int32_t*, int,
-                                         int64_t, int64_t, void*, float*, uint32_t*, int, int, int64_t, float,
-                                         float, float, cudaStream_t);
-template int launch_extend_tc<128, false>(const void*, const void*, const void*, const void*, const void*, void*,
-                                         void*, const int32_t*, int64_t, const int32_t*, const int32_t*, int,
-                                         int64_t, int64_t, void*, float*, uint32_t*, int, int, int64_t, float,
-                                         float, float, cudaStream_t);
-template int launch_extend_tc<128, true>(const void*, const void*, const void*, const void*, const void*, void*,
-                                         void*, const int32_t*, int64_t, const int32_t*, const int32_t*, int,
-                                         int64_t, int64_t, void*, float*, uint32_t*, int, int, int64_t, float,
-                                         float, float, cudaStream_t);
+#define SGL_LAUNCH_EXTEND_TC(D, KV)                                                                                    \
+    template int launch_extend_tc<D, KV>(const void*, const void*, const void*, const void*, const void*, void*, void*, \
+                                         const int32_t*, int64_t, const int32_t*, const int32_t*, int, int64_t,         \
+                                         int64_t, void*, float*, uint32_t*, int, int, int64_t, float, float, float,     \
+                                         cudaStream_t)
+SGL_LAUNCH_EXTEND_TC(64, kKvBf16);
+SGL_LAUNCH_EXTEND_TC(128, kKvBf16);
+SGL_LAUNCH_EXTEND_TC(64, kKvE4m3);
+SGL_LAUNCH_EXTEND_TC(128, kKvE4m3);
+SGL_LAUNCH_EXTEND_TC(64, kKvFp4);
+SGL_LAUNCH_EXTEND_TC(128, kKvFp4);
+#undef SGL_LAUNCH_EXTEND_TC
 
 }  // namespace sgl

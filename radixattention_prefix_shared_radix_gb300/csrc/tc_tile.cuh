@@ -46,11 +46,17 @@
 #include <cuda.h>
 
 #include "device_common.cuh"
+#include "fp4.cuh"
 
 namespace sgl {
 namespace tc {
 
 using namespace sgldev;
+
+// what the pools hold
+constexpr int kKvBf16 = 0;
+constexpr int kKvE4m3 = 1;               // FP8 codes
+constexpr int kKvFp4 = 2;                // 4-bit rows (fp4.cuh)
 
 constexpr int kQRegion = 128 * 128;      // SW128 region of a 128-row tile: 128 rows x 128 bytes
 constexpr int kTileBar = 1;              // named barrier of the tile threads
@@ -186,9 +192,10 @@ struct TcArgs {
     int Hq, Hkv, G;
     int64_t num_slots;
     float scale_log2;
-    // decode with an FP8 (E4M3) pool: per-tensor dequantisation scales (K's
-    // goes into the score scale, V's into the normalisation)
+    // FP8 and 4-bit pools: per-tensor dequantisation scales (K's goes into
+    // the score scale, V's into the normalisation)
     float k_scale, v_scale;
+    int row_bytes;   // 4-bit pools: bytes of a pool row
 };
 
 // Shared memory of the tile roles (offsets from a 1024-byte aligned base):
@@ -196,10 +203,10 @@ struct TcArgs {
 // KEEP on is used only while the tiles run, so a kernel may reuse it once
 // its tiles are done: NQ query tiles (extend: 128B-swizzled smem tiles;
 // decode: none, Q lives in TMEM), NS K stages and NS V stages of BN
-// positions, the barriers and, with FP8 pools, the codes of two blocks' K
-// and V rows as copied (BN x D bytes per part) before their conversion into
-// the stages.
-template <int D, bool DEC, int NQ, int NS, int BN, bool F8 = false>
+// positions, the barriers and, with FP8 or 4-bit pools, the codes (a 4-bit
+// block's scales after them) of two blocks' K and V rows as copied, before
+// their conversion into the stages.
+template <int D, bool DEC, int NQ, int NS, int BN, int KV = kKvBf16>
 struct TcLayout {
     static constexpr int OFF_TMEM = 0;                   // TMEM base address
     static constexpr int OFF_INFO = 16;                  // tile description broadcast (16 ints)
@@ -212,8 +219,8 @@ struct TcLayout {
     static constexpr int OFF_V = OFF_K + NS * KTILE;
     static constexpr int OFF_BAR = OFF_V + NS * KTILE;
     static constexpr int OFF_STG = (OFF_BAR + 48 * 8 + 127) / 128 * 128;
-    static constexpr int STG = BN * D;
-    static constexpr int END = OFF_STG + (F8 ? 4 * STG : 0);
+    static constexpr int STG = KV == kKvFp4 ? BN * fp4_head_bytes(D) : BN * D;
+    static constexpr int END = OFF_STG + (KV != kKvBf16 ? 4 * STG : 0);
 };
 
 // Tile roles and their barriers for NQ query tiles that share one K/V stream
@@ -226,11 +233,11 @@ struct TcLayout {
 // q * 256 + NSB * BN; decode's Q after O.  P_j (bf16 pairs) overwrites the
 // first BN / 2 columns of its own S buffer.
 //
-// F8: the pools hold FP8 E4M3 codes.  The gather team copies
-// them into a staging area with 16-byte cp.async and stores them, converted
-// to f16 (exact), into the same SW128 tiles; Q and P are f16 too, so the MMAs
-// are kind::f16 with f16 operands.
-template <int D, bool DEC, int NQ, int NS, int NG, int BN, int NSB, bool F8 = false>
+// KV != kKvBf16: the pools hold FP8 E4M3 codes or 4-bit rows.  The gather team
+// copies them into a staging area with 16-byte cp.async and stores them,
+// converted to f16 (exact), into the same SW128 tiles; Q and P are f16 too, so
+// the MMAs are kind::f16 with f16 operands.
+template <int D, bool DEC, int NQ, int NS, int NG, int BN, int NSB, int KV = kKvBf16>
 struct TcCfg {
     static_assert(NQ == 1 || (NQ == 2 && !DEC), "decode tiles use one query tile (Q lives in TMEM)");
     static_assert(BN == 64 || BN == 128, "KV block of 64 or 128 positions");
@@ -238,10 +245,11 @@ struct TcCfg {
     static_assert(NS >= NSB, "the S lookahead needs as many K stages as score buffers");
     static_assert(NSB * BN + 128 + (DEC ? D / 2 : 0) <= (NQ == 2 ? 256 : 512), "TMEM columns");
     static_assert(NQ == 1 || NSB == 1, "two query tiles alternate on one score buffer each");
-    using Lay = TcLayout<D, DEC, NQ, NS, BN, F8>;
+    using Lay = TcLayout<D, DEC, NQ, NS, BN, KV>;
     static constexpr int kD = D, kNQ = NQ, kNS = NS, kNG = NG, kBN = BN, kNSB = NSB;
     static constexpr bool kDec = DEC;
-    static constexpr bool kF8 = F8;
+    static constexpr bool kF8 = KV != kKvBf16;    // codes, f16 operands
+    static constexpr bool kF4 = KV == kKvFp4;
     static constexpr int kThreads = 32 * (4 * NQ + 1 + NG);
     static constexpr int kMmaWarp = 4 * NQ;
     static constexpr int kOCol = NSB * BN;               // O's column within a query tile's 256
@@ -276,7 +284,7 @@ struct TcCfg {
 // gives the gather of K_{j+2} a whole block more (two with FP8 pools, whose
 // staging area takes the room).
 template <int D, bool F8 = false>
-using DecCfg = TcCfg<D, true, 1, F8 ? 2 : 3, 10, 128, 2, F8>;
+using DecCfg = TcCfg<D, true, 1, F8 ? 2 : 3, 10, 128, 2, F8 ? kKvE4m3 : kKvBf16>;
 
 struct TileInfo {
     int kv_row, kv_begin, kv_end, kvh;
@@ -339,7 +347,7 @@ __device__ __forceinline__ void tc_tile_run(const TcArgs& a, const CUtensorMap* 
     using Lay = typename C::Lay;
     constexpr int D = C::kD, NQ = C::kNQ, NS = C::kNS, NG = C::kNG, BN = C::kBN, NSB = C::kNSB;
     constexpr int KR = Lay::KREGION;
-    constexpr bool DEC = C::kDec, F8 = C::kF8;
+    constexpr bool DEC = C::kDec, F8 = C::kF8, F4 = C::kF4;
     const uint32_t sQ = smem_u32(sm + Lay::OFF_Q);
     const uint32_t sK = smem_u32(sm + Lay::OFF_K);
     const uint32_t sV = smem_u32(sm + Lay::OFF_V);
@@ -434,8 +442,11 @@ __device__ __forceinline__ void tc_tile_run(const TcArgs& a, const CUtensorMap* 
             // barrier.  A block's slots are looked up one block before its
             // copies are issued and checked only then, so no lookup stalls
             // the conversions.  Positions past the range re-read the range's
-            // last position.
-            constexpr int CH = D / 16;
+            // last position.  4-bit pools: 32 codes per piece; the first
+            // piece's lane also copies the row's D / 16 scales (pieces of a
+            // row belong to one warp), which go into the f16 values (exact).
+            constexpr int CH = F4 ? D / 32 : D / 16;
+            constexpr int RB = F4 ? D / 2 : D;          // code bytes of a row
             constexpr int NIT = BN * CH;
             constexpr int TPT = (NIT + 32 * NG - 1) / (32 * NG);
             const int t0 = g * 32 + lane;
@@ -464,7 +475,7 @@ __device__ __forceinline__ void tc_tile_run(const TcArgs& a, const CUtensorMap* 
                         if (j < nb && it < NIT && it % CH == 0) atomicOr(a_err, 1u);
                         s1 = 0;
                     }
-                    rw[i] = s1 * a_Hkv + kvh;
+                    rw[i] = F4 ? s1 : s1 * a_Hkv + kvh;
                 }
 #pragma unroll
                 for (int part = 0; part < 2; ++part) {
@@ -472,9 +483,18 @@ __device__ __forceinline__ void tc_tile_run(const TcArgs& a, const CUtensorMap* 
 #pragma unroll
                         for (int i = 0; i < TPT; ++i) {
                             const int it = t0 + i * 32 * NG;
-                            if (it < NIT)
-                                cp_async16(sb + part * Lay::STG + it * 16,
-                                           (part ? vp8 : kp8) + (int64_t)rw[i] * D + (it % CH) * 16, true);
+                            if (it >= NIT) continue;
+                            const uint8_t* row;
+                            if constexpr (F4) {
+                                row = (part ? vp8 : kp8) + (int64_t)rw[i] * a.row_bytes;
+                                if (it % CH == 0)
+                                    cp_async_small<D / 16>(sb + part * Lay::STG + BN * RB + it / CH * (D / 16),
+                                                           row + fp4_scale_off(kvh, a_Hkv, D));
+                                row += fp4_code_off(kvh, D);
+                            } else {
+                                row = (part ? vp8 : kp8) + (int64_t)rw[i] * D;
+                            }
+                            cp_async16(sb + part * Lay::STG + it * 16, row + (it % CH) * 16, true);
                         }
                     }
                     cp_async_commit();
@@ -506,6 +526,7 @@ __device__ __forceinline__ void tc_tile_run(const TcArgs& a, const CUtensorMap* 
                         stop = true;
                         break;
                     }
+                    if constexpr (F4) __syncwarp();   // (a row's scales: its first piece's lane's copy)
                     const uint32_t base = (part ? sV : sK) + st * Lay::KTILE;
 #pragma unroll
                     for (int i = 0; i < TPT; ++i) {
@@ -516,6 +537,20 @@ __device__ __forceinline__ void tc_tile_run(const TcArgs& a, const CUtensorMap* 
                             asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];\n"
                                          : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
                                          : "r"(sb + part * Lay::STG + it * 16));
+                            if constexpr (F4) {
+                                const uint32_t sf = e4m3x2_to_f16(
+                                    ld_shared_u16(sb + part * Lay::STG + BN * RB + r * (D / 16) + 2 * c));
+                                const uint32_t s2[2] = {__byte_perm(sf, sf, 0x1010), __byte_perm(sf, sf, 0x3232)};
+#pragma unroll
+                                for (int k = 0; k < 4; ++k) {
+                                    uint32_t h[4];
+                                    e2m1x8_to_f16(w[k], h);
+                                    st_shared_v4(base + sw128(r, 4 * c + k, KR), hmul2_u(h[0], s2[k / 2]),
+                                                 hmul2_u(h[1], s2[k / 2]), hmul2_u(h[2], s2[k / 2]),
+                                                 hmul2_u(h[3], s2[k / 2]));
+                                }
+                                continue;
+                            }
                             uint32_t h[8];
                             e4m3x4_to_f16(w[0], h[0], h[1]);
                             e4m3x4_to_f16(w[1], h[2], h[3]);
@@ -955,6 +990,9 @@ int encode_pool_maps(const void* kp, const void* vp, int64_t num_slots, int Hkv,
 // Host: the same view of any [rows, D] bf16 tensor (not cached), with boxes
 // of 64 columns x box_rows rows.
 int encode_rows_map(const void* base, int64_t rows, int D, CUtensorMap* m, int box_rows = 1);
+// Host: a [rows, row_bytes] byte tensor as 32-bit words, boxes of one row's
+// box_bytes (multiples of 16), no swizzle.
+int encode_bytes_map(const void* base, int64_t rows, int row_bytes, int box_bytes, CUtensorMap* m);
 
 }  // namespace tc
 }  // namespace sgl
