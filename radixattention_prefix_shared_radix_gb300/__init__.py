@@ -200,19 +200,31 @@ def _ptr32(a):
     return a.ctypes.data_as(_I32P)
 
 
+_T = None    # torch, bound at the first call that takes tensors (the host functions work without it)
+
+
+def _torch():
+    global _T
+    if _T is None:
+        import torch
+        _T = torch
+    return _T
+
+
 def _dev(t, what):
-    import torch
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+    if not isinstance(t, (_T or _torch()).Tensor) or not t.is_cuda:
         raise TypeError("%s must be a CUDA tensor" % what)
     if not t.is_contiguous():
         raise ValueError("%s must be contiguous" % what)
-    return ctypes.c_void_p(t.data_ptr())
+    return t.data_ptr()
 
 
 def _stream(stream):
-    import torch
-    s = stream if stream is not None else torch.cuda.current_stream()
-    return ctypes.c_void_p(s.cuda_stream)
+    if stream is not None:
+        return stream.cuda_stream
+    # torch.cuda.current_stream().cuda_stream without the object (it costs 4 us of a call's 13)
+    c = (_T or _torch())._C
+    return c._cuda_getCurrentRawStream(c._cuda_getDevice())
 
 
 # ------------------------------------------------------------------ tree
@@ -538,12 +550,11 @@ def sgl_decode_attn(q, k_pool, v_pool, req_to_token, seq_lens, plan, o, lse, wor
 
 
 def _host(t, what):
-    import torch
-    if not isinstance(t, torch.Tensor) or t.is_cuda:
+    if not isinstance(t, (_T or _torch()).Tensor) or t.is_cuda:
         raise TypeError("%s must be a host tensor" % what)
     if not t.is_contiguous():
         raise ValueError("%s must be contiguous" % what)
-    return ctypes.c_void_p(t.data_ptr())
+    return t.data_ptr()
 
 
 def _in_region(t, region, what):
@@ -674,51 +685,70 @@ def sgl_rope_create(head_dim, rot_dim=0, rot_offset=0, layout=SGL_ROPE_HALF, sca
     return Rope(h, p.head_dim, p.rot_dim)
 
 
-def _rows(t, what, heads=None, dim=None, dtype=None, n=None):
-    """A CUDA tensor [rows, heads, dim] whose heads are contiguous in each row: (address, row stride)."""
-    import torch
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+def _rows(t, what, heads, dim, dtype, n, dev):
+    """A tensor [n, heads, dim] on device `dev` whose heads are contiguous in each row: (address, row stride).
+    heads and n None: any."""
+    if isinstance(t, _T.Tensor) and t.dim() == 3:
+        r, h, w = t.shape
+        a, b, c = t.stride()
+        if (w == dim and (h == heads or heads is None) and (r == n or n is None) and t.dtype is dtype and c == 1
+                and (b == dim or h <= 1) and t.get_device() == dev):
+            return t.data_ptr(), (a if r > 1 else h * dim)
+    _refuse(t, what, dtype, (n or "rows", heads or "heads", dim), dev, "hold each row's heads contiguously")
+
+
+def _flat(t, what, dev, dtype=None, shape=None):
+    """The address of a contiguous tensor on device `dev` (of a dtype and shape, where given)."""
+    if (isinstance(t, _T.Tensor) and t.get_device() == dev and (dtype is None or t.dtype is dtype)
+            and (shape is None or t.shape == shape) and t.is_contiguous()):
+        return t.data_ptr()
+    _refuse(t, what, dtype, shape, dev, "be contiguous")
+
+
+def _refuse(t, what, dtype, shape, dev, layout):
+    """Raise for a tensor argument that one of the checks above did not pass."""
+    if not isinstance(t, _T.Tensor) or not t.is_cuda:
         raise TypeError("%s must be a CUDA tensor" % what)
-    if t.dim() != 3 or (heads is not None and t.shape[1] != heads) or (dim is not None and t.shape[2] != dim):
-        raise ValueError("%s must have shape [rows, %s, %s]" % (what, "heads" if heads is None else heads, dim))
-    if n is not None and t.shape[0] != n:
-        raise ValueError("%s must have %d rows" % (what, n))
     if dtype is not None and t.dtype != dtype:
         raise TypeError("%s must be %s" % (what, dtype))
-    if (t.shape[2] > 1 and t.stride(2) != 1) or (t.shape[1] > 1 and t.stride(1) != t.shape[2]):
-        raise ValueError("%s must hold each row's heads contiguously" % what)
-    return t.data_ptr(), (t.stride(0) if t.shape[0] > 1 else t.shape[1] * t.shape[2])
-
-
-def _ints(t, what, shape):
-    import torch
-    p = _dev(t, what)
-    if t.dtype != torch.int32 or tuple(t.shape) != shape:
-        raise ValueError("%s must be int32 of shape %s" % (what, shape))
-    return p
+    if t.get_device() != dev:
+        raise ValueError("%s must be on the current device" % what)
+    if shape is not None and (t.dim() != len(shape) or any(isinstance(x, int) and x != y for x, y in zip(shape, t.shape))):
+        raise ValueError("%s must have shape (%s), not %s" % (what, ", ".join(map(str, shape)), tuple(t.shape)))
+    raise ValueError("%s must %s" % (what, layout))
 
 
 def sgl_rope(rope, q, k, positions, q_out=None, k_out=None, stream=None):
     """Rotary positions of q [N, Hq, head_dim] and k [N, Hk, head_dim] (either may be None; rows may be strided, as
     columns of a fused projection are) into q_out and k_out (None: in place).  positions: int32 [N]."""
-    import torch
+    T = _T or _torch()
     some = q if q is not None else k
-    if some is None:
-        raise ValueError("q or k must be given")
-    n, dt = some.shape[0], some.dtype
-    if dt not in (torch.float32, torch.bfloat16):
+    if not isinstance(some, T.Tensor):
+        raise TypeError("q or k must be given, as CUDA tensors")
+    dt = some.dtype
+    if dt == T.bfloat16:
+        kind = SGL_DTYPE_BF16
+    elif dt == T.float32:
+        kind = SGL_DTYPE_F32
+    else:
         raise TypeError("q and k must be float32 or bfloat16")
-    args = []
-    for x, out, what in ((q, q_out, "q"), (k, k_out, "k")):
-        if x is None:
-            args.append((None, 0, 0, None, 0))
-            continue
-        p, st = _rows(x, what, None, rope.head_dim, dt, n)
-        po, so = _rows(x if out is None else out, what + "_out", x.shape[1], rope.head_dim, dt, n)
-        args.append((p, st, x.shape[1], po, so))
-    (pq, sq, hq, pqo, sqo), (pk, sk, hk, pko, sko) = args
-    _ok(_lib().sgl_rope(rope.handle, SGL_DTYPE_F32 if dt == torch.float32 else SGL_DTYPE_BF16, pq, sq, hq, pk, sk, hk,
-                        _ints(positions, "positions", (n,)), n, pqo, sqo, pko, sko, _stream(stream)), "sgl_rope")
+    n, d, dev = some.shape[0], rope.head_dim, T._C._cuda_getDevice()
+    pq = pqo = pk = pko = None
+    hq = hk = sq = sk = sqo = sko = 0
+    if q is not None:
+        pq, sq = pqo, sqo = _rows(q, "q", None, d, dt, n, dev)
+        hq = q.shape[1]
+        if q_out is not None:
+            pqo, sqo = _rows(q_out, "q_out", hq, d, dt, n, dev)
+    if k is not None:
+        pk, sk = pko, sko = _rows(k, "k", None, d, dt, n, dev)
+        hk = k.shape[1]
+        if k_out is not None:
+            pko, sko = _rows(k_out, "k_out", hk, d, dt, n, dev)
+    st = _lib().sgl_rope(rope.handle, kind, pq, sq, hq, pk, sk, hk, _flat(positions, "positions", dev, T.int32, (n,)), n,
+                         pqo, sqo, pko, sko, _stream(stream))
+    if st:
+        raise SglError(st, "sgl_rope")
 
 
 def sgl_kv_append(rope, params, q, k_new, v_new, k_pool, v_pool, req_to_token, lens, extend_lens, q_out, workspace,
@@ -727,42 +757,48 @@ def sgl_kv_append(rope, params, q, k_new, v_new, k_pool, v_pool, req_to_token, l
     rotated; q and q_out None: keys and values only).  extend_lens given: N = the sum of extend_lens (or more, in a
     padded batch) rows ordered by request, row i of request r at position lens[r] + i; None: row r is request r's
     newest token, at position lens[r] - 1."""
-    import torch
-    dt = torch.float32 if params.dtype == SGL_DTYPE_F32 else torch.bfloat16
-    n, hkv, d = k_new.shape[0], params.num_kv_heads, params.head_dim
-    pk, sk = _rows(k_new, "k_new", hkv, d, dt)
-    pv, sv = _rows(v_new, "v_new", hkv, d, dt, n)
+    T = _T or _torch()
+    dt = T.float32 if params.dtype == SGL_DTYPE_F32 else T.bfloat16
+    hkv, d, dev = params.num_kv_heads, params.head_dim, T._C._cuda_getDevice()
+    pk, sk = _rows(k_new, "k_new", hkv, d, dt, None, dev)
+    n = k_new.shape[0]
+    pv, sv = _rows(v_new, "v_new", hkv, d, dt, n, dev)
     pq = pqo = None
     sq = sqo = 0
     if q is not None:
-        pq, sq = _rows(q, "q", params.num_qo_heads, d, dt, n)
+        pq, sq = _rows(q, "q", params.num_qo_heads, d, dt, n, dev)
     if q_out is not None:
-        pqo, sqo = _rows(q_out, "q_out", params.num_qo_heads, d, dt, n)
+        pqo, sqo = _rows(q_out, "q_out", params.num_qo_heads, d, dt, n, dev)
     B = (params.batch,)
-    _ok(_lib().sgl_kv_append(None if rope is None else rope.handle, ctypes.byref(params), pq, sq, pk, sk, pv, sv,
-                             _dev(k_pool, "k_pool"), _dev(v_pool, "v_pool"), _dev(req_to_token, "req_to_token"),
-                             req_to_token.shape[1], _ints(lens, "lens", B),
-                             None if extend_lens is None else _ints(extend_lens, "extend_lens", B), n, pqo, sqo,
-                             _dev(workspace, "workspace"), workspace.numel() * workspace.element_size(),
-                             _stream(stream)), "sgl_kv_append")
+    rows = req_to_token.shape
+    st = _lib().sgl_kv_append(None if rope is None else rope.handle, ctypes.byref(params), pq, sq, pk, sk, pv, sv,
+                              _flat(k_pool, "k_pool", dev), _flat(v_pool, "v_pool", dev),
+                              _flat(req_to_token, "req_to_token", dev, T.int32), rows[1],
+                              _flat(lens, "lens", dev, T.int32, B),
+                              None if extend_lens is None else _flat(extend_lens, "extend_lens", dev, T.int32, B), n, pqo,
+                              sqo, _flat(workspace, "workspace", dev), workspace.nbytes, _stream(stream))
+    if st:
+        raise SglError(st, "sgl_kv_append")
 
 
 def sgl_mla_kv_append(rope, params, q, kv_new, kv_pool, req_to_token, lens, extend_lens, q_out, workspace, stream=None):
     """sgl_kv_append for an MLA pool: kv_new [N, 576] (latent, then position part), q [N, Hq, 576], bf16."""
-    import torch
-    dt, d = torch.bfloat16, params.latent_dim + params.rope_dim
+    T = _T or _torch()
+    dt, d, dev = T.bfloat16, params.latent_dim + params.rope_dim, T._C._cuda_getDevice()
+    pk, sk = _rows(kv_new.unsqueeze(1) if kv_new.dim() == 2 else kv_new, "kv_new", 1, d, dt, None, dev)
     n = kv_new.shape[0]
-    pk, sk = _rows(kv_new.unsqueeze(1) if kv_new.dim() == 2 else kv_new, "kv_new", 1, d, dt)
     pq = pqo = None
     sq = sqo = 0
     if q is not None:
-        pq, sq = _rows(q, "q", params.num_qo_heads, d, dt, n)
+        pq, sq = _rows(q, "q", params.num_qo_heads, d, dt, n, dev)
     if q_out is not None:
-        pqo, sqo = _rows(q_out, "q_out", params.num_qo_heads, d, dt, n)
+        pqo, sqo = _rows(q_out, "q_out", params.num_qo_heads, d, dt, n, dev)
     B = (params.batch,)
-    _ok(_lib().sgl_mla_kv_append(None if rope is None else rope.handle, ctypes.byref(params), pq, sq, pk, sk,
-                                 _dev(kv_pool, "kv_pool"), _dev(req_to_token, "req_to_token"), req_to_token.shape[1],
-                                 _ints(lens, "lens", B),
-                                 None if extend_lens is None else _ints(extend_lens, "extend_lens", B), n, pqo, sqo,
-                                 _dev(workspace, "workspace"), workspace.numel() * workspace.element_size(),
-                                 _stream(stream)), "sgl_mla_kv_append")
+    rows = req_to_token.shape
+    st = _lib().sgl_mla_kv_append(None if rope is None else rope.handle, ctypes.byref(params), pq, sq, pk, sk,
+                                  _flat(kv_pool, "kv_pool", dev), _flat(req_to_token, "req_to_token", dev, T.int32),
+                                  rows[1], _flat(lens, "lens", dev, T.int32, B),
+                                  None if extend_lens is None else _flat(extend_lens, "extend_lens", dev, T.int32, B), n,
+                                  pqo, sqo, _flat(workspace, "workspace", dev), workspace.nbytes, _stream(stream))
+    if st:
+        raise SglError(st, "sgl_mla_kv_append")

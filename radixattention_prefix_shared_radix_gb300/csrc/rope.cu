@@ -20,8 +20,9 @@
 // threads compute the tokens' sines and cosines into shared memory, once for
 // all heads; then each thread takes units of 16 elements -- two 16-byte (32
 // for fp32) pieces that the rotation pairs up -- from the new rows to the
-// outputs.  The first unit's loads are issued before the positions are
-// known.  Memory-bound: rows are read and written once.
+// outputs, the next unit's loads in flight; the first are issued before the
+// positions are known.  Memory-bound: rows are
+// read and written once.
 //
 // ["SGLang 深度解读" (luoboask.github.io) section "5. Attention 层": the new
 // tokens' K/V are stored into token_to_kv_pool at their req_to_token slots
@@ -39,7 +40,7 @@
 // Frequencies of the rotated pairs (host object).
 struct sgl_rope_table {
     sgl_rope_params p;
-    float amplitude;                 // multiplies cos and sin
+    double amplitude;                // multiplies cos and sin
     uint64_t turn[SGL_ROPE_MAX_DIM / 2];   // 2^64 / (2 pi) radians per position, rounded
 };
 
@@ -69,10 +70,11 @@ struct RopeArgs {
     int B, Hq, Hk, Hv, d;
     int rot, off;                    // rotated part [off, off + rot) of a head (rot 0: none)
     int pairs;                       // layout
-    int T, units, slice;             // tokens per CTA, units per token, units per CTA and token
+    int T, slice, lg;                // tokens per CTA; heads per CTA and token; log2 of a power of two of units per head
     int row_bytes;                   // bytes of a pool row
+    uint32_t uph_inv;                // ceil(2^32 / units per head): exact quotients of units below 2^16
     bool copy_q;                     // q_out is not q: the part that is not rotated is copied
-    float k_scale, v_scale, amplitude;
+    float k_scale, v_scale, amp_hi, amp_lo;
     uint64_t turn[kMaxHalf];
 };
 
@@ -108,14 +110,45 @@ __device__ __forceinline__ bool find_request(const int32_t* ext, int B, int64_t 
     return false;
 }
 
-// cos and sin of the angle `ph` / 2^64 turns
-__device__ __forceinline__ float2 cos_sin_turn(uint64_t ph) {
+// cos and sin of the angle `ph` / 2^64 turns, times the amplitude (hi + lo),
+// each within a little over half a unit in the last place: appended keys are
+// quantised next, and a wrong last bit can move a code.  After the nearest
+// quarter turn is taken off, the angle x = xh + xl (two floats) is at most
+// pi / 4; sine and cosine are the Taylor sums to x^11 and x^12 (the terms left
+// out are below 2^-36), ordered so that everything but one addition is small.
+__device__ __forceinline__ float2 cos_sin_turn(uint64_t ph, float amp_hi, float amp_lo) {
     const uint32_t quarter = (uint32_t)((ph + (1ull << 61)) >> 62);
     const int64_t rest = (int64_t)(ph - ((uint64_t)quarter << 62));     // [-1/8, 1/8) turn
-    // half turns = rest / 2^63; 32 of its bits (an angle below 2^-34 turns is
-    // below the last bit of the products it enters)
-    float s, c;
-    sincospif((float)(int32_t)(rest >> 30) * 0x1p-33f, &s, &c);
+    // rest = 2^26 n + .. : n (36 bits) as the sum of two floats, in turns of 2^-38
+    const int64_t n = rest >> 26;
+    const float nh = (float)(int32_t)(n >> 12) * 4096.f;
+    const float nl = (float)((int32_t)(n - ((int64_t)(int32_t)(n >> 12) << 12)));
+    // 2 pi 2^-38 as the sum of two floats
+    constexpr double kTurn = 6.283185307179586476925286766559 * 0x1p-38;
+    constexpr float kH = (float)kTurn, kL = (float)(kTurn - (double)kH);
+    const float xh0 = nh * kH;
+    const float xl0 = fmaf(nh, kL, fmaf(nl, kH, fmaf(nh, kH, -xh0)));
+    const float x = xh0 + xl0, xl = xl0 - (x - xh0);
+    const float z = x * x;
+    float ps = fmaf(z, -1.f / 39916800.f, 1.f / 362880.f);
+    ps = fmaf(z, ps, -1.f / 5040.f);
+    ps = fmaf(z, ps, 1.f / 120.f);
+    ps = fmaf(z, ps, -1.f / 6.f);
+    float pc = fmaf(z, 1.f / 479001600.f, -1.f / 3628800.f);
+    pc = fmaf(z, pc, 1.f / 40320.f);
+    pc = fmaf(z, pc, -1.f / 720.f);
+    pc = fmaf(z, pc, 1.f / 24.f);
+    // sin = x + (x z ps + xl cos): sh + sl; cos = 1 - z / 2 + (z^2 pc - x xl): ch + cl
+    const float half = 0.5f * z, ch0 = 1.f - half;
+    const float zl = fmaf(x, x, -z);                       // x^2 = z + zl
+    const float st = fmaf(x * z, ps, xl * ch0);
+    const float ct = ((1.f - ch0) - half) + (fmaf(z * z, pc, -x * xl) - 0.5f * zl);
+    // times the amplitude, rounded once: (h + l) (amp_hi + amp_lo)
+    auto times = [&](float h, float l) {
+        const float t = h * amp_hi;
+        return t + (fmaf(h, amp_hi, -t) + fmaf(l, amp_hi, h * amp_lo));
+    };
+    const float s = times(x, st), c = times(ch0, ct);
     float2 r = (quarter & 1u) ? make_float2(-s, c) : make_float2(c, s);
     if (quarter & 2u) r = make_float2(-r.x, -r.y);
     return r;
@@ -164,42 +197,6 @@ struct Eight<float> {
         x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
     }
 };
-// a unit of 16 elements of one head of one token
-struct Unit {
-    int part;        // 0: q, 1: k, 2: v
-    int h;           // head
-    int e0, e1;      // its two runs of eight elements within the head
-    int fr;          // first frequency, or -1: not rotated
-};
-__device__ __forceinline__ Unit unit_of(const RopeArgs& a, int u) {
-    const int uph = a.d >> 4;
-    int hh = u / uph;
-    const int c = u - hh * uph;
-    Unit x;
-    x.part = 0;
-    if (hh >= a.Hq) {
-        hh -= a.Hq;
-        x.part = 1;
-        if (hh >= a.Hk) {
-            hh -= a.Hk;
-            x.part = 2;
-        }
-    }
-    x.h = hh;
-    const int rc = c - (a.off >> 4);
-    x.e0 = 16 * c;
-    x.e1 = x.e0 + 8;
-    x.fr = -1;
-    if (x.part < 2 && rc >= 0 && rc < (a.rot >> 4)) {
-        x.fr = 8 * rc;
-        if (!a.pairs) {
-            x.e0 = a.off + 8 * rc;
-            x.e1 = x.e0 + (a.rot >> 1);
-        }
-    }
-    return x;
-}
-
 // largest magnitude of eight bf16 values as a pair of 16-bit patterns
 // (patterns order like magnitudes, NaN above infinity)
 __device__ __forceinline__ uint32_t amax8(uint4 w) {
@@ -207,38 +204,102 @@ __device__ __forceinline__ uint32_t amax8(uint4 w) {
     return __vmaxu2(__vmaxu2(w.x & m, w.y & m), __vmaxu2(w.z & m, w.w & m));
 }
 
-template <typename T, int POOL>
-__global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ RopeArgs a) {
-    __shared__ __align__(16) float2 cs[kMaxT][kMaxHalf];
+// c = z / f for eight bf16 values of magnitudes up to `m` (16-bit patterns), f
+// >= 0; zeros where f is 0.  Exact ties are common (bf16 over a product of few
+// bits) and must round as the quotient does, so a multiplication by 1 / f
+// alone will not do.  One correction makes it the rounded quotient
+// (Markstein 1990: q = z y, q + (z - q f) y with y the rounded reciprocal);
+// blocks whose magnitudes could leave the range of its products, and
+// infinities and NaN, are divided.
+__device__ __forceinline__ void divide8(const float* z, float f, uint32_t m, float* c) {
+    if (f >= 0x1p-60f && f <= 0x1p60f && max(m & 0xffffu, m >> 16) < 0x7f80u) {
+        const float y = __frcp_rn(f);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const float q = z[j] * y;
+            c[j] = fmaf(fmaf(-q, f, z[j]), y, q);
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) c[j] = f > 0.f ? __fdiv_rn(z[j], f) : z[j] * 0.f;
+    }
+}
+
+// The units that a thread works on, one after another: unit c of head h (of
+// this CTA's Hs heads of each token) of token t.  POW2: a head has a power of
+// two of units, so c stays and h moves by a fixed step.
+template <bool POW2>
+struct Cursor {
+    int t, h, c, i;
+    __device__ __forceinline__ void settle(int T, int Hs) {
+        while (h >= Hs && t < T) {
+            h -= Hs;
+            ++t;
+        }
+    }
+    __device__ __forceinline__ void start(const RopeArgs& a, int tid, int Hs) {
+        t = 0;
+        if constexpr (POW2) {
+            c = tid & ((a.d >> 4) - 1);
+            h = tid >> a.lg;
+            settle(a.T, Hs);
+        } else {
+            i = tid;
+            place(a, Hs);
+        }
+    }
+    __device__ __forceinline__ void next(const RopeArgs& a, int Hs) {
+        if constexpr (POW2) {
+            h += kThreads >> a.lg;
+            settle(a.T, Hs);
+        } else {
+            i += kThreads;
+            place(a, Hs);
+        }
+    }
+    __device__ __forceinline__ void place(const RopeArgs& a, int Hs) {
+        const int g = (int)__umulhi((uint32_t)i, a.uph_inv);       // i / units per head
+        c = i - g * (a.d >> 4);
+        t = 0;
+        h = g;
+        settle(a.T, Hs);
+    }
+};
+
+template <typename T, int POOL, bool POW2>
+__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 3) rope_kernel(const __grid_constant__ RopeArgs a) {
+    __shared__ __align__(16) float cs[kMaxT][2][kMaxHalf];     // cosines, sines
     __shared__ int s_pos[kMaxT], s_slot[kMaxT];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int64_t n0 = (int64_t)blockIdx.x * a.T;
-    const int u0 = blockIdx.y * a.slice;                       // this CTA's units of each token
-    const int nu = min(a.slice, a.units - u0);
-    const int total = a.T * nu;
+    const int hb = blockIdx.y * a.slice;                       // this CTA's heads of each token (q, then k, then v)
+    const int Hs = min(a.slice, a.Hq + a.Hk + a.Hv - hb);
     grid_dep_wait();      // launched as a programmatic dependent: inputs may come from the kernel before
     grid_dep_launch();
-    auto row_ptr = [&](const Unit& x, int64_t n, int64_t* at) -> const void* {
-        *at = n * (x.part == 0 ? a.qs : x.part == 1 ? a.ks : a.vs) + (int64_t)x.h * a.d;
-        return x.part == 0 ? a.q : x.part == 1 ? a.k : a.v;
-    };
-    // the first unit's elements, in flight while the positions are looked up
+    const int rblk = a.off >> 4, rend = rblk + (a.rot >> 4);   // rotated units of a head
+    // a unit's two runs of eight elements
+    auto run0 = [&](int c, bool rot) { return rot && !a.pairs ? a.off + 8 * (c - rblk) : 16 * c; };
+    auto run1 = [&](int c, bool rot) { return rot && !a.pairs ? a.off + 8 * (c - rblk) + (a.rot >> 1) : 16 * c + 8; };
+    // the next unit's elements, the first in flight while the positions are looked up
     Eight<T> x0, x1;
-    Unit un{};
-    int tok = 0;
-    auto fetch = [&](int i) {
-        tok = i / nu;
-        if (i >= total || n0 + tok >= a.n_rows) {
-            tok = -1;
-            return;
-        }
-        un = unit_of(a, u0 + i - tok * nu);
-        int64_t at;
-        const void* p = row_ptr(un, n0 + tok, &at);
-        x0.load(p, at + un.e0);
-        x1.load(p, at + un.e1);
+    Cursor<POW2> cur{};
+    auto fetch = [&]() {
+        const int64_t n = n0 + cur.t;
+        if (cur.t >= a.T || n >= a.n_rows) return;
+        const int hh = hb + cur.h;
+        const T* p;
+        if (hh < a.Hq)
+            p = static_cast<const T*>(a.q) + n * a.qs + hh * a.d;
+        else if (hh < a.Hq + a.Hk)
+            p = static_cast<const T*>(a.k) + n * a.ks + (hh - a.Hq) * a.d;
+        else
+            p = static_cast<const T*>(a.v) + n * a.vs + (hh - a.Hq - a.Hk) * a.d;
+        const bool rot = hh < a.Hq + a.Hk && cur.c >= rblk && cur.c < rend;
+        x0.load(p, run0(cur.c, rot));
+        x1.load(p, run1(cur.c, rot));
     };
-    fetch(tid);
+    cur.start(a, tid, Hs);
+    fetch();
     // position and slot of each token: -1 where there is nothing to do
     if (warp < a.T) {
         const int64_t n = n0 + warp;
@@ -278,117 +339,119 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
         const int t = i / half, j = i - t * half;
         const int p = s_pos[t];
         if (p >= 0) {
-            const float2 v = cos_sin_turn((uint64_t)(uint32_t)p * a.turn[j]);
-            cs[t][j] = make_float2(v.x * a.amplitude, v.y * a.amplitude);
+            const float2 v = cos_sin_turn((uint64_t)(uint32_t)p * a.turn[j], a.amp_hi, a.amp_lo);
+            cs[t][0][j] = v.x;
+            cs[t][1][j] = v.y;
         }
     }
     __syncthreads();
     // (whole warps go round: 4-bit blocks are finished across lanes)
-    for (int i0 = warp * 32; i0 < total; i0 += kThreads) {
-        const int t = tok;
-        const Unit x = un;
-        const bool live = t >= 0 && s_pos[t < 0 ? 0 : t] >= 0;
-        const int slot = live ? s_slot[t] : -1;
+    while (__any_sync(0xffffffffu, cur.t < a.T)) {
+        const int t = min(cur.t, a.T - 1), c = cur.c, hh = hb + cur.h;
+        const bool live = cur.t < a.T && s_pos[t] >= 0;
         Eight<T> r0 = x0, r1 = x1;      // (what is not rotated keeps its bits)
-        fetch(i0 + kThreads + lane);
-        if (live && x.fr >= 0) {
-            float y[16];
+        cur.next(a, Hs);
+        fetch();
+        const int part = hh < a.Hq ? 0 : hh < a.Hq + a.Hk ? 1 : 2;
+        const bool rot = part < 2 && c >= rblk && c < rend;
+        const int e0 = run0(c, rot), e1 = run1(c, rot);
+        if (rot) {
+            const int fr = 8 * (c - rblk);
+            float y[16], co[8], si[8];
             r0.get(y);
             r1.get(y + 8);
-            // (written out, so that every instantiation rounds alike)
-            const float4* c4 = reinterpret_cast<const float4*>(&cs[t][x.fr]);
-            float c[8], s[8];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const float4 v = c4[j];
-                c[2 * j] = v.x;
-                s[2 * j] = v.y;
-                c[2 * j + 1] = v.z;
-                s[2 * j + 1] = v.w;
+            for (int j = 0; j < 8; j += 4) {
+                const float4 u = *reinterpret_cast<const float4*>(&cs[t][0][fr + j]);
+                const float4 w = *reinterpret_cast<const float4*>(&cs[t][1][fr + j]);
+                co[j] = u.x; co[j + 1] = u.y; co[j + 2] = u.z; co[j + 3] = u.w;
+                si[j] = w.x; si[j + 1] = w.y; si[j + 2] = w.z; si[j + 3] = w.w;
             }
+            // (written out, so that every instantiation rounds alike)
             if (a.pairs) {
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
                     const float p = y[2 * j], q = y[2 * j + 1];
-                    y[2 * j] = __fmaf_rn(p, c[j], -__fmul_rn(q, s[j]));
-                    y[2 * j + 1] = __fmaf_rn(q, c[j], __fmul_rn(p, s[j]));
+                    y[2 * j] = __fmaf_rn(p, co[j], -__fmul_rn(q, si[j]));
+                    y[2 * j + 1] = __fmaf_rn(q, co[j], __fmul_rn(p, si[j]));
                 }
             } else {
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
                     const float p = y[j], q = y[j + 8];
-                    y[j] = __fmaf_rn(p, c[j], -__fmul_rn(q, s[j]));
-                    y[j + 8] = __fmaf_rn(q, c[j], __fmul_rn(p, s[j]));
+                    y[j] = __fmaf_rn(p, co[j], -__fmul_rn(q, si[j]));
+                    y[j + 8] = __fmaf_rn(q, co[j], __fmul_rn(p, si[j]));
                 }
             }
             r0.set(y);
             r1.set(y + 8);
         }
         const int64_t n = n0 + t;
-        if (x.part == 0 || POOL == kPoolNone) {
-            if (live && (x.fr >= 0 || a.copy_q)) {
-                T* dst = x.part == 0 ? static_cast<T*>(a.qo) + n * a.qos : static_cast<T*>(a.ko) + n * a.kos;
-                dst += (int64_t)x.h * a.d;
-                r0.put(dst + x.e0);
-                r1.put(dst + x.e1);
+        if (part == 0 || POOL == kPoolNone) {
+            if (live && (rot || a.copy_q)) {
+                T* dst = part == 0 ? static_cast<T*>(a.qo) + n * a.qos + hh * a.d
+                                   : static_cast<T*>(a.ko) + n * a.kos + (hh - a.Hq) * a.d;
+                r0.put(dst + e0);
+                r1.put(dst + e1);
             }
+            if (POOL != kPoolFp4) continue;
         }
+        const int slot = live && part > 0 ? s_slot[t] : -1;
+        const int h = hh - a.Hq - (part == 2 ? a.Hk : 0);
+        uint8_t* row = (part == 1 ? a.kp : a.vp) + (int64_t)max(slot, 0) * a.row_bytes;
         if constexpr (POOL == kPoolSame) {
-            if (x.part > 0 && slot >= 0) {
-                T* dst = reinterpret_cast<T*>((x.part == 1 ? a.kp : a.vp) + (int64_t)slot * a.row_bytes) + x.h * a.d;
-                r0.put(dst + x.e0);
-                r1.put(dst + x.e1);
+            if (slot >= 0) {
+                T* dst = reinterpret_cast<T*>(row) + h * a.d;
+                r0.put(dst + e0);
+                r1.put(dst + e1);
             }
-        } else if constexpr (POOL == kPoolE4m3 || POOL == kPoolFp4) {
+        } else if constexpr (POOL == kPoolE4m3) {
             // quantised pools hold codes of the rows' bf16 values, as an
             // unfused rotation would have left them
-            const float scale = x.part == 1 ? a.k_scale : a.v_scale;
-            uint8_t* row = (x.part == 1 ? a.kp : a.vp) + (int64_t)max(slot, 0) * a.row_bytes;
-            float z[16];
-            r0.get(z);
-            r1.get(z + 8);
-            if constexpr (POOL == kPoolE4m3) {
-                if (x.part > 0 && slot >= 0) {
+            if (slot >= 0) {
+                const float scale = part == 1 ? a.k_scale : a.v_scale;
 #pragma unroll
-                    for (int b = 0; b < 2; ++b) {
-                        uint32_t c[4];
+                for (int b = 0; b < 2; ++b) {
+                    float z[8];
+                    (b ? r1 : r0).get(z);
+                    uint32_t w[4];
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            uint16_t h;
-                            const float lo = __fdiv_rn(z[8 * b + 2 * j], scale), hi = __fdiv_rn(z[8 * b + 2 * j + 1], scale);
-                            asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(h) : "f"(hi), "f"(lo));
-                            c[j] = h;
-                        }
-                        *reinterpret_cast<uint2*>(row + x.h * a.d + (b ? x.e1 : x.e0)) =
-                            make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
+                    for (int j = 0; j < 4; ++j) {
+                        uint16_t x;
+                        const float lo = __fdiv_rn(z[2 * j], scale), hi = __fdiv_rn(z[2 * j + 1], scale);
+                        asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(x) : "f"(hi), "f"(lo));
+                        w[j] = x;
                     }
+                    *reinterpret_cast<uint2*>(row + h * a.d + (b ? e1 : e0)) =
+                        make_uint2(w[0] | (w[1] << 16), w[2] | (w[3] << 16));
                 }
-            } else {
-                // The scale of each run's block of 16.  The runs are the two
-                // halves of one block (one amax), or, rotated in the half
-                // layout, half of one block each, whose other halves the
-                // neighbouring unit holds.
-                uint32_t m0 = amax8(r0.w), m1 = amax8(r1.w);
-                const bool split = x.fr >= 0 && !a.pairs && a.rot > 16;
-                const int other = split ? ((x.fr & 8) ? lane - 1 : lane + 1) : lane;
-                const uint32_t o0 = __shfl_sync(0xffffffffu, m0, other & 31), o1 = __shfl_sync(0xffffffffu, m1, other & 31);
-                m0 = __vmaxu2(m0, split ? o0 : m1);
-                m1 = split ? __vmaxu2(m1, o1) : m0;
-                if (x.part > 0 && slot >= 0) {
-                    const int co = fp4_code_off(x.h, a.d), so = fp4_scale_off(x.h, x.part == 1 ? a.Hk : a.Hv, a.d);
+            }
+        } else if constexpr (POOL == kPoolFp4) {
+            // The scale of each run's block of 16.  The runs are the two
+            // halves of one block (one amax), or, rotated in the half layout,
+            // half of one block each, whose other halves the neighbouring
+            // unit holds.
+            uint32_t m0 = amax8(r0.w), m1 = amax8(r1.w);
+            const bool split = rot && !a.pairs && a.rot > 16;
+            const int other = (split ? (((c - rblk) & 1) ? lane - 1 : lane + 1) : lane) & 31;
+            const uint32_t o0 = __shfl_sync(0xffffffffu, m0, other), o1 = __shfl_sync(0xffffffffu, m1, other);
+            m0 = __vmaxu2(m0, split ? o0 : m1);
+            m1 = split ? __vmaxu2(m1, o1) : m0;
+            if (slot >= 0) {
+                const float scale = part == 1 ? a.k_scale : a.v_scale;
+                row += fp4_code_off(h, a.d);
+                uint8_t* const sfs = row - fp4_code_off(h, a.d) + fp4_scale_off(h, part == 1 ? a.Hk : a.Hv, a.d);
 #pragma unroll
-                    for (int b = 0; b < 2; ++b) {
-                        const uint32_t m = b ? m1 : m0;
-                        const float amax = __uint_as_float(max(m & 0xffffu, m >> 16) << 16);
-                        const uint32_t sf = e4m3_of(__fdiv_rn(amax, 6.f * scale));
-                        const float f = e4m3_value(sf) * scale;
-                        float c[8];
-#pragma unroll
-                        for (int j = 0; j < 8; ++j) c[j] = f > 0.f ? __fdiv_rn(z[8 * b + j], f) : z[8 * b + j] * 0.f;
-                        const int e = b ? x.e1 : x.e0;
-                        *reinterpret_cast<uint32_t*>(row + co + e / 2) = e2m1x8_of(c);
-                        if ((e & 8) == 0) row[so + e / 16] = (uint8_t)sf;
-                    }
+                for (int b = 0; b < 2; ++b) {
+                    const uint32_t m = b ? m1 : m0;
+                    const float amax = __uint_as_float(max(m & 0xffffu, m >> 16) << 16);
+                    const uint32_t sf = e4m3_of(__fdiv_rn(amax, 6.f * scale));
+                    float z[8], q[8];
+                    (b ? r1 : r0).get(z);
+                    divide8(z, e4m3_value(sf) * scale, m, q);
+                    const int e = b ? e1 : e0;
+                    *reinterpret_cast<uint32_t*>(row + e / 2) = e2m1x8_of(q);
+                    if ((e & 8) == 0) sfs[e / 16] = (uint8_t)sf;
                 }
             }
         }
@@ -410,18 +473,23 @@ bool rows_ok(const void* p, int64_t stride, int heads, int d, int es) {
     return p && aligned16(p) && stride >= (int64_t)heads * d && stride * es % 16 == 0;
 }
 
-template <typename T, int POOL>
-int launch(RopeArgs& a, cudaStream_t s) {
-    if (a.n_rows == 0 || a.units == 0) return SGL_OK;
-    // Tokens per CTA and slices of a token's heads: four tokens share a CTA
-    // once that leaves every SM its eight CTAs; below one CTA per SM a
-    // token's heads are spread over several (of at least 64 units each).
+template <typename T, int POOL, bool POW2>
+int launch_as(RopeArgs& a, cudaStream_t s) {
+    // Tokens per CTA and slices of a token's heads: up to four tokens share a
+    // CTA (one chain of lookups for more work) as long as every SM still has
+    // one; below one token per SM a token's heads are spread over several
+    // CTAs (of at least 64 units each).
     constexpr int kSms = 152;
-    a.T = a.n_rows >= (int64_t)kMaxT * kSms * 4 ? kMaxT : 1;
+    const int heads = a.Hq + a.Hk + a.Hv, uph = a.d / 16;
+    if ((int64_t)heads * uph > 0xffff / kMaxT) return SGL_ERR_UNSUPPORTED;   // (the cursor's quotients)
+    a.T = (int)std::min<int64_t>(kMaxT, std::max<int64_t>(1, a.n_rows / kSms));
     int slices = 1;
-    if (a.n_rows < kSms) slices = (int)std::min<int64_t>((kSms + a.n_rows - 1) / a.n_rows, (a.units + 63) / 64);
-    a.slice = ((a.units + slices - 1) / slices + 31) / 32 * 32;
-    slices = (a.units + a.slice - 1) / a.slice;
+    if (a.n_rows < kSms) slices = (int)std::min<int64_t>((kSms + a.n_rows - 1) / a.n_rows, (heads * uph + 63) / 64);
+    a.slice = (heads + slices - 1) / slices;
+    slices = (heads + a.slice - 1) / a.slice;
+    a.uph_inv = uph > 1 ? (uint32_t)(((1ull << 32) + uph - 1) / uph) : 0u;
+    a.lg = 0;
+    while ((1 << a.lg) < uph) ++a.lg;
     const int64_t ctas = (a.n_rows + a.T - 1) / a.T;
     if (ctas > INT32_MAX) return SGL_ERR_UNSUPPORTED;
     cudaLaunchAttribute pdl[1];
@@ -433,7 +501,16 @@ int launch(RopeArgs& a, cudaStream_t s) {
     cfg.stream = s;
     cfg.attrs = pdl;
     cfg.numAttrs = 1;
-    return cuda_status(cudaLaunchKernelEx(&cfg, rope_kernel<T, POOL>, a));
+    return cuda_status(cudaLaunchKernelEx(&cfg, rope_kernel<T, POOL, POW2>, a));
+}
+
+template <typename T, int POOL>
+int launch(RopeArgs& a, cudaStream_t s) {
+    if (a.n_rows == 0 || a.Hq + a.Hk + a.Hv == 0) return SGL_OK;
+    if ((a.d & (a.d - 1)) == 0) return launch_as<T, POOL, true>(a, s);
+    // other widths: rotation alone and MLA rows (the pools' heads are 64 or 128 wide)
+    if constexpr (POOL == kPoolNone || (POOL == kPoolSame && sizeof(T) == 2)) return launch_as<T, POOL, false>(a, s);
+    return SGL_ERR_UNSUPPORTED;
 }
 
 void set_table(RopeArgs& a, const sgl_rope_table* t) {
@@ -441,7 +518,8 @@ void set_table(RopeArgs& a, const sgl_rope_table* t) {
     a.rot = t->p.rot_dim;
     a.off = t->p.rot_offset;
     a.pairs = t->p.layout == SGL_ROPE_PAIRS;
-    a.amplitude = t->amplitude;
+    a.amp_hi = (float)t->amplitude;
+    a.amp_lo = (float)(t->amplitude - (double)a.amp_hi);
     std::memcpy(a.turn, t->turn, sizeof(uint64_t) * (size_t)(t->p.rot_dim / 2));
 }
 
@@ -541,7 +619,7 @@ int sgl_rope_create(const sgl_rope_params* p, sgl_rope_table** out) {
     }
     double amp = p->attention_factor;
     if (amp == 0.0) amp = kind == SGL_ROPE_SCALE_YARN ? 0.1 * std::log(by) + 1.0 : 1.0;
-    t->amplitude = (float)amp;
+    t->amplitude = amp;
     *out = t;
     return SGL_OK;
 }
@@ -579,7 +657,6 @@ int sgl_rope(const sgl_rope_table* rope, int32_t dtype, const void* q, int64_t q
     a.Hq = num_q_heads;
     a.Hk = num_k_heads;
     a.d = d;
-    a.units = (num_q_heads + num_k_heads) * (d / 16);
     a.copy_q = (num_q_heads > 0 && q != q_out) || (num_k_heads > 0 && k != k_out);
     auto s = reinterpret_cast<cudaStream_t>(stream);
     return es == 4 ? launch<float, kPoolNone>(a, s) : launch<bf16, kPoolNone>(a, s);
@@ -609,7 +686,6 @@ int sgl_kv_append(const sgl_rope_table* rope, const sgl_attn_params* params, con
     a.vp = static_cast<uint8_t*>(v_pool);
     a.num_slots = params->num_slots;
     a.Hk = a.Hv = Hkv;
-    a.units = (a.Hq + 2 * Hkv) * (d / 16);
     a.k_scale = params->k_scale;
     a.v_scale = params->v_scale;
     auto s = reinterpret_cast<cudaStream_t>(stream);
@@ -642,7 +718,6 @@ int sgl_mla_kv_append(const sgl_rope_table* rope, const sgl_mla_params* params, 
     a.num_slots = params->num_slots;
     a.Hk = 1;
     a.Hv = 0;
-    a.units = (a.Hq + 1) * (d / 16);
     a.row_bytes = d * 2;
     return launch<bf16, kPoolSame>(a, reinterpret_cast<cudaStream_t>(stream));
 }
