@@ -1,26 +1,30 @@
-// Decode attention over a 4-bit cache (SGL_DTYPE_BF16_FP4KV): the persistent
-// launch of decode_fused.cu -- shared prefixes on tcgen05 tiles, everything
-// else streamed, then the log-sum-exp merge -- with streams of their own.
+// Decode attention over a 4-bit cache (SGL_DTYPE_BF16_FP4KV): work items, tiles
+// and merge as in decode_fused.cu, streams of its own.
 //
 // At 4.5 bits a value a token's K and V of 8 heads of 128 are 1152 bytes
 // instead of 4096, so per byte the streams do 3.5 times the conversions and
 // products of the bf16 ones, and per token the copies are as many.  What
 // differs from decode_fused.cu, and why:
 //   * TMA gathers of four rows instead of a bulk copy per row.  Measured on
-//     GB300 (random 576-byte rows, all SMs): two warps issuing gathers move
-//     7.6 TB/s, four / eight warps of bulk copies 6.4 / 7.1.  The price is
-//     that rows land back to back (no padding): bank conflicts are kept at
-//     two ways by the order in which the MMA rows take the positions (pi).
-//   * Steps of 32 positions, so that the softmax's shuffles, votes and the
-//     barriers are paid half as often.
-//   * One consumer warp per KV head for up to 16 query rows, which takes the
-//     rows in one or two 8-row MMA columns: codes are converted once for both
-//     (decode_fused.cu gives a head with more than 8 rows two warps, which
-//     would convert everything twice).  That takes registers: 12 warps of up
-//     to 168 instead of 15 of 128.
+//     GB300 (random 576-byte rows, all SMs): two warps per SM issuing gathers
+//     move 7.6 TB/s, four / eight warps of bulk copies 6.4 / 7.1.  The price
+//     is that rows land back to back (no padding): bank conflicts are kept at
+//     two ways by the order in which the MMA rows take the positions (pi16).
+//   * Steps of 32 positions, and a running maximum that a step only has to
+//     vote on, so that barriers and shuffles are paid half as often or not at
+//     all.
+//   * Two streaming CTAs per SM, 16 consumer warps in all.  A consumer warp is
+//     a chain of conversion, scaling and product that issues an instruction
+//     every four to five clocks; eight of them (one CTA of 12 warps with up to
+//     168 registers, which also converted a head's codes once for 16 query
+//     rows) left the issue slots 44% used and took 69 us for what the copies
+//     alone do in 45.
+//   * The tiles (shared prefixes) are a launch of their own, because their
+//     roles need 128 registers a thread.  The streams are launched behind it
+//     and start at once on the SMs that it leaves free.
 //
-// Roles after the tiles (12 warps): warp 1 lookup, warps 2 and 3 producers (K
-// rows, V rows), warps 4-11 consumers, one KV head each.
+// Streaming roles (10 warps): 0 lookup, 1 producer, 2-9 consumers (one KV head
+// each for up to 8 query rows, two warps per head for up to 16).
 //
 // Consumer step (mma.sync m16n8k16, f16 in, fp32 acc), per 16 positions:
 //   S^T [16 pos x 8 rows] = K [16 x d] . Q^T,  O^T [d x 8 rows] += V^T . P^T
@@ -43,76 +47,95 @@
 namespace sgl {
 namespace {
 
-constexpr int kHB = kDecHeadBlock;          // consumer warps = KV heads of a piece (at most)
+constexpr int kHB = kDecHeadBlock;          // consumer warps
 constexpr int kNP = 32;                     // KV positions per step
 constexpr int kQuads = kNP / 4;             // gathers per pool and step
-constexpr int kLookup = 1;
-constexpr int kFirstProducer = 2;
-constexpr int kProducers = 2;               // K, V
-constexpr int kFirstConsumer = 4;
-constexpr int kFp4Threads = 32 * (kFirstConsumer + kHB);
+constexpr int kLookup = 0;
+constexpr int kProducer = 1;
+constexpr int kFirstConsumer = 2;
+constexpr int kStreamThreads = 32 * (kFirstConsumer + kHB);
+constexpr int kStreamCtas = 2;              // per SM
 using Ent = SlotEntry<kNP>;
 
-// the tile roles: all 12 warps (7 of them gather), two K/V stages and the staging area
+// the tile roles: 15 warps (10 of them gather), two K/V stages and the staging area
 template <int D>
-using Fp4Cfg = TcCfg<D, true, 1, 2, 7, 128, 2, kKvFp4>;
-static_assert(Fp4Cfg<128>::kThreads == kFp4Threads && Fp4Cfg<64>::kThreads == kFp4Threads,
-              "the tile roles take the whole CTA");
+using Fp4Cfg = TcCfg<D, true, 1, 2, 10, 128, 2, kKvFp4>;
 
-// bytes of a piece's row (its head block), as the gathers copy them
+// bytes of a piece's row (its block of up to `heads` heads), as the gathers copy them
 template <int D>
-__host__ __device__ constexpr int fp4_box_bytes(int hkv) {
-    return fp4_row_bytes(hkv < kHB ? hkv : kHB, D);
+__host__ __device__ constexpr int fp4_box_bytes(int hkv, int heads) {
+    return fp4_row_bytes(hkv < heads ? hkv : heads, D);
 }
 
 template <int D>
 struct Fp4Layout {
-    using TL = typename Fp4Cfg<D>::Lay;
-    static constexpr int BOX = fp4_box_bytes<D>(kHB);            // the widest row
+    static constexpr int BOX = fp4_box_bytes<D>(kHB, kHB);       // the widest row
     static constexpr int QP = (4 * BOX + 127) / 128 * 128;       // a quad of rows (TMA destinations: 128-byte aligned)
     static constexpr int STAGE = 2 * kQuads * QP;                // K quads, then V quads
-    static constexpr int SLOTW = kSQ * Ent::kBytes;
+    static constexpr int NSF = D == 128 ? 3 : 6;                 // ring stages
     static constexpr int DESC = 64;
-    static constexpr int FIXED = 1024 + SLOTW + 12 * DESC + 64 + (2 * 12 + 2 * kSQ) * 8 + 1024;
-    static constexpr int NSF0 = (232448 - FIXED) / STAGE;
-    static constexpr int NSF = NSF0 > 12 ? 12 : NSF0;
-    static constexpr int OFF_RING = 1024;
-    static constexpr int OFF_SLOT = OFF_RING + NSF * STAGE;
-    static constexpr int OFF_DESC = OFF_SLOT + SLOTW;
+    static constexpr int OFF_SLOT = NSF * STAGE;
+    static constexpr int OFF_DESC = OFF_SLOT + kSQ * Ent::kBytes;
     static constexpr int OFF_LREC = OFF_DESC + NSF * DESC;       // launch piece: record (32 B), members (32 B)
-    static constexpr int END_S = OFF_LREC + 64;
-    // the streaming barriers: clear of the tile roles' area, which the rest overlaps
-    static constexpr int OFF_SBAR = ((END_S > TL::END ? END_S : TL::END) + 7) / 8 * 8;
-    static constexpr int END = OFF_SBAR + (2 * NSF + 2 * kSQ) * 8;
-    static constexpr int TOTAL = END + 1024;                     // + alignment slack
-    static_assert(NSF >= 4 && TOTAL <= 232448, "ring depth, shared memory per CTA");
-    static_assert(TL::KEEP <= OFF_RING, "the ring clears the tile roles' kept area");
-    static_assert(TOTAL > 116 * 1024, "one CTA per SM: tiles allocate all 512 TMEM columns");
+    static constexpr int OFF_BAR = OFF_LREC + 64;
+    static constexpr int END = OFF_BAR + (2 * NSF + 2 * kSQ) * 8;
+    static constexpr int TOTAL = END + 128;                      // + alignment slack
+    static_assert(kStreamCtas * (TOTAL + 1024) <= 228 * 1024, "shared memory of an SM");
 };
 
-// stage descriptor: position of the step, flags, mask of its positions that
-// hold data; a piece's first step: its fields and member requests
-constexpr int kDescP0 = 0, kDescFlags = 4, kDescMask = 8, kDescCm = 12, kDescPb = 16, kDescRows = 20, kDescNh = 24,
-              kDescKvh = 28, kDescMem = 32;
+// stage descriptor: flags and the mask of the step's positions that hold data;
+// a piece's first step: its fields and member requests
+constexpr int kDescFlags = 0, kDescMask = 4, kDescPb = 8, kDescRows = 12, kDescNh = 16, kDescKvh = 20, kDescMem = 32;
+
+// What a streaming CTA works with.
+struct Fp4Args {
+    FusedArgs f;
+    int box8, box4;        // bytes of a piece's row: blocks of up to 8 heads, of up to 4 (more than 8 query rows)
+    int after_tiles;       // launched behind the tiles
+};
 
 // ---------------------------------------------------------------------------
-// Producer warp pw (0: K, 1: V): per step waits for the slot entry and a free
-// stage, then lane q < 8 gathers rows 4q .. 4q + 3.  Rows without data
-// (positions past the end, slots outside the pool) are masked by the
-// consumers; a quad of them is not copied, in a mixed quad they repeat a row.
+// Lookup: as in decode_fused.cu, up to 8 steps ahead of the copies; the
+// piece's query rows are fetched into L1 meanwhile (what the ring leaves of it
+// holds them), since the consumers' first use of them holds up the stage.
 // ---------------------------------------------------------------------------
 template <int D>
-__device__ __noinline__ void fp4_producer(const FusedArgs& f, const CUtensorMap* tm, int pw, uint32_t box, uint32_t ring,
-                                          uint32_t sring, uint32_t desc, uint32_t full, uint32_t empty, uint32_t sfull,
-                                          uint32_t sfree, int lane) {
+__device__ __forceinline__ void fp4_lookup(const Fp4Args& p, int gw, uint32_t lrec, uint32_t sring, uint32_t sfull,
+                                        uint32_t sfree, int lane) {
+    const FusedArgs& f = p.f;
+    stream_lookup<kNP>(f, gw, lrec, sring, sfull, sfree, lane, [&](int kvh, int nh, int nm, int mem) {
+        const int lines = nh * f.t.G * D * 2 / 128;   // of a member's rows of these heads, which are contiguous
+        for (int i = 0; i < nm; ++i) {
+            const int r = __shfl_sync(0xffffffffu, mem, i);
+            const char* row = reinterpret_cast<const char*>(f.t.q + ((int64_t)r * f.t.Hq + kvh * f.t.G) * D);
+            for (int l = lane; l < lines; l += 32) prefetch_l1(row + 128 * l);
+        }
+    });
+}
+
+// ---------------------------------------------------------------------------
+// Producer: per step waits for the slot entry and a free stage, then lane i
+// gathers rows 4i .. 4i + 3 of K (i < 8) or 4i - 32 .. of V.  Rows without
+// data (positions past the end, slots outside the pool) are masked by the
+// consumers; a quad of them is not copied, in a mixed quad they repeat a row.
+// tm: the K and V views with rows of 8 heads, then with rows of 4.
+// ---------------------------------------------------------------------------
+template <int D>
+__device__ __forceinline__ void fp4_producer(const Fp4Args& p, const CUtensorMap* k8, const CUtensorMap* v8,
+                                          const CUtensorMap* k4, const CUtensorMap* v4, uint32_t ring, uint32_t sring,
+                                          uint32_t desc, uint32_t full, uint32_t empty, uint32_t sfull, uint32_t sfree,
+                                          int lane) {
     using Lay = Fp4Layout<D>;
     constexpr int NS = Lay::NSF;
-    uint32_t* const err = f.t.err;
-    const int G = f.t.G;
-    const int64_t num_slots = f.t.num_slots;
-    const bool lead = pw == 0;
+    uint32_t* const err = p.f.t.err;
+    const int G = p.f.t.G;
+    const int64_t num_slots = p.f.t.num_slots;
+    const bool v = lane >= kQuads;                 // (lanes 8 .. 15)
+    const int quad = lane & (kQuads - 1);
     int last_armed = -1, last_arrived = -1;
-    int cur_nh = 0;
+    const CUtensorMap* tm = nullptr;
+    uint32_t box = 0u;
+    int cm = 0;                                    // end of the current piece
     for (int r = 0;; ++r) {
         const int ent = r & (kSQ - 1);
         const uint32_t eb = sring + ent * Ent::kBytes;
@@ -120,62 +143,69 @@ __device__ __noinline__ void fp4_producer(const FusedArgs& f, const CUtensorMap*
             atomicOr(err, 4u);
             break;
         }
+        // everything about the step is read before its stage is waited for,
+        // so that its copies leave as soon as the stage is free
         const int kvh = ld_shared_s32(eb + Ent::kKvh);
         const int flags = ld_shared_s32(eb + Ent::kFlags);
         const int st = r % NS;
+        const uint32_t db = desc + st * Lay::DESC;
+        const uint32_t fb = full + 8 * st;
+        const bool first = kvh >= 0 && (flags & kFirst) != 0;
+        int pb = 0, nh = 0, nm = 0, mem = 0;
+        if (first) {
+            pb = ld_shared_s32(eb + Ent::kPb);
+            nh = ld_shared_s32(eb + Ent::kNh);
+            nm = ld_shared_s32(eb + Ent::kNm);
+            cm = ld_shared_s32(eb + Ent::kCm);
+            mem = lane < kDecPieceMembers ? ld_shared_s32(eb + Ent::kMem + 4 * lane) : 0;
+            const bool wide = nm * G > 8;
+            tm = wide ? (v ? v4 : k4) : (v ? v8 : k8);
+            box = (uint32_t)(wide ? p.box4 : p.box8);
+        }
+        const int32_t mine = ld_shared_s32(eb + 4 * lane);
+        const bool past = mine == kPastEnd || ld_shared_s32(eb + Ent::kP0) + lane >= cm;
+        const bool ok = kvh >= 0 && !past && mine >= 0 && mine < num_slots;
+        if (kvh >= 0 && !ok && !past) atomicOr(err, 1u);
+        const uint32_t mask = __ballot_sync(0xffffffffu, ok);
+        int32_t row[4];
+        const uint32_t qm = lane < 2 * kQuads ? (mask >> (4 * quad)) & 15u : 0u;
+        const int some = 4 * quad + (qm ? __ffs(qm) - 1 : 0);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) row[i] = __shfl_sync(0xffffffffu, mine, (qm >> i) & 1u ? 4 * quad + i : some);
+        const uint32_t quads = __ballot_sync(0xffffffffu, qm != 0);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(sfree + 8 * ent);     // every lane has read the entry
         if (!mbar_wait(empty + 8 * st, ((r / NS) & 1) ^ 1)) {
             atomicOr(err, 4u);
             break;
         }
-        const uint32_t db = desc + st * Lay::DESC;
-        const uint32_t fb = full + 8 * st;
         if (kvh < 0) {
             if (lane == 0) {
-                if (lead) st_shared_s32(db + kDescFlags, kEnd);
+                st_shared_s32(db + kDescFlags, kEnd);
                 mbar_arrive(fb);
             }
             last_arrived = r;
-            __syncwarp();
-            if (lane == 0) mbar_arrive(sfree + 8 * ent);
             break;
         }
-        const bool first = (flags & kFirst) != 0;
-        if (first) cur_nh = ld_shared_s32(eb + Ent::kNh);
-        const int32_t mine = ld_shared_s32(eb + 4 * lane);
-        const bool ok = mine >= 0 && mine < num_slots;
-        if (lead && !ok && mine != kPastEnd) atomicOr(err, 1u);
-        const uint32_t mask = __ballot_sync(0xffffffffu, ok);
-        int32_t row[4];
-        const uint32_t qm = lane < kQuads ? (mask >> (4 * lane)) & 15u : 0u;
-        if (qm) {
-            const int some = ld_shared_s32(eb + 4 * (4 * lane + __ffs(qm) - 1));
-#pragma unroll
-            for (int i = 0; i < 4; ++i) row[i] = (qm >> i) & 1u ? ld_shared_s32(eb + 4 * (4 * lane + i)) : some;
-        }
-        const uint32_t quads = __ballot_sync(0xffffffffu, qm != 0);
-        if (lead && lane == 0) {
-            st_shared_s32(db + kDescP0, ld_shared_s32(eb + Ent::kP0));
+        if (lane == 0) mbar_expect_tx_only(fb, (uint32_t)__popc(quads) * 4u * box);
+        __syncwarp();
+        if (qm)
+            tma_gather4(ring + st * Lay::STAGE + lane * Lay::QP, tm, (kvh >> 2) * (4 * fp4_head_bytes(D)) / 4, row[0],
+                        row[1], row[2], row[3], fb);
+        if (lane == 0) {
             st_shared_s32(db + kDescFlags, flags);
             st_shared_s32(db + kDescMask, (int32_t)mask);
             if (first) {
-                st_shared_s32(db + kDescCm, ld_shared_s32(eb + Ent::kCm));
-                st_shared_s32(db + kDescPb, ld_shared_s32(eb + Ent::kPb));
-                st_shared_s32(db + kDescRows, ld_shared_s32(eb + Ent::kNm) * G);
-                st_shared_s32(db + kDescNh, cur_nh);
+                st_shared_s32(db + kDescPb, pb);
+                st_shared_s32(db + kDescRows, nm * G);
+                st_shared_s32(db + kDescNh, nh);
                 st_shared_s32(db + kDescKvh, kvh);
             }
         }
-        if (lead && first && lane < kDecPieceMembers)
-            st_shared_s32(db + kDescMem + 4 * lane, ld_shared_s32(eb + Ent::kMem + 4 * lane));
+        if (first && lane < kDecPieceMembers) st_shared_s32(db + kDescMem + 4 * lane, mem);
         __syncwarp();
-        if (lane == 0) mbar_expect_tx(fb, (uint32_t)__popc(quads) * 4u * box);
-        __syncwarp();
-        if (qm)
-            tma_gather4(ring + st * Lay::STAGE + (pw * kQuads + lane) * Lay::QP, tm,
-                        (kvh >> 2) * (4 * fp4_head_bytes(D)) / 4, row[0], row[1], row[2], row[3], fb);
+        if (lane == 0) mbar_arrive(fb);                  // the descriptor is written
         last_armed = last_arrived = r;
-        __syncwarp();   // every lane has read the entry
-        if (lane == 0) mbar_arrive(sfree + 8 * ent);
     }
     // this warp's copies have landed before it leaves (as in decode_fused.cu)
     const int s0 = last_arrived - NS + 1 > 0 ? last_arrived - NS + 1 : 0;
@@ -184,220 +214,270 @@ __device__ __noinline__ void fp4_producer(const FusedArgs& f, const CUtensorMap*
 }
 
 // ---------------------------------------------------------------------------
-// Consumer warp c: KV head kvh + c of each piece
+// Consumer warp c: 8 query rows of one KV head of each piece
 // ---------------------------------------------------------------------------
 
+// Products and stage loads that the compiler may move (the barrier operations
+// around them stay in order): D[16x8] += A[16x16] B[16x8], f16 in, fp32 sums.
+__device__ __forceinline__ void mma_f16(float* c, const uint32_t* a, uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// D = A B
+__device__ __forceinline__ void mma_f16_first(float* c, const uint32_t* a, uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};\n"
+        : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
+}
+__device__ __forceinline__ uint32_t lds_u8(uint32_t addr) {
+    uint32_t v;
+    asm volatile("ld.shared.u8 %0, [%1];\n" : "=r"(v) : "r"(addr));
+    return v;
+}
+__device__ __forceinline__ uint32_t lds_u16(uint32_t addr) {
+    uint16_t v;
+    asm volatile("ld.shared.u16 %0, [%1];\n" : "=h"(v) : "r"(addr));
+    return v;
+}
+__device__ __forceinline__ uint32_t lds_u32(uint32_t addr) {
+    uint32_t v;
+    asm volatile("ld.shared.b32 %0, [%1];\n" : "=r"(v) : "r"(addr));
+    return v;
+}
+
 // The position (0 .. 15) that MMA row m of a 16-position group takes.  A
-// gathered row is 16 words off the banks of the one before it (d = 128; 8 for
-// d = 64), so rows of both parities among every other m keep the V reads at
-// two-way conflicts; neighbouring m differ in parity for the K reads.
+// gathered row of 8 heads is 16 words off the banks of the one before it (d =
+// 128; 8 for d = 64), so rows of both parities among every other m keep the V
+// reads at two-way conflicts; neighbouring m differ in parity for the K reads.
 __device__ __forceinline__ int pi16(int m) { return m ^ ((m >> 1) & 1); }
 
-struct PieceState {
-    uint32_t ring, desc, full, empty;   // shared addresses
-    uint32_t box;
-    int cs;                             // steps consumed so far
-    bool stop;
-};
-
-// All steps of one piece, from its first (whose FULL barrier has been waited
-// for) to the next piece's first or the end (left for the caller), for NT
-// columns of 8 query rows.
-template <int D, int NT>
-__device__ __forceinline__ void fp4_piece(const FusedArgs& f, PieceState& ps, int c, int lane) {
+// (Registers: two CTAs of 10 warps leave 96 a thread, and a spill would go to
+// L2, since the ring takes nearly all of L1: what a piece's end needs is two
+// row numbers, what a step needs five addresses.)
+template <int D>
+__device__ __forceinline__ void fp4_consumer(const Fp4Args& p, int c, uint32_t ring, uint32_t desc, uint32_t full,
+                                          uint32_t empty, int lane) {
     using Lay = Fp4Layout<D>;
     constexpr int NS = Lay::NSF;
     constexpr int MT = D / 16;
     constexpr int KW = D / 32;                  // words of K codes per row and lane
     constexpr int VW = D / 64;                  // words of V codes per row and lane
     const int g = lane >> 2, t = lane & 3;
-    uint32_t* const err = f.t.err;
-    const int G = f.t.G, Hq = f.t.Hq, Hkv = f.t.Hkv;
-    const float sc = f.t.scale_log2 * f.t.k_scale;
-    const uint32_t box = ps.box;
-    uint32_t db = ps.desc + (ps.cs % NS) * Lay::DESC;
-    const int cm = ld_shared_s32(db + kDescCm), pb = ld_shared_s32(db + kDescPb), rows = ld_shared_s32(db + kDescRows),
-              nh = ld_shared_s32(db + kDescNh), kvh = ld_shared_s32(db + kDescKvh);
-    const int h = kvh + c;
-    // this head's codes and scales within a piece's row
-    const int coff = fp4_code_off(c, D);
-    const int soff = fp4_scale_off(c, Hkv - kvh, D);
-    // Q^T: row nt * 8 + g, the lane's run of d / 4 elements in order, as f16
-    uint32_t q[NT][D / 8];
-    uint32_t bad = 0u;
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-        const int rq = nt * 8 + g;
-        const bool ok = rq < rows;
-        const int mq = ok ? ld_shared_s32(db + kDescMem + 4 * (rq / G)) : 0;
-        const uint4* src = reinterpret_cast<const uint4*>(f.t.q + ((int64_t)mq * Hq + h * G + rq % G) * D + (D / 4) * t);
-#pragma unroll
-        for (int j = 0; j < D / 32; ++j) {
-            const uint4 v = ok ? __ldg(src + j) : make_uint4(0u, 0u, 0u, 0u);
-            q[nt][4 * j] = bf16x2_to_f16x2_chk(v.x, bad);
-            q[nt][4 * j + 1] = bf16x2_to_f16x2_chk(v.y, bad);
-            q[nt][4 * j + 2] = bf16x2_to_f16x2_chk(v.z, bad);
-            q[nt][4 * j + 3] = bf16x2_to_f16x2_chk(v.w, bad);
-        }
-    }
-    if (bad) atomicOr(err, kErrQRange);
-    float o[NT][MT][4], m[NT][2], l[NT][2];
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-#pragma unroll
-        for (int i = 0; i < MT; ++i) o[nt][i][0] = o[nt][i][1] = o[nt][i][2] = o[nt][i][3] = 0.f;
-        m[nt][0] = m[nt][1] = -INFINITY;
-        l[nt][0] = l[nt][1] = 0.f;
-    }
-    // rows of this lane within a 16-position group, as stage offsets: K rows
-    // g, g + 8; V rows 2t, 2t + 1, 2t + 8, 2t + 9
-    auto roff = [&](int mrow) {
-        const int p = pi16(mrow);
-        return (uint32_t)((p >> 2) * Lay::QP) + (uint32_t)(p & 3) * box;
-    };
-    const uint32_t kr0 = roff(g), kr1 = roff(g + 8);
-    const uint32_t vr[4] = {roff(2 * t), roff(2 * t + 1), roff(2 * t + 8), roff(2 * t + 9)};
+    const float sc = p.f.t.scale_log2 * p.f.t.k_scale;
 
-    for (bool first = true;; first = false) {
-        const int st = ps.cs % NS;
-        db = ps.desc + st * Lay::DESC;
-        if (!first) {
-            if (!mbar_wait(ps.full + 8 * st, (ps.cs / NS) & 1)) {
-                atomicOr(err, 4u);
-                ps.stop = true;
-                break;
-            }
-            if (ld_shared_s32(db + kDescFlags) & (kFirst | kEnd)) break;
+    uint32_t q[D / 8];
+    float o[MT][4];
+    float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
+    int pr0 = -1, pr1 = -1;                     // partial rows of this lane's two query rows
+    bool have = false, active = false;
+    uint32_t ka = 0u, ks = 0u, va = 0u, vs = 0u, dv = 0u;   // offsets within a stage (see below)
+    auto finish_item = [&]() {
+        float s0 = l0, s1 = l1;
+#pragma unroll
+        for (int off = 4; off < 32; off <<= 1) {
+            s0 += __shfl_xor_sync(0xffffffffu, s0, off);
+            s1 += __shfl_xor_sync(0xffffffffu, s1, off);
         }
-        const int left = cm - ld_shared_s32(db + kDescP0);      // positions of the step before the end
-        uint32_t mask = (uint32_t)ld_shared_s32(db + kDescMask);
-        if (left < kNP) mask &= left > 0 ? (1u << left) - 1u : 0u;
-        const uint32_t sk = ps.ring + st * Lay::STAGE, sv = sk + kQuads * Lay::QP;
-        ++ps.cs;
-        if (mask == 0u) {   // nothing to attend to (an empty piece)
+#pragma unroll
+        for (int hh = 0; hh < 2; ++hh) {
+            const int64_t prow = hh ? pr1 : pr0;
+            if (prow >= 0) {
+                const float ll = hh ? s1 : s0, mm = hh ? m1 : m0;
+                const float inv = ll > 0.f ? p.f.t.v_scale / ll : 0.f;
+                float* dst = p.f.t.po + prow * D + (D / 8) * g;
+#pragma unroll
+                for (int i = 0; i < MT; ++i)
+                    *reinterpret_cast<float2*>(dst + 2 * i) = make_float2(o[i][hh] * inv, o[i][2 + hh] * inv);
+                if (g == 0) p.f.t.plse[prow] = ll > 0.f ? (mm + log2f(ll)) * kLn2 : -INFINITY;
+            }
+        }
+    };
+
+    int st = 0;
+    uint32_t ph = 0u;
+    for (;;) {
+        if (!mbar_wait(full + 8 * st, ph)) {
+            atomicOr(p.f.t.err, 4u);
+            break;
+        }
+        const uint32_t db = desc + st * Lay::DESC;
+        const int flags = ld_shared_s32(db + kDescFlags);
+        const uint32_t live = (uint32_t)ld_shared_s32(db + kDescMask);    // positions of the step with data
+        if (flags & kEnd) break;
+        if (flags & kFirst) {
+            if (have && active) finish_item();
+            have = true;
+            const int rows = ld_shared_s32(db + kDescRows), nh = ld_shared_s32(db + kDescNh),
+                      kvh = ld_shared_s32(db + kDescKvh), G = p.f.t.G;
+            const int wph = rows > 8 ? 2 : 1;   // consumer warps per head
+            const int hw = c / wph, r0 = (c - hw * wph) * 8;
+            active = hw < nh && r0 < rows;
+            if (active) {
+                const int pb = ld_shared_s32(db + kDescPb), r = r0 + 2 * t;   // row: member r / G, query head r % G
+                pr0 = r < rows ? pb + ((r / G) * nh + hw) * G + r % G : -1;
+                pr1 = r + 1 < rows ? pb + (((r + 1) / G) * nh + hw) * G + (r + 1) % G : -1;
+                // this lane's first rows of a 16-position group: K row g (the
+                // other, g + 8, lies two quads on), V row 2t (2t + 1 lies dv
+                // on, 2t + 8 and 2t + 9 two quads on); the head's codes and
+                // scales in them
+                const uint32_t box = (uint32_t)(rows > 8 ? p.box4 : p.box8);
+                const uint32_t coff = (uint32_t)fp4_code_off(hw, D), soff = (uint32_t)fp4_scale_off(hw, p.f.t.Hkv - kvh, D);
+                auto roff = [&](int mrow) {
+                    const int x = pi16(mrow);
+                    return (uint32_t)((x >> 2) * Lay::QP) + (uint32_t)(x & 3) * box;
+                };
+                ka = roff(g) + coff + (D / 8) * t;
+                ks = roff(g) + soff + (D / 64) * t;
+                va = kQuads * Lay::QP + roff(2 * t) + coff + (D / 16) * g;
+                vs = kQuads * Lay::QP + roff(2 * t) + soff + g * (D / 8) / 16;
+                dv = roff(2 * t + 1) - roff(2 * t);
+                // Q^T: row r0 + g, the lane's run of d / 4 elements in order, as f16
+                const int rq = r0 + g;
+                const bool ok = rq < rows;
+                const int mq = ok ? ld_shared_s32(db + kDescMem + 4 * (rq / G)) : 0;
+                const uint4* src = reinterpret_cast<const uint4*>(
+                    p.f.t.q + ((int64_t)mq * p.f.t.Hq + (kvh + hw) * G + rq % G) * D + (D / 4) * t);
+                uint32_t bad = 0u;
+#pragma unroll
+                for (int j = 0; j < D / 32; ++j) {
+                    const uint4 v = ok ? __ldg(src + j) : make_uint4(0u, 0u, 0u, 0u);
+                    q[4 * j] = bf16x2_to_f16x2_chk(v.x, bad);
+                    q[4 * j + 1] = bf16x2_to_f16x2_chk(v.y, bad);
+                    q[4 * j + 2] = bf16x2_to_f16x2_chk(v.z, bad);
+                    q[4 * j + 3] = bf16x2_to_f16x2_chk(v.w, bad);
+                }
+                if (bad) atomicOr(p.f.t.err, kErrQRange);
+            }
+#pragma unroll
+            for (int i = 0; i < MT; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
+            m0 = m1 = -INFINITY;
+            l0 = l1 = 0.f;
+        }
+        const uint32_t sb = ring + st * Lay::STAGE;
+        const uint32_t eb = empty + 8 * st;
+        if (++st == NS) {
+            st = 0;
+            ph ^= 1u;
+        }
+        if (!active || live == 0u) {            // (an empty piece has nothing to attend to)
             __syncwarp();
-            if (lane == 0) mbar_arrive(ps.empty + 8 * st);
+            if (lane == 0) mbar_arrive(eb);
             continue;
         }
-        // ---- S^T
-        float s[NT][2][4];
+        // ---- S^T of the two position groups; in each, even and odd k-steps
+        // are chains of their own (a product waits for the one before it in
+        // its chain)
+        float s[2][4];
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
-            const uint32_t kb = sk + u * (4 * Lay::QP);
-            uint32_t kw[2][KW], ksc[2];
+            uint32_t kw[2][KW], sf[2];
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                const uint32_t rb = kb + (e ? kr1 : kr0);
+                const uint32_t ro = sb + (4 * u + 2 * e) * Lay::QP;
                 if constexpr (D == 128) {
-                    lds128(rb + coff + 16 * t, kw[e]);
-                    ksc[e] = ld_shared_u16(rb + soff + 2 * t);
+                    lds128(ro + ka, kw[e]);
+                    sf[e] = e4m3x2_to_f16(lds_u16(ro + ks));
                 } else {
-                    lds64(rb + coff + 8 * t, kw[e]);
-                    ksc[e] = ld_shared_u8(rb + soff + t);
+                    lds64(ro + ka, kw[e]);
+                    sf[e] = e4m3x2_to_f16(lds_u8(ro + ks));
                 }
             }
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) s[nt][u][0] = s[nt][u][1] = s[nt][u][2] = s[nt][u][3] = 0.f;
-            const uint32_t f0 = e4m3x2_to_f16(ksc[0]), f1 = e4m3x2_to_f16(ksc[1]);
+            float s2[4];
 #pragma unroll
             for (int w = 0; w < KW; ++w) {
                 // the scale of these 8 codes
-                const uint32_t s0 = __byte_perm(f0, f0, w < 2 ? 0x1010 : 0x3232);
-                const uint32_t s1 = __byte_perm(f1, f1, w < 2 ? 0x1010 : 0x3232);
+                const uint32_t s0 = __byte_perm(sf[0], 0u, w < 2 ? 0x1010 : 0x3232);
+                const uint32_t s1 = __byte_perm(sf[1], 0u, w < 2 ? 0x1010 : 0x3232);
                 uint32_t h0[4], h1[4];
                 e2m1x8_to_f16(kw[0][w], h0);
                 e2m1x8_to_f16(kw[1][w], h1);
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
-                    const uint32_t ka[4] = {hmul2_u(h0[2 * k], s0), hmul2_u(h1[2 * k], s1), hmul2_u(h0[2 * k + 1], s0),
-                                            hmul2_u(h1[2 * k + 1], s1)};
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
-                        mma16816_f16(s[nt][u], ka, q[nt][4 * w + 2 * k], q[nt][4 * w + 2 * k + 1]);
+                    const uint32_t a[4] = {hmul2_u(h0[2 * k], s0), hmul2_u(h1[2 * k], s1), hmul2_u(h0[2 * k + 1], s0),
+                                           hmul2_u(h1[2 * k + 1], s1)};
+                    if (w == 0)
+                        mma_f16_first(k ? s2 : s[u], a, q[4 * w + 2 * k], q[4 * w + 2 * k + 1]);
+                    else
+                        mma_f16(k ? s2 : s[u], a, q[4 * w + 2 * k], q[4 * w + 2 * k + 1]);
                 }
             }
-        }
-        // ---- softmax (base 2, lazy running maximum)
-        uint32_t pf[NT][2][2];   // P^T fragments per 16 positions
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-            float x0 = -INFINITY, x1 = -INFINITY;
+            for (int e = 0; e < 4; ++e) s[u][e] += s2[e];
+        }
+        // ---- softmax (base 2).  The maximum that P is taken against moves
+        // only when a score exceeds it by more than 8 (a factor 2^8: P stays
+        // within f16), so a step needs no maximum over the lanes, only a vote
+        // that nothing exceeds it.
+        if (live != 0xffffffffu) {
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
-#pragma unroll
-                for (int e = 0; e < 4; ++e) s[nt][u][e] *= sc;
-                if (mask != 0xffffffffu) {
-                    const bool ok0 = (mask >> (16 * u + pi16(g))) & 1u, ok1 = (mask >> (16 * u + pi16(g + 8))) & 1u;
-                    s[nt][u][0] = ok0 ? s[nt][u][0] : -INFINITY;
-                    s[nt][u][1] = ok0 ? s[nt][u][1] : -INFINITY;
-                    s[nt][u][2] = ok1 ? s[nt][u][2] : -INFINITY;
-                    s[nt][u][3] = ok1 ? s[nt][u][3] : -INFINITY;
-                }
-                x0 = fmax3f(x0, s[nt][u][0], s[nt][u][2]);
-                x1 = fmax3f(x1, s[nt][u][1], s[nt][u][3]);
+                const bool ok0 = (live >> (16 * u + pi16(g))) & 1u, ok1 = (live >> (16 * u + pi16(g + 8))) & 1u;
+                s[u][0] = ok0 ? s[u][0] : -INFINITY;
+                s[u][1] = ok0 ? s[u][1] : -INFINITY;
+                s[u][2] = ok1 ? s[u][2] : -INFINITY;
+                s[u][3] = ok1 ? s[u][3] : -INFINITY;
             }
+        }
+        float x0 = fmaxf(fmax3f(s[0][0], s[0][2], s[1][0]), s[1][2]) * sc;
+        float x1 = fmaxf(fmax3f(s[0][1], s[0][3], s[1][1]), s[1][3]) * sc;
+        if (__any_sync(0xffffffffu, x0 > m0 + 8.f || x1 > m1 + 8.f)) {
 #pragma unroll
             for (int off = 4; off < 32; off <<= 1) {
                 x0 = fmaxf(x0, __shfl_xor_sync(0xffffffffu, x0, off));
                 x1 = fmaxf(x1, __shfl_xor_sync(0xffffffffu, x1, off));
             }
-            // the maximum that P is taken against moves only when it is
-            // exceeded by more than 8 (a factor 2^8: P stays within f16)
-            const bool up0 = x0 > m[nt][0] + 8.f, up1 = x1 > m[nt][1] + 8.f;
-            if (__any_sync(0xffffffffu, up0 || up1)) {
-                const float n0 = up0 ? x0 : m[nt][0], n1 = up1 ? x1 : m[nt][1];
-                const float a0 = m[nt][0] == -INFINITY ? 0.f : exp2f(m[nt][0] - n0);
-                const float a1 = m[nt][1] == -INFINITY ? 0.f : exp2f(m[nt][1] - n1);
-                m[nt][0] = n0;
-                m[nt][1] = n1;
-                l[nt][0] *= a0;
-                l[nt][1] *= a1;
+            const float n0 = fmaxf(x0, m0), n1 = fmaxf(x1, m1);
+            const float a0 = m0 == -INFINITY ? 0.f : exp2f(m0 - n0);
+            const float a1 = m1 == -INFINITY ? 0.f : exp2f(m1 - n1);
+            m0 = n0;
+            m1 = n1;
+            l0 *= a0;
+            l1 *= a1;
 #pragma unroll
-                for (int i = 0; i < MT; ++i) {
-                    o[nt][i][0] *= a0;
-                    o[nt][i][1] *= a1;
-                    o[nt][i][2] *= a0;
-                    o[nt][i][3] *= a1;
-                }
+            for (int i = 0; i < MT; ++i) {
+                o[i][0] *= a0;
+                o[i][1] *= a1;
+                o[i][2] *= a0;
+                o[i][3] *= a1;
             }
-            const float u0 = m[nt][0] == -INFINITY ? 0.f : m[nt][0], u1 = m[nt][1] == -INFINITY ? 0.f : m[nt][1];
+        }
+        const float u0 = m0 == -INFINITY ? 0.f : -m0, u1 = m1 == -INFINITY ? 0.f : -m1;
+        uint32_t pf[2][2];                      // P^T fragments of the two groups
 #pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                const float p0 = ex2_ftz(s[nt][u][0] - u0), p1 = ex2_ftz(s[nt][u][1] - u1);
-                const float p2 = ex2_ftz(s[nt][u][2] - u0), p3 = ex2_ftz(s[nt][u][3] - u1);
-                l[nt][0] += p0 + p2;
-                l[nt][1] += p1 + p3;
-                pf[nt][u][0] = movtrans(pack_f16(p0, p1));
-                pf[nt][u][1] = movtrans(pack_f16(p2, p3));
-            }
+        for (int u = 0; u < 2; ++u) {
+            const float p00 = ex2_ftz(fmaf(s[u][0], sc, u0)), p01 = ex2_ftz(fmaf(s[u][1], sc, u1));
+            const float p10 = ex2_ftz(fmaf(s[u][2], sc, u0)), p11 = ex2_ftz(fmaf(s[u][3], sc, u1));
+            l0 += p00 + p10;
+            l1 += p01 + p11;
+            pf[u][0] = movtrans(pack_f16(p00, p01));
+            pf[u][1] = movtrans(pack_f16(p10, p11));
         }
         // ---- O^T
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
-            const uint32_t vb = sv + u * (4 * Lay::QP);
-            uint32_t vw[4][VW], vs[4];
+            uint32_t vw[4][VW], sf[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                const uint32_t rb = vb + vr[e];
-                if constexpr (D == 128) {
-                    lds64(rb + coff + 8 * g, vw[e]);
-                    vs[e] = ld_shared_u8(rb + soff + g);
-                } else {
-                    vw[e][0] = (uint32_t)ld_shared_s32(rb + coff + 4 * g);
-                    vs[e] = ld_shared_u8(rb + soff + (g >> 1));
-                }
+                const uint32_t ro = sb + (4 * u + 2 * (e >> 1)) * Lay::QP + (e & 1 ? dv : 0u);
+                if constexpr (D == 128)
+                    lds64(ro + va, vw[e]);
+                else
+                    vw[e][0] = lds_u32(ro + va);
+                sf[e] = lds_u8(ro + vs);
             }
             if (u == 1) {
                 __syncwarp();
-                if (lane == 0) mbar_arrive(ps.empty + 8 * st);   // the stage may be refilled
+                if (lane == 0) mbar_arrive(eb);   // the stage may be refilled
             }
-            if (mask != 0xffffffffu) {
+            if (live != 0xffffffffu) {
                 // a row without data counts nothing, whatever its scale says
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
-                    if (!((mask >> (16 * u + pi16(2 * t + (e & 1) + 8 * (e >> 1)))) & 1u)) vs[e] = 0u;
+                    if (!((live >> (16 * u + pi16(2 * t + (e & 1) + 8 * (e >> 1)))) & 1u)) sf[e] = 0u;
             }
-            const uint32_t s01 = e4m3x2_to_f16(vs[0] | (vs[1] << 8)), s23 = e4m3x2_to_f16(vs[2] | (vs[3] << 8));
+            const uint32_t s01 = e4m3x2_to_f16(__byte_perm(sf[0], sf[1], 0x5540));
+            const uint32_t s23 = e4m3x2_to_f16(__byte_perm(sf[2], sf[3], 0x5540));
 #pragma unroll
             for (int w = 0; w < VW; ++w) {
                 // byte j: elements 2j (lo) or 2j + 1 (hi) of a pair of rows
@@ -409,113 +489,91 @@ __device__ __forceinline__ void fp4_piece(const FusedArgs& f, PieceState& ps, in
                 e2m1x8_to_f16(((vw[2][w] >> 4) & M) | (vw[3][w] & ~M), a3);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    const uint32_t va[4] = {hmul2_u(a0[j], s01), hmul2_u(a1[j], s01), hmul2_u(a2[j], s23),
-                                            hmul2_u(a3[j], s23)};
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) mma16816_f16(o[nt][4 * w + j], va, pf[nt][u][0], pf[nt][u][1]);
+                    const uint32_t a[4] = {hmul2_u(a0[j], s01), hmul2_u(a1[j], s01), hmul2_u(a2[j], s23),
+                                           hmul2_u(a3[j], s23)};
+                    mma_f16(o[4 * w + j], a, pf[u][0], pf[u][1]);
                 }
             }
         }
     }
-    // ---- the piece's partial rows
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-        float s0 = l[nt][0], s1 = l[nt][1];
-#pragma unroll
-        for (int off = 4; off < 32; off <<= 1) {
-            s0 += __shfl_xor_sync(0xffffffffu, s0, off);
-            s1 += __shfl_xor_sync(0xffffffffu, s1, off);
-        }
-#pragma unroll
-        for (int hh = 0; hh < 2; ++hh) {
-            const int r = nt * 8 + 2 * t + hh;   // query row of this head: member r / G, query head r % G
-            if (r < rows) {
-                const int64_t prow = (int64_t)pb + ((r / G) * nh + c) * G + r % G;
-                const float ll = hh ? s1 : s0, mm = m[nt][hh];
-                const float inv = ll > 0.f ? f.t.v_scale / ll : 0.f;
-                float* dst = f.t.po + prow * D + (D / 8) * g;
-#pragma unroll
-                for (int i = 0; i < MT; ++i)
-                    *reinterpret_cast<float2*>(dst + 2 * i) = make_float2(o[nt][i][hh] * inv, o[nt][i][2 + hh] * inv);
-                if (g == 0) f.t.plse[prow] = ll > 0.f ? (mm + log2f(ll)) * kLn2 : -INFINITY;
-            }
-        }
-    }
+    if (have && active) finish_item();
 }
 
+// ---------------------------------------------------------------------------
+// Tiles: CTA b runs wide items wptr[b] .. wptr[b + 1] - 1 one after another
+// ---------------------------------------------------------------------------
 template <int D>
-__device__ __noinline__ void fp4_consumer(const FusedArgs& f, int c, PieceState ps, int lane) {
-    using Lay = Fp4Layout<D>;
-    constexpr int NS = Lay::NSF;
-    bool have = false;   // the step at ps.cs has been waited for
-    while (!ps.stop) {
-        const int st = ps.cs % NS;
-        if (!have && !mbar_wait(ps.full + 8 * st, (ps.cs / NS) & 1)) {
-            atomicOr(f.t.err, 4u);
-            break;
-        }
-        const uint32_t db = ps.desc + st * Lay::DESC;
-        const int flags = ld_shared_s32(db + kDescFlags);
-        if (flags & kEnd) break;
-        have = false;
-        // (only a piece's first step carries the piece's head count)
-        if ((flags & kFirst) && c < ld_shared_s32(db + kDescNh)) {
-            if (ld_shared_s32(db + kDescRows) > 8)
-                fp4_piece<D, 2>(f, ps, c, lane);
-            else
-                fp4_piece<D, 1>(f, ps, c, lane);
-            have = true;
-        } else {   // a piece without this warp's head
-            ++ps.cs;
-            __syncwarp();
-            if (lane == 0) mbar_arrive(ps.empty + 8 * st);
-        }
-    }
-}
-
-template <int D>
-__global__ void __launch_bounds__(kFp4Threads, 1) decode_fp4_kernel(const __grid_constant__ FusedArgs f,
-                                                                    const __grid_constant__ CUtensorMap tmk,
-                                                                    const __grid_constant__ CUtensorMap tmv) {
-    using Lay = Fp4Layout<D>;
+__global__ void __launch_bounds__(Fp4Cfg<D>::kThreads, 1) decode_fp4_tiles(const __grid_constant__ FusedArgs f) {
     using TC = Fp4Cfg<D>;
     using TL = typename TC::Lay;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t* sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    // Until the dependency wait only shared memory, TMEM and the plan tables
-    // are touched (see decode_fused.cu).
+    const int tid = threadIdx.x, warp = tid >> 5;
     const int w0 = __ldg(f.wptr + blockIdx.x), w1 = __ldg(f.wptr + blockIdx.x + 1);
-    const bool tiles = w1 > w0;
     uint32_t* tslot = reinterpret_cast<uint32_t*>(sm + TL::OFF_TMEM);
     int* info = reinterpret_cast<int*>(sm + TL::OFF_INFO);
-    constexpr int NSF = Lay::NSF;
-    const uint32_t sbar = smem_u32(sm + Lay::OFF_SBAR);
-    const uint32_t sfull = sbar, sempty = sbar + 8 * NSF;
-    const uint32_t slfull = sbar + 16 * NSF, slfree = slfull + 8 * kSQ;
     if (tid == 0) {
-        if (tiles) tc_init_barriers<TC>(smem_u32(sm + TL::OFF_BAR));
-        for (int s = 0; s < NSF; ++s) {
-            mbar_init(sfull + 8 * s, kProducers);
-            mbar_init(sempty + 8 * s, kHB);
-        }
-        for (int e = 0; e < kSQ; ++e) {
-            mbar_init(slfull + 8 * e, 33);          // the lookup lanes' cp.async + the fields
-            mbar_init(slfree + 8 * e, kProducers);
-        }
+        tc_init_barriers<TC>(smem_u32(sm + TL::OFF_BAR));
         mbar_fence_init();
     }
-    if (tiles && warp == TC::kMmaWarp) {
+    if (warp == TC::kMmaWarp) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;\n" ::"r"(smem_u32(tslot)));
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;\n");
     }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (tiles && tid == 0) prefetch_l1(f.t.items + w0);
-    const int gw = !tiles && (int)blockIdx.x >= f.n_tile_ctas ? (int)blockIdx.x - f.n_tile_ctas : -1;
+    // what came before is complete and visible from here on, also to the
+    // streams, which start only when every CTA has come to the launch below
+    grid_dep_wait();
+    grid_dep_launch();
+    const uint32_t tbase = *tslot;
+    TcState st{0u, 0u, false};
+    for (int w = w0; w < w1; ++w) {
+        if (tid == 0) dec_tile_info(f.t, w, info);
+        named_bar(kTileBar, TC::kThreads);
+        const TileInfo ti{info[0], info[1], info[2], info[3], {info[4], 0}, {info[5], 0}, {info[6], 0}, INT_MAX, 0};
+        tc_tile_run<TC>(f.t, nullptr, nullptr, nullptr, nullptr, ti, sm, tbase, st, tid);
+        named_bar(kTileBar, TC::kThreads);
+    }
+    if (tid < 128) bulk_wait_all();   // the partial rows left as bulk copies
+    tc_fence_before();
+    __syncthreads();
+    if (warp == TC::kMmaWarp) {
+        tc_fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;\n" ::"r"(tbase));
+    }
+}
+
+template <int D>
+__global__ void __launch_bounds__(kStreamThreads, kStreamCtas)
+    decode_fp4_streams(const __grid_constant__ Fp4Args p, const __grid_constant__ CUtensorMap k8,
+                       const __grid_constant__ CUtensorMap v8, const __grid_constant__ CUtensorMap k4,
+                       const __grid_constant__ CUtensorMap v4) {
+    using Lay = Fp4Layout<D>;
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    uint8_t* sm = smem_raw + ((128u - (smem_u32(smem_raw) & 127u)) & 127u);
+    const FusedArgs& f = p.f;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    constexpr int NSF = Lay::NSF;
+    const uint32_t full = smem_u32(sm + Lay::OFF_BAR), empty = full + 8 * NSF;
+    const uint32_t sfull = empty + 8 * NSF, sfree = sfull + 8 * kSQ;
+    if (tid == 0) {
+        for (int s = 0; s < NSF; ++s) {
+            mbar_init(full + 8 * s, 1);
+            mbar_init(empty + 8 * s, kHB);
+        }
+        for (int e = 0; e < kSQ; ++e) {
+            mbar_init(sfull + 8 * e, 33);           // the lookup lanes' cp.async + the fields
+            mbar_init(sfree + 8 * e, 1);
+        }
+        mbar_fence_init();
+    }
+    // Until the dependency wait only shared memory and the plan tables are
+    // touched (see decode_fused.cu): the launch piece's record and members
+    const int gw = (int)blockIdx.x;
     const uint32_t lrec = smem_u32(sm + Lay::OFF_LREC);
-    if (warp == kLookup && gw >= 0 && gw < f.n_init) {
+    if (warp == kLookup && gw < f.n_init) {
         const int4* rp = reinterpret_cast<const int4*>(f.narrow + gw);
         const int4 x = __ldg(rp), y = __ldg(rp + 1);
         if (lane == 0) {
@@ -526,43 +584,22 @@ __global__ void __launch_bounds__(kFp4Threads, 1) decode_fp4_kernel(const __grid
             st_shared_s32(lrec + 32 + 4 * lane, lane < y.y ? __ldg(f.t.members + y.x + lane) : 0);
         __syncwarp();
     }
-    grid_dep_wait();
+    __syncthreads();
+    // Behind the tiles, what came before them is complete already, and the
+    // wait is for the tiles themselves: at the end, so that the merge, which
+    // waits for this grid, comes after both.
+    if (!p.after_tiles) grid_dep_wait();
     grid_dep_launch();
-
-    if (tiles) {
-        const uint32_t tbase = *tslot;
-        TcState st{0u, 0u, false};
-        for (int w = w0; w < w1; ++w) {
-            if (tid == 0) dec_tile_info(f.t, w, info);
-            named_bar(kTileBar, TC::kThreads);
-            const TileInfo ti{info[0], info[1], info[2], info[3], {info[4], 0}, {info[5], 0}, {info[6], 0}, INT_MAX, 0};
-            tc_tile_run<TC>(f.t, nullptr, nullptr, nullptr, nullptr, ti, sm, tbase, st, tid);
-            named_bar(kTileBar, TC::kThreads);
-        }
-        // the streaming areas overlap the tile roles' barriers
-        if (tid == 0) tc_inval_barriers<TC>(smem_u32(sm + TL::OFF_BAR));
-        named_bar(kTileBar, TC::kThreads);
-    }
-    const uint32_t ring = smem_u32(sm + Lay::OFF_RING);
+    const uint32_t ring = smem_u32(sm);
     const uint32_t desc = smem_u32(sm + Lay::OFF_DESC);
     const uint32_t sring = smem_u32(sm + Lay::OFF_SLOT);
-    const uint32_t box = (uint32_t)fp4_box_bytes<D>(f.t.Hkv);
-    if (warp == kLookup) {
-        stream_lookup<kNP>(f, gw, lrec, sring, slfull, slfree, lane);
-    } else if (warp >= kFirstProducer && warp < kFirstConsumer) {
-        const int pw = warp - kFirstProducer;
-        fp4_producer<D>(f, pw ? &tmv : &tmk, pw, box, ring, sring, desc, sfull, sempty, slfull, slfree, lane);
-    } else if (warp >= kFirstConsumer) {
-        fp4_consumer<D>(f, warp - kFirstConsumer, PieceState{ring, desc, sfull, sempty, box, 0, false}, lane);
-    }
-    // the tiles' partial rows went out as bulk copies from threads 0-127
-    if (tiles && tid < 128) bulk_wait_all();
-    tc_fence_before();
-    __syncthreads();
-    if (tiles && warp == TC::kMmaWarp) {
-        tc_fence_after();
-        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;\n" ::"r"(*tslot));
-    }
+    if (warp == kLookup)
+        fp4_lookup<D>(p, gw, lrec, sring, sfull, sfree, lane);
+    else if (warp == kProducer)
+        fp4_producer<D>(p, &k8, &v8, &k4, &v4, ring, sring, desc, full, empty, sfull, sfree, lane);
+    else
+        fp4_consumer<D>(p, warp - kFirstConsumer, ring, desc, full, empty, lane);
+    if (p.after_tiles) grid_dep_wait();
 }
 
 }  // namespace
@@ -571,18 +608,29 @@ template <int D>
 int launch_decode_fp4(const sgl_plan* plan, const void* q, const void* kp, const void* vp, const int32_t* r2t, int64_t ld,
                       const int32_t* seq_lens, void* o, float* lse, unsigned char* ws, float scale_log2, cudaStream_t s) {
     using Lay = Fp4Layout<D>;
-    static const int attr = (int)cudaFuncSetAttribute(decode_fp4_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                      Lay::TOTAL);
+    // (+ alignment slack; too much for two tile CTAs per SM: each allocates all TMEM columns)
+    constexpr int kTileSmem = Fp4Cfg<D>::Lay::END + 1024 > 120 * 1024 ? Fp4Cfg<D>::Lay::END + 1024 : 120 * 1024;
+    static_assert(kTileSmem <= 232448, "shared memory per CTA");
+    static const int attr = [] {
+        const cudaError_t e = cudaFuncSetAttribute(decode_fp4_streams<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                   Lay::TOTAL);
+        return (int)(e ? e : cudaFuncSetAttribute(decode_fp4_tiles<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                  kTileSmem));
+    }();
     if (attr) return attr;
     const sgl_attn_params& p = plan->params;
     const int row = fp4_row_bytes(p.num_kv_heads, D);
-    CUtensorMap mk{}, mv{};
+    Fp4Args x{};
+    x.box8 = fp4_box_bytes<D>(p.num_kv_heads, 8);
+    x.box4 = fp4_box_bytes<D>(p.num_kv_heads, 4);
+    CUtensorMap k8{}, v8{}, k4{}, v4{};
     if (plan->n_narrow > 0 && p.num_slots > 0) {
-        const int box = fp4_box_bytes<D>(p.num_kv_heads);
-        if (const int e = tc::encode_bytes_map(kp, p.num_slots, row, box, &mk)) return e;
-        if (const int e = tc::encode_bytes_map(vp, p.num_slots, row, box, &mv)) return e;
+        if (const int e = tc::encode_bytes_map(kp, p.num_slots, row, x.box8, &k8)) return e;
+        if (const int e = tc::encode_bytes_map(vp, p.num_slots, row, x.box8, &v8)) return e;
+        if (const int e = tc::encode_bytes_map(kp, p.num_slots, row, x.box4, &k4)) return e;
+        if (const int e = tc::encode_bytes_map(vp, p.num_slots, row, x.box4, &v4)) return e;
     }
-    FusedArgs f{};
+    FusedArgs& f = x.f;
     TcArgs& a = f.t;
     a.q = static_cast<const bf16*>(q);
     a.kp = static_cast<const bf16*>(kp);
@@ -613,14 +661,21 @@ int launch_decode_fp4(const sgl_plan* plan, const void* q, const void* kp, const
     pdl[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     pdl[0].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)plan->n_ctas);
-    cfg.blockDim = dim3(kFp4Threads);
-    cfg.dynamicSmemBytes = Lay::TOTAL;
     cfg.stream = s;
     cfg.attrs = pdl;
     cfg.numAttrs = 1;
-    int e = (int)cudaLaunchKernelEx(&cfg, decode_fp4_kernel<D>, f, mk, mv);
-    if (e) return e;
+    if (plan->n_wide > 0) {
+        cfg.gridDim = dim3((unsigned)plan->n_tile_ctas);
+        cfg.blockDim = dim3(Fp4Cfg<D>::kThreads);
+        cfg.dynamicSmemBytes = kTileSmem;
+        if (const int e = (int)cudaLaunchKernelEx(&cfg, decode_fp4_tiles<D>, f)) return e;
+        x.after_tiles = 1;
+    }
+    // (every request has a trailing piece, so there are streams whenever there are requests)
+    cfg.gridDim = dim3((unsigned)(kStreamCtas * plan->n_ctas));
+    cfg.blockDim = dim3(kStreamThreads);
+    cfg.dynamicSmemBytes = Lay::TOTAL;
+    if (const int e = (int)cudaLaunchKernelEx(&cfg, decode_fp4_streams<D>, x, k8, v8, k4, v4)) return e;
     MergeArgs m{a.po, a.plse, reinterpret_cast<const int32_t*>(ws + plan->off_mptr),
                 reinterpret_cast<const int32_t*>(ws + plan->off_ment), o, lse, a.Hq, a.Hkv, a.G};
     const int n_pairs = p.batch * a.Hkv;

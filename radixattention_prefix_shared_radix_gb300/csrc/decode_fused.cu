@@ -498,6 +498,11 @@ __device__ __noinline__ void stream_consumer(const FusedArgs& f, int c, uint32_t
     if (have && active) finish_item();
 }
 
+__device__ __noinline__ void fused_lookup(const FusedArgs& f, int gw, uint32_t lrec, uint32_t sring, uint32_t sfull,
+                                          uint32_t sfree, int lane) {
+    stream_lookup<kNP>(f, gw, lrec, sring, sfull, sfree, lane, [](int, int, int, int) {});
+}
+
 template <int D, bool F8>
 __global__ void __maxnreg__(128) decode_fused_kernel(const __grid_constant__ FusedArgs f,
                                                      const __grid_constant__ CUtensorMap tmk,
@@ -584,7 +589,7 @@ __global__ void __maxnreg__(128) decode_fused_kernel(const __grid_constant__ Fus
     const uint32_t desc = smem_u32(sm + Lay::OFF_DESC);
     const uint32_t sring = smem_u32(sm + Lay::OFF_SLOT);
     if (warp == kLookup) {
-        stream_lookup<kNP>(f, gw, lrec, sring, slfull, slfree, lane);
+        fused_lookup(f, gw, lrec, sring, slfull, slfree, lane);
     } else if (warp >= kFirstProducer && warp < kFirstConsumer) {
         stream_producer<D, F8>(f, warp - kFirstProducer, ring, sring, desc, sfull, sempty, slfull,
                                slfree, lane);

@@ -25,6 +25,7 @@
 #include <algorithm>
 #include <cmath>
 #include <cstring>
+#include <functional>
 #include <new>
 #include <vector>
 
@@ -129,10 +130,8 @@ int sgl_decode_plan(const sgl_attn_params* p, const int32_t* seq_lens, const sgl
     // CTA): up to 8 heads with one consumer warp each when a head has at
     // most 8 query rows, else up to 4 heads with two consumer warps each;
     // the fp32 kernel runs one item per CTA and takes one head per item.
-    // (The 4-bit streams give a head one warp for up to 16 rows.)
     auto head_block = [&](int32_t nmem) -> int32_t {
         if (p->dtype == SGL_DTYPE_F32) return 1;
-        if (p->dtype == SGL_DTYPE_BF16_FP4KV) return std::min<int32_t>(Hkv, sgl::kDecHeadBlock);
         return std::min<int32_t>(Hkv, nmem * G <= 8 ? sgl::kDecHeadBlock : sgl::kDecHeadBlock / 2);
     };
     struct Unit {   // narrow work: one member block of a segment for a block of KV heads
@@ -232,21 +231,66 @@ int sgl_decode_plan(const sgl_attn_params* p, const int32_t* seq_lens, const sgl
 
     // Narrow units are cut into pieces of at most Pmax positions (about half
     // an even share of a stream, so that the run-time counter can balance
-    // the tail; a cut makes one more partial to merge), no
-    // piece shorter than one step (16 positions; 32 of a 4-bit pool) unless its unit is, ordered
+    // the tail; a cut makes one more partial to merge), no piece shorter than
+    // one step (16 positions; 32 of a 4-bit pool) unless its unit is, ordered
     // longest first.  Each streaming CTA starts on its own piece; the rest
     // (and all work of tile CTAs' streams, once their tiles are done) are
     // handed out at run time from a counter, so SMs that stream faster take
     // more.
-    const int64_t n_cons = n_ctas - n_tile_ctas;
+    // (a 4-bit pool's streams are two CTAs per SM)
+    const int64_t n_cons = (n_ctas - n_tile_ctas) * (p->dtype == SGL_DTYPE_BF16_FP4KV ? 2 : 1);
     // (in position-heads, so that a piece of a 4-head block is as long in
     // bytes as one of an 8-head block)
     const int64_t step = p->dtype == SGL_DTYPE_BF16_FP4KV ? 32 : 16;   // positions per streaming step
-    const int64_t Pph = (int64_t)std::ceil((double)units_n / (double)std::max<int64_t>(1, 2 * n_cons));
+    int64_t Pph = (int64_t)std::ceil((double)units_n / (double)std::max<int64_t>(1, 2 * n_cons));
+    const bool fp4 = p->dtype == SGL_DTYPE_BF16_FP4KV;
+    int64_t cap = 2048;                        // longest piece
+    if (fp4) {
+        // 4-bit streams: a piece costs a stream as much as 100 positions
+        // beyond its own (its query rows, its partial rows and their merge),
+        // and the two streams of an SM share what it reads and computes.
+        // Measured on 64 requests of 1 to 8192 tokens: pieces of 288, 416,
+        // 544 and 800 positions took 74, 68, 66 and 60 us, which
+        //   (positions of the fullest SM, dealt longest first) / 2 + 100 pieces / streams
+        // at 0.065 us a position gives within 6%.  The piece length with the
+        // smallest estimate around an even share is taken.
+        const int64_t sms_s = std::max<int64_t>(1, n_ctas - n_tile_ctas);
+        const double share = (double)units_n / (double)(2 * sms_s);
+        double best = 1e300;
+        std::vector<int64_t> len, load((size_t)sms_s);
+        for (const double by : {1.0, 1.04, 1.08, 1.13, 1.2, 1.3, 1.5}) {
+            const int64_t pph = std::max<int64_t>(1, (int64_t)std::ceil(share * by));
+            len.clear();
+            for (const Unit& u : units) {
+                const int64_t P = std::max<int64_t>(step, ((pph + u.nh - 1) / u.nh + step - 1) / step * step);
+                for (int64_t left = u.e - u.b; left > 0;) {
+                    const int64_t take = left - P < step ? left : P;
+                    len.push_back(take * u.nh);
+                    left -= take;
+                }
+            }
+            std::sort(len.begin(), len.end(), std::greater<int64_t>());
+            std::fill(load.begin(), load.end(), 0);
+            auto least = std::greater<int64_t>();              // (a heap with the emptiest SM on top)
+            for (const int64_t x : len) {
+                std::pop_heap(load.begin(), load.end(), least);
+                load.back() += x;
+                std::push_heap(load.begin(), load.end(), least);
+            }
+            const double cost = 0.5 * (double)*std::max_element(load.begin(), load.end()) +
+                                100.0 * sgl::kDecHeadBlock * (double)len.size() / (double)(2 * sms_s);
+            if (cost < best) {
+                best = cost;
+                Pph = pph;
+            }
+            if ((int64_t)len.size() > 8 * sms_s) break;        // many short requests: the cut hardly matters
+        }
+        cap = INT32_MAX / 2;
+    }
     std::vector<std::pair<int32_t, sgl::DecItem>> cut;   // (planned length, piece)
     for (const Unit& u : units) {
         int64_t Pmax = (Pph + u.nh - 1) / u.nh;
-        Pmax = std::min<int64_t>(2048, std::max<int64_t>(32, (Pmax + step - 1) / step * step));
+        Pmax = std::min<int64_t>(cap, std::max<int64_t>(32, (Pmax + step - 1) / step * step));
         for (int64_t pos = u.b; pos < u.e || (pos == u.b && u.tail);) {
             int64_t take = std::min<int64_t>(u.e - pos, Pmax);
             if (u.e - pos - take < step) take = u.e - pos;   // no tail piece under one step
