@@ -57,9 +57,9 @@ constexpr int kStreamThreads = 32 * (kFirstConsumer + kHB);
 constexpr int kStreamCtas = 2;              // per SM
 using Ent = SlotEntry<kNP>;
 
-// the tile roles: 15 warps (10 of them gather), two K/V stages and the staging area
+// the tile roles: 15 warps (10 of them gather), three K/V stages and the staging area
 template <int D>
-using Fp4Cfg = TcCfg<D, true, 1, 2, 10, 128, 2, kKvFp4>;
+using Fp4Cfg = TcCfg<D, true, 1, 3, 10, 128, 2, kKvFp4>;
 
 // bytes of a piece's row (its block of up to `heads` heads), as the gathers copy them
 template <int D>

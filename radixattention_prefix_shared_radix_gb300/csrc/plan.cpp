@@ -33,6 +33,11 @@
 
 #include "common.h"
 
+namespace {
+// a 4-bit tile's cost in us: fixed, and per 128-position block (measured)
+constexpr double kFp4Tile0 = 4.0, kFp4Tile1 = 1.45;
+}  // namespace
+
 namespace sgl {
 
 int query_num_sms(int32_t requested) {
@@ -192,13 +197,36 @@ int sgl_decode_plan(const sgl_attn_params* p, const int32_t* seq_lens, const sgl
         }
         return n;
     };
-    const double rate = 88.0 * 128.0 / p->head_dim;   // streamed position-heads per us per SM
+    const bool fp4 = p->dtype == SGL_DTYPE_BF16_FP4KV;
+    const double rate = (fp4 ? 230.0 : 88.0) * 128.0 / p->head_dim;   // streamed position-heads per us per SM
     int64_t Cw = 128, n_tile_ctas = 0;
     if (max_wide > 0) {
         double best = 1e300;
         const int64_t top = std::min<int64_t>((max_wide + 127) / 128 * 128, 128 * 256);
         for (int64_t c = 128; c <= top; c += 128) {
             const int64_t nw = wide_items_for(c);
+            if (fp4) {
+                // 4-bit streams take over the tiles' SMs as they finish (a
+                // launch of their own) and keep up better than the tiles, so
+                // any number of tile CTAs that deals the items evenly is
+                // tried, and the streams' share of those SMs counts
+                for (int64_t per = 1; per <= 8; ++per) {
+                    const int64_t T = (nw + per - 1) / per;
+                    if (T > n_ctas - std::max<int64_t>(1, n_ctas / 16) && per < 8) continue;
+                    const int64_t Tc = std::max<int64_t>(1, std::min<int64_t>(T, n_ctas - std::max<int64_t>(1, n_ctas / 16)));
+                    const double tile_us = (double)((nw + Tc - 1) / Tc) * (kFp4Tile0 + kFp4Tile1 * (double)c / 128.0) + 2.0;
+                    const double work = (double)units_n / rate;               // SM-us of streaming
+                    const double early = 4.0 + work / (double)std::max<int64_t>(1, n_ctas - Tc);   // without the tiles' SMs
+                    const double late = (work + 4.0 * (double)(n_ctas - Tc) + (tile_us + 3.0) * (double)Tc) / (double)n_ctas;
+                    const double F = std::max(tile_us, early <= tile_us ? early : late);
+                    if (F < best) {
+                        best = F;
+                        Cw = c;
+                        n_tile_ctas = Tc;
+                    }
+                }
+                continue;
+            }
             const int64_t T = std::max<int64_t>(1, std::min<int64_t>(nw, n_ctas / 2));
             const double per = (double)((nw + T - 1) / T);
             const double tile_us = per * (2.0 + 2.5 * (double)c / 128.0);
@@ -243,7 +271,6 @@ int sgl_decode_plan(const sgl_attn_params* p, const int32_t* seq_lens, const sgl
     // bytes as one of an 8-head block)
     const int64_t step = p->dtype == SGL_DTYPE_BF16_FP4KV ? 32 : 16;   // positions per streaming step
     int64_t Pph = (int64_t)std::ceil((double)units_n / (double)std::max<int64_t>(1, 2 * n_cons));
-    const bool fp4 = p->dtype == SGL_DTYPE_BF16_FP4KV;
     int64_t cap = 2048;                        // longest piece
     if (fp4) {
         // 4-bit streams: a piece costs a stream as much as 100 positions

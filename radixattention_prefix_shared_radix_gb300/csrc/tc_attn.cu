@@ -30,27 +30,72 @@ using namespace tc;
 // two query tiles, 128-position blocks (S MMAs of N = 128: an M = 128
 // tcgen05 MMA costs about the same time for N = 64 as for N = 128), one score
 // buffer each, 2 K/V stages (4 for d = 64), a gather team of 6 warps.  With
-// an FP8 or 4-bit pool (codes staged by the gather team and converted to f16) one
+// an FP8 pool (codes staged by the gather team and converted to f16) one
 // stage for d = 128, whose staging area takes the second stage's room.
 template <int D, int KV>
-using ExtCfg = TcCfg<D, false, 2, (KV != kKvBf16 && D == 128) ? 1 : 2 * (128 / D), 6, 128, 1, KV>;
+using ExtCfg = TcCfg<D, false, 2, (KV == kKvE4m3 && D == 128) ? 1 : 2 * (128 / D), 6, 128, 1, KV>;
 
-// Query tile pair (blockIdx.x, blockIdx.y) of the extend batch; false if empty.
-__device__ bool extend_tile_info(const TcArgs& a, int* info) {
-    const int tq = 128 / a.G;
-    int acc_c = 0, acc_q = 0, req = -1, c0 = 0, qoff = 0;
-    for (int r = 0; r < a.B; ++r) {
-        const int e = __ldg(a.extend_lens + r);
-        const int nt = e > 0 ? (e + tq - 1) / tq : 0;
-        const int nc = (nt + 1) / 2;
-        if ((int)blockIdx.x < acc_c + nc) {
-            req = r;
-            c0 = acc_c;
-            qoff = acc_q;
-            break;
+// The request of tile pair `c`, the pairs and new tokens before it, by one
+// warp, 128 requests at a time; -1 past the last.
+__device__ __forceinline__ int find_extend_request(const int32_t* extend_lens, int B, int tq, int c, int* c0, int* qoff) {
+    const int lane = threadIdx.x & 31;
+    int acc_c = 0, acc_q = 0;
+    for (int b = 0; b < B; b += 128) {
+        int ev[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) ev[k] = b + 32 * k + lane < B ? max(__ldg(extend_lens + b + 32 * k + lane), 0) : 0;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const int nc = ((ev[k] + tq - 1) / tq + 1) / 2;      // the request's tile pairs
+            int sc = nc, sq = ev[k];                             // sums up to this lane
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int yc = __shfl_up_sync(0xffffffffu, sc, o), yq = __shfl_up_sync(0xffffffffu, sq, o);
+                if (lane >= o) {
+                    sc += yc;
+                    sq += yq;
+                }
+            }
+            const uint32_t hit = __ballot_sync(0xffffffffu, c < acc_c + sc);
+            if (hit) {
+                const int l = __ffs(hit) - 1;
+                *c0 = acc_c + __shfl_sync(0xffffffffu, sc - nc, l);
+                *qoff = acc_q + __shfl_sync(0xffffffffu, sq - ev[k], l);
+                return b + 32 * k + l;
+            }
+            acc_c += __shfl_sync(0xffffffffu, sc, 31);
+            acc_q += __shfl_sync(0xffffffffu, sq, 31);
         }
-        acc_c += nc;
-        acc_q += e > 0 ? e : 0;
+    }
+    return -1;
+}
+
+// Query tile pair (blockIdx.x, blockIdx.y) of the extend batch, into info by
+// lane 0 of the calling warp; false if empty.  A few requests are walked, more
+// are searched by the warp: the walk is a chain of loads (100 requests of 16
+// new tokens: 94 us walked, 54 searched; 3 requests: 18.0 and 18.5).  Not
+// inlined: the kernel's registers are the tile roles', whose loops came out up
+// to 9% slower with it.
+__device__ __noinline__ bool extend_tile_info(const TcArgs& a, int* info) {
+    const int tq = 128 / a.G, lane = threadIdx.x & 31;
+    int req = -1, c0 = 0, qoff = 0;
+    if (a.B > 8) {
+        req = find_extend_request(a.extend_lens, a.B, tq, (int)blockIdx.x, &c0, &qoff);
+    } else {
+        int acc_c = 0, acc_q = 0;
+        for (int r = 0; r < a.B; ++r) {
+            const int e = __ldg(a.extend_lens + r);
+            const int nt = e > 0 ? (e + tq - 1) / tq : 0;
+            const int nc = (nt + 1) / 2;
+            if ((int)blockIdx.x < acc_c + nc) {
+                req = r;
+                c0 = acc_c;
+                qoff = acc_q;
+                break;
+            }
+            acc_c += nc;
+            acc_q += e > 0 ? e : 0;
+        }
     }
     if (req < 0) return false;
     const int pre = __ldg(a.prefix_lens + req), ext = __ldg(a.extend_lens + req);
@@ -58,9 +103,10 @@ __device__ bool extend_tile_info(const TcArgs& a, int* info) {
     const int na = min(tq, ext - t0), nb2 = min(tq, ext - t0 - tq);
     const int ntok = na + (nb2 > 0 ? nb2 : 0);
     if (pre < 0 || na <= 0 || (int64_t)pre + ext > a.ld || (int64_t)qoff + t0 + ntok > a.n_rows) {
-        atomicOr(a.err, 2u);
+        if (lane == 0) atomicOr(a.err, 2u);
         return false;
     }
+    if (lane != 0) return true;
     info[0] = req;                        // KV row
     info[1] = 0;                          // kv_begin
     info[2] = pre + t0 + ntok;            // kv_end
@@ -89,7 +135,10 @@ __global__ void __launch_bounds__(ExtCfg<D, KV>::kThreads, 1)
     int* info = reinterpret_cast<int*>(sm + Lay::OFF_INFO);
     uint32_t* tslot = reinterpret_cast<uint32_t*>(sm + Lay::OFF_TMEM);
     const int tid = threadIdx.x, warp = tid >> 5;
-    if (tid == 0) info[15] = extend_tile_info(a, info) ? 1 : 0;
+    if (warp == 0) {
+        const bool some = extend_tile_info(a, info);
+        if (tid == 0) info[15] = some ? 1 : 0;
+    }
     __syncthreads();
     if (!info[15]) return;
     if (tid == 0) {

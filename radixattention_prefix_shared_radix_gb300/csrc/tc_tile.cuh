@@ -203,9 +203,10 @@ struct TcArgs {
 // KEEP on is used only while the tiles run, so a kernel may reuse it once
 // its tiles are done: NQ query tiles (extend: 128B-swizzled smem tiles;
 // decode: none, Q lives in TMEM), NS K stages and NS V stages of BN
-// positions, the barriers and, with FP8 or 4-bit pools, the codes (a 4-bit
-// block's scales after them) of two blocks' K and V rows as copied, before
-// their conversion into the stages.
+// positions, the barriers and, with FP8 or 4-bit pools, K and V rows as copied
+// (a 4-bit block's scales behind its codes), before their conversion into the
+// stages: four buffers of one block's K or V rows, three with 4-bit pools (which
+// leaves room for one more stage).
 template <int D, bool DEC, int NQ, int NS, int BN, int KV = kKvBf16>
 struct TcLayout {
     static constexpr int OFF_TMEM = 0;                   // TMEM base address
@@ -220,7 +221,8 @@ struct TcLayout {
     static constexpr int OFF_BAR = OFF_V + NS * KTILE;
     static constexpr int OFF_STG = (OFF_BAR + 48 * 8 + 127) / 128 * 128;
     static constexpr int STG = KV == kKvFp4 ? BN * fp4_head_bytes(D) : BN * D;
-    static constexpr int END = OFF_STG + (KV != kKvBf16 ? 4 * STG : 0);
+    static constexpr int PARTS = KV == kKvFp4 ? 3 : 4;   // staging buffers
+    static constexpr int END = OFF_STG + (KV != kKvBf16 ? PARTS * STG : 0);
 };
 
 // Tile roles and their barriers for NQ query tiles that share one K/V stream
@@ -431,7 +433,125 @@ __device__ __forceinline__ void tc_tile_run(const TcArgs& a, const CUtensorMap* 
         }
         int issued = 0;
         const int32_t* trow = a_r2t + (int64_t)kv_row * a_ld;
-        if constexpr (F8) {
+        if constexpr (F4) {
+            // 4-bit pools: as FP8 pools below, but 32 codes per 16-byte piece;
+            // the lane of a row's first piece also copies the row's D / 16
+            // scales (the pieces of a row belong to one warp), which go into
+            // the f16 values (exact).  Parts K_0, V_0, K_1, .. take the
+            // staging buffers in turn, so that two parts are in flight beside
+            // the one that is converted.
+            constexpr int CH = D / 32;
+            constexpr int NIT = BN * CH;
+            constexpr int TPT = (NIT + 32 * NG - 1) / (32 * NG);
+            constexpr int CODES = BN * D / 2;           // a part's scales lie behind its codes
+            static_assert(Lay::PARTS == 3, "the order of copies below");
+            const int t0 = g * 32 + lane;
+            const uint32_t stg = smem_u32(sm + Lay::OFF_STG);
+            const int64_t rb = a.row_bytes;
+            const uint8_t* const kp4 = reinterpret_cast<const uint8_t*>(a_kp) + fp4_code_off(kvh, D);
+            const uint8_t* const vp4 = reinterpret_cast<const uint8_t*>(a_vp) + fp4_code_off(kvh, D);
+            const int soff = fp4_scale_off(kvh, a_Hkv, D) - fp4_code_off(kvh, D);
+            int32_t sl[TPT], rw[TPT];   // this lane's slots of the next block; rows of the block being copied
+            auto lookup = [&](int j) {
+#pragma unroll
+                for (int i = 0; i < TPT; ++i) {
+                    const int it = t0 + i * 32 * NG;
+                    const int p = min(kv_begin + j * BN + it / CH, kv_end - 1);
+                    sl[i] = (it < NIT && j < nb) ? __ldg(trow + p) : 0;
+                }
+            };
+            // the rows of block j, looked up before
+            auto rows_of = [&](int j) {
+#pragma unroll
+                for (int i = 0; i < TPT; ++i) {
+                    const int it = t0 + i * 32 * NG;
+                    rw[i] = sl[i];
+                    if (rw[i] < 0 || rw[i] >= a_num_slots) {
+                        if (j < nb && it < NIT && it % CH == 0) atomicOr(a_err, 1u);
+                        rw[i] = 0;
+                    }
+                }
+            };
+            // part n (block n / 2; odd: V) into its buffer, as one cp.async
+            // group (empty past the range, which keeps the count)
+            auto copy = [&](int n) {
+                const uint32_t sb = stg + (uint32_t)(n % Lay::PARTS) * Lay::STG;
+                if (n < 2 * nb) {
+#pragma unroll
+                    for (int i = 0; i < TPT; ++i) {
+                        const int it = t0 + i * 32 * NG;
+                        if (it >= NIT) continue;
+                        const uint8_t* row = (n & 1 ? vp4 : kp4) + rw[i] * rb;
+                        if (it % CH == 0) cp_async_small<D / 16>(sb + CODES + it / CH * (D / 16), row + soff);
+                        cp_async16(sb + it * 16, row + (it % CH) * 16, true);
+                    }
+                }
+                cp_async_commit();
+            };
+            lookup(0);
+            rows_of(0);
+            lookup(1);
+            copy(0);
+            copy(1);
+            rows_of(1);
+            lookup(2);
+            copy(2);
+            for (int n = 0; n < 2 * nb; ++n) {
+                const int j = n >> 1;
+                const bool v = n & 1;
+                const uint32_t J = J0 + j;
+                const int st = (int)(J % (uint32_t)NS);
+                const uint32_t ph = (J / (uint32_t)NS) & 1u;
+                const uint32_t sb = stg + (uint32_t)(n % Lay::PARTS) * Lay::STG;
+                cp_async_wait<Lay::PARTS - 1>();
+                wait(v ? C::VEMPTY(st) : C::KEMPTY(st), ph ^ 1u);
+                // store nothing into a stage that may be in use (decided for
+                // the whole warp)
+                if (__any_sync(0xffffffffu, stt.timed_out)) {
+                    stt.timed_out = true;
+                    break;
+                }
+                __syncwarp();   // a row's scales are its first piece's lane's copy
+                const uint32_t base = (v ? sV : sK) + st * Lay::KTILE;
+#pragma unroll
+                for (int i = 0; i < TPT; ++i) {
+                    const int it = t0 + i * 32 * NG;
+                    if (it < NIT) {
+                        const int r = it / CH, c = it % CH;
+                        uint32_t w[4];
+                        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];\n"
+                                     : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                                     : "r"(sb + it * 16));
+                        const uint32_t sf = e4m3x2_to_f16(ld_shared_u16(sb + CODES + r * (D / 16) + 2 * c));
+                        const uint32_t s2[2] = {__byte_perm(sf, sf, 0x1010), __byte_perm(sf, sf, 0x3232)};
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            uint32_t h[4];
+                            e2m1x8_to_f16(w[k], h);
+                            st_shared_v4(base + sw128(r, 4 * c + k, KR), hmul2_u(h[0], s2[k / 2]),
+                                         hmul2_u(h[1], s2[k / 2]), hmul2_u(h[2], s2[k / 2]), hmul2_u(h[3], s2[k / 2]));
+                        }
+                    }
+                }
+                // each lane fences its own stores for the tensor cores, then
+                // one arrival for the warp
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(v ? C::VFULL(st) : C::KFULL(st)));
+                // this buffer is free: the third part from here (V of the
+                // next block, or K of the one after it) into it
+                if (v) {
+                    rows_of(j + 2);
+                    copy(n + 3);
+                    lookup(j + 3);
+                } else {
+                    copy(n + 3);
+                }
+                issued = j + 1;
+            }
+            // no copy in flight when the tile ends (the staging area is the next tile's)
+            asm volatile("cp.async.wait_all;\n" ::: "memory");
+        } else if constexpr (F8) {
             // FP8 pools: lane t of the team copies 16-code pieces t, t + 32 NG,
             // ... of a block's K and V rows (CH pieces per row) with 16-byte
             // cp.async into one of two staging buffers (no registers held
@@ -442,11 +562,8 @@ __device__ __forceinline__ void tc_tile_run(const TcArgs& a, const CUtensorMap* 
             // barrier.  A block's slots are looked up one block before its
             // copies are issued and checked only then, so no lookup stalls
             // the conversions.  Positions past the range re-read the range's
-            // last position.  4-bit pools: 32 codes per piece; the first
-            // piece's lane also copies the row's D / 16 scales (pieces of a
-            // row belong to one warp), which go into the f16 values (exact).
-            constexpr int CH = F4 ? D / 32 : D / 16;
-            constexpr int RB = F4 ? D / 2 : D;          // code bytes of a row
+            // last position.
+            constexpr int CH = D / 16;
             constexpr int NIT = BN * CH;
             constexpr int TPT = (NIT + 32 * NG - 1) / (32 * NG);
             const int t0 = g * 32 + lane;
@@ -475,7 +592,7 @@ __device__ __forceinline__ void tc_tile_run(const TcArgs& a, const CUtensorMap* 
                         if (j < nb && it < NIT && it % CH == 0) atomicOr(a_err, 1u);
                         s1 = 0;
                     }
-                    rw[i] = F4 ? s1 : s1 * a_Hkv + kvh;
+                    rw[i] = s1 * a_Hkv + kvh;
                 }
 #pragma unroll
                 for (int part = 0; part < 2; ++part) {
@@ -483,18 +600,9 @@ __device__ __forceinline__ void tc_tile_run(const TcArgs& a, const CUtensorMap* 
 #pragma unroll
                         for (int i = 0; i < TPT; ++i) {
                             const int it = t0 + i * 32 * NG;
-                            if (it >= NIT) continue;
-                            const uint8_t* row;
-                            if constexpr (F4) {
-                                row = (part ? vp8 : kp8) + (int64_t)rw[i] * a.row_bytes;
-                                if (it % CH == 0)
-                                    cp_async_small<D / 16>(sb + part * Lay::STG + BN * RB + it / CH * (D / 16),
-                                                           row + fp4_scale_off(kvh, a_Hkv, D));
-                                row += fp4_code_off(kvh, D);
-                            } else {
-                                row = (part ? vp8 : kp8) + (int64_t)rw[i] * D;
-                            }
-                            cp_async16(sb + part * Lay::STG + it * 16, row + (it % CH) * 16, true);
+                            if (it < NIT)
+                                cp_async16(sb + part * Lay::STG + it * 16,
+                                           (part ? vp8 : kp8) + (int64_t)rw[i] * D + (it % CH) * 16, true);
                         }
                     }
                     cp_async_commit();
@@ -526,7 +634,6 @@ __device__ __forceinline__ void tc_tile_run(const TcArgs& a, const CUtensorMap* 
                         stop = true;
                         break;
                     }
-                    if constexpr (F4) __syncwarp();   // (a row's scales: its first piece's lane's copy)
                     const uint32_t base = (part ? sV : sK) + st * Lay::KTILE;
 #pragma unroll
                     for (int i = 0; i < TPT; ++i) {
@@ -537,20 +644,6 @@ __device__ __forceinline__ void tc_tile_run(const TcArgs& a, const CUtensorMap* 
                             asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];\n"
                                          : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
                                          : "r"(sb + part * Lay::STG + it * 16));
-                            if constexpr (F4) {
-                                const uint32_t sf = e4m3x2_to_f16(
-                                    ld_shared_u16(sb + part * Lay::STG + BN * RB + r * (D / 16) + 2 * c));
-                                const uint32_t s2[2] = {__byte_perm(sf, sf, 0x1010), __byte_perm(sf, sf, 0x3232)};
-#pragma unroll
-                                for (int k = 0; k < 4; ++k) {
-                                    uint32_t h[4];
-                                    e2m1x8_to_f16(w[k], h);
-                                    st_shared_v4(base + sw128(r, 4 * c + k, KR), hmul2_u(h[0], s2[k / 2]),
-                                                 hmul2_u(h[1], s2[k / 2]), hmul2_u(h[2], s2[k / 2]),
-                                                 hmul2_u(h[3], s2[k / 2]));
-                                }
-                                continue;
-                            }
                             uint32_t h[8];
                             e4m3x4_to_f16(w[0], h[0], h[1]);
                             e4m3x4_to_f16(w[1], h[2], h[3]);
