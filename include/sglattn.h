@@ -603,6 +603,7 @@ int sgl_rope(const sgl_rope_table* rope, int32_t dtype, const void* q, int64_t q
  *   rope         rotation of q and k (head_dim must match), or NULL: none
  *   params       dtype, batch, heads, head_dim, num_slots, k_scale, v_scale
  *                (the other fields are not used)
+ *   n_rows       at most 2^24
  *   q            device [n_rows, Hq, d], rows q_stride elements apart, or
  *                NULL with q_out NULL; rotated into q_out (rows q_out_stride
  *                apart; may be q itself, and must not overlap it otherwise)

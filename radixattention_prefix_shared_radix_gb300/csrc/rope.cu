@@ -15,14 +15,20 @@
 // and no range reduction.  The nearest quarter turn is split off before the
 // conversion to fp32, so that the fp32 angle is at most an eighth of a turn.
 //
-// Work: a CTA takes T tokens (and, for a few tokens, a slice of their
-// heads).  One warp per token finds its request, position and slot; then all
-// threads compute the tokens' sines and cosines into shared memory, once for
-// all heads; then each thread takes units of 16 elements -- two 16-byte (32
-// for fp32) pieces that the rotation pairs up -- from the new rows to the
-// outputs, the next unit's loads in flight; the first are issued before the
-// positions are known.  Memory-bound: rows are
-// read and written once.
+// Work: a warp works on one token by itself -- it finds the request, position
+// and slot, puts the token's sines and cosines into its own piece of shared
+// memory, and takes units of 16 elements (two 16-byte pieces that the rotation
+// pairs up; 32 bytes for fp32) from the new rows to the outputs.  A token's
+// heads are dealt to the two or four warps of its CTA, or to several CTAs.  The
+// loads of a warp's next group of units are in flight while it works on one,
+// the first ones before the position is known.
+// Memory-bound: rows are read and written once, and what counts is how many
+// warps have loads in flight: 36 of them per SM (56 registers) with one group
+// ahead, 16384 bf16 rows of 72 heads take 91.4 us (6.6 TB/s, 0.97 of the
+// measured copy); 32 warps two groups ahead 92-95, 24 warps 96-102.  8192 prompt
+// tokens of 32 + 2 * 8 heads into a 4-bit pool take 33 us (26 at the copy's
+// rate; 43 with lookups and tables shared by a CTA between barriers and units
+// dealt thread by thread, whose bookkeeping cost more than the rotation).
 //
 // ["SGLang 深度解读" (luoboask.github.io) section "5. Attention 层": the new
 // tokens' K/V are stored into token_to_kv_pool at their req_to_token slots
@@ -48,8 +54,8 @@ namespace {
 
 using namespace sgldev;
 
-constexpr int kThreads = 256;
-constexpr int kMaxT = 4;             // tokens per CTA
+constexpr int kThreads = 128;
+constexpr int kWarps = kThreads / 32;
 constexpr int kMaxHalf = SGL_ROPE_MAX_DIM / 2;
 
 enum { kPoolNone = 0, kPoolSame = 1, kPoolE4m3 = 2, kPoolFp4 = 3 };
@@ -70,38 +76,44 @@ struct RopeArgs {
     int B, Hq, Hk, Hv, d;
     int rot, off;                    // rotated part [off, off + rot) of a head (rot 0: none)
     int pairs;                       // layout
-    int T, slice, lg;                // tokens per CTA; heads per CTA and token; log2 of a power of two of units per head
+    int lt, lg;                      // log2 of the tokens per CTA, of a power of two of units per head
+    int groups, gq, gk;              // groups of 32 units of a token: in all; of q, of q and k (powers of two)
     int row_bytes;                   // bytes of a pool row
     uint32_t uph_inv;                // ceil(2^32 / units per head): exact quotients of units below 2^16
     bool copy_q;                     // q_out is not q: the part that is not rotated is copied
     float k_scale, v_scale, amp_hi, amp_lo;
+    float k_six, v_six, k_sixth, v_sixth;    // 6 k_scale, 6 v_scale and their reciprocals
     uint64_t turn[kMaxHalf];
 };
 
 // request and index within it of new row n: the first r with
-// ext[0] + .. + ext[r] > n.  One warp, 128 requests per round of loads.
-__device__ __forceinline__ bool find_request(const int32_t* ext, int B, int64_t n, int lane, int* req, int* idx) {
-    int64_t acc = 0;
+// ext[0] + .. + ext[r] > n.  One warp, 128 requests per round of loads.  (Rows
+// and their sums stay below 2^30: at most kMaxRows rows a call, a length counts
+// at most that.)
+constexpr int kMaxRows = 1 << 24;
+__device__ __forceinline__ bool find_request(const int32_t* ext, int B, int n, int lane, int* req, int* idx) {
+    int acc = 0;
     for (int b = 0; b < B; b += 128) {
         int e[4];
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
             const int r = b + 32 * c + lane;
-            e[c] = r < B ? max(__ldg(ext + r), 0) : 0;
+            e[c] = r < B ? min(max(__ldg(ext + r), 0), kMaxRows) : 0;
         }
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
-            int64_t s = e[c];
+            if (b + 32 * c >= B) break;
+            int s = e[c];
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
-                const int64_t y = __shfl_up_sync(0xffffffffu, s, o);
+                const int y = __shfl_up_sync(0xffffffffu, s, o);
                 if (lane >= o) s += y;
             }
             const uint32_t hit = __ballot_sync(0xffffffffu, acc + s > n);
             if (hit) {
                 const int l = __ffs(hit) - 1;
                 *req = b + 32 * c + l;
-                *idx = (int)(n - acc - __shfl_sync(0xffffffffu, s - e[c], l));
+                *idx = n - acc - __shfl_sync(0xffffffffu, s - e[c], l);
                 return true;
             }
             acc += __shfl_sync(0xffffffffu, s, 31);
@@ -204,169 +216,176 @@ __device__ __forceinline__ uint32_t amax8(uint4 w) {
     return __vmaxu2(__vmaxu2(w.x & m, w.y & m), __vmaxu2(w.z & m, w.w & m));
 }
 
-// c = z / f for eight bf16 values of magnitudes up to `m` (16-bit patterns), f
-// >= 0; zeros where f is 0.  Exact ties are common (bf16 over a product of few
-// bits) and must round as the quotient does, so a multiplication by 1 / f
-// alone will not do.  One correction makes it the rounded quotient
-// (Markstein 1990: q = z y, q + (z - q f) y with y the rounded reciprocal);
-// blocks whose magnitudes could leave the range of its products, and
-// infinities and NaN, are divided.
-__device__ __forceinline__ void divide8(const float* z, float f, uint32_t m, float* c) {
-    if (f >= 0x1p-60f && f <= 0x1p60f && max(m & 0xffffu, m >> 16) < 0x7f80u) {
+// Exact ties are common where a bf16 value is divided by a product of few bits,
+// and must round as the quotient does, so a multiplication by a reciprocal
+// alone will not do.  One correction makes it the rounded quotient (Markstein
+// 1990: q = z y, then q + (z - q f) y, with y the rounded reciprocal of f),
+// within this range of f and for a finite z; other operands are divided.
+__device__ __forceinline__ bool quick_range(float f) { return f >= 0x1p-60f && f <= 0x1p60f; }
+__device__ __forceinline__ float quotient(float z, float f, float y) {
+    const float q = z * y;
+    return fmaf(fmaf(-q, f, z), y, q);
+}
+
+// Code of a block's scale: the E4M3 value nearest to amax / s6, amax the
+// block's largest magnitude (the larger of two bf16 patterns), s6 = 6 scale
+// and y6 its rounded reciprocal.
+__device__ __forceinline__ uint32_t block_scale(uint32_t m, float s6, float y6) {
+    const uint32_t bits = max(m & 0xffffu, m >> 16);
+    const float amax = __uint_as_float(bits << 16);
+    return e4m3_of(bits < 0x7f80u && quick_range(s6) ? quotient(amax, s6, y6) : __fdiv_rn(amax, s6));
+}
+
+// c = z / f for a block of bf16 values of magnitudes up to `m` (a pair of
+// patterns), f >= 0; zeros where f is 0.
+__device__ __forceinline__ void divide16(const float* z, float f, uint32_t m, float* c) {
+    if (quick_range(f) && max(m & 0xffffu, m >> 16) < 0x7f80u) {
         const float y = __frcp_rn(f);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const float q = z[j] * y;
-            c[j] = fmaf(fmaf(-q, f, z[j]), y, q);
-        }
+        for (int j = 0; j < 16; ++j) c[j] = quotient(z[j], f, y);
     } else {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) c[j] = f > 0.f ? __fdiv_rn(z[j], f) : z[j] * 0.f;
+        for (int j = 0; j < 16; ++j) c[j] = f > 0.f ? __fdiv_rn(z[j], f) : z[j] * 0.f;
     }
 }
 
-// The units that a thread works on, one after another: unit c of head h (of
-// this CTA's Hs heads of each token) of token t.  POW2: a head has a power of
-// two of units, so c stays and h moves by a fixed step.
-template <bool POW2>
-struct Cursor {
-    int t, h, c, i;
-    __device__ __forceinline__ void settle(int T, int Hs) {
-        while (h >= Hs && t < T) {
-            h -= Hs;
-            ++t;
-        }
+// What a lane works on in group `id` of its token: unit c of head h of q, k or
+// v (part 0, 1, 2).  PART >= 0 (a head has a power of two of units up to 32):
+// a lane's c stays and a group lies within one part, which the caller knows,
+// so that the part's arguments are plain constants; PART < 0: found per lane.
+struct Place {
+    int part, h, c;
+    bool ok;
+};
+template <int PART>
+__device__ __forceinline__ Place place(const RopeArgs& a, int id, int lane) {
+    Place x;
+    if constexpr (PART >= 0) {
+        x.part = PART;
+        id -= PART == 0 ? 0 : PART == 1 ? a.gq : a.gk;
+        x.h = (id << (5 - a.lg)) + (lane >> a.lg);
+        x.c = lane & ((1 << a.lg) - 1);
+        x.ok = x.h < (PART == 0 ? a.Hq : PART == 1 ? a.Hk : a.Hv);
+    } else {
+        const int u = id * 32 + lane, uph = a.d >> 4;
+        x.h = (int)__umulhi((uint32_t)u, a.uph_inv);         // u / uph
+        x.c = u - x.h * uph;
+        x.ok = x.h < a.Hq + a.Hk + a.Hv;
+        x.part = x.h < a.Hq ? 0 : x.h < a.Hq + a.Hk ? 1 : 2;
+        x.h -= x.part == 0 ? 0 : x.part == 1 ? a.Hq : a.Hq + a.Hk;
     }
-    __device__ __forceinline__ void start(const RopeArgs& a, int tid, int Hs) {
-        t = 0;
-        if constexpr (POW2) {
-            c = tid & ((a.d >> 4) - 1);
-            h = tid >> a.lg;
-            settle(a.T, Hs);
-        } else {
-            i = tid;
-            place(a, Hs);
-        }
-    }
-    __device__ __forceinline__ void next(const RopeArgs& a, int Hs) {
-        if constexpr (POW2) {
-            h += kThreads >> a.lg;
-            settle(a.T, Hs);
-        } else {
-            i += kThreads;
-            place(a, Hs);
-        }
-    }
-    __device__ __forceinline__ void place(const RopeArgs& a, int Hs) {
-        const int g = (int)__umulhi((uint32_t)i, a.uph_inv);       // i / units per head
-        c = i - g * (a.d >> 4);
-        t = 0;
-        h = g;
-        settle(a.T, Hs);
-    }
+    return x;
+}
+template <int N>
+struct Part {
+    static constexpr int value = N;
 };
 
 template <typename T, int POOL, bool POW2>
-__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 3) rope_kernel(const __grid_constant__ RopeArgs a) {
-    __shared__ __align__(16) float cs[kMaxT][2][kMaxHalf];     // cosines, sines
-    __shared__ int s_pos[kMaxT], s_slot[kMaxT];
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int64_t n0 = (int64_t)blockIdx.x * a.T;
-    const int hb = blockIdx.y * a.slice;                       // this CTA's heads of each token (q, then k, then v)
-    const int Hs = min(a.slice, a.Hq + a.Hk + a.Hv - hb);
+__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 9 : 6) rope_kernel(const __grid_constant__ RopeArgs a) {
+    __shared__ __align__(16) float cs[kWarps][2][kMaxHalf];    // cosines, sines of a warp's token
+    const int lane = threadIdx.x & 31;
+    const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0);    // (known to be the same for the warp)
+    const int64_t n = ((int64_t)blockIdx.x << a.lt) + (warp & ((1 << a.lt) - 1));
+    const int step = (kWarps >> a.lt) * gridDim.y;             // warps per token
+    const int id0 = (warp >> a.lt) + (kWarps >> a.lt) * blockIdx.y;
     grid_dep_wait();      // launched as a programmatic dependent: inputs may come from the kernel before
     grid_dep_launch();
+    if (n >= a.n_rows || id0 >= a.groups) return;
     const int rblk = a.off >> 4, rend = rblk + (a.rot >> 4);   // rotated units of a head
+    const T* const qrow = static_cast<const T*>(a.q) + n * a.qs;
+    const T* const krow = static_cast<const T*>(a.k) + n * a.ks;
+    const T* const vrow = static_cast<const T*>(a.v) + n * a.vs;
+    T* const qout = static_cast<T*>(a.qo) + n * a.qos;
+    T* const kout = static_cast<T*>(a.ko) + n * a.kos;
+    auto rotated = [&](const Place& x) { return x.part < 2 && x.c >= rblk && x.c < rend; };
     // a unit's two runs of eight elements
-    auto run0 = [&](int c, bool rot) { return rot && !a.pairs ? a.off + 8 * (c - rblk) : 16 * c; };
-    auto run1 = [&](int c, bool rot) { return rot && !a.pairs ? a.off + 8 * (c - rblk) + (a.rot >> 1) : 16 * c + 8; };
-    // the next unit's elements, the first in flight while the positions are looked up
-    Eight<T> x0, x1;
-    Cursor<POW2> cur{};
-    auto fetch = [&]() {
-        const int64_t n = n0 + cur.t;
-        if (cur.t >= a.T || n >= a.n_rows) return;
-        const int hh = hb + cur.h;
-        const T* p;
-        if (hh < a.Hq)
-            p = static_cast<const T*>(a.q) + n * a.qs + hh * a.d;
-        else if (hh < a.Hq + a.Hk)
-            p = static_cast<const T*>(a.k) + n * a.ks + (hh - a.Hq) * a.d;
-        else
-            p = static_cast<const T*>(a.v) + n * a.vs + (hh - a.Hq - a.Hk) * a.d;
-        const bool rot = hh < a.Hq + a.Hk && cur.c >= rblk && cur.c < rend;
-        x0.load(p, run0(cur.c, rot));
-        x1.load(p, run1(cur.c, rot));
+    auto run0 = [&](const Place& x, bool rot) { return rot && !a.pairs ? a.off + 8 * (x.c - rblk) : 16 * x.c; };
+    auto run1 = [&](const Place& x, bool rot) {
+        return rot && !a.pairs ? a.off + 8 * (x.c - rblk) + (a.rot >> 1) : 16 * x.c + 8;
     };
-    cur.start(a, tid, Hs);
-    fetch();
-    // position and slot of each token: -1 where there is nothing to do
-    if (warp < a.T) {
-        const int64_t n = n0 + warp;
-        int pos = -1, slot = -1;
-        if (n < a.n_rows) {
-            if constexpr (POOL == kPoolNone) {
-                pos = __ldg(a.positions + n);
-            } else {
-                int r = (int)n, i = 0;
-                bool ok = true;
-                if (a.ext)
-                    ok = find_request(a.ext, a.B, n, lane, &r, &i);
-                if (ok) {
-                    const int64_t p = a.ext ? (int64_t)__ldg(a.lens + r) + i : (int64_t)__ldg(a.lens + r) - 1;
-                    // no context (decode): nothing to append; past the table: an error
-                    if (p >= a.ld || (p < 0 && a.ext)) {
-                        if (lane == 0) atomicOr(a.err, 2u);
-                    } else if (p >= 0) {
-                        pos = (int)p;
-                        slot = __ldg(a.r2t + (int64_t)r * a.ld + p);
-                        if (slot < 0 || slot >= a.num_slots) {
-                            if (lane == 0) atomicOr(a.err, 1u);
-                            slot = -1;
-                        }
-                    }
+    Eight<T> nx[2];       // the next group's
+    auto fetch_of = [&](auto part, int id) {
+        const Place x = place<decltype(part)::value>(a, id, lane);
+        if (!x.ok) return;
+        const T* p = (x.part == 0 ? qrow : x.part == 1 ? krow : vrow) + x.h * a.d;
+        const bool rot = rotated(x);
+        nx[0].load(p, run0(x, rot));
+        nx[1].load(p, run1(x, rot));
+    };
+    // f(part, ..) for the part that group id lies in
+    auto by_part = [&](int id, auto f) {
+        if constexpr (!POW2)
+            f(Part<-1>{});
+        else if (id < a.gq)
+            f(Part<0>{});
+        else if (id < a.gk)
+            f(Part<1>{});
+        else
+            f(Part<2>{});
+    };
+    auto fetch = [&](int id) {
+        if (id < a.groups) by_part(id, [&](auto part) { fetch_of(part, id); });
+    };
+    fetch(id0);
+    // position and slot: -1 where there is nothing to do
+    int pos = -1, slot = -1;
+    if constexpr (POOL == kPoolNone) {
+        pos = __ldg(a.positions + n);
+    } else {
+        int r = (int)n, i = 0;
+        if (!a.ext || find_request(a.ext, a.B, (int)n, lane, &r, &i)) {
+            const int64_t p = a.ext ? (int64_t)__ldg(a.lens + r) + i : (int64_t)__ldg(a.lens + r) - 1;
+            // no context (decode): nothing to append; past the table: an error
+            if (p >= a.ld || (p < 0 && a.ext)) {
+                if (lane == 0 && id0 == 0) atomicOr(a.err, 2u);
+            } else if (p >= 0) {
+                pos = (int)p;
+                slot = __ldg(a.r2t + (int64_t)r * a.ld + p);
+                if (slot < 0 || slot >= a.num_slots) {
+                    if (lane == 0 && id0 == 0) atomicOr(a.err, 1u);
+                    slot = -1;
                 }
             }
         }
-        if (lane == 0) {
-            s_pos[warp] = pos;
-            s_slot[warp] = slot;
-        }
     }
-    __syncthreads();
+    if (pos < 0) return;
     const int half = a.rot >> 1;
-    for (int i = tid; i < a.T * half; i += kThreads) {
-        const int t = i / half, j = i - t * half;
-        const int p = s_pos[t];
-        if (p >= 0) {
-            const float2 v = cos_sin_turn((uint64_t)(uint32_t)p * a.turn[j], a.amp_hi, a.amp_lo);
-            cs[t][0][j] = v.x;
-            cs[t][1][j] = v.y;
-        }
+    for (int j = lane; j < half; j += 32) {
+        // (an ordinary load: the lanes' indices differ, which the constant
+        // cache would serve one by one)
+        uint64_t turn;
+        asm("ld.b64 %0, [%1];" : "=l"(turn) : "l"(&a.turn[j]));
+        const float2 v = cos_sin_turn((uint64_t)(uint32_t)pos * turn, a.amp_hi, a.amp_lo);
+        cs[warp][0][j] = v.x;
+        cs[warp][1][j] = v.y;
     }
-    __syncthreads();
-    // (whole warps go round: 4-bit blocks are finished across lanes)
-    while (__any_sync(0xffffffffu, cur.t < a.T)) {
-        const int t = min(cur.t, a.T - 1), c = cur.c, hh = hb + cur.h;
-        const bool live = cur.t < a.T && s_pos[t] >= 0;
-        Eight<T> r0 = x0, r1 = x1;      // (what is not rotated keeps its bits)
-        cur.next(a, Hs);
-        fetch();
-        const int part = hh < a.Hq ? 0 : hh < a.Hq + a.Hk ? 1 : 2;
-        const bool rot = part < 2 && c >= rblk && c < rend;
-        const int e0 = run0(c, rot), e1 = run1(c, rot);
+    __syncwarp();
+    // the cosines and sines of unit c's eight pairs
+    float co[8], si[8];
+    auto angles = [&](int c) {
+#pragma unroll
+        for (int j = 0; j < 8; j += 4) {
+            const float4 u = *reinterpret_cast<const float4*>(&cs[warp][0][8 * (c - rblk) + j]);
+            const float4 w = *reinterpret_cast<const float4*>(&cs[warp][1][8 * (c - rblk) + j]);
+            co[j] = u.x; co[j + 1] = u.y; co[j + 2] = u.z; co[j + 3] = u.w;
+            si[j] = w.x; si[j + 1] = w.y; si[j + 2] = w.z; si[j + 3] = w.w;
+        }
+    };
+    if constexpr (POW2) {
+        const int c = lane & ((1 << a.lg) - 1);
+        if (c >= rblk && c < rend) angles(c);
+    }
+    auto work_of = [&](auto part, Eight<T> (&w)[2], int id) {
+        const Place x = place<decltype(part)::value>(a, id, lane);
+        const bool rot = rotated(x);
+        const int e0 = run0(x, rot), e1 = run1(x, rot);
+        Eight<T> r0 = w[0], r1 = w[1];          // (what is not rotated keeps its bits)
         if (rot) {
-            const int fr = 8 * (c - rblk);
-            float y[16], co[8], si[8];
+            if constexpr (!POW2) angles(x.c);
+            float y[16];
             r0.get(y);
             r1.get(y + 8);
-#pragma unroll
-            for (int j = 0; j < 8; j += 4) {
-                const float4 u = *reinterpret_cast<const float4*>(&cs[t][0][fr + j]);
-                const float4 w = *reinterpret_cast<const float4*>(&cs[t][1][fr + j]);
-                co[j] = u.x; co[j + 1] = u.y; co[j + 2] = u.z; co[j + 3] = u.w;
-                si[j] = w.x; si[j + 1] = w.y; si[j + 2] = w.z; si[j + 3] = w.w;
-            }
             // (written out, so that every instantiation rounds alike)
             if (a.pairs) {
 #pragma unroll
@@ -386,75 +405,82 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 3) rope_kernel(
             r0.set(y);
             r1.set(y + 8);
         }
-        const int64_t n = n0 + t;
-        if (part == 0 || POOL == kPoolNone) {
-            if (live && (rot || a.copy_q)) {
-                T* dst = part == 0 ? static_cast<T*>(a.qo) + n * a.qos + hh * a.d
-                                   : static_cast<T*>(a.ko) + n * a.kos + (hh - a.Hq) * a.d;
+        if (x.part == 0 || POOL == kPoolNone) {
+            if (x.ok && (rot || a.copy_q)) {
+                T* dst = (x.part == 0 ? qout : kout) + x.h * a.d;
                 r0.put(dst + e0);
                 r1.put(dst + e1);
             }
-            if (POOL != kPoolFp4) continue;
+            return;
         }
-        const int slot = live && part > 0 ? s_slot[t] : -1;
-        const int h = hh - a.Hq - (part == 2 ? a.Hk : 0);
-        uint8_t* row = (part == 1 ? a.kp : a.vp) + (int64_t)max(slot, 0) * a.row_bytes;
+        uint8_t* row = (x.part == 1 ? a.kp : a.vp) + (int64_t)max(slot, 0) * a.row_bytes;
+        [[maybe_unused]] const bool live = x.ok && slot >= 0;
         if constexpr (POOL == kPoolSame) {
-            if (slot >= 0) {
-                T* dst = reinterpret_cast<T*>(row) + h * a.d;
+            if (live) {
+                T* dst = reinterpret_cast<T*>(row) + x.h * a.d;
                 r0.put(dst + e0);
                 r1.put(dst + e1);
             }
         } else if constexpr (POOL == kPoolE4m3) {
             // quantised pools hold codes of the rows' bf16 values, as an
             // unfused rotation would have left them
-            if (slot >= 0) {
-                const float scale = part == 1 ? a.k_scale : a.v_scale;
+            if (live) {
+                const float scale = x.part == 1 ? a.k_scale : a.v_scale;
 #pragma unroll
                 for (int b = 0; b < 2; ++b) {
                     float z[8];
                     (b ? r1 : r0).get(z);
-                    uint32_t w[4];
+                    uint32_t v[4];
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
-                        uint16_t x;
+                        uint16_t y;
                         const float lo = __fdiv_rn(z[2 * j], scale), hi = __fdiv_rn(z[2 * j + 1], scale);
-                        asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(x) : "f"(hi), "f"(lo));
-                        w[j] = x;
+                        asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(y) : "f"(hi), "f"(lo));
+                        v[j] = y;
                     }
-                    *reinterpret_cast<uint2*>(row + h * a.d + (b ? e1 : e0)) =
-                        make_uint2(w[0] | (w[1] << 16), w[2] | (w[3] << 16));
+                    *reinterpret_cast<uint2*>(row + x.h * a.d + (b ? e1 : e0)) =
+                        make_uint2(v[0] | (v[1] << 16), v[2] | (v[3] << 16));
                 }
             }
         } else if constexpr (POOL == kPoolFp4) {
-            // The scale of each run's block of 16.  The runs are the two
-            // halves of one block (one amax), or, rotated in the half layout,
-            // half of one block each, whose other halves the neighbouring
-            // unit holds.
-            uint32_t m0 = amax8(r0.w), m1 = amax8(r1.w);
-            const bool split = rot && !a.pairs && a.rot > 16;
-            const int other = (split ? (((c - rblk) & 1) ? lane - 1 : lane + 1) : lane) & 31;
-            const uint32_t o0 = __shfl_sync(0xffffffffu, m0, other), o1 = __shfl_sync(0xffffffffu, m1, other);
-            m0 = __vmaxu2(m0, split ? o0 : m1);
-            m1 = split ? __vmaxu2(m1, o1) : m0;
-            if (slot >= 0) {
-                const float scale = part == 1 ? a.k_scale : a.v_scale;
-                row += fp4_code_off(h, a.d);
-                uint8_t* const sfs = row - fp4_code_off(h, a.d) + fp4_scale_off(h, part == 1 ? a.Hk : a.Hv, a.d);
-#pragma unroll
-                for (int b = 0; b < 2; ++b) {
-                    const uint32_t m = b ? m1 : m0;
-                    const float amax = __uint_as_float(max(m & 0xffffu, m >> 16) << 16);
-                    const uint32_t sf = e4m3_of(__fdiv_rn(amax, 6.f * scale));
-                    float z[8], q[8];
-                    (b ? r1 : r0).get(z);
-                    divide8(z, e4m3_value(sf) * scale, m, q);
-                    const int e = b ? e1 : e0;
-                    *reinterpret_cast<uint32_t*>(row + e / 2) = e2m1x8_of(q);
-                    if ((e & 8) == 0) sfs[e / 16] = (uint8_t)sf;
+            // One block of 16 per lane.  A unit's runs are the halves of one
+            // block, or, rotated in the half layout, halves of two, whose other
+            // halves the neighbouring unit's lane holds: the even unit takes
+            // the first block, the odd one the second (a group is of one part:
+            // the whole warp is here).
+            int e = e0;
+            if (decltype(part)::value == 1 && !a.pairs && a.rot > 16) {
+                const bool odd = (x.c - rblk) & 1;
+                uint4 give = odd ? r0.w : r1.w;
+                const int other = rot ? (odd ? lane - 1 : lane + 1) : lane;
+                give.x = __shfl_sync(0xffffffffu, give.x, other);
+                give.y = __shfl_sync(0xffffffffu, give.y, other);
+                give.z = __shfl_sync(0xffffffffu, give.z, other);
+                give.w = __shfl_sync(0xffffffffu, give.w, other);
+                if (rot && odd) {
+                    r0.w = give;
+                    e = e1 - 8;
+                } else if (rot) {
+                    r1.w = give;
                 }
             }
+            if (live) {
+                const bool key = x.part == 1;
+                const uint32_t m = __vmaxu2(amax8(r0.w), amax8(r1.w));
+                const uint32_t sf = block_scale(m, key ? a.k_six : a.v_six, key ? a.k_sixth : a.v_sixth);
+                float z[16], y[16];
+                r0.get(z);
+                r1.get(z + 8);
+                divide16(z, e4m3_value(sf) * (key ? a.k_scale : a.v_scale), m, y);
+                *reinterpret_cast<uint2*>(row + fp4_code_off(x.h, a.d) + e / 2) = make_uint2(e2m1x8_of(y), e2m1x8_of(y + 8));
+                row[fp4_scale_off(x.h, key ? a.Hk : a.Hv, a.d) + e / 16] = (uint8_t)sf;
+            }
         }
+    };
+    for (int id = id0; id < a.groups; id += step) {
+        Eight<T> now[2] = {nx[0], nx[1]};
+        fetch(id + step);
+        by_part(id, [&](auto part) { work_of(part, now, id); });
     }
 }
 
@@ -475,22 +501,29 @@ bool rows_ok(const void* p, int64_t stride, int heads, int d, int es) {
 
 template <typename T, int POOL, bool POW2>
 int launch_as(RopeArgs& a, cudaStream_t s) {
-    // Tokens per CTA and slices of a token's heads: up to four tokens share a
-    // CTA (one chain of lookups for more work) as long as every SM still has
-    // one; below one token per SM a token's heads are spread over several
-    // CTAs (of at least 64 units each).
+    // Two tokens share a CTA (two warps each) once every SM has one; below one
+    // token per SM a token's groups are spread over several CTAs.  Measured
+    // with 1, 2 and 4 tokens per CTA: 8192 rows into a 4-bit pool 36.8, 32.9
+    // and 34.2 us, 16384 rows of 72 heads 91.7, 91.4 and 95.6.
     constexpr int kSms = 152;
     const int heads = a.Hq + a.Hk + a.Hv, uph = a.d / 16;
-    if ((int64_t)heads * uph > 0xffff / kMaxT) return SGL_ERR_UNSUPPORTED;   // (the cursor's quotients)
-    a.T = (int)std::min<int64_t>(kMaxT, std::max<int64_t>(1, a.n_rows / kSms));
-    int slices = 1;
-    if (a.n_rows < kSms) slices = (int)std::min<int64_t>((kSms + a.n_rows - 1) / a.n_rows, (heads * uph + 63) / 64);
-    a.slice = (heads + slices - 1) / slices;
-    slices = (heads + a.slice - 1) / a.slice;
+    if ((int64_t)heads * uph > 0xffff - 32) return SGL_ERR_UNSUPPORTED;     // (unit numbers and their quotients)
+    a.lt = a.n_rows >= 2 * kSms ? 1 : 0;
     a.uph_inv = uph > 1 ? (uint32_t)(((1ull << 32) + uph - 1) / uph) : 0u;
     a.lg = 0;
     while ((1 << a.lg) < uph) ++a.lg;
-    const int64_t ctas = (a.n_rows + a.T - 1) / a.T;
+    const int per = std::max(1, 32 / uph);                                  // heads per group
+    if (POW2) {
+        a.gq = (a.Hq + per - 1) / per;
+        a.gk = a.gq + (a.Hk + per - 1) / per;
+        a.groups = a.gk + (a.Hv + per - 1) / per;
+    } else {
+        a.groups = (heads * uph + 31) / 32;
+    }
+    int slices = 1;
+    if (a.n_rows < kSms)
+        slices = (int)std::min<int64_t>((kSms + a.n_rows - 1) / a.n_rows, (a.groups + kWarps - 1) / kWarps);
+    const int64_t ctas = (a.n_rows + (1 << a.lt) - 1) >> a.lt;
     if (ctas > INT32_MAX) return SGL_ERR_UNSUPPORTED;
     cudaLaunchAttribute pdl[1];
     pdl[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -507,7 +540,7 @@ int launch_as(RopeArgs& a, cudaStream_t s) {
 template <typename T, int POOL>
 int launch(RopeArgs& a, cudaStream_t s) {
     if (a.n_rows == 0 || a.Hq + a.Hk + a.Hv == 0) return SGL_OK;
-    if ((a.d & (a.d - 1)) == 0) return launch_as<T, POOL, true>(a, s);
+    if ((a.d & (a.d - 1)) == 0 && a.d <= 512) return launch_as<T, POOL, true>(a, s);
     // other widths: rotation alone and MLA rows (the pools' heads are 64 or 128 wide)
     if constexpr (POOL == kPoolNone || (POOL == kPoolSame && sizeof(T) == 2)) return launch_as<T, POOL, false>(a, s);
     return SGL_ERR_UNSUPPORTED;
@@ -529,6 +562,7 @@ int append_rows(RopeArgs& a, const sgl_rope_table* rope, int es, int64_t n_rows,
                 void* q_out, int64_t q_out_stride, int Hq, int d, void* workspace, size_t ws_bytes) {
     if (n_rows < 0 || ld < 0 || (rope && rope->p.head_dim != d)) return SGL_ERR_INVALID_ARG;
     if (!extend_lens && n_rows > batch) return SGL_ERR_INVALID_ARG;
+    if (n_rows > kMaxRows) return SGL_ERR_UNSUPPORTED;
     if (!workspace || (reinterpret_cast<uintptr_t>(workspace) % sgl::kWsAlign) != 0 || ws_bytes < sgl::kWsAlign)
         return SGL_ERR_WORKSPACE;
     if (n_rows > 0 && (!req_to_token || !lens)) return SGL_ERR_INVALID_ARG;
@@ -688,6 +722,10 @@ int sgl_kv_append(const sgl_rope_table* rope, const sgl_attn_params* params, con
     a.Hk = a.Hv = Hkv;
     a.k_scale = params->k_scale;
     a.v_scale = params->v_scale;
+    a.k_six = 6.f * a.k_scale;
+    a.v_six = 6.f * a.v_scale;
+    a.k_sixth = 1.f / a.k_six;
+    a.v_sixth = 1.f / a.v_six;
     auto s = reinterpret_cast<cudaStream_t>(stream);
     switch (params->dtype) {
         case SGL_DTYPE_F32: a.row_bytes = Hkv * d * 4; return launch<float, kPoolSame>(a, s);
