@@ -90,28 +90,10 @@ constexpr int kDescFlags = 0, kDescMask = 4, kDescPb = 8, kDescRows = 12, kDescN
 // What a streaming CTA works with.
 struct Fp4Args {
     FusedArgs f;
+    int lg;                // log2 of the query heads per KV head
     int box8, box4;        // bytes of a piece's row: blocks of up to 8 heads, of up to 4 (more than 8 query rows)
     int after_tiles;       // launched behind the tiles
 };
-
-// ---------------------------------------------------------------------------
-// Lookup: as in decode_fused.cu, up to 8 steps ahead of the copies; the
-// piece's query rows are fetched into L1 meanwhile (what the ring leaves of it
-// holds them), since the consumers' first use of them holds up the stage.
-// ---------------------------------------------------------------------------
-template <int D>
-__device__ __forceinline__ void fp4_lookup(const Fp4Args& p, int gw, uint32_t lrec, uint32_t sring, uint32_t sfull,
-                                        uint32_t sfree, int lane) {
-    const FusedArgs& f = p.f;
-    stream_lookup<kNP>(f, gw, lrec, sring, sfull, sfree, lane, [&](int kvh, int nh, int nm, int mem) {
-        const int lines = nh * f.t.G * D * 2 / 128;   // of a member's rows of these heads, which are contiguous
-        for (int i = 0; i < nm; ++i) {
-            const int r = __shfl_sync(0xffffffffu, mem, i);
-            const char* row = reinterpret_cast<const char*>(f.t.q + ((int64_t)r * f.t.Hq + kvh * f.t.G) * D);
-            for (int l = lane; l < lines; l += 32) prefetch_l1(row + 128 * l);
-        }
-    });
-}
 
 // ---------------------------------------------------------------------------
 // Producer: per step waits for the slot entry and a free stage, then lane i
@@ -309,14 +291,16 @@ __device__ __forceinline__ void fp4_consumer(const Fp4Args& p, int c, uint32_t r
             if (have && active) finish_item();
             have = true;
             const int rows = ld_shared_s32(db + kDescRows), nh = ld_shared_s32(db + kDescNh),
-                      kvh = ld_shared_s32(db + kDescKvh), G = p.f.t.G;
+                      kvh = ld_shared_s32(db + kDescKvh);
             const int wph = rows > 8 ? 2 : 1;   // consumer warps per head
             const int hw = c / wph, r0 = (c - hw * wph) * 8;
             active = hw < nh && r0 < rows;
             if (active) {
-                const int pb = ld_shared_s32(db + kDescPb), r = r0 + 2 * t;   // row: member r / G, query head r % G
-                pr0 = r < rows ? pb + ((r / G) * nh + hw) * G + r % G : -1;
-                pr1 = r + 1 < rows ? pb + (((r + 1) / G) * nh + hw) * G + (r + 1) % G : -1;
+                // row r of a head: member r / G, query head r % G
+                const int pb = ld_shared_s32(db + kDescPb), r = r0 + 2 * t, G1 = (1 << p.lg) - 1;
+                auto prow = [&](int x) { return x < rows ? pb + ((((x >> p.lg) * nh + hw) << p.lg) | (x & G1)) : -1; };
+                pr0 = prow(r);
+                pr1 = prow(r + 1);
                 // this lane's first rows of a 16-position group: K row g (the
                 // other, g + 8, lies two quads on), V row 2t (2t + 1 lies dv
                 // on, 2t + 8 and 2t + 9 two quads on); the head's codes and
@@ -335,9 +319,9 @@ __device__ __forceinline__ void fp4_consumer(const Fp4Args& p, int c, uint32_t r
                 // Q^T: row r0 + g, the lane's run of d / 4 elements in order, as f16
                 const int rq = r0 + g;
                 const bool ok = rq < rows;
-                const int mq = ok ? ld_shared_s32(db + kDescMem + 4 * (rq / G)) : 0;
+                const int mq = ok ? ld_shared_s32(db + kDescMem + 4 * (rq >> p.lg)) : 0;
                 const uint4* src = reinterpret_cast<const uint4*>(
-                    p.f.t.q + ((int64_t)mq * p.f.t.Hq + (kvh + hw) * G + rq % G) * D + (D / 4) * t);
+                    p.f.t.q + ((int64_t)mq * p.f.t.Hq + ((kvh + hw) << p.lg) + (rq & G1)) * D + (D / 4) * t);
                 uint32_t bad = 0u;
 #pragma unroll
                 for (int j = 0; j < D / 32; ++j) {
@@ -569,6 +553,11 @@ __global__ void __launch_bounds__(kStreamThreads, kStreamCtas)
         }
         mbar_fence_init();
     }
+    // (before the dependency wait: the first copy finds the descriptors in the cache)
+    if (warp == kProducer && lane < 4) {
+        const CUtensorMap* m = lane == 0 ? &k8 : lane == 1 ? &v8 : lane == 2 ? &k4 : &v4;
+        asm volatile("prefetch.tensormap [%0];\n" ::"l"(m) : "memory");
+    }
     // Until the dependency wait only shared memory and the plan tables are
     // touched (see decode_fused.cu): the launch piece's record and members
     const int gw = (int)blockIdx.x;
@@ -594,7 +583,7 @@ __global__ void __launch_bounds__(kStreamThreads, kStreamCtas)
     const uint32_t desc = smem_u32(sm + Lay::OFF_DESC);
     const uint32_t sring = smem_u32(sm + Lay::OFF_SLOT);
     if (warp == kLookup)
-        fp4_lookup<D>(p, gw, lrec, sring, sfull, sfree, lane);
+        stream_lookup<kNP>(p.f, gw, lrec, sring, sfull, sfree, lane);   // up to 8 steps ahead of the copies
     else if (warp == kProducer)
         fp4_producer<D>(p, &k8, &v8, &k4, &v4, ring, sring, desc, full, empty, sfull, sfree, lane);
     else
@@ -646,6 +635,7 @@ int launch_decode_fp4(const sgl_plan* plan, const void* q, const void* kp, const
     a.Hq = p.num_qo_heads;
     a.Hkv = p.num_kv_heads;
     a.G = plan->G;
+    while ((1 << x.lg) < a.G) ++x.lg;
     a.num_slots = p.num_slots;
     a.scale_log2 = scale_log2;
     a.k_scale = p.k_scale;

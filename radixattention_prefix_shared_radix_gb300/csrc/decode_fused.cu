@@ -500,7 +500,7 @@ __device__ __noinline__ void stream_consumer(const FusedArgs& f, int c, uint32_t
 
 __device__ __noinline__ void fused_lookup(const FusedArgs& f, int gw, uint32_t lrec, uint32_t sring, uint32_t sfull,
                                           uint32_t sfree, int lane) {
-    stream_lookup<kNP>(f, gw, lrec, sring, sfull, sfree, lane, [](int, int, int, int) {});
+    stream_lookup<kNP>(f, gw, lrec, sring, sfull, sfree, lane);
 }
 
 template <int D, bool F8>

@@ -79,11 +79,9 @@ struct SlotEntry {
 // fields; the producers free it (SLOTFREE).  An entry with no KV head ends
 // the stream.  Global loads (the counter, records, seq_lens) stall only this
 // warp, which runs ahead of the copies.
-// on_piece(kvh, nh, nm, mem): called once a piece's record is known, mem the
-// lane's member request.
-template <int NP, class OnPiece>
+template <int NP>
 __device__ __forceinline__ void stream_lookup(const FusedArgs& f, int gw, uint32_t lrec, uint32_t sring,
-                                              uint32_t sfull, uint32_t sfree, int lane, OnPiece on_piece) {
+                                              uint32_t sfull, uint32_t sfree, int lane) {
     using Ent = SlotEntry<NP>;
     const int32_t* const r2t = f.t.r2t;
     const int32_t* const members = f.t.members;
@@ -156,7 +154,6 @@ __device__ __forceinline__ void stream_lookup(const FusedArgs& f, int gw, uint32
             mem = lane < nm ? __ldg(members + mb + lane) : 0;
         }
         first_piece = false;
-        on_piece(kvh, nh, nm, mem);
         int len = __ldg(seq_lens + row);
         if (e == kDecToSeqEnd) {
             // a request's trailing piece runs to its length now (within its
