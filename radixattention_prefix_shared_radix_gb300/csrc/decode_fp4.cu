@@ -93,6 +93,8 @@ struct Fp4Args {
     int lg;                // log2 of the query heads per KV head
     int box8, box4;        // bytes of a piece's row: blocks of up to 8 heads, of up to 4 (more than 8 query rows)
     int after_tiles;       // launched behind the tiles
+    bf16* o;               // every request is one piece per head: results go here (and to lse), without a merge;
+    float* lse;            //   else null
 };
 
 // ---------------------------------------------------------------------------
@@ -251,7 +253,7 @@ __device__ __forceinline__ void fp4_consumer(const Fp4Args& p, int c, uint32_t r
     uint32_t q[D / 8];
     float o[MT][4];
     float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
-    int pr0 = -1, pr1 = -1;                     // partial rows of this lane's two query rows
+    int pr0 = -1, pr1 = -1;                     // partial rows (rows of o) of this lane's two query rows
     bool have = false, active = false;
     uint32_t ka = 0u, ks = 0u, va = 0u, vs = 0u, dv = 0u;   // offsets within a stage (see below)
     auto finish_item = [&]() {
@@ -267,11 +269,22 @@ __device__ __forceinline__ void fp4_consumer(const Fp4Args& p, int c, uint32_t r
             if (prow >= 0) {
                 const float ll = hh ? s1 : s0, mm = hh ? m1 : m0;
                 const float inv = ll > 0.f ? p.f.t.v_scale / ll : 0.f;
-                float* dst = p.f.t.po + prow * D + (D / 8) * g;
+                if (p.o) {
+                    uint4* dst = reinterpret_cast<uint4*>(p.o + prow * D + (D / 8) * g);
 #pragma unroll
-                for (int i = 0; i < MT; ++i)
-                    *reinterpret_cast<float2*>(dst + 2 * i) = make_float2(o[i][hh] * inv, o[i][2 + hh] * inv);
-                if (g == 0) p.f.t.plse[prow] = ll > 0.f ? (mm + log2f(ll)) * kLn2 : -INFINITY;
+                    for (int i = 0; i < MT; i += 4)
+                        dst[i / 4] = make_uint4(pack_bf16(o[i][hh] * inv, o[i][2 + hh] * inv),
+                                                pack_bf16(o[i + 1][hh] * inv, o[i + 1][2 + hh] * inv),
+                                                pack_bf16(o[i + 2][hh] * inv, o[i + 2][2 + hh] * inv),
+                                                pack_bf16(o[i + 3][hh] * inv, o[i + 3][2 + hh] * inv));
+                } else {
+                    float* dst = p.f.t.po + prow * D + (D / 8) * g;
+#pragma unroll
+                    for (int i = 0; i < MT; i += 2)
+                        *reinterpret_cast<float4*>(dst + 2 * i) =
+                            make_float4(o[i][hh] * inv, o[i][2 + hh] * inv, o[i + 1][hh] * inv, o[i + 1][2 + hh] * inv);
+                }
+                if (g == 0) (p.o ? p.lse : p.f.t.plse)[prow] = ll > 0.f ? (mm + log2f(ll)) * kLn2 : -INFINITY;
             }
         }
     };
@@ -298,7 +311,11 @@ __device__ __forceinline__ void fp4_consumer(const Fp4Args& p, int c, uint32_t r
             if (active) {
                 // row r of a head: member r / G, query head r % G
                 const int pb = ld_shared_s32(db + kDescPb), r = r0 + 2 * t, G1 = (1 << p.lg) - 1;
-                auto prow = [&](int x) { return x < rows ? pb + ((((x >> p.lg) * nh + hw) << p.lg) | (x & G1)) : -1; };
+                auto prow = [&](int x) {
+                    if (x >= rows) return -1;
+                    return (p.o ? ld_shared_s32(db + kDescMem + 4 * (x >> p.lg)) * p.f.t.Hq + ((kvh + hw) << p.lg)
+                                : pb + (((x >> p.lg) * nh + hw) << p.lg)) + (x & G1);
+                };
                 pr0 = prow(r);
                 pr1 = prow(r + 1);
                 // this lane's first rows of a 16-position group: K row g (the
@@ -600,11 +617,17 @@ int launch_decode_fp4(const sgl_plan* plan, const void* q, const void* kp, const
     // (+ alignment slack; too much for two tile CTAs per SM: each allocates all TMEM columns)
     constexpr int kTileSmem = Fp4Cfg<D>::Lay::END + 1024 > 120 * 1024 ? Fp4Cfg<D>::Lay::END + 1024 : 120 * 1024;
     static_assert(kTileSmem <= 232448, "shared memory per CTA");
+    constexpr int kMergeSmem = 216 * 1024;
     static const int attr = [] {
         const cudaError_t e = cudaFuncSetAttribute(decode_fp4_streams<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                    Lay::TOTAL);
-        return (int)(e ? e : cudaFuncSetAttribute(decode_fp4_tiles<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                  kTileSmem));
+        const cudaError_t e1 = cudaFuncSetAttribute(decode_fp4_tiles<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                    kTileSmem);
+        const cudaError_t e2 = cudaFuncSetAttribute(decode_merge_kernel<bf16, D, 4>,
+                                                    cudaFuncAttributeMaxDynamicSharedMemorySize, kMergeSmem);
+        const cudaError_t e3 = cudaFuncSetAttribute(decode_merge_kernel<bf16, D, 16>,
+                                                    cudaFuncAttributeMaxDynamicSharedMemorySize, kMergeSmem);
+        return (int)(e ? e : e1 ? e1 : e2 ? e2 : e3);
     }();
     if (attr) return attr;
     const sgl_attn_params& p = plan->params;
@@ -662,17 +685,37 @@ int launch_decode_fp4(const sgl_plan* plan, const void* q, const void* kp, const
         x.after_tiles = 1;
     }
     // (every request has a trailing piece, so there are streams whenever there are requests)
-    cfg.gridDim = dim3((unsigned)(kStreamCtas * plan->n_ctas));
+    // (when every piece is dealt at launch, a CTA for each)
+    cfg.gridDim = dim3((unsigned)(plan->n_narrow <= plan->n_init ? plan->n_narrow : kStreamCtas * plan->n_ctas));
     cfg.blockDim = dim3(kStreamThreads);
     cfg.dynamicSmemBytes = Lay::TOTAL;
+    // one piece per request and head: nothing to merge (64 requests of 64 tokens: 10.7 -> 6.6 us)
+    const bool direct = plan->n_wide == 0 && plan->n_merge_entries == p.batch * p.num_kv_heads;
+    if (direct) {
+        x.o = static_cast<bf16*>(o);
+        x.lse = lse;
+    }
     if (const int e = (int)cudaLaunchKernelEx(&cfg, decode_fp4_streams<D>, x, k8, v8, k4, v4)) return e;
+    if (direct) return 0;
     MergeArgs m{a.po, a.plse, reinterpret_cast<const int32_t*>(ws + plan->off_mptr),
                 reinterpret_cast<const int32_t*>(ws + plan->off_ment), o, lse, a.Hq, a.Hkv, a.G};
     const int n_pairs = p.batch * a.Hkv;
     cfg.gridDim = dim3((unsigned)merge_blocks<D>(n_pairs, a.G));
     cfg.blockDim = dim3(128);
-    cfg.dynamicSmemBytes = 0;
-    return (int)cudaLaunchKernelEx(&cfg, decode_merge_kernel<bf16, D>, m, n_pairs);
+    // The merge's CTAs come to SMs as the streams leave them.  Where there are
+    // more streams than SMs, the first SMs to be left would take many of them
+    // and the last none, so each takes shared memory for its share of an SM (33
+    // requests of 1024 tokens: 18.9 -> 16.7 us by fours, 16.4 -> 16.0 by
+    // sixteens; with one stream per SM the merge gets in beside it, and the
+    // share would keep it out: 12.4 -> 15.4 us for 33 of 512).  Up to four
+    // entries are merged four at a time, in CTAs that need a third of the
+    // registers (33 of 512 in pieces of 128: 15.3 -> 12.4; 152 of 512: 29.2 ->
+    // 27.7; with eight entries sixteens are better: 12.9 -> 12.3).
+    const int per = ((int)cfg.gridDim.x + plan->n_ctas - 1) / plan->n_ctas;
+    cfg.dynamicSmemBytes = plan->n_narrow + plan->n_tile_ctas > plan->n_ctas ? (size_t)(kMergeSmem / per & ~1023) : 0;
+    if (plan->max_entries_per_request <= 4)
+        return (int)cudaLaunchKernelEx(&cfg, decode_merge_kernel<bf16, D, 4>, m, n_pairs);
+    return (int)cudaLaunchKernelEx(&cfg, decode_merge_kernel<bf16, D, 16>, m, n_pairs);
 }
 
 template int launch_decode_fp4<64>(const sgl_plan*, const void*, const void*, const void*, const int32_t*, int64_t,

@@ -91,6 +91,7 @@ __device__ __forceinline__ void stream_lookup(const FusedArgs& f, int gw, uint32
     const DecItem* const pieces = f.narrow;
     const int n_narrow = f.n_narrow;
     uint32_t* const sched = f.sched;
+    const bool dealt = n_narrow <= f.n_init;   // every piece was dealt at launch: the counter is not used
     const bool launch = gw >= 0 && gw < f.n_init;
     bool timed_out = false;
     int nlook = 0;
@@ -143,6 +144,7 @@ __device__ __forceinline__ void stream_lookup(const FusedArgs& f, int gw, uint32
             pb = ld_shared_s32(lrec + 24); nh = ld_shared_s32(lrec + 28);
             mem = lane < kDecPieceMembers ? ld_shared_s32(lrec + 32 + 4 * lane) : 0;
         } else {
+            if (dealt) break;
             int taken = 0;
             if (lane == 0) taken = (int)atomicAdd(sched, 1u);
             taken = __shfl_sync(0xffffffffu, taken, 0);
@@ -173,7 +175,7 @@ __device__ __forceinline__ void stream_lookup(const FusedArgs& f, int gw, uint32
     cp_async_wait<0>();
     // The last lookup warp to finish restores the counter for the next call
     // (every CTA has taken its last number by then).
-    if (lane == 0) {
+    if (lane == 0 && !dealt) {
         if (atomicAdd(sched + 1, 1u) + 1 == gridDim.x) {
             sched[0] = (uint32_t)f.n_init;
             sched[1] = 0u;

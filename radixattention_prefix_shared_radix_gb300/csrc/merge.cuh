@@ -9,7 +9,7 @@
 // which equals attention over the concatenated chunks ("SGLang 深度拆解"
 // (chenxutan.com/d/5669.html) §3.2 PagedDecode, split along the KV
 // sequence).  Every lane accumulates two or four columns of one query head;
-// the entries are taken in batches of 16 whose rows and LSEs are all in
+// the entries are taken in batches of 16 (U) whose rows and LSEs are all in
 // flight together, with the running maximum rescaling earlier batches
 // (online form of the same sum).
 // Partials are read with ld.global.cg: they were written by other SMs during
@@ -56,14 +56,13 @@ inline int merge_blocks(int n_pairs, int G) {
 // Columns col0 .. col0 + kCols - 1 of head j of pair idx = (request, KV
 // head), whose entries are ment[e0 .. e0+E): entry e's row for head j is
 // ment[e0 + e] + j.  `first` is ment[e0 + lane] for lane < min(E, 32),
-// already loaded by the caller.  Every entry row of a batch of 16 is
+// already loaded by the caller.  Every entry row of a batch of U is
 // requested before the batch's LSEs are used, so a batch costs one round
 // trip.
-template <typename OutT, int D>
+template <typename OutT, int D, int U>
 __device__ __noinline__ void merge_head(const MergeArgs& m, int idx, int j, int col0, int e0, int E, int lane,
                                         int first) {
     constexpr int VPL = MergeShape<D>::kVPL;
-    constexpr int U = 16;
     const int r = idx / m.Hkv, h = idx - r * m.Hkv;
     float M = -INFINITY, L = 0.f, acc[VPL];
 #pragma unroll
@@ -140,8 +139,8 @@ __device__ __noinline__ void merge_head(const MergeArgs& m, int idx, int j, int 
 // are plan tables (uploaded from the host before the launch before), so
 // they are read while the launch before is still running; only the partial
 // rows and LSEs, which it writes, are read after the dependency wait.
-template <typename OutT, int D>
-__global__ void __launch_bounds__(128, 4) decode_merge_kernel(const MergeArgs m, int n_pairs) {
+template <typename OutT, int D, int U = 16>
+__global__ void __launch_bounds__(128, U > 4 ? 4 : 12) decode_merge_kernel(const MergeArgs m, int n_pairs) {
     constexpr int SPLIT = MergeShape<D>::kSplit, COLS = MergeShape<D>::kCols;
     const int w = blockIdx.x * 4 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
     const int hw = w / SPLIT, sl = w - hw * SPLIT;
@@ -163,7 +162,7 @@ __global__ void __launch_bounds__(128, 4) decode_merge_kernel(const MergeArgs m,
         if (lane == 0 && sl == 0) m.lse[orow] = -INFINITY;
         return;
     }
-    merge_head<OutT, D>(m, idx, j, sl * COLS, e0, E, lane, first);
+    merge_head<OutT, D, U>(m, idx, j, sl * COLS, e0, E, lane, first);
 }
 
 }  // namespace sgl

@@ -272,45 +272,79 @@ int sgl_decode_plan(const sgl_attn_params* p, const int32_t* seq_lens, const sgl
     const int64_t step = p->dtype == SGL_DTYPE_BF16_FP4KV ? 32 : 16;   // positions per streaming step
     int64_t Pph = (int64_t)std::ceil((double)units_n / (double)std::max<int64_t>(1, 2 * n_cons));
     int64_t cap = 2048;                        // longest piece
+    int64_t tail = step;                       // a remainder below it joins the piece before
     if (fp4) {
-        // 4-bit streams: a piece costs a stream as much as 100 positions
-        // beyond its own (its query rows, its partial rows and their merge),
-        // and the two streams of an SM share what it reads and computes.
-        // Measured on 64 requests of 1 to 8192 tokens: pieces of 288, 416,
-        // 544 and 800 positions took 74, 68, 66 and 60 us, which
-        //   (positions of the fullest SM, dealt longest first) / 2 + 100 pieces / streams
-        // at 0.065 us a position gives within 6%.  The piece length with the
-        // smallest estimate around an even share is taken.
+        // 4-bit streams: of piece lengths around an even share of a stream and
+        // of one to eight steps, the one with the smallest estimate of
+        //   the longest piece alone on its SM, or the fullest SM's positions
+        //   (dealt longest first) + a cost per piece and SM + the merge
+        // is taken, and no cut at all where that leaves one piece per request
+        // and head (the streams write the results themselves then).  Measured
+        // at d = 128, in us: 0.0405 a position of a piece alone on its SM,
+        // 0.0322 with another; 0.6 a piece for an SM's first two, 1.9 for each
+        // after (0.7 without cuts); the merge 2.6, 0.6 per thousand rows and
+        // 0.1 per entry of a row after six.  It gives within 8%: 64 requests of
+        // 64 / 180 / 512 tokens whole 6.6 / 11.4 / 24.4, cut 10.5 / 12.9 / 16.4;
+        // 152 of 512 whole 25.1, cut 27.7; 33 of 1024 in pieces of 256 / 128
+        // 17.3 / 16.0; 64 of 1 to 8192 in pieces of 288 / 544 / 800 74 / 66 / 60.
         const int64_t sms_s = std::max<int64_t>(1, n_ctas - n_tile_ctas);
         const double share = (double)units_n / (double)(2 * sms_s);
+        const double wide_d = p->head_dim == 64 ? 0.5 : 1.0;
+        const double merge_us = 2.6 + 0.0006 * (double)B * (double)p->num_qo_heads;
+        const int32_t HP = head_block(1);
+        const bool whole = max_wide == 0 && (int64_t)units.size() == (int64_t)B * ((Hkv + HP - 1) / HP);
+        std::vector<int64_t> tries;                            // position-heads per piece
+        if (whole) tries.push_back(INT32_MAX);
+        for (const double by : {1.0, 1.04, 1.08, 1.13, 1.2, 1.3, 1.5})
+            tries.push_back(std::max<int64_t>(1, (int64_t)std::ceil(share * by)));
+        for (const int64_t n : {1, 2, 3, 4, 6, 8})
+            if ((double)(n * step * HP) > 1.5 * share) tries.push_back(n * step * HP);
         double best = 1e300;
-        std::vector<int64_t> len, load((size_t)sms_s);
-        for (const double by : {1.0, 1.04, 1.08, 1.13, 1.2, 1.3, 1.5}) {
-            const int64_t pph = std::max<int64_t>(1, (int64_t)std::ceil(share * by));
-            len.clear();
-            for (const Unit& u : units) {
-                const int64_t P = std::max<int64_t>(step, ((pph + u.nh - 1) / u.nh + step - 1) / step * step);
-                for (int64_t left = u.e - u.b; left > 0;) {
-                    const int64_t take = left - P < step ? left : P;
-                    len.push_back(take * u.nh);
-                    left -= take;
+        int64_t last_P = 0;
+        std::vector<int64_t> load((size_t)sms_s);
+        std::vector<std::pair<int64_t, int64_t>> len;          // (position-heads, positions) of each piece
+        for (const int64_t pph : tries) {
+            auto piece = [&](int32_t nh) { return std::max<int64_t>(step, ((pph + nh - 1) / nh + step - 1) / step * step); };
+            if (piece(HP) == last_P) continue;
+            last_P = piece(HP);
+            for (const int64_t least_tail : {step, (int64_t)1}) {
+                len.clear();
+                int64_t longest = 0, most = 0;
+                for (const Unit& u : units) {
+                    const int64_t P = piece(u.nh), before = (int64_t)len.size();
+                    for (int64_t left = u.e - u.b; left > 0;) {
+                        const int64_t take = left - P < least_tail ? left : P;
+                        const int64_t pos = (take + step - 1) / step * step;
+                        len.push_back({pos * u.nh, pos});
+                        longest = std::max(longest, pos);
+                        left -= take;
+                    }
+                    most = std::max(most, (int64_t)len.size() - before);
                 }
+                std::sort(len.begin(), len.end(), std::greater<std::pair<int64_t, int64_t>>());
+                std::fill(load.begin(), load.end(), 0);
+                auto least = std::greater<int64_t>();          // (a heap with the emptiest SM on top)
+                for (const auto& x : len) {
+                    std::pop_heap(load.begin(), load.end(), least);
+                    load.back() += x.first;
+                    std::push_heap(load.begin(), load.end(), least);
+                }
+                const double fullest = (double)*std::max_element(load.begin(), load.end()) / sgl::kDecHeadBlock;
+                const double each = (double)len.size() / (double)sms_s;
+                double cost = wide_d * std::max(0.0405 * (double)longest, 0.0322 * fullest);
+                if (pph == INT32_MAX)
+                    cost += 0.7 * each;
+                else
+                    cost += 0.6 * std::min(each, 2.0) + 1.9 * std::max(each - 2.0, 0.0) + merge_us +
+                            0.1 * (double)std::max<int64_t>(0, most - 6);
+                if (cost < best) {
+                    best = cost;
+                    Pph = pph;
+                    tail = least_tail;
+                }
+                if (pph == INT32_MAX || (int64_t)len.size() > sms_s) break;   // (short tails pay where SMs are free)
             }
-            std::sort(len.begin(), len.end(), std::greater<int64_t>());
-            std::fill(load.begin(), load.end(), 0);
-            auto least = std::greater<int64_t>();              // (a heap with the emptiest SM on top)
-            for (const int64_t x : len) {
-                std::pop_heap(load.begin(), load.end(), least);
-                load.back() += x;
-                std::push_heap(load.begin(), load.end(), least);
-            }
-            const double cost = 0.5 * (double)*std::max_element(load.begin(), load.end()) +
-                                100.0 * sgl::kDecHeadBlock * (double)len.size() / (double)(2 * sms_s);
-            if (cost < best) {
-                best = cost;
-                Pph = pph;
-            }
-            if ((int64_t)len.size() > 8 * sms_s) break;        // many short requests: the cut hardly matters
+            if (pph != INT32_MAX && (int64_t)len.size() > 8 * sms_s) break;   // many short requests: the cut hardly matters
         }
         cap = INT32_MAX / 2;
     }
@@ -320,7 +354,7 @@ int sgl_decode_plan(const sgl_attn_params* p, const int32_t* seq_lens, const sgl
         Pmax = std::min<int64_t>(cap, std::max<int64_t>(32, (Pmax + step - 1) / step * step));
         for (int64_t pos = u.b; pos < u.e || (pos == u.b && u.tail);) {
             int64_t take = std::min<int64_t>(u.e - pos, Pmax);
-            if (u.e - pos - take < step) take = u.e - pos;   // no tail piece under one step
+            if (u.e - pos - take < tail) take = u.e - pos;
             const bool last = pos + take == u.e;
             cut.push_back({(int32_t)take,
                            {u.rep_row, (int32_t)pos, last && u.tail ? sgl::kDecToSeqEnd : (int32_t)(pos + take), u.kvh,
@@ -337,6 +371,10 @@ int sgl_decode_plan(const sgl_attn_params* p, const int32_t* seq_lens, const sgl
     narrow.reserve(cut.size());
     for (const auto& c : cut) narrow.push_back(c.second);
     const int64_t n_init = std::min<int64_t>((int64_t)narrow.size(), n_cons);
+    // 4-bit: an SM's second streaming CTA is about that many CTAs after its
+    // first, so the pieces dealt to the first CTAs are put shortest first, and
+    // the next longest pieces come to the shortest.
+    if (fp4) std::reverse(narrow.begin(), narrow.begin() + std::min<int64_t>(n_init, n_cons / 2));
 
     // wide items round-robin over the tile CTAs (the first n_tile_ctas)
     std::vector<std::vector<sgl::DecItem>> cta_items((size_t)n_ctas);

@@ -204,6 +204,51 @@ def test_long_context_and_growing_scores():
     b.check(out)
 
 
+@pytest.mark.parametrize("hq,hkv,d", [(32, 8, 128), (64, 8, 64), (8, 1, 128), (12, 12, 64)])
+@pytest.mark.parametrize("n", [1, 170, 330])
+def test_requests_of_one_piece(hq, hkv, d, n):
+    """Short requests are not cut: the streams write their results, empty requests' among them, without a merge; with
+    lengths that grow past the planned ones, in a graph, over poisoned partial rows."""
+    rng = np.random.default_rng(n + d)
+    lens = rng.integers(1, 40, n)
+    lens[1::7] = 0
+    b = Batch(_own(lens), hq, hkv, d, seed=n, extra=40)
+    plan = b.plan()
+    assert sgl.sgl_plan_info(plan)["num_merge_entries"] == b.B * hkv
+    ws = torch.full((plan.workspace_bytes,), 0xFF, dtype=torch.uint8, device="cuda")
+    ws[:256] = 0
+    sgl.sgl_plan_upload(plan, ws)
+    at = 0
+    for r in range(n):                       # slots for the tokens to come
+        grow = int(rng.integers(0, 40))
+        take = b.free[at:at + grow]
+        at += len(take)
+        b.table[r, lens[r]:lens[r] + len(take)] = take
+        lens[r] += len(take)
+    new = b.table[b.table >= 0]
+    for pool, s, i in ((b.kp, KS, 3), (b.vp, VS, 4)):
+        pool[new] = _pool(b.slots, hkv, d, s, n + i)[new]
+    kp, vp, t, dl = b.device()
+    q = b.q.cuda()
+    o = torch.full((n, hq, d), 7.0, dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((n, hq), 7.0, device="cuda")
+    sgl.sgl_decode_attn(q, kp, vp, t, dl, plan, o, lse, ws)
+    sgl.sgl_check(ws)
+    rows = rng.permutation(n)[:16]
+    b.check((o.double().cpu().numpy(), lse.double().cpu().numpy()), rows)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        for _ in range(2):
+            sgl.sgl_decode_attn(q, kp, vp, t, dl, plan, o, lse, ws)
+    o.fill_(7.0)
+    lse.fill_(7.0)
+    b.lens[:] = lens
+    dl.copy_(torch.from_numpy(b.lens))
+    g.replay()
+    sgl.sgl_check(ws)
+    b.check((o.double().cpu().numpy(), lse.double().cpu().numpy()), rows)
+
+
 def test_slots_outside_the_pool_are_skipped_and_reported():
     b = Batch(_own([100, 77, 5]), 32, 8, 128, seed=8)
     bad = b.table.copy()
