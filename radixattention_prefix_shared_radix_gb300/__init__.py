@@ -735,6 +735,8 @@ def sgl_rope(rope, q, k, positions, q_out=None, k_out=None, stream=None):
     n, d, dev = some.shape[0], rope.head_dim, T._C._cuda_getDevice()
     pq = pqo = pk = pko = None
     hq = hk = sq = sk = sqo = sko = 0
+    if (q is None and q_out is not None) or (k is None and k_out is not None):
+        raise ValueError("an output is given without its input")
     if q is not None:
         pq, sq = pqo, sqo = _rows(q, "q", None, d, dt, n, dev)
         hq = q.shape[1]
@@ -771,6 +773,8 @@ def sgl_kv_append(rope, params, q, k_new, v_new, k_pool, v_pool, req_to_token, l
         pqo, sqo = _rows(q_out, "q_out", params.num_qo_heads, d, dt, n, dev)
     B = (params.batch,)
     rows = req_to_token.shape
+    if len(rows) != 2 or rows[0] < B[0]:
+        raise ValueError("req_to_token must have a row per request")
     st = _lib().sgl_kv_append(None if rope is None else rope.handle, ctypes.byref(params), pq, sq, pk, sk, pv, sv,
                               _flat(k_pool, "k_pool", dev), _flat(v_pool, "v_pool", dev),
                               _flat(req_to_token, "req_to_token", dev, T.int32), rows[1],
@@ -795,6 +799,8 @@ def sgl_mla_kv_append(rope, params, q, kv_new, kv_pool, req_to_token, lens, exte
         pqo, sqo = _rows(q_out, "q_out", params.num_qo_heads, d, dt, n, dev)
     B = (params.batch,)
     rows = req_to_token.shape
+    if len(rows) != 2 or rows[0] < B[0]:
+        raise ValueError("req_to_token must have a row per request")
     st = _lib().sgl_mla_kv_append(None if rope is None else rope.handle, ctypes.byref(params), pq, sq, pk, sk,
                                   _flat(kv_pool, "kv_pool", dev), _flat(req_to_token, "req_to_token", dev, T.int32),
                                   rows[1], _flat(lens, "lens", dev, T.int32, B),

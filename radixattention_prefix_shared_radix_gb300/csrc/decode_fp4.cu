@@ -571,7 +571,7 @@ __global__ void __launch_bounds__(kStreamThreads, kStreamCtas)
         mbar_fence_init();
     }
     // (before the dependency wait: the first copy finds the descriptors in the cache)
-    if (warp == kProducer && lane < 4) {
+    if (warp == kProducer && lane < 4 && f.t.num_slots > 0) {
         const CUtensorMap* m = lane == 0 ? &k8 : lane == 1 ? &v8 : lane == 2 ? &k4 : &v4;
         asm volatile("prefetch.tensormap [%0];\n" ::"l"(m) : "memory");
     }

@@ -608,9 +608,8 @@ int sgl_rope_create(const sgl_rope_params* p, sgl_rope_table** out) {
     const int n = p->rot_dim;
     if (p->head_dim <= 0 || n <= 0 || p->rot_offset < 0 || (int64_t)p->rot_offset + n > p->head_dim)
         return SGL_ERR_INVALID_ARG;
-    if (!(p->theta > 1.0) || !std::isfinite(p->theta) || !(p->attention_factor >= 0.0) ||
-        !std::isfinite(p->attention_factor))
-        return SGL_ERR_INVALID_ARG;
+    if (!(p->theta > 1.0) || !std::isfinite(p->theta)) return SGL_ERR_INVALID_ARG;
+    if (!(p->attention_factor >= 0.0) || !std::isfinite((float)p->attention_factor)) return SGL_ERR_INVALID_ARG;
     if (p->layout != SGL_ROPE_HALF && p->layout != SGL_ROPE_PAIRS) return SGL_ERR_UNSUPPORTED;
     if (p->head_dim % 16 || p->head_dim > 1024 || n % 16 || n > SGL_ROPE_MAX_DIM || p->rot_offset % 16)
         return SGL_ERR_UNSUPPORTED;

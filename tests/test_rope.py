@@ -83,7 +83,7 @@ def _status(fn, *args):
     (dict(head_dim=64, scaling=5), -3), (dict(head_dim=64, scaling=1, factor=0.5), -1),
     (dict(head_dim=64, scaling=3, factor=4.0, low=1.0, high=32.0), -1),
     (dict(head_dim=64, scaling=4, factor=4.0, original_positions=4096, low=4.0, high=1.0), -1),
-    (dict(head_dim=64, attention_factor=-1.0), -1),
+    (dict(head_dim=64, attention_factor=-1.0), -1), (dict(head_dim=64, attention_factor=1e39), -1),
 ])
 def test_rope_create_refuses(kw, status):
     with pytest.raises(sgl.SglError) as e:
@@ -210,9 +210,24 @@ def test_python_arguments_are_checked():
     for bad in (lambda: sgl.sgl_rope(r, q.cpu(), None, pos), lambda: sgl.sgl_rope(r, q.half(), None, pos),
                 lambda: sgl.sgl_rope(r, q, None, pos.long()), lambda: sgl.sgl_rope(r, q, None, pos[:3]),
                 lambda: sgl.sgl_rope(r, q[..., :32], None, pos), lambda: sgl.sgl_rope(r, q.transpose(0, 1), None, pos),
-                lambda: sgl.sgl_rope(r, q, q.float(), pos), lambda: sgl.sgl_rope(r, None, None, pos)):
+                lambda: sgl.sgl_rope(r, q, q.float(), pos), lambda: sgl.sgl_rope(r, None, None, pos),
+                lambda: sgl.sgl_rope(r, q, None, pos, k_out=q), lambda: sgl.sgl_rope(r, None, q, pos, q_out=q)):
         with pytest.raises((TypeError, ValueError)):
             bad()
+    p = sgl.make_params(sgl.SGL_DTYPE_BF16, 4, 2, 2, 64, 16)
+    pool = torch.zeros(16, 2, 64, dtype=torch.bfloat16, device="cuda")
+    table = torch.zeros(4, 8, dtype=torch.int32, device="cuda")
+    ws = torch.zeros(256, dtype=torch.uint8, device="cuda")
+    good = dict(rope=r, params=p, q=None, k_new=q, v_new=q, k_pool=pool, v_pool=pool, req_to_token=table, lens=pos,
+                extend_lens=None, q_out=None, workspace=ws)
+    for bad in (dict(req_to_token=table[:3]), dict(req_to_token=table[0]), dict(req_to_token=table.long()),
+                dict(lens=pos[:3]), dict(k_new=q[:3]), dict(v_new=q.float()), dict(k_pool=pool.cpu()),
+                dict(extend_lens=pos.long()), dict(q=q[:, :1], q_out=q), dict(workspace=ws.cpu())):
+        with pytest.raises((TypeError, ValueError)):
+            sgl.sgl_kv_append(**dict(good, **bad))
+    sgl.sgl_kv_append(**good)                     # (lengths of zero: nothing to append)
+    sgl.sgl_check(ws)
+    assert not pool.any()
 
 
 # ------------------------------------------------------------------ append (GPU)
