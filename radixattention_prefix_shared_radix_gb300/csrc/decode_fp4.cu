@@ -91,6 +91,7 @@ constexpr int kDescFlags = 0, kDescMask = 4, kDescPb = 8, kDescRows = 12, kDescN
 struct Fp4Args {
     FusedArgs f;
     int lg;                // log2 of the query heads per KV head
+    float sc;              // softmax scale in base 2, times the K scale
     int box8, box4;        // bytes of a piece's row: blocks of up to 8 heads, of up to 4 (more than 8 query rows)
     int after_tiles;       // launched behind the tiles
     bf16* o;               // every request is one piece per head: results go here (and to lse), without a merge;
@@ -241,14 +242,14 @@ __device__ __forceinline__ int pi16(int m) { return m ^ ((m >> 1) & 1); }
 // row numbers, what a step needs five addresses.)
 template <int D>
 __device__ __forceinline__ void fp4_consumer(const Fp4Args& p, int c, uint32_t ring, uint32_t desc, uint32_t full,
-                                          uint32_t empty, int lane) {
+                                          uint32_t empty, uint32_t lrec, int lane) {
     using Lay = Fp4Layout<D>;
     constexpr int NS = Lay::NSF;
     constexpr int MT = D / 16;
     constexpr int KW = D / 32;                  // words of K codes per row and lane
     constexpr int VW = D / 64;                  // words of V codes per row and lane
     const int g = lane >> 2, t = lane & 3;
-    const float sc = p.f.t.scale_log2 * p.f.t.k_scale;
+    const float sc = p.sc;
 
     uint32_t q[D / 8];
     float o[MT][4];
@@ -289,6 +290,65 @@ __device__ __forceinline__ void fp4_consumer(const Fp4Args& p, int c, uint32_t r
         }
     };
 
+    // a piece's fields and query rows: rows of nh heads from kvh on, partial rows
+    // from pb on, member requests at mem in shared memory
+    auto start_item = [&](int rows, int nh, int kvh, int pb, uint32_t mem) {
+        const int wph = rows > 8 ? 2 : 1;   // consumer warps per head
+        const int hw = c / wph, r0 = (c - hw * wph) * 8;
+        active = hw < nh && r0 < rows;
+        if (active) {
+            // row r of a head: member r / G, query head r % G
+            const int r = r0 + 2 * t, G1 = (1 << p.lg) - 1;
+            auto prow = [&](int x) {
+                if (x >= rows) return -1;
+                return (p.o ? ld_shared_s32(mem + 4 * (x >> p.lg)) * p.f.t.Hq + ((kvh + hw) << p.lg)
+                            : pb + (((x >> p.lg) * nh + hw) << p.lg)) + (x & G1);
+            };
+            pr0 = prow(r);
+            pr1 = prow(r + 1);
+            // this lane's first rows of a 16-position group: K row g (the
+            // other, g + 8, lies two quads on), V row 2t (2t + 1 lies dv
+            // on, 2t + 8 and 2t + 9 two quads on); the head's codes and
+            // scales in them
+            const uint32_t box = (uint32_t)(rows > 8 ? p.box4 : p.box8);
+            const uint32_t coff = (uint32_t)fp4_code_off(hw, D), soff = (uint32_t)fp4_scale_off(hw, p.f.t.Hkv - kvh, D);
+            auto roff = [&](int mrow) {
+                const int x = pi16(mrow);
+                return (uint32_t)((x >> 2) * Lay::QP) + (uint32_t)(x & 3) * box;
+            };
+            ka = roff(g) + coff + (D / 8) * t;
+            ks = roff(g) + soff + (D / 64) * t;
+            va = kQuads * Lay::QP + roff(2 * t) + coff + (D / 16) * g;
+            vs = kQuads * Lay::QP + roff(2 * t) + soff + g * (D / 8) / 16;
+            dv = roff(2 * t + 1) - roff(2 * t);
+            // Q^T: row r0 + g, the lane's run of d / 4 elements in order, as f16
+            const int rq = r0 + g;
+            const bool ok = rq < rows;
+            const int mq = ok ? ld_shared_s32(mem + 4 * (rq >> p.lg)) : 0;
+            const uint4* src = reinterpret_cast<const uint4*>(
+                p.f.t.q + ((int64_t)mq * p.f.t.Hq + ((kvh + hw) << p.lg) + (rq & G1)) * D + (D / 4) * t);
+            uint32_t bad = 0u;
+#pragma unroll
+            for (int j = 0; j < D / 32; ++j) {
+                const uint4 v = ok ? __ldg(src + j) : make_uint4(0u, 0u, 0u, 0u);
+                q[4 * j] = bf16x2_to_f16x2_chk(v.x, bad);
+                q[4 * j + 1] = bf16x2_to_f16x2_chk(v.y, bad);
+                q[4 * j + 2] = bf16x2_to_f16x2_chk(v.z, bad);
+                q[4 * j + 3] = bf16x2_to_f16x2_chk(v.w, bad);
+            }
+            if (bad) atomicOr(p.f.t.err, kErrQRange);
+        }
+#pragma unroll
+        for (int i = 0; i < MT; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
+        m0 = m1 = -INFINITY;
+        l0 = l1 = 0.f;
+    };
+    // the launch piece's are fetched while its first data is on the way
+    const bool launch = (int)blockIdx.x < p.f.n_init;
+    if (launch)
+        start_item(ld_shared_s32(lrec + 20) << p.lg, ld_shared_s32(lrec + 28), ld_shared_s32(lrec + 12),
+                   ld_shared_s32(lrec + 24), lrec + 32);
+
     int st = 0;
     uint32_t ph = 0u;
     for (;;) {
@@ -302,58 +362,10 @@ __device__ __forceinline__ void fp4_consumer(const Fp4Args& p, int c, uint32_t r
         if (flags & kEnd) break;
         if (flags & kFirst) {
             if (have && active) finish_item();
+            if (have || !launch)
+                start_item(ld_shared_s32(db + kDescRows), ld_shared_s32(db + kDescNh), ld_shared_s32(db + kDescKvh),
+                           ld_shared_s32(db + kDescPb), db + kDescMem);
             have = true;
-            const int rows = ld_shared_s32(db + kDescRows), nh = ld_shared_s32(db + kDescNh),
-                      kvh = ld_shared_s32(db + kDescKvh);
-            const int wph = rows > 8 ? 2 : 1;   // consumer warps per head
-            const int hw = c / wph, r0 = (c - hw * wph) * 8;
-            active = hw < nh && r0 < rows;
-            if (active) {
-                // row r of a head: member r / G, query head r % G
-                const int pb = ld_shared_s32(db + kDescPb), r = r0 + 2 * t, G1 = (1 << p.lg) - 1;
-                auto prow = [&](int x) {
-                    if (x >= rows) return -1;
-                    return (p.o ? ld_shared_s32(db + kDescMem + 4 * (x >> p.lg)) * p.f.t.Hq + ((kvh + hw) << p.lg)
-                                : pb + (((x >> p.lg) * nh + hw) << p.lg)) + (x & G1);
-                };
-                pr0 = prow(r);
-                pr1 = prow(r + 1);
-                // this lane's first rows of a 16-position group: K row g (the
-                // other, g + 8, lies two quads on), V row 2t (2t + 1 lies dv
-                // on, 2t + 8 and 2t + 9 two quads on); the head's codes and
-                // scales in them
-                const uint32_t box = (uint32_t)(rows > 8 ? p.box4 : p.box8);
-                const uint32_t coff = (uint32_t)fp4_code_off(hw, D), soff = (uint32_t)fp4_scale_off(hw, p.f.t.Hkv - kvh, D);
-                auto roff = [&](int mrow) {
-                    const int x = pi16(mrow);
-                    return (uint32_t)((x >> 2) * Lay::QP) + (uint32_t)(x & 3) * box;
-                };
-                ka = roff(g) + coff + (D / 8) * t;
-                ks = roff(g) + soff + (D / 64) * t;
-                va = kQuads * Lay::QP + roff(2 * t) + coff + (D / 16) * g;
-                vs = kQuads * Lay::QP + roff(2 * t) + soff + g * (D / 8) / 16;
-                dv = roff(2 * t + 1) - roff(2 * t);
-                // Q^T: row r0 + g, the lane's run of d / 4 elements in order, as f16
-                const int rq = r0 + g;
-                const bool ok = rq < rows;
-                const int mq = ok ? ld_shared_s32(db + kDescMem + 4 * (rq >> p.lg)) : 0;
-                const uint4* src = reinterpret_cast<const uint4*>(
-                    p.f.t.q + ((int64_t)mq * p.f.t.Hq + ((kvh + hw) << p.lg) + (rq & G1)) * D + (D / 4) * t);
-                uint32_t bad = 0u;
-#pragma unroll
-                for (int j = 0; j < D / 32; ++j) {
-                    const uint4 v = ok ? __ldg(src + j) : make_uint4(0u, 0u, 0u, 0u);
-                    q[4 * j] = bf16x2_to_f16x2_chk(v.x, bad);
-                    q[4 * j + 1] = bf16x2_to_f16x2_chk(v.y, bad);
-                    q[4 * j + 2] = bf16x2_to_f16x2_chk(v.z, bad);
-                    q[4 * j + 3] = bf16x2_to_f16x2_chk(v.w, bad);
-                }
-                if (bad) atomicOr(p.f.t.err, kErrQRange);
-            }
-#pragma unroll
-            for (int i = 0; i < MT; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
-            m0 = m1 = -INFINITY;
-            l0 = l1 = 0.f;
         }
         const uint32_t sb = ring + st * Lay::STAGE;
         const uint32_t eb = empty + 8 * st;
@@ -557,7 +569,8 @@ __global__ void __launch_bounds__(kStreamThreads, kStreamCtas)
     const FusedArgs& f = p.f;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     constexpr int NSF = Lay::NSF;
-    const uint32_t full = smem_u32(sm + Lay::OFF_BAR), empty = full + 8 * NSF;
+    const uint32_t ring = smem_u32(sm);            // (addresses: one register and constants)
+    const uint32_t full = ring + Lay::OFF_BAR, empty = full + 8 * NSF;
     const uint32_t sfull = empty + 8 * NSF, sfree = sfull + 8 * kSQ;
     if (tid == 0) {
         for (int s = 0; s < NSF; ++s) {
@@ -578,7 +591,7 @@ __global__ void __launch_bounds__(kStreamThreads, kStreamCtas)
     // Until the dependency wait only shared memory and the plan tables are
     // touched (see decode_fused.cu): the launch piece's record and members
     const int gw = (int)blockIdx.x;
-    const uint32_t lrec = smem_u32(sm + Lay::OFF_LREC);
+    const uint32_t lrec = ring + Lay::OFF_LREC;
     if (warp == kLookup && gw < f.n_init) {
         const int4* rp = reinterpret_cast<const int4*>(f.narrow + gw);
         const int4 x = __ldg(rp), y = __ldg(rp + 1);
@@ -596,15 +609,13 @@ __global__ void __launch_bounds__(kStreamThreads, kStreamCtas)
     // waits for this grid, comes after both.
     if (!p.after_tiles) grid_dep_wait();
     grid_dep_launch();
-    const uint32_t ring = smem_u32(sm);
-    const uint32_t desc = smem_u32(sm + Lay::OFF_DESC);
-    const uint32_t sring = smem_u32(sm + Lay::OFF_SLOT);
+    const uint32_t desc = ring + Lay::OFF_DESC, sring = ring + Lay::OFF_SLOT;
     if (warp == kLookup)
         stream_lookup<kNP>(p.f, gw, lrec, sring, sfull, sfree, lane);   // up to 8 steps ahead of the copies
     else if (warp == kProducer)
         fp4_producer<D>(p, &k8, &v8, &k4, &v4, ring, sring, desc, full, empty, sfull, sfree, lane);
     else
-        fp4_consumer<D>(p, warp - kFirstConsumer, ring, desc, full, empty, lane);
+        fp4_consumer<D>(p, warp - kFirstConsumer, ring, desc, full, empty, lrec, lane);
     if (p.after_tiles) grid_dep_wait();
 }
 
@@ -662,6 +673,7 @@ int launch_decode_fp4(const sgl_plan* plan, const void* q, const void* kp, const
     a.num_slots = p.num_slots;
     a.scale_log2 = scale_log2;
     a.k_scale = p.k_scale;
+    x.sc = scale_log2 * p.k_scale;
     a.v_scale = p.v_scale;
     a.row_bytes = row;
     f.wptr = reinterpret_cast<const int32_t*>(ws + plan->off_wptr);
