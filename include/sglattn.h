@@ -524,9 +524,10 @@ int sgl_sim_run(sgl_tree* tree, const sgl_sim_config* cfg, int32_t n, const sgl_
  * Otherwise as sgl_extend_attn, whose result this call equals after the
  * same rows have been written: new token i of request r attends to the
  * cached positions 0..prefix_lens[r]-1 (read from the pool) and to new
- * tokens 0..i (read from k_new / v_new directly in the bf16 path; the fp32
- * and FP8-pool paths write the pool first and read it, so with an FP8 pool
- * the new tokens are seen as their stored E4M3 values).  An out-of-pool slot is not
+ * tokens 0..i (read from k_new / v_new directly in the bf16 path; the fp32,
+ * FP8-pool and 4-bit-pool paths write the pool first and read it, so with an
+ * FP8 or 4-bit pool the new tokens are seen as their stored values; a 4-bit
+ * pool takes at most 2^24 new rows a call).  An out-of-pool slot is not
  * written and sets SGL_ERR_BOUNDS for sgl_check.  Repeated calls over the
  * chunks of a long prompt (prefix_lens = tokens already cached) are a
  * chunked prefill.

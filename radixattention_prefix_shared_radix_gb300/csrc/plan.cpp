@@ -259,9 +259,9 @@ int sgl_decode_plan(const sgl_attn_params* p, const int32_t* seq_lens, const sgl
 
     // Narrow units are cut into pieces of at most Pmax positions (about half
     // an even share of a stream, so that the run-time counter can balance
-    // the tail; a cut makes one more partial to merge), no piece shorter than
-    // one step (16 positions; 32 of a 4-bit pool) unless its unit is, ordered
-    // longest first.  Each streaming CTA starts on its own piece; the rest
+    // the tail; a cut makes one more partial to merge; 4-bit pools: by an
+    // estimate, below), no piece shorter than one step (16 positions; 32 of a
+    // 4-bit pool) unless its unit or its remainder is, ordered longest first.  Each streaming CTA starts on its own piece; the rest
     // (and all work of tile CTAs' streams, once their tiles are done) are
     // handed out at run time from a counter, so SMs that stream faster take
     // more.
