@@ -249,6 +249,50 @@ def test_requests_of_one_piece(hq, hkv, d, n):
     b.check((o.double().cpu().numpy(), lse.double().cpu().numpy()), rows)
 
 
+def test_offsets_past_32_bits():
+    """Slots whose rows lie more than 2^31 bytes into the pools give what the same rows give in small pools, bit for
+    bit: streams, tiles, extend and append."""
+    hq, hkv, d = 32, 8, 128
+    b = Batch(_star(20, 200, 1, 40), hq, hkv, d, seed=21)
+    far = 2 ** 31 // sgl.sgl_fp4_row_bytes(hkv, d) + 1000
+    rng = np.random.default_rng(22)
+    pre = b.lens // 2
+    ext = b.lens - pre
+    n = int(ext.sum())
+    q = torch.from_numpy(rng.standard_normal((n, hq, d)).astype(np.float32)).bfloat16().cuda()
+    new = [torch.from_numpy(rng.standard_normal((b.B, hkv, d)).astype(np.float32)).bfloat16().cuda() for _ in "kv"]
+    got = []
+    for shift in (0, far):
+        slots = b.slots + shift
+        pools = []
+        for x in (b.kp, b.vp):
+            p = torch.zeros(slots, x.shape[1], dtype=torch.uint8, device="cuda")
+            p[shift:] = torch.from_numpy(x).cuda()
+            pools.append(p)
+        table = torch.from_numpy(b.table + shift * (b.table >= 0)).int().cuda()
+        lens, pd, ed = (torch.from_numpy(x.astype(np.int32)).cuda() for x in (b.lens, pre, ext))
+        g = sgl.sgl_groups_create()
+        sgl.sgl_groups_from_table(b.table, b.lens, g)
+        mk = lambda **kw: sgl.make_params(sgl.SGL_DTYPE_BF16_FP4KV, b.B, hq, hkv, d, slots, k_scale=KS, v_scale=VS, **kw)  # noqa: E731
+        plan = sgl.sgl_decode_plan(mk(), b.lens, sgl.sgl_groups_view(g))
+        assert sgl.sgl_plan_info(plan)["num_wide_items"] > 0
+        ws = torch.zeros(plan.workspace_bytes, dtype=torch.uint8, device="cuda")
+        sgl.sgl_plan_upload(plan, ws)
+        o, lse = torch.zeros(b.B, hq, d, dtype=torch.bfloat16, device="cuda"), torch.zeros(b.B, hq, device="cuda")
+        sgl.sgl_decode_attn(b.q.cuda(), *pools, table, lens, plan, o, lse, ws)
+        p = mk(host_prefix_lens=pre, host_extend_lens=ext)
+        oe, le = torch.zeros_like(q), torch.zeros(n, hq, device="cuda")
+        sgl.sgl_extend_attn(q, *pools, table, pd, ed, p, oe, le, ws)
+        sgl.sgl_kv_append(None, mk(), None, *new, *pools, table, lens, None, None, ws)
+        sgl.sgl_check(ws)
+        got.append([o, lse, oe, le] + [x[shift:].clone() for x in pools])
+        sgl.sgl_groups_destroy(g)
+        del pools
+    for x, y in zip(*got):
+        assert torch.equal(x, y)
+    b.check((got[0][0].double().cpu().numpy(), got[0][1].double().cpu().numpy()))
+
+
 def test_slots_outside_the_pool_are_skipped_and_reported():
     b = Batch(_own([100, 77, 5]), 32, 8, 128, seed=8)
     bad = b.table.copy()
