@@ -686,22 +686,27 @@ def sgl_rope_create(head_dim, rot_dim=0, rot_offset=0, layout=SGL_ROPE_HALF, sca
 
 
 def _rows(t, what, heads, dim, dtype, n, dev):
-    """A tensor [n, heads, dim] on device `dev` whose heads are contiguous in each row: (address, row stride).
-    heads and n None: any."""
-    if isinstance(t, _T.Tensor) and t.dim() == 3:
+    """A tensor [n, heads, dim] on device `dev` whose heads are contiguous in each row: (address, row stride, rows,
+    heads).  heads and n None: any."""
+    try:
         r, h, w = t.shape
         a, b, c = t.stride()
         if (w == dim and (h == heads or heads is None) and (r == n or n is None) and t.dtype is dtype and c == 1
                 and (b == dim or h <= 1) and t.get_device() == dev):
-            return t.data_ptr(), (a if r > 1 else h * dim)
+            return t.data_ptr(), (a if r > 1 else h * dim), r, h
+    except (AttributeError, TypeError, ValueError):
+        pass          # not a tensor, or not of three dimensions
     _refuse(t, what, dtype, (n or "rows", heads or "heads", dim), dev, "hold each row's heads contiguously")
 
 
 def _flat(t, what, dev, dtype=None, shape=None):
     """The address of a contiguous tensor on device `dev` (of a dtype and shape, where given)."""
-    if (isinstance(t, _T.Tensor) and t.get_device() == dev and (dtype is None or t.dtype is dtype)
-            and (shape is None or t.shape == shape) and t.is_contiguous()):
-        return t.data_ptr()
+    try:
+        if (t.get_device() == dev and (dtype is None or t.dtype is dtype) and (shape is None or t.shape == shape)
+                and t.is_contiguous()):
+            return t.data_ptr()
+    except (AttributeError, TypeError):
+        pass          # not a tensor
     _refuse(t, what, dtype, shape, dev, "be contiguous")
 
 
@@ -732,21 +737,22 @@ def sgl_rope(rope, q, k, positions, q_out=None, k_out=None, stream=None):
         kind = SGL_DTYPE_F32
     else:
         raise TypeError("q and k must be float32 or bfloat16")
-    n, d, dev = some.shape[0], rope.head_dim, T._C._cuda_getDevice()
+    d, dev = rope.head_dim, T._C._cuda_getDevice()
+    n = None
     pq = pqo = pk = pko = None
     hq = hk = sq = sk = sqo = sko = 0
     if (q is None and q_out is not None) or (k is None and k_out is not None):
         raise ValueError("an output is given without its input")
     if q is not None:
-        pq, sq = pqo, sqo = _rows(q, "q", None, d, dt, n, dev)
-        hq = q.shape[1]
+        pq, sq, n, hq = _rows(q, "q", None, d, dt, None, dev)
+        pqo, sqo = pq, sq
         if q_out is not None:
-            pqo, sqo = _rows(q_out, "q_out", hq, d, dt, n, dev)
+            pqo, sqo, _, _ = _rows(q_out, "q_out", hq, d, dt, n, dev)
     if k is not None:
-        pk, sk = pko, sko = _rows(k, "k", None, d, dt, n, dev)
-        hk = k.shape[1]
+        pk, sk, n, hk = _rows(k, "k", None, d, dt, n, dev)
+        pko, sko = pk, sk
         if k_out is not None:
-            pko, sko = _rows(k_out, "k_out", hk, d, dt, n, dev)
+            pko, sko, _, _ = _rows(k_out, "k_out", hk, d, dt, n, dev)
     st = _lib().sgl_rope(rope.handle, kind, pq, sq, hq, pk, sk, hk, _flat(positions, "positions", dev, T.int32, (n,)), n,
                          pqo, sqo, pko, sko, _stream(stream))
     if st:
@@ -762,15 +768,14 @@ def sgl_kv_append(rope, params, q, k_new, v_new, k_pool, v_pool, req_to_token, l
     T = _T or _torch()
     dt = T.float32 if params.dtype == SGL_DTYPE_F32 else T.bfloat16
     hkv, d, dev = params.num_kv_heads, params.head_dim, T._C._cuda_getDevice()
-    pk, sk = _rows(k_new, "k_new", hkv, d, dt, None, dev)
-    n = k_new.shape[0]
-    pv, sv = _rows(v_new, "v_new", hkv, d, dt, n, dev)
+    pk, sk, n, _ = _rows(k_new, "k_new", hkv, d, dt, None, dev)
+    pv, sv, _, _ = _rows(v_new, "v_new", hkv, d, dt, n, dev)
     pq = pqo = None
     sq = sqo = 0
     if q is not None:
-        pq, sq = _rows(q, "q", params.num_qo_heads, d, dt, n, dev)
+        pq, sq, _, _ = _rows(q, "q", params.num_qo_heads, d, dt, n, dev)
     if q_out is not None:
-        pqo, sqo = _rows(q_out, "q_out", params.num_qo_heads, d, dt, n, dev)
+        pqo, sqo, _, _ = _rows(q_out, "q_out", params.num_qo_heads, d, dt, n, dev)
     B = (params.batch,)
     rows = req_to_token.shape
     if len(rows) != 2 or rows[0] < B[0]:
@@ -789,14 +794,13 @@ def sgl_mla_kv_append(rope, params, q, kv_new, kv_pool, req_to_token, lens, exte
     """sgl_kv_append for an MLA pool: kv_new [N, 576] (latent, then position part), q [N, Hq, 576], bf16."""
     T = _T or _torch()
     dt, d, dev = T.bfloat16, params.latent_dim + params.rope_dim, T._C._cuda_getDevice()
-    pk, sk = _rows(kv_new.unsqueeze(1) if kv_new.dim() == 2 else kv_new, "kv_new", 1, d, dt, None, dev)
-    n = kv_new.shape[0]
+    pk, sk, n, _ = _rows(kv_new.unsqueeze(1) if kv_new.dim() == 2 else kv_new, "kv_new", 1, d, dt, None, dev)
     pq = pqo = None
     sq = sqo = 0
     if q is not None:
-        pq, sq = _rows(q, "q", params.num_qo_heads, d, dt, n, dev)
+        pq, sq, _, _ = _rows(q, "q", params.num_qo_heads, d, dt, n, dev)
     if q_out is not None:
-        pqo, sqo = _rows(q_out, "q_out", params.num_qo_heads, d, dt, n, dev)
+        pqo, sqo, _, _ = _rows(q_out, "q_out", params.num_qo_heads, d, dt, n, dev)
     B = (params.batch,)
     rows = req_to_token.shape
     if len(rows) != 2 or rows[0] < B[0]:
