@@ -382,6 +382,41 @@ def test_no_alloc_decode():
     b.check((o.double().cpu().numpy(), lse.double().cpu().numpy()))
 
 
+@pytest.mark.parametrize("shared", [False, True])
+def test_decode_step_from_host_memory(shared):
+    """One call from host memory (copies, decode with and without a merge, copies back) gives the separate calls'
+    bytes."""
+    b = Batch(_star(20, 200, 1, 30) if shared else _own([30, 0, 7, 50]), 32, 8, 128, seed=31)
+    plan = b.plan()
+    kp, vp, table, lens = b.device()
+    ws = torch.zeros(plan.workspace_bytes, dtype=torch.uint8, device="cuda")
+    sgl.sgl_plan_upload(plan, ws)
+    parts = [b.q, torch.from_numpy(b.table), torch.from_numpy(b.lens)]
+    up = lambda n: (n + 255) // 256 * 256  # noqa: E731
+    at, spans = 0, []
+    for x in parts:
+        spans.append((at, x.numel() * x.element_size()))
+        at += up(spans[-1][1])
+    hin = torch.zeros(at, dtype=torch.uint8).pin_memory()
+    for x, (o0, n) in zip(parts, spans):
+        hin[o0:o0 + n] = x.reshape(-1).view(torch.uint8)
+    din = torch.zeros(at, dtype=torch.uint8, device="cuda")
+    q, t, sl = (din[o0:o0 + n].view(x.dtype).view(x.shape) for x, (o0, n) in zip(parts, spans))
+    ob = up(b.q.numel() * 2)
+    dout = torch.zeros(ob + b.B * b.hq * 4, dtype=torch.uint8, device="cuda")
+    hout = torch.zeros(dout.numel(), dtype=torch.uint8).pin_memory()
+    o = dout[:b.q.numel() * 2].view(torch.bfloat16).view(b.q.shape)
+    lse = dout[ob:].view(torch.float32).view(b.B, b.hq)
+    sgl.sgl_decode_step(hin, din, q, kp, vp, t, sl, plan, o, lse, dout, hout, ws)
+    torch.cuda.synchronize()
+    sgl.sgl_check(ws)
+    o2, lse2 = torch.zeros_like(o), torch.zeros_like(lse)
+    sgl.sgl_decode_attn(b.q.cuda(), kp, vp, table, lens, plan, o2, lse2, ws)
+    assert torch.equal(hout[:b.q.numel() * 2], o2.reshape(-1).view(torch.uint8).cpu())
+    assert torch.equal(hout[ob:], lse2.reshape(-1).view(torch.uint8).cpu())
+    b.check((o2.double().cpu().numpy(), lse2.double().cpu().numpy()))
+
+
 def test_refusals():
     from ctypes import byref
     b = Batch(_own([4]), 8, 2, 128)
