@@ -38,7 +38,7 @@
 // conversion and half a packed multiplication (its scale).
 // Conversions, packed multiplications and integer operations each run at 64
 // lanes per clock and SM, mma.sync at one m16n8k16 per two clocks (measured).
-// Measured: 64 requests of 1 to 8192 tokens (273 MB) 57.5 us, of which the
+// Measured: 64 requests of 1 to 8192 tokens (273 MB) 57.1 us, of which the
 // merge is 4; an SM's two streams take 0.032 us a position (8 heads of 128),
 // 0.026 being the copy's rate, with 57% of the issue slots and half of the
 // integer pipe busy.  One request of 180 tokens: 7.0 us, 2.6 of them the merge.
@@ -121,6 +121,7 @@ __device__ __forceinline__ void fp4_producer(const Fp4Args& p, const CUtensorMap
     const int64_t num_slots = p.f.t.num_slots;
     const bool v = lane >= kQuads;                 // (lanes 8 .. 15)
     const int quad = lane & (kQuads - 1);
+    const uint64_t kv_pol = l2_evict_first_policy();   // (read once; 58.0 -> 57.1 us on 64 requests of 1 to 8192 tokens)
     int last_armed = -1, last_arrived = -1;
     const CUtensorMap* tm = nullptr;
     uint32_t box = 0u;
@@ -179,8 +180,8 @@ __device__ __forceinline__ void fp4_producer(const Fp4Args& p, const CUtensorMap
         if (lane == 0) mbar_expect_tx_only(fb, (uint32_t)__popc(quads) * 4u * box);
         __syncwarp();
         if (qm)
-            tma_gather4(ring + st * Lay::STAGE + lane * Lay::QP, tm, (kvh >> 2) * (4 * fp4_head_bytes(D)) / 4, row[0],
-                        row[1], row[2], row[3], fb);
+            tma_gather4_hint(ring + st * Lay::STAGE + lane * Lay::QP, tm, (kvh >> 2) * (4 * fp4_head_bytes(D)) / 4, row[0],
+                        row[1], row[2], row[3], fb, kv_pol);
         if (lane == 0) {
             st_shared_s32(db + kDescFlags, flags);
             st_shared_s32(db + kDescMask, (int32_t)mask);

@@ -13,7 +13,7 @@ using namespace tc;
 struct FusedArgs {
     TcArgs t;
     const int32_t* wptr;   // [n_ctas + 1] wide items of each CTA
-    const DecItem* narrow; // narrow pieces, longest first
+    const DecItem* narrow; // narrow pieces, in the order in which they are dealt and handed out
     int n_narrow;
     int n_init;            // pieces assigned at launch: streaming CTA w starts on piece w
     int n_tile_ctas;       // CTAs 0 .. n_tile_ctas-1 run the wide items first

@@ -394,6 +394,15 @@ __device__ __forceinline__ void tma_gather4(uint32_t dst, const void* tmap, int 
         "l"(tmap), "r"(x), "r"(r0), "r"(r1), "r"(r2), "r"(r3), "r"(bar)
         : "memory");
 }
+// the same with an L2 policy
+__device__ __forceinline__ void tma_gather4_hint(uint32_t dst, const void* tmap, int x, int r0, int r1, int r2, int r3,
+                                                 uint32_t bar, uint64_t pol) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes.L2::cache_hint [%0], "
+        "[%1, {%2, %3, %4, %5, %6}], [%7], %8;\n" ::"r"(dst),
+        "l"(tmap), "r"(x), "r"(r0), "r"(r1), "r"(r2), "r"(r3), "r"(bar), "l"(pol)
+        : "memory");
+}
 // TMA load of one 128-byte row piece: row y, columns x..x+63 (bf16) of the
 // 2-D tensor `tmap` (box 64 x 1, 128-byte swizzle) into `dst`.
 __device__ __forceinline__ void tma_load_row(uint32_t dst, const void* tmap, int x, int y, uint32_t bar) {
