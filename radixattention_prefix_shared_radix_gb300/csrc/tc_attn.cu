@@ -78,17 +78,23 @@ __device__ __forceinline__ int find_extend_request(const int32_t* extend_lens, i
 // to 9% slower with it.
 __device__ __noinline__ bool extend_tile_info(const TcArgs& a, int* info) {
     const int tq = 128 / a.G, lane = threadIdx.x & 31;
-    int req = -1, c0 = 0, qoff = 0;
+    int req = -1, c0 = 0, qoff = 0, pre = 0, ext = 0;
     if (a.B > 8) {
         req = find_extend_request(a.extend_lens, a.B, tq, (int)blockIdx.x, &c0, &qoff);
+        if (req < 0) return false;
+        pre = __ldg(a.prefix_lens + req);
+        ext = __ldg(a.extend_lens + req);
     } else {
+        const int ev = lane < a.B ? __ldg(a.extend_lens + lane) : 0, pv = lane < a.B ? __ldg(a.prefix_lens + lane) : 0;
         int acc_c = 0, acc_q = 0;
         for (int r = 0; r < a.B; ++r) {
-            const int e = __ldg(a.extend_lens + r);
+            const int e = __shfl_sync(0xffffffffu, ev, r);
             const int nt = e > 0 ? (e + tq - 1) / tq : 0;
             const int nc = (nt + 1) / 2;
             if ((int)blockIdx.x < acc_c + nc) {
                 req = r;
+                pre = __shfl_sync(0xffffffffu, pv, r);
+                ext = e;
                 c0 = acc_c;
                 qoff = acc_q;
                 break;
@@ -98,7 +104,6 @@ __device__ __noinline__ bool extend_tile_info(const TcArgs& a, int* info) {
         }
     }
     if (req < 0) return false;
-    const int pre = __ldg(a.prefix_lens + req), ext = __ldg(a.extend_lens + req);
     const int t0 = ((int)blockIdx.x - c0) * 2 * tq;
     const int na = min(tq, ext - t0), nb2 = min(tq, ext - t0 - tq);
     const int ntok = na + (nb2 > 0 ? nb2 : 0);
@@ -135,13 +140,11 @@ __global__ void __launch_bounds__(ExtCfg<D, KV>::kThreads, 1)
     int* info = reinterpret_cast<int*>(sm + Lay::OFF_INFO);
     uint32_t* tslot = reinterpret_cast<uint32_t*>(sm + Lay::OFF_TMEM);
     const int tid = threadIdx.x, warp = tid >> 5;
+    // (side by side: which tiles, the barriers, TMEM)
     if (warp == 0) {
         const bool some = extend_tile_info(a, info);
         if (tid == 0) info[15] = some ? 1 : 0;
-    }
-    __syncthreads();
-    if (!info[15]) return;
-    if (tid == 0) {
+    } else if (tid == 32) {
         tc_init_barriers<C>(smem_u32(sm + Lay::OFF_BAR));
         mbar_fence_init();
     }
@@ -156,7 +159,7 @@ __global__ void __launch_bounds__(ExtCfg<D, KV>::kThreads, 1)
     const TileInfo ti{info[0], info[1], info[2], info[3], {info[4], info[5]}, {info[6], info[7]}, {info[8], info[9]},
                       info[10], info[11]};
     TcState st{0u, 0u, false};
-    tc_tile_run<C>(a, &tmk, &tmv, &tnk, &tnv, ti, sm, tbase, st, tid);
+    if (info[15]) tc_tile_run<C>(a, &tmk, &tmv, &tnk, &tnv, ti, sm, tbase, st, tid);
     tc_fence_before();
     __syncthreads();
     if (warp == C::kMmaWarp) {

@@ -7,13 +7,14 @@
 //
 // Roles, by warp of the C::kThreads tile threads:
 //   warps 0 .. 4 NQ - 1   softmax: query tile w / 4, thread = query row =
-//                         TMEM lane;
+//                         TMEM lane; before that, Q into TMEM (decode) or,
+//                         extend, its tiles into shared memory (cp.async);
 //   warp 4 NQ             one thread issues every MMA (the warp owns TMEM);
 //   the next NG warps     the gather team: the K and V rows of every block
 //                         as TMA tile::gather4 copies (four rows of 128
 //                         bytes each, rows of the pool viewed as a 2-D
 //                         tensor [slot * Hkv + head, d]) into 128B-swizzled
-//                         tiles; extend's Q tiles with 16-byte cp.async.
+//                         tiles.
 // Measured on GB300: a warp gets one random-row gather through every ~110
 // cycles, whether one lane or many issue them, so the gather rate grows with
 // the number of warps that issue; hence a team.
@@ -314,8 +315,8 @@ __device__ __forceinline__ void tc_inval_barriers(uint32_t bar0) {
 template <class C>
 __device__ __forceinline__ void tc_init_barriers(uint32_t bar0) {
     auto bar = [&](int i) { return bar0 + 8u * (uint32_t)i; };
-    // Q writers: the softmax threads (decode) or the gather team's lanes (extend)
-    mbar_init(bar(C::QFULL), C::kDec ? 128 : 32 * C::kNG);
+    // Q writers: the softmax threads
+    mbar_init(bar(C::QFULL), 128 * C::kNQ);
     // FULL: one arrival per gather warp (an expect_tx whose bytes its TMA
     // gathers complete, or with FP8 pools a plain arrival once its lanes'
     // stores are done); EMPTY: the MMA thread's commit
@@ -369,6 +370,7 @@ __device__ __forceinline__ void tc_tile_run(const TcArgs& a, const CUtensorMap* 
     float* const a_lse = a.lse;
     uint32_t* const a_err = a.err;
     const int a_Hq = a.Hq, a_Hkv = a.Hkv, a_G = a.G;
+    const int lgG = 31 - __clz(a_G);               // (query heads per KV head: 1, 2, 4 or 8)
     const int64_t a_num_slots = a.num_slots;
     const float a_scale = a.scale_log2;
     const int warp = tid >> 5, lane = tid & 31;
@@ -388,49 +390,6 @@ __device__ __forceinline__ void tc_tile_run(const TcArgs& a, const CUtensorMap* 
     if (warp > C::kMmaWarp) {
         // ------------------------------------------------------------ gather
         const int g = warp - C::kMmaWarp - 1;
-        if constexpr (!DEC) {
-            // Q: 128 rows per query tile (once, 16-byte cp.async, zero-filled
-            // past the tile's rows)
-            constexpr int CPR = D / 8;
-            constexpr int RPI = 32 / CPR;
-            constexpr int QI = 128 / RPI;
-            const int sub = lane / CPR, ch = lane % CPR;
-#pragma unroll
-            for (int q = 0; q < NQ; ++q) {
-                const int rq = q ? ti.rows[1] : ti.rows[0], i6q = q ? ti.i6[1] : ti.i6[0];
-                for (int t = g; t < QI; t += NG) {
-                    const int r = t * RPI + sub;
-                    const bool ok = r < rq;
-                    const int64_t qr = ((int64_t)i6q + r / a_G) * a_Hq + kvh * a_G + r % a_G;
-                    const bf16* src = ok ? a_q + qr * D + ch * 8 : a_q;
-                    cp_async16(sQ + q * Lay::QTILE + sw128(r, ch, kQRegion), src, ok);
-                }
-            }
-            if constexpr (F8) {
-                // f16 operands against the f16 K tiles: each lane converts
-                // the Q chunks it copied, in place, once they have landed
-                cp_async_commit();
-                cp_async_wait<0>();
-                uint32_t qbad = 0u;
-#pragma unroll
-                for (int q = 0; q < NQ; ++q) {
-                    for (int t = g; t < QI; t += NG) {
-                        const uint32_t qa = sQ + q * Lay::QTILE + sw128(t * RPI + sub, ch, kQRegion);
-                        uint32_t w[4];
-                        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];\n"
-                                     : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
-                                     : "r"(qa));
-                        st_shared_v4(qa, bf16x2_to_f16x2_chk(w[0], qbad), bf16x2_to_f16x2_chk(w[1], qbad),
-                                     bf16x2_to_f16x2_chk(w[2], qbad), bf16x2_to_f16x2_chk(w[3], qbad));
-                    }
-                }
-                if (qbad) atomicOr(a_err, kErrQRange);
-                fence_proxy_async_smem();
-                mbar_arrive(bar(C::QFULL));
-            } else {
-                cp_async_arrive_noinc(bar(C::QFULL));
-            }
-        }
         int issued = 0;
         const int32_t* trow = a_r2t + (int64_t)kv_row * a_ld;
         if constexpr (F4) {
@@ -880,15 +839,15 @@ __device__ __forceinline__ void tc_tile_run(const TcArgs& a, const CUtensorMap* 
         const uint32_t lq = (uint32_t)((warp & 3) * 32) << 16;
         const uint32_t tl = tbase + 256 * q + lq;
         const uint32_t tlO = tl + C::kOCol;
-        const int lim = DEC ? 0x7fffffff : i7 + i / a_G;
+        const int lim = DEC ? 0x7fffffff : i7 + (i >> lgG);
         const float sc = F8 ? a_scale * a.k_scale : a_scale;
         float m_used = -INFINITY, l0 = 0.f, l1 = 0.f;   // l = l0 + l1 (packed pair sums)
         if constexpr (DEC) {
             // this row's query (member request i / G, head kvh * G + i % G) into TMEM
             const uint32_t tlQ = tbase + C::kQCol + lq;
             const bool ok = i < rows;
-            const int mem = ok ? __ldg(a_members + i6 + i / a_G) : 0;
-            const uint4* src = reinterpret_cast<const uint4*>(a_q + ((int64_t)mem * a_Hq + kvh * a_G + i % a_G) * D);
+            const int mem = ok ? __ldg(a_members + i6 + (i >> lgG)) : 0;
+            const uint4* src = reinterpret_cast<const uint4*>(a_q + ((int64_t)mem * a_Hq + kvh * a_G + (i & (a_G - 1))) * D);
 #pragma unroll
             for (int c = 0; c < D / 64; ++c) {
                 uint32_t w[32];
@@ -910,6 +869,49 @@ __device__ __forceinline__ void tc_tile_run(const TcArgs& a, const CUtensorMap* 
             }
             tc_fence_before();
             mbar_arrive(bar(C::QFULL));
+        } else {
+            // Q: 128 rows per query tile (once, 16-byte cp.async, zero-filled
+            // past the tile's rows), by these warps, which have nothing else
+            // to do yet, while the gather warps look up and copy K and V (100
+            // requests of 16 new tokens: 59.7 -> 54.1 us over 4-bit pools with
+            // their conversion, 49.3 -> 45.8 over bf16 ones)
+            constexpr int CPR = D / 8, RPI = 32 / CPR, QI = 128 / RPI;
+            const int sub = lane / CPR, ch = lane % CPR;
+#pragma unroll
+            for (int t2 = 0; t2 < NQ; ++t2) {
+                const int rq = t2 ? ti.rows[1] : ti.rows[0], i6q = t2 ? ti.i6[1] : ti.i6[0];
+                for (int t = warp; t < QI; t += 4 * NQ) {
+                    const int r = t * RPI + sub;
+                    const bool ok = r < rq;
+                    const int64_t qr = ((int64_t)i6q + (r >> lgG)) * a_Hq + kvh * a_G + (r & (a_G - 1));
+                    const bf16* src = ok ? a_q + qr * D + ch * 8 : a_q;
+                    cp_async16(sQ + t2 * Lay::QTILE + sw128(r, ch, kQRegion), src, ok);
+                }
+            }
+            if constexpr (F8) {
+                // f16 operands against the f16 K tiles: each lane converts
+                // the Q chunks it copied, in place, once they have landed
+                cp_async_commit();
+                cp_async_wait<0>();
+                uint32_t qbad = 0u;
+#pragma unroll
+                for (int t2 = 0; t2 < NQ; ++t2) {
+                    for (int t = warp; t < QI; t += 4 * NQ) {
+                        const uint32_t qa = sQ + t2 * Lay::QTILE + sw128(t * RPI + sub, ch, kQRegion);
+                        uint32_t w[4];
+                        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];\n"
+                                     : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                                     : "r"(qa));
+                        st_shared_v4(qa, bf16x2_to_f16x2_chk(w[0], qbad), bf16x2_to_f16x2_chk(w[1], qbad),
+                                     bf16x2_to_f16x2_chk(w[2], qbad), bf16x2_to_f16x2_chk(w[3], qbad));
+                    }
+                }
+                if (qbad) atomicOr(a_err, kErrQRange);
+                fence_proxy_async_smem();
+                mbar_arrive(bar(C::QFULL));
+            } else {
+                cp_async_arrive_noinc(bar(C::QFULL));
+            }
         }
         // O (rows of this warp) times f, in TMEM
         auto scale_o = [&](float f) {
@@ -1029,6 +1031,7 @@ __device__ __forceinline__ void tc_tile_run(const TcArgs& a, const CUtensorMap* 
             constexpr int OPITCH = D * 4 + 16;
             static_assert(!DEC || 128 * OPITCH <= 2 * NS * Lay::KTILE, "the O rows fit the K and V stages");
             const uint32_t so = sK + (uint32_t)(i * OPITCH);
+            [[maybe_unused]] const bool wide_o = (reinterpret_cast<uintptr_t>(a_o) & 31u) == 0;
 #pragma unroll 1
             for (int c = 0; c < D / 32; c += 2) {
                 float v[64];
@@ -1047,13 +1050,22 @@ __device__ __forceinline__ void tc_tile_run(const TcArgs& a, const CUtensorMap* 
                                      __float_as_uint(v[k + 1] * inv), __float_as_uint(v[k + 2] * inv),
                                      __float_as_uint(v[k + 3] * inv));
                 } else if (i < rows) {
-                    const int64_t orow = ((int64_t)i6 + i / a_G) * a_Hq + kvh * a_G + i % a_G;
+                    const int64_t orow = ((int64_t)i6 + (i >> lgG)) * a_Hq + kvh * a_G + (i & (a_G - 1));
                     bf16* dst = a_o + orow * D + 32 * c;
+                    // 32 bytes per lane where the output's alignment allows
+                    // it: a store instruction goes to 32 rows, a line each, and
+                    // takes a clock per line whatever its width
+                    uint32_t w[32];
 #pragma unroll
-                    for (int k = 0; k < 64; k += 8)
-                        *reinterpret_cast<uint4*>(dst + k) = make_uint4(
-                            pack_bf16(v[k] * inv, v[k + 1] * inv), pack_bf16(v[k + 2] * inv, v[k + 3] * inv),
-                            pack_bf16(v[k + 4] * inv, v[k + 5] * inv), pack_bf16(v[k + 6] * inv, v[k + 7] * inv));
+                    for (int k = 0; k < 32; ++k) w[k] = pack_bf16(v[2 * k] * inv, v[2 * k + 1] * inv);
+                    if (wide_o) {
+#pragma unroll
+                        for (int k = 0; k < 32; k += 8) st_global_v8(dst + 2 * k, w + k);
+                    } else {
+#pragma unroll
+                        for (int k = 0; k < 32; k += 4)
+                            *reinterpret_cast<uint4*>(dst + 2 * k) = make_uint4(w[k], w[k + 1], w[k + 2], w[k + 3]);
+                    }
                 }
             }
             if constexpr (DEC) {
@@ -1065,9 +1077,10 @@ __device__ __forceinline__ void tc_tile_run(const TcArgs& a, const CUtensorMap* 
                 }
                 bulk_wait_read_all();   // the stages are free again once read
             } else if (i < rows) {
-                a_lse[((int64_t)i6 + i / a_G) * a_Hq + kvh * a_G + i % a_G] = lse;
+                a_lse[((int64_t)i6 + (i >> lgG)) * a_Hq + kvh * a_G + (i & (a_G - 1))] = lse;
             }
         }
+        if constexpr (!DEC) asm volatile("cp.async.wait_all;\n" ::: "memory");   // (Q's, long landed)
         tc_fence_before();
     }
     stt.J = J0 + (uint32_t)(nb > 0 ? nb : 0);
