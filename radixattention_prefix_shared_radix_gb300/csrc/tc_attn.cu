@@ -37,7 +37,7 @@ using ExtCfg = TcCfg<D, false, 2, (KV == kKvE4m3 && D == 128) ? 1 : 2 * (128 / D
 
 // The request of tile pair `c`, the pairs and new tokens before it, by one
 // warp, 128 requests at a time; -1 past the last.
-__device__ __forceinline__ int find_extend_request(const int32_t* extend_lens, int B, int tq, int c, int* c0, int* qoff) {
+__device__ __forceinline__ int find_extend_request(const int32_t* extend_lens, int B, int lt, int c, int* c0, int* qoff) {
     const int lane = threadIdx.x & 31;
     int acc_c = 0, acc_q = 0;
     for (int b = 0; b < B; b += 128) {
@@ -46,7 +46,7 @@ __device__ __forceinline__ int find_extend_request(const int32_t* extend_lens, i
         for (int k = 0; k < 4; ++k) ev[k] = b + 32 * k + lane < B ? max(__ldg(extend_lens + b + 32 * k + lane), 0) : 0;
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-            const int nc = ((ev[k] + tq - 1) / tq + 1) / 2;      // the request's tile pairs
+            const int nc = (((ev[k] + (1 << lt) - 1) >> lt) + 1) >> 1;   // the request's tile pairs
             int sc = nc, sq = ev[k];                             // sums up to this lane
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
@@ -71,16 +71,17 @@ __device__ __forceinline__ int find_extend_request(const int32_t* extend_lens, i
 }
 
 // Query tile pair (blockIdx.x, blockIdx.y) of the extend batch, into info by
-// lane 0 of the calling warp; false if empty.  A few requests are walked, more
-// are searched by the warp: the walk is a chain of loads (100 requests of 16
-// new tokens: 94 us walked, 54 searched; 3 requests: 18.0 and 18.5).  Not
+// lane 0 of the calling warp; false if empty.  A few requests are walked, their
+// lengths loaded by as many lanes; more are searched by the warp (when the walk
+// was a chain of loads, 100 requests of 16 new tokens took 94 us walked and 54
+// searched, 3 requests 18.0 and 18.5).  Not
 // inlined: the kernel's registers are the tile roles', whose loops came out up
 // to 9% slower with it.
 __device__ __noinline__ bool extend_tile_info(const TcArgs& a, int* info) {
-    const int tq = 128 / a.G, lane = threadIdx.x & 31;
+    const int lt = 7 - (31 - __clz(a.G)), tq = 1 << lt, lane = threadIdx.x & 31;   // new tokens per tile
     int req = -1, c0 = 0, qoff = 0, pre = 0, ext = 0;
     if (a.B > 8) {
-        req = find_extend_request(a.extend_lens, a.B, tq, (int)blockIdx.x, &c0, &qoff);
+        req = find_extend_request(a.extend_lens, a.B, lt, (int)blockIdx.x, &c0, &qoff);
         if (req < 0) return false;
         pre = __ldg(a.prefix_lens + req);
         ext = __ldg(a.extend_lens + req);
@@ -89,8 +90,8 @@ __device__ __noinline__ bool extend_tile_info(const TcArgs& a, int* info) {
         int acc_c = 0, acc_q = 0;
         for (int r = 0; r < a.B; ++r) {
             const int e = __shfl_sync(0xffffffffu, ev, r);
-            const int nt = e > 0 ? (e + tq - 1) / tq : 0;
-            const int nc = (nt + 1) / 2;
+            const int nt = e > 0 ? (e + tq - 1) >> lt : 0;
+            const int nc = (nt + 1) >> 1;
             if ((int)blockIdx.x < acc_c + nc) {
                 req = r;
                 pre = __shfl_sync(0xffffffffu, pv, r);
