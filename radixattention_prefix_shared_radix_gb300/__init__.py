@@ -212,11 +212,14 @@ def _torch():
 
 
 def _dev(t, what):
+    try:
+        if t.is_cuda and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass          # not a tensor
     if not isinstance(t, (_T or _torch()).Tensor) or not t.is_cuda:
         raise TypeError("%s must be a CUDA tensor" % what)
-    if not t.is_contiguous():
-        raise ValueError("%s must be contiguous" % what)
-    return t.data_ptr()
+    raise ValueError("%s must be contiguous" % what)
 
 
 def _stream(stream):
@@ -546,7 +549,7 @@ def sgl_decode_attn(q, k_pool, v_pool, req_to_token, seq_lens, plan, o, lse, wor
     _ok(_lib().sgl_decode_attn(_dev(q, "q"), _dev(k_pool, "k_pool"), _dev(v_pool, "v_pool"),
                                _dev(req_to_token, "req_to_token"), req_to_token.shape[1], _dev(seq_lens, "seq_lens"),
                                plan.handle, _dev(o, "o"), _dev(lse, "lse"), _dev(workspace, "workspace"),
-                               workspace.numel() * workspace.element_size(), _stream(stream)), "sgl_decode_attn")
+                               workspace.nbytes, _stream(stream)), "sgl_decode_attn")
 
 
 def _host(t, what):
@@ -627,7 +630,7 @@ def sgl_extend_attn(q_new, k_pool, v_pool, req_to_token, prefix_lens, extend_len
                                _dev(req_to_token, "req_to_token"), req_to_token.shape[1],
                                _dev(prefix_lens, "prefix_lens"), _dev(extend_lens, "extend_lens"),
                                ctypes.byref(params), _dev(o, "o"), _dev(lse, "lse"), _dev(workspace, "workspace"),
-                               workspace.numel() * workspace.element_size(), _stream(stream)), "sgl_extend_attn")
+                               workspace.nbytes, _stream(stream)), "sgl_extend_attn")
 
 
 def sgl_extend_attn_kvwrite(q_new, k_new, v_new, k_pool, v_pool, req_to_token, prefix_lens, extend_lens, params, o,
@@ -637,7 +640,7 @@ def sgl_extend_attn_kvwrite(q_new, k_new, v_new, k_pool, v_pool, req_to_token, p
                                        _dev(req_to_token, "req_to_token"), req_to_token.shape[1],
                                        _dev(prefix_lens, "prefix_lens"), _dev(extend_lens, "extend_lens"),
                                        ctypes.byref(params), _dev(o, "o"), _dev(lse, "lse"),
-                                       _dev(workspace, "workspace"), workspace.numel() * workspace.element_size(),
+                                       _dev(workspace, "workspace"), workspace.nbytes,
                                        _stream(stream)), "sgl_extend_attn_kvwrite")
 
 
