@@ -220,11 +220,14 @@ __device__ __forceinline__ uint32_t amax8(uint4 w) {
 // and must round as the quotient does, so a multiplication by a reciprocal
 // alone will not do.  One correction makes it the rounded quotient (Markstein
 // 1990: q = z y, then q + (z - q f) y, with y the rounded reciprocal of f),
-// within this range of f and for a finite z; other operands are divided.
+// within this range of f and for |z| < 2^60, so that no product overflows (an
+// infinite q would be corrected to NaN); other operands are divided.  The
+// remainder is taken as q f - z, which keeps the sign of a zero.
 __device__ __forceinline__ bool quick_range(float f) { return f >= 0x1p-60f && f <= 0x1p60f; }
+constexpr uint32_t kQuickTop = (127u + 60u) << 7;      // bf16 pattern of 2^60
 __device__ __forceinline__ float quotient(float z, float f, float y) {
     const float q = z * y;
-    return fmaf(fmaf(-q, f, z), y, q);
+    return fmaf(fmaf(q, f, -z), -y, q);
 }
 
 // Code of a block's scale: the E4M3 value nearest to amax / s6, amax the
@@ -233,13 +236,13 @@ __device__ __forceinline__ float quotient(float z, float f, float y) {
 __device__ __forceinline__ uint32_t block_scale(uint32_t m, float s6, float y6) {
     const uint32_t bits = max(m & 0xffffu, m >> 16);
     const float amax = __uint_as_float(bits << 16);
-    return e4m3_of(bits < 0x7f80u && quick_range(s6) ? quotient(amax, s6, y6) : __fdiv_rn(amax, s6));
+    return e4m3_of(bits < kQuickTop && quick_range(s6) ? quotient(amax, s6, y6) : __fdiv_rn(amax, s6));
 }
 
 // c = z / f for a block of bf16 values of magnitudes up to `m` (a pair of
 // patterns), f >= 0; zeros where f is 0.
 __device__ __forceinline__ void divide16(const float* z, float f, uint32_t m, float* c) {
-    if (quick_range(f) && max(m & 0xffffu, m >> 16) < 0x7f80u) {
+    if (quick_range(f) && max(m & 0xffffu, m >> 16) < kQuickTop) {
         const float y = __frcp_rn(f);
 #pragma unroll
         for (int j = 0; j < 16; ++j) c[j] = quotient(z[j], f, y);
