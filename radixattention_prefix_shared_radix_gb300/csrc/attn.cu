@@ -166,7 +166,8 @@ __global__ void __launch_bounds__(128)
 #pragma unroll
             for (int off = 16; off > 0; off >>= 1) cmax = fmaxf(cmax, __shfl_xor_sync(0xffffffffu, cmax, off));
             const float mn = fmaxf(m, cmax);
-            if (mn == -INFINITY) continue;   // nothing in this chunk (nor before)
+            // nothing in this chunk (nor before); a NaN score is something
+            if (mn == -INFINITY && !__any_sync(0xffffffffu, s != s)) continue;
             const float a = exp2f(m - mn);   // 0 while nothing was accumulated
             const float pj = exp2f(s - mn);  // 0 for masked positions
             float psum = pj;
@@ -188,10 +189,10 @@ __global__ void __launch_bounds__(128)
             m = mn;
         }
         const int64_t prow = (int64_t)it.partial_base + r;
-        const float inv = l > 0.f ? 1.f / l : 0.f;
+        const float inv = l > 0.f ? 1.f / l : l;   // (0, or a NaN that is kept)
 #pragma unroll
         for (int e = 0; e < E; ++e) po[prow * D + lane + 32 * e] = o[e] * inv;
-        if (lane == 0) plse[prow] = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
+        if (lane == 0) plse[prow] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
         __syncwarp();   // qs[warp] is rewritten for the next row
     }
 }
@@ -256,10 +257,10 @@ __global__ void __launch_bounds__(128)
         for (int e = 0; e < E; ++e) ov[e] = fmaf(p, vr[e], ov[e] * a);
         m = mn;
     }
-    const float inv = l > 0.f ? 1.f / l : 0.f;
+    const float inv = l > 0.f ? 1.f / l : l;   // (0, or a NaN that is kept)
 #pragma unroll
     for (int e = 0; e < E; ++e) o[(nrow * Hq + h) * D + lane * E + e] = ov[e] * inv;
-    if (lane == 0) lse[nrow * Hq + h] = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
+    if (lane == 0) lse[nrow * Hq + h] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
 }
 
 // KV write (fp32 path): new token i of request r -> pool slot

@@ -274,7 +274,7 @@ __device__ __forceinline__ void fp4_consumer(const Fp4Args& p, int c, uint32_t r
             const int64_t prow = hh ? pr1 : pr0;
             if (prow >= 0) {
                 const float ll = hh ? s1 : s0, mm = hh ? m1 : m0;
-                const float inv = ll > 0.f ? p.f.t.v_scale / ll : 0.f;
+                const float inv = ll > 0.f ? p.f.t.v_scale / ll : ll;   // (0, or a NaN that is kept)
                 if (p.o) {
                     uint4* dst = reinterpret_cast<uint4*>(p.o + prow * D + (D / 8) * g);
 #pragma unroll
@@ -290,7 +290,7 @@ __device__ __forceinline__ void fp4_consumer(const Fp4Args& p, int c, uint32_t r
                         *reinterpret_cast<float4*>(dst + 2 * i) =
                             make_float4(o[i][hh] * inv, o[i][2 + hh] * inv, o[i + 1][hh] * inv, o[i + 1][2 + hh] * inv);
                 }
-                if (g == 0) (p.o ? p.lse : p.f.t.plse)[prow] = ll > 0.f ? (mm + log2f(ll)) * kLn2 : -INFINITY;
+                if (g == 0) (p.o ? p.lse : p.f.t.plse)[prow] = ll == 0.f ? -INFINITY : (mm + log2f(ll)) * kLn2;
             }
         }
     };

@@ -306,7 +306,7 @@ __device__ __noinline__ void stream_consumer(const FusedArgs& f, int c, uint32_t
             if (r < cur_rows) {
                 const int64_t prow = (int64_t)cur_pb + ((r / G) * cur_nh + hw) * G + r % G;
                 const float ll = hh ? s1 : s0, mm = hh ? m1 : m0;
-                const float inv = ll > 0.f ? vsc / ll : 0.f;
+                const float inv = ll > 0.f ? vsc / ll : ll;   // (0, or a NaN that is kept)
                 if constexpr (F8) {
                     // m-tile i rows g, g + 8 stand for d = (D/8) g + 2i, + 1
                     float* dst = po + prow * D + (D / 8) * g;
@@ -321,7 +321,7 @@ __device__ __noinline__ void stream_consumer(const FusedArgs& f, int c, uint32_t
                         dst[16 * i + 8] = o[i][2 + hh] * inv;
                     }
                 }
-                if (g == 0) plse[prow] = ll > 0.f ? (mm + log2f(ll)) * kLn2 : -INFINITY;
+                if (g == 0) plse[prow] = ll == 0.f ? -INFINITY : (mm + log2f(ll)) * kLn2;
             }
         }
     };

@@ -8,7 +8,9 @@
 //   O = sum_e w_e O_e / sum_e w_e,   LSE = M + log(sum_e w_e),
 // which equals attention over the concatenated chunks ("SGLang 深度拆解"
 // (chenxutan.com/d/5669.html) §3.2 PagedDecode, split along the KV
-// sequence).  Every lane accumulates two or four columns of one query head;
+// sequence).  A chunk with nothing to attend to has lse_e = -inf and counts
+// nothing; one that met a NaN score has lse_e = NaN, and so has the result.
+// Every lane accumulates two or four columns of one query head;
 // the entries are taken in batches of 16 (U) whose rows and LSEs are all in
 // flight together, with the running maximum rescaling earlier batches
 // (online form of the same sum).
@@ -99,7 +101,12 @@ __device__ __noinline__ void merge_head(const MergeArgs& m, int idx, int j, int 
             float mx = M;
 #pragma unroll
             for (int u = 0; u < U; ++u) mx = fmaxf(mx, lu[u]);
-            if (mx == -INFINITY) continue;
+            if (mx == -INFINITY) {   // nothing yet (the maximum leaves NaN out)
+#pragma unroll
+                for (int u = 0; u < U; ++u)
+                    if (lu[u] != lu[u]) L = lu[u];
+                continue;
+            }
             const float sc = exp2f((M - mx) * kLog2e);   // 0 while nothing was accumulated
             L *= sc;
 #pragma unroll
@@ -114,7 +121,7 @@ __device__ __noinline__ void merge_head(const MergeArgs& m, int idx, int j, int 
             M = mx;
         }
     }
-    const float inv = L > 0.f ? 1.f / L : 0.f;
+    const float inv = L > 0.f ? 1.f / L : L;   // (0, or a NaN that is kept)
     const int64_t orow = (int64_t)r * m.Hq + h * m.G + j;
     OutT* dst = static_cast<OutT*>(m.o) + orow * D + col0 + lane * VPL;
     if constexpr (sizeof(OutT) == 2) {
@@ -130,7 +137,7 @@ __device__ __noinline__ void merge_head(const MergeArgs& m, int idx, int j, int 
 #pragma unroll
         for (int v = 0; v < VPL; ++v) dst[v] = acc[v] * inv;
     }
-    if (lane == 0 && col0 == 0) m.lse[orow] = L > 0.f ? M + logf(L) : -INFINITY;
+    if (lane == 0 && col0 == 0) m.lse[orow] = L == 0.f ? -INFINITY : M + logf(L);
 }
 
 // One warp per (request, KV head, query head of the group, column slice):

@@ -319,13 +319,13 @@ __global__ void __launch_bounds__(kThreads, 1) mla_decode_kernel(const __grid_co
             const int row = g + 8 * hh;
             if (row >= R) continue;
             const float L = hh ? L1 : L0, m = hh ? m1 : m0;
-            const float inv = L > 0.f ? 1.f / L : 0.f;
+            const float inv = L > 0.f ? 1.f / L : L;   // (0, or a NaN that is kept)
             float* dst = a.po + ((int64_t)it.partial_base + row) * kDV + 32 * warp + 2 * t;
 #pragma unroll
             for (int n = 0; n < 4; ++n)
                 *reinterpret_cast<float2*>(dst + 8 * n) = make_float2(o4[n][2 * hh] * inv, o4[n][2 * hh + 1] * inv);
             if (warp == 0 && t == 0)
-                a.plse[(int64_t)it.partial_base + row] = L > 0.f ? (m + log2f(L)) * kLn2 : -INFINITY;
+                a.plse[(int64_t)it.partial_base + row] = L == 0.f ? -INFINITY : (m + log2f(L)) * kLn2;
         }
         return;
     }
@@ -461,12 +461,12 @@ __global__ void __launch_bounds__(kThreads, 1) mla_decode_kernel(const __grid_co
         const int row = r0 + g + 8 * hh;
         if (row >= R) continue;
         const float L = hh ? L1 : L0, m = hh ? m1 : m0;
-        const float inv = L > 0.f ? 1.f / L : 0.f;
+        const float inv = L > 0.f ? 1.f / L : L;   // (0, or a NaN that is kept)
         float* dst = a.po + ((int64_t)it.partial_base + row) * kDV + 128 * wq + 2 * t;
 #pragma unroll
         for (int n = 0; n < 16; ++n)
             *reinterpret_cast<float2*>(dst + 8 * n) = make_float2(o[n][2 * hh] * inv, o[n][2 * hh + 1] * inv);
-        if (wq == 0 && t == 0) a.plse[(int64_t)it.partial_base + row] = L > 0.f ? (m + log2f(L)) * kLn2 : -INFINITY;
+        if (wq == 0 && t == 0) a.plse[(int64_t)it.partial_base + row] = L == 0.f ? -INFINITY : (m + log2f(L)) * kLn2;
     }
 }
 

@@ -410,7 +410,7 @@ __device__ __forceinline__ void mla_tile_run(const TileArgs& a, const CUtensorMa
         wait(Lay::DONE, 0);
         tc_fence_after();
         const float l = l0 + l1;
-        const float inv = l > 0.f ? 1.f / l : 0.f;
+        const float inv = l > 0.f ? 1.f / l : l;   // (0, or a NaN that is kept)
         const int u = i >> 6, ri = i & 63;
         const bool ok = ri < (u ? rows1 : rows0);
         const int64_t prow = (int64_t)(u ? u1.partial_base : u0.partial_base) + ri;
@@ -438,7 +438,7 @@ __device__ __forceinline__ void mla_tile_run(const TileArgs& a, const CUtensorMa
         if (ok) {
             bulk_s2g(a.po + prow * kDV + kOCols * h, so, (uint32_t)(kOCols * 4));
             bulk_commit();
-            if (h == 0) a.plse[prow] = l > 0.f ? (m_used + log2f(l)) * kLn2 : -INFINITY;
+            if (h == 0) a.plse[prow] = l == 0.f ? -INFINITY : (m_used + log2f(l)) * kLn2;
         }
         bulk_wait_all();   // written before the grid completes
     }

@@ -1022,8 +1022,8 @@ __device__ __forceinline__ void tc_tile_run(const TcArgs& a, const CUtensorMap* 
             wait(C::DONE, stt.T & 1);
             tc_fence_after();
             const float l = l0 + l1;
-            const float inv = l > 0.f ? (F8 ? a.v_scale : 1.f) / l : 0.f;
-            const float lse = l > 0.f ? (m_used + log2f(l)) * kLn2 : -INFINITY;
+            const float inv = l > 0.f ? (F8 ? a.v_scale : 1.f) / l : l;   // (0, or a NaN that is kept)
+            const float lse = l == 0.f ? -INFINITY : (m_used + log2f(l)) * kLn2;
             // decode: the row goes through shared memory (the K/V stages are
             // idle once every MMA is done; rows padded by 16 bytes, so a
             // warp's 16-byte stores meet no bank twice) and out with one bulk
