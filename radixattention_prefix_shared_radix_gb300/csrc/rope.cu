@@ -131,13 +131,23 @@ __device__ __forceinline__ bool find_request(const int32_t* ext, int B, int n, i
 __device__ __forceinline__ float2 cos_sin_turn(uint64_t ph, float amp_hi, float amp_lo) {
     const uint32_t quarter = (uint32_t)((ph + (1ull << 61)) >> 62);
     const int64_t rest = (int64_t)(ph - ((uint64_t)quarter << 62));     // [-1/8, 1/8) turn
-    // rest = 2^26 n + .. : n (36 bits) as the sum of two floats, in turns of 2^-38
-    const int64_t n = rest >> 26;
-    const float nh = (float)(int32_t)(n >> 12) * 4096.f;
-    const float nl = (float)((int32_t)(n - ((int64_t)(int32_t)(n >> 12) << 12)));
-    // 2 pi 2^-38 as the sum of two floats
-    constexpr double kTurn = 6.283185307179586476925286766559 * 0x1p-38;
-    constexpr float kH = (float)kTurn, kL = (float)(kTurn - (double)kH);
+    // rest = 2^8 (nh + nl) to within 2^8, nh a float of its bits from 40 on and
+    // nl of the 32 below; angles below 2^-19 of a turn are taken 2^16 times as
+    // large, so that nh holds the leading bits and the sum is good to 2^-30 of
+    // itself, however small
+    uint32_t lo = (uint32_t)rest;
+    int32_t hi = (int32_t)(rest >> 32);
+    const bool small = (uint32_t)(hi + (1 << 13)) < (1u << 14);
+    if (small) {
+        hi = (int32_t)__funnelshift_l(lo, (uint32_t)hi, 16);
+        lo <<= 16;
+    }
+    const float nh = (float)(hi & ~0xff) * 0x1p24f;
+    const float nl = (float)__funnelshift_l(lo, (uint32_t)hi, 24);
+    // 2 pi 2^-56 as the sum of two floats
+    constexpr double kTurn = 6.283185307179586476925286766559 * 0x1p-56;
+    constexpr float kTurnH = (float)kTurn, kTurnL = (float)(kTurn - (double)kTurnH);
+    const float kH = small ? kTurnH * 0x1p-16f : kTurnH, kL = small ? kTurnL * 0x1p-16f : kTurnL;
     const float xh0 = nh * kH;
     const float xl0 = fmaf(nh, kL, fmaf(nl, kH, fmaf(nh, kH, -xh0)));
     const float x = xh0 + xl0, xl = xl0 - (x - xh0);
