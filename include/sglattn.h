@@ -597,7 +597,9 @@ void sgl_rope_destroy(sgl_rope_table* rope);
  *                copied); may be q and k themselves (same stride), and must
  *                not overlap them in any other way
  * Pointers and row strides are multiples of 16 bytes.  The products are fp32,
- * rounded once; angles are exact to fp32 at every position. */
+ * rounded once.  The angle is the position times f_j as a double, off by
+ * 2^-64 of a turn per position (2^-30 of a radian at most); cos and sin of it
+ * are fp32 values within one unit in the last place. */
 int sgl_rope(const sgl_rope_table* rope, int32_t dtype, const void* q, int64_t q_stride, int32_t num_q_heads,
              const void* k, int64_t k_stride, int32_t num_k_heads, const int32_t* positions, int64_t n_rows, void* q_out,
              int64_t q_out_stride, void* k_out, int64_t k_out_stride, sgl_stream_t stream);

@@ -9,10 +9,11 @@
 // Angles: a table of cosines and sines would have to be read (512 bytes per
 // token of a 128-wide head, and a table as long as the longest context), and
 // p f_j in fp32 is off by p 2^-24 radians, which is wrong beyond a few
-// thousand positions.  Instead a frequency is a 64-bit fixed-point fraction
-// of a turn: p times it, modulo 2^64, is the fraction of a turn that the
-// angle stands at, off by p 2^-65 turns at most, with one integer product
-// and no range reduction.  The nearest quarter turn is split off before the
+// thousand positions.  Instead a frequency (f_j as a double) is a 64-bit
+// fixed-point fraction of a turn: p times it, modulo 2^64, is the fraction of
+// a turn that the angle stands at, off by p 2^-64 turns at most (2^-30 of a
+// radian at the farthest position), with one integer product and no range
+// reduction.  The nearest quarter turn is split off before the
 // conversion to fp32, so that the fp32 angle is at most an eighth of a turn.
 //
 // Work: a warp works on one token by itself -- it finds the request, position
@@ -47,7 +48,7 @@
 struct sgl_rope_table {
     sgl_rope_params p;
     double amplitude;                // multiplies cos and sin
-    uint64_t turn[SGL_ROPE_MAX_DIM / 2];   // 2^64 / (2 pi) radians per position, rounded
+    uint64_t turn[SGL_ROPE_MAX_DIM / 2];   // f_j 2^64 / (2 pi): fractions of a turn per position
 };
 
 namespace {
@@ -569,6 +570,17 @@ void set_table(RopeArgs& a, const sgl_rope_table* t) {
     std::memcpy(a.turn, t->turn, sizeof(uint64_t) * (size_t)(t->p.rot_dim / 2));
 }
 
+// 2^64 f / (2 pi), to the nearest whole number or its neighbour: f times 1 / (2 pi) as the sum
+// of two doubles (a quotient in doubles is off by 2^-53 of itself, which the
+// position multiplies: a millionth of a radian at positions near 2^31).  f <= 1
+// radian, so the fraction of a turn is below 1/6.
+uint64_t turn_of(double f) {
+    constexpr double kHi = 0x1.45f306dc9c883p-3, kLo = -0x1.6b01ec5417056p-57;
+    const double p = f * kHi, e = std::fma(f, kHi, -p) + f * kLo;
+    const double whole = std::floor(std::ldexp(p, 64));
+    return (uint64_t)whole + (uint64_t)(int64_t)std::nearbyint((std::ldexp(p, 64) - whole) + std::ldexp(e, 64));
+}
+
 // the arguments that both appends share, checked
 int append_rows(RopeArgs& a, const sgl_rope_table* rope, int es, int64_t n_rows, const int32_t* req_to_token, int64_t ld,
                 const int32_t* lens, const int32_t* extend_lens, int32_t batch, const void* q, int64_t q_stride,
@@ -660,8 +672,7 @@ int sgl_rope_create(const sgl_rope_params* p, sgl_rope_table** out) {
             const double w = std::fmin(std::fmax((orig * f / two_pi - p->low) / (p->high - p->low), 0.0), 1.0);
             f = f / by * (1.0 - w) + f * w;
         }
-        // f < 1 radian, so the fraction of a turn is below 1/6
-        t->turn[j] = (uint64_t)std::nearbyint(std::ldexp(f / two_pi, 64));
+        t->turn[j] = turn_of(f);
     }
     double amp = p->attention_factor;
     if (amp == 0.0) amp = kind == SGL_ROPE_SCALE_YARN ? 0.1 * std::log(by) + 1.0 : 1.0;

@@ -3,7 +3,7 @@
 With b = 0 a rotated pair is (a cos t, a sin t).  Sine and cosine are fp32 values within one unit in the last place
 (2^-23 of themselves), the product and the amplitude's share round once each (2^-24): together under 2^-22 of the
 result.  The angle is the position times the frequency as a double; the library holds it as a fraction of a turn, off by
-2^-65 turns per position, and the reference's product rounds it by 2^-53: under 2^-51 of the angle together, which
+2^-64 turns per position, and the reference's product rounds it by 2^-53: under 2^-51 of the angle together, which
 matters only next to a zero of the function.
 """
 
@@ -44,3 +44,15 @@ def test_small_and_nearly_whole_turns(d, theta, kind, kw):
     for got, want in ((c, np.cos(t)), (s, np.sin(t))):
         err, tol = np.abs(got - want), 2.0 ** -22 * np.abs(want) + 2.0 ** -51 * t
         assert (err <= tol).all(), "worst %.3g of the bound" % (err / np.maximum(tol, 1e-300)).max()
+
+
+def test_far_positions():
+    """At the farthest positions the angle of pair 0 (frequency one) is that of the position itself."""
+    pos = [2 ** 31 - 1 - i for i in range(50)] + [2 ** 30 + 17 * i for i in range(50)] + [2 ** 24 + i for i in range(9)]
+    c, s, t = _angles(64, 10000.0, pos)
+    for got, want in ((c, np.cos(t)), (s, np.sin(t))):
+        # (pair 0: its angle is exact in float64, and in the library off by 2^-64 turns per position)
+        err, tol = np.abs(got - want)[:, 0], (2.0 ** -22 * np.abs(want) + 2.0 ** -62 * t)[:, 0]
+        assert (err <= tol).all(), "worst %.3g of the bound" % (err / tol).max()
+        err, tol = np.abs(got - want), 2.0 ** -22 * np.abs(want) + 2.0 ** -51 * t
+        assert (err <= tol).all(), "worst %.3g of the bound" % (err / tol).max()
