@@ -634,18 +634,14 @@ int launch_decode_fp4(const sgl_plan* plan, const void* q, const void* kp, const
     constexpr int kTileSmem = Fp4Cfg<D>::Lay::END + 1024 > 120 * 1024 ? Fp4Cfg<D>::Lay::END + 1024 : 120 * 1024;
     static_assert(kTileSmem <= 232448, "shared memory per CTA");
     constexpr int kMergeSmem = 216 * 1024;
-    static const int attr = [] {
-        const cudaError_t e = cudaFuncSetAttribute(decode_fp4_streams<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                   Lay::TOTAL);
-        const cudaError_t e1 = cudaFuncSetAttribute(decode_fp4_tiles<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                    kTileSmem);
-        const cudaError_t e2 = cudaFuncSetAttribute(decode_merge_kernel<bf16, D, 4>,
-                                                    cudaFuncAttributeMaxDynamicSharedMemorySize, kMergeSmem);
-        const cudaError_t e3 = cudaFuncSetAttribute(decode_merge_kernel<bf16, D, 16>,
-                                                    cudaFuncAttributeMaxDynamicSharedMemorySize, kMergeSmem);
-        return (int)(e ? e : e1 ? e1 : e2 ? e2 : e3);
-    }();
-    if (attr) return attr;
+    static PerDevice smem;
+    if (const int e = ready_here(smem, [] {
+            if (const int e0 = large_smem(decode_fp4_streams<D>, Lay::TOTAL)) return e0;
+            if (const int e1 = large_smem(decode_fp4_tiles<D>, kTileSmem)) return e1;
+            if (const int e2 = large_smem(decode_merge_kernel<bf16, D, 4>, kMergeSmem)) return e2;
+            return large_smem(decode_merge_kernel<bf16, D, 16>, kMergeSmem);
+        }))
+        return e;
     const sgl_attn_params& p = plan->params;
     const int row = fp4_row_bytes(p.num_kv_heads, D);
     Fp4Args x{};

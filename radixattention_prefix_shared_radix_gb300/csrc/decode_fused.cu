@@ -614,9 +614,8 @@ int launch_decode_fused(const sgl_plan* plan, const void* q, const void* kp, con
                         int64_t ld, const int32_t* seq_lens, void* o, float* lse, unsigned char* ws, float scale_log2,
                         cudaStream_t s) {
     using Lay = FusedLayout<D, F8>;
-    static const int attr = (int)cudaFuncSetAttribute(decode_fused_kernel<D, F8>,
-                                                      cudaFuncAttributeMaxDynamicSharedMemorySize, Lay::TOTAL);
-    if (attr) return attr;
+    static PerDevice smem;
+    if (const int e = ready_here(smem, [] { return large_smem(decode_fused_kernel<D, F8>, Lay::TOTAL); })) return e;
     const sgl_attn_params& p = plan->params;
     // the tiles' TMA views of the pools (unused, and left zero, without tiles
     // or with an FP8 pool, whose tiles load the codes with plain loads)

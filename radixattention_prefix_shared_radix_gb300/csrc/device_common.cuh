@@ -9,6 +9,7 @@
 #include <cstdint>
 
 #include "common.h"
+#include "per_device.h"
 
 namespace sgldev {
 
@@ -443,6 +444,19 @@ __device__ __forceinline__ void fence_proxy_async_smem() {
 }
 __device__ __forceinline__ void named_bar(int id, int threads) {
     asm volatile("bar.sync %0, %1;\n" ::"r"(id), "r"(threads) : "memory");
+}
+
+// Host: set() (0, or a cudaError_t) at the first call on the current device.
+template <class Set>
+inline int ready_here(sgl::PerDevice& state, Set set) {
+    int dev = 0;
+    if (const cudaError_t e = cudaGetDevice(&dev)) return (int)e;
+    return state.ready(dev, set);
+}
+// Host: let a kernel use `bytes` of dynamic shared memory on the current device.
+template <class Kernel>
+inline int large_smem(Kernel* kernel, int bytes) {
+    return (int)cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
 }
 
 }  // namespace sgldev

@@ -488,10 +488,9 @@ extern "C" int sgl_mla_decode_attn(const void* q, const void* kv_pool, const int
     auto* ws = static_cast<unsigned char*>(workspace);
     auto s = reinterpret_cast<cudaStream_t>(stream);
     constexpr int kSmem = MlaLayout::TOTAL > mlat::Lay::TOTAL ? MlaLayout::TOTAL : mlat::Lay::TOTAL;
-    static const cudaError_t attr =
-        cudaFuncSetAttribute(mla_decode_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
-    if (attr != cudaSuccess) {
-        set_cuda_error((int)attr);
+    static PerDevice smem;
+    if (const int se = ready_here(smem, [] { return large_smem(mla_decode_kernel, kSmem); })) {
+        set_cuda_error(se);
         return SGL_ERR_CUDA;
     }
     MlaArgs a{};

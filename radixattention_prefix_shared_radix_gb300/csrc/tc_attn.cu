@@ -262,9 +262,8 @@ int launch_extend_tc(const void* q, const void* kp, const void* vp, const void* 
                      int64_t ctas, void* o, float* lse,
                      uint32_t* err, int Hq, int Hkv, int64_t num_slots, float scale_log2, float k_scale, float v_scale,
                      cudaStream_t s) {
-    static const int attr = (int)cudaFuncSetAttribute(extend_tc_kernel<D, KV>,
-                                                      cudaFuncAttributeMaxDynamicSharedMemorySize, extend_smem<D, KV>());
-    if (attr) return attr;
+    static PerDevice smem;
+    if (const int e = ready_here(smem, [] { return large_smem(extend_tc_kernel<D, KV>, extend_smem<D, KV>()); })) return e;
     // the pools' TMA views (FP8 and 4-bit pools are copied with cp.async:
     // their maps stay zero and unused)
     CUtensorMap mk{}, mv{}, nk{}, nv{};
