@@ -633,10 +633,28 @@ def sgl_extend_attn(q_new, k_pool, v_pool, req_to_token, prefix_lens, extend_len
                                workspace.nbytes, _stream(stream)), "sgl_extend_attn")
 
 
+def _row_bytes(params):
+    """Bytes of one pool row (a token's K or V of every head)."""
+    n, kind = params.num_kv_heads * params.head_dim, params.dtype
+    if kind == SGL_DTYPE_BF16_FP4KV:
+        return (n // 2 + n // 16 + 15) // 16 * 16
+    return n << (2 if kind == SGL_DTYPE_F32 else 1 if kind == SGL_DTYPE_BF16 else 0)
+
+
+def _writable(p, t, what, need):
+    """The address p of a pool that a call writes, which must hold its num_slots rows (`need` bytes: of any dtype, since
+    FP8 and 4-bit pools come as bytes)."""
+    if t.nbytes < need:
+        raise ValueError("%s must hold num_slots rows (%d bytes), not %d bytes" % (what, need, t.nbytes))
+    return p
+
+
 def sgl_extend_attn_kvwrite(q_new, k_new, v_new, k_pool, v_pool, req_to_token, prefix_lens, extend_lens, params, o,
                             lse, workspace, stream=None):
+    need = params.num_slots * _row_bytes(params)
     _ok(_lib().sgl_extend_attn_kvwrite(_dev(q_new, "q_new"), _dev(k_new, "k_new"), _dev(v_new, "v_new"),
-                                       _dev(k_pool, "k_pool"), _dev(v_pool, "v_pool"),
+                                       _writable(_dev(k_pool, "k_pool"), k_pool, "k_pool", need),
+                                       _writable(_dev(v_pool, "v_pool"), v_pool, "v_pool", need),
                                        _dev(req_to_token, "req_to_token"), req_to_token.shape[1],
                                        _dev(prefix_lens, "prefix_lens"), _dev(extend_lens, "extend_lens"),
                                        ctypes.byref(params), _dev(o, "o"), _dev(lse, "lse"),
@@ -783,8 +801,10 @@ def sgl_kv_append(rope, params, q, k_new, v_new, k_pool, v_pool, req_to_token, l
     rows = req_to_token.shape
     if len(rows) != 2 or rows[0] < B[0]:
         raise ValueError("req_to_token must have a row per request")
+    need = params.num_slots * _row_bytes(params)
     st = _lib().sgl_kv_append(None if rope is None else rope.handle, ctypes.byref(params), pq, sq, pk, sk, pv, sv,
-                              _flat(k_pool, "k_pool", dev), _flat(v_pool, "v_pool", dev),
+                              _writable(_flat(k_pool, "k_pool", dev), k_pool, "k_pool", need),
+                              _writable(_flat(v_pool, "v_pool", dev), v_pool, "v_pool", need),
                               _flat(req_to_token, "req_to_token", dev, T.int32), rows[1],
                               _flat(lens, "lens", dev, T.int32, B),
                               None if extend_lens is None else _flat(extend_lens, "extend_lens", dev, T.int32, B), n, pqo,
@@ -808,9 +828,9 @@ def sgl_mla_kv_append(rope, params, q, kv_new, kv_pool, req_to_token, lens, exte
     rows = req_to_token.shape
     if len(rows) != 2 or rows[0] < B[0]:
         raise ValueError("req_to_token must have a row per request")
-    st = _lib().sgl_mla_kv_append(None if rope is None else rope.handle, ctypes.byref(params), pq, sq, pk, sk,
-                                  _flat(kv_pool, "kv_pool", dev), _flat(req_to_token, "req_to_token", dev, T.int32),
-                                  rows[1], _flat(lens, "lens", dev, T.int32, B),
+    pool = _writable(_flat(kv_pool, "kv_pool", dev), kv_pool, "kv_pool", params.num_slots * d * 2)
+    st = _lib().sgl_mla_kv_append(None if rope is None else rope.handle, ctypes.byref(params), pq, sq, pk, sk, pool,
+                                  _flat(req_to_token, "req_to_token", dev, T.int32), rows[1], _flat(lens, "lens", dev, T.int32, B),
                                   None if extend_lens is None else _flat(extend_lens, "extend_lens", dev, T.int32, B), n,
                                   pqo, sqo, _flat(workspace, "workspace", dev), workspace.nbytes, _stream(stream))
     if st:
