@@ -81,7 +81,7 @@ enum { SGL_DTYPE_F32 = 0, SGL_DTYPE_BF16 = 1, SGL_DTYPE_BF16_FP8KV = 2, SGL_DTYP
  * SGL_DTYPE_BF16_FP4KV: Q and O bf16, the K and V pools in 4 bits: E2M1 codes
  * (0, 0.5, 1, 1.5, 2, 3, 4, 6 and their negatives) with one E4M3 scale for 16
  * consecutive elements of a head; K = k_scale * sf * code value, likewise V
- * (scales finite and > 0).  A pool is uint8 [num_slots, row], row =
+ * (scales > 0, 6 * scale finite).  A pool is uint8 [num_slots, row], row =
  * sgl_fp4_row_bytes(Hkv, d), base 16-byte aligned.  A row holds its token's
  * heads in blocks of four (the last block may hold fewer): first the block's
  * codes, d / 2 bytes per head, element 2i in the low half of byte i; then the

@@ -58,8 +58,9 @@ int check_params(const sgl_attn_params* p) {
         p->dtype != SGL_DTYPE_BF16_FP4KV)
         return SGL_ERR_UNSUPPORTED;
     if (p->dtype == SGL_DTYPE_BF16_FP8KV && !(p->k_scale > 0.f && p->v_scale > 0.f)) return SGL_ERR_INVALID_ARG;
-    if (p->dtype == SGL_DTYPE_BF16_FP4KV && !(p->k_scale > 0.f && p->v_scale > 0.f && std::isfinite(p->k_scale) &&
-                                              std::isfinite(p->v_scale)))
+    // (six scales are what a block's largest magnitude is divided by)
+    if (p->dtype == SGL_DTYPE_BF16_FP4KV && !(p->k_scale > 0.f && p->v_scale > 0.f && std::isfinite(6.f * p->k_scale) &&
+                                              std::isfinite(6.f * p->v_scale)))
         return SGL_ERR_INVALID_ARG;
     if (p->head_dim != 64 && p->head_dim != 128) return SGL_ERR_UNSUPPORTED;
     if (p->num_qo_heads % p->num_kv_heads) return SGL_ERR_UNSUPPORTED;
