@@ -58,11 +58,12 @@ __device__ __forceinline__ void cp_async16_pol(uint32_t dst, const void* src, bo
 __device__ __forceinline__ void cp_async4(uint32_t dst, const void* src) {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4;\n" ::"r"(dst), "l"(src) : "memory");
 }
-// N-byte copy, N = 4 or 8 (cached in L1), no zero fill.
+// N-byte copy, N = 4 or 8 (cached in L1), zeros where not valid (src is not read then).
 template <int N>
-__device__ __forceinline__ void cp_async_small(uint32_t dst, const void* src) {
+__device__ __forceinline__ void cp_async_small(uint32_t dst, const void* src, bool valid) {
     static_assert(N == 4 || N == 8, "copy size");
-    asm volatile("cp.async.ca.shared.global [%0], [%1], %2;\n" ::"r"(dst), "l"(src), "n"(N) : "memory");
+    const int n = valid ? N : 0;
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;\n" ::"r"(dst), "l"(src), "n"(N), "r"(n) : "memory");
 }
 __device__ __forceinline__ void st_shared_s32(uint32_t addr, int32_t v) {
     asm volatile("st.shared.b32 [%0], %1;\n" ::"r"(addr), "r"(v) : "memory");

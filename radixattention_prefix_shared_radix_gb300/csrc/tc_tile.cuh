@@ -419,7 +419,8 @@ __device__ __forceinline__ void tc_tile_run(const TcArgs& a, const CUtensorMap* 
                     sl[i] = (it < NIT && j < nb) ? __ldg(trow + p) : 0;
                 }
             };
-            // the rows of block j, looked up before
+            // the rows of block j, looked up before (-1, a row of zeros, for a
+            // slot outside the pool)
             auto rows_of = [&](int j) {
 #pragma unroll
                 for (int i = 0; i < TPT; ++i) {
@@ -427,7 +428,7 @@ __device__ __forceinline__ void tc_tile_run(const TcArgs& a, const CUtensorMap* 
                     rw[i] = sl[i];
                     if (rw[i] < 0 || rw[i] >= a_num_slots) {
                         if (j < nb && it < NIT && it % CH == 0) atomicOr(a_err, 1u);
-                        rw[i] = 0;
+                        rw[i] = -1;
                     }
                 }
             };
@@ -440,9 +441,10 @@ __device__ __forceinline__ void tc_tile_run(const TcArgs& a, const CUtensorMap* 
                     for (int i = 0; i < TPT; ++i) {
                         const int it = t0 + i * 32 * NG;
                         if (it >= NIT) continue;
+                        const bool ok = rw[i] >= 0;
                         const uint8_t* row = (n & 1 ? vp4 : kp4) + rw[i] * rb;
-                        if (it % CH == 0) cp_async_small<D / 16>(sb + CODES + it / CH * (D / 16), row + soff);
-                        cp_async16(sb + it * 16, row + (it % CH) * 16, true);
+                        if (it % CH == 0) cp_async_small<D / 16>(sb + CODES + it / CH * (D / 16), row + soff, ok);
+                        cp_async16(sb + it * 16, row + (it % CH) * 16, ok);
                     }
                 }
                 cp_async_commit();
@@ -546,12 +548,11 @@ __device__ __forceinline__ void tc_tile_run(const TcArgs& a, const CUtensorMap* 
 #pragma unroll
                 for (int i = 0; i < TPT; ++i) {
                     const int it = t0 + i * 32 * NG;
-                    int32_t s1 = sl[i];
-                    if (s1 < 0 || s1 >= a_num_slots) {
+                    rw[i] = sl[i] * a_Hkv + kvh;
+                    if (sl[i] < 0 || sl[i] >= a_num_slots) {   // (a row of zeros)
                         if (j < nb && it < NIT && it % CH == 0) atomicOr(a_err, 1u);
-                        s1 = 0;
+                        rw[i] = -1;
                     }
-                    rw[i] = s1 * a_Hkv + kvh;
                 }
 #pragma unroll
                 for (int part = 0; part < 2; ++part) {
@@ -561,7 +562,7 @@ __device__ __forceinline__ void tc_tile_run(const TcArgs& a, const CUtensorMap* 
                             const int it = t0 + i * 32 * NG;
                             if (it < NIT)
                                 cp_async16(sb + part * Lay::STG + it * 16,
-                                           (part ? vp8 : kp8) + (int64_t)rw[i] * D + (it % CH) * 16, true);
+                                           (part ? vp8 : kp8) + (int64_t)rw[i] * D + (it % CH) * 16, rw[i] >= 0);
                         }
                     }
                     cp_async_commit();
