@@ -149,6 +149,7 @@ __global__ void __launch_bounds__(ExtCfg<D, KV>::kThreads, 1)
         tc_init_barriers<C>(smem_u32(sm + Lay::OFF_BAR));
         mbar_fence_init();
     }
+    if (KV == kKvFp4 && warp == 2 && tid < 64 + D / 16) reinterpret_cast<int*>(sm + Lay::OFF_MARK)[tid - 64] = INT_MAX;
     if (warp == C::kMmaWarp) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;\n" ::"r"(smem_u32(tslot)));
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;\n");

@@ -212,6 +212,7 @@ template <int D, bool DEC, int NQ, int NS, int BN, int KV = kKvBf16>
 struct TcLayout {
     static constexpr int OFF_TMEM = 0;                   // TMEM base address
     static constexpr int OFF_INFO = 16;                  // tile description broadcast (16 ints)
+    static constexpr int OFF_MARK = 96;                  // extend, 4-bit pools: D / 16 ints (see below)
     static constexpr int KEEP = 128;
     static constexpr int QTILE = DEC ? 0 : 128 * D * 2;
     static constexpr int KREGION = BN * 128;             // SW128 region: BN rows x 64 columns
@@ -312,6 +313,21 @@ __device__ __forceinline__ void tc_inval_barriers(uint32_t bar0) {
         asm volatile("mbarrier.inval.shared::cta.b64 [%0];\n" ::"r"(bar0 + 8u * (uint32_t)i) : "memory");
 }
 
+// A NaN among the values of positions that only some query rows of a tile see
+// would reach the others as 0 * NaN in P V.  So (4-bit pools in extend, where a
+// NaN is a block's scale) such a scale is taken as zero, and the block's first
+// position with one is kept in shared memory: rows that see it get the NaN
+// when they are written.  Two scales of the row at `pos`, marks at `mark`.
+__device__ __forceinline__ uint32_t mark_nan(uint32_t sf, uint32_t mark, int pos) {
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+        if (((sf >> (8 * k)) & 0x7fu) == 0x7fu) {
+            asm volatile("red.shared.min.s32 [%0], %1;\n" ::"r"(mark + 4 * k), "r"(pos) : "memory");
+            sf &= ~(0xffu << (8 * k));
+        }
+    return sf;
+}
+
 template <class C>
 __device__ __forceinline__ void tc_init_barriers(uint32_t bar0) {
     auto bar = [&](int i) { return bar0 + 8u * (uint32_t)i; };
@@ -410,6 +426,7 @@ __device__ __forceinline__ void tc_tile_run(const TcArgs& a, const CUtensorMap* 
             const uint8_t* const kp4 = reinterpret_cast<const uint8_t*>(a_kp) + fp4_code_off(kvh, D);
             const uint8_t* const vp4 = reinterpret_cast<const uint8_t*>(a_vp) + fp4_code_off(kvh, D);
             const int soff = fp4_scale_off(kvh, a_Hkv, D) - fp4_code_off(kvh, D);
+            const uint32_t mark = smem_u32(sm + Lay::OFF_MARK);
             int32_t sl[TPT], rw[TPT];   // this lane's slots of the next block; rows of the block being copied
             auto lookup = [&](int j) {
 #pragma unroll
@@ -474,6 +491,9 @@ __device__ __forceinline__ void tc_tile_run(const TcArgs& a, const CUtensorMap* 
                 }
                 __syncwarp();   // a row's scales are its first piece's lane's copy
                 const uint32_t base = (v ? sV : sK) + st * Lay::KTILE;
+                // (extend) values that not every query row of the tiles sees
+                const int last_seen = DEC ? INT_MAX : ti.i7[0] - (kv_begin + j * BN);
+                const bool partly = v && last_seen < BN - 1;
 #pragma unroll
                 for (int i = 0; i < TPT; ++i) {
                     const int it = t0 + i * 32 * NG;
@@ -483,7 +503,9 @@ __device__ __forceinline__ void tc_tile_run(const TcArgs& a, const CUtensorMap* 
                         asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];\n"
                                      : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
                                      : "r"(sb + it * 16));
-                        const uint32_t sf = e4m3x2_to_f16(ld_shared_u16(sb + CODES + r * (D / 16) + 2 * c));
+                        uint32_t sfc = ld_shared_u16(sb + CODES + r * (D / 16) + 2 * c);
+                        if (partly && r > last_seen) sfc = mark_nan(sfc, mark + 8 * c, kv_begin + j * BN + r);
+                        const uint32_t sf = e4m3x2_to_f16(sfc);
                         const uint32_t s2[2] = {__byte_perm(sf, sf, 0x1010), __byte_perm(sf, sf, 0x3232)};
 #pragma unroll
                         for (int k = 0; k < 4; ++k) {
@@ -1050,6 +1072,16 @@ __device__ __forceinline__ void tc_tile_run(const TcArgs& a, const CUtensorMap* 
                 } else {
 #pragma unroll
                     for (int k = 0; k < 64; ++k) v[k] = 0.f;
+                }
+                if constexpr (F4 && !DEC) {
+                    // blocks of 16 in which the row sees a NaN (see mark_nan)
+                    uint32_t mk[4];
+                    lds128(smem_u32(sm + Lay::OFF_MARK) + 8 * c, mk);
+                    if (min(min((int)mk[0], (int)mk[1]), min((int)mk[2], (int)mk[3])) <= lim) {
+#pragma unroll
+                        for (int k = 0; k < 64; ++k)
+                            if ((int)mk[k / 16] <= lim) v[k] = __int_as_float(0x7fffffff);
+                    }
                 }
                 if constexpr (DEC) {
 #pragma unroll
