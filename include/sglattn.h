@@ -59,7 +59,7 @@ typedef struct CUstream_st* sgl_stream_t;
 
 enum {
     SGL_OK = 0,
-    SGL_ERR_INVALID_ARG = -1, /* null pointer, negative size, bad handle, malformed input */
+    SGL_ERR_INVALID_ARG = -1, /* null pointer, negative size, bad handle, malformed input; no host memory left */
     SGL_ERR_NO_SLOTS = -2,    /* pool exhausted even after evicting every unreferenced leaf */
     SGL_ERR_UNSUPPORTED = -3, /* dtype / head_dim / group size outside the supported set */
     SGL_ERR_CUDA = -4,        /* a CUDA call failed; see sgl_last_cuda_error() */

@@ -25,6 +25,7 @@
 
 #include <algorithm>
 #include <cstring>
+#include <exception>
 #include <deque>
 #include <memory>
 #include <new>
@@ -736,7 +737,7 @@ int sgl_tree_cache_finished_batch(sgl_tree* t, int32_t B, const int32_t* const* 
 }
 
 int sgl_groups_from_table(const int32_t* table, int64_t ld, const int32_t* seq_lens, int32_t B,
-                          sgl_groups* g) {
+                          sgl_groups* g) try {
     if (!g || B < 0 || (B > 0 && (!table || !seq_lens))) return SGL_ERR_INVALID_ARG;
     for (int32_t r = 0; r < B; ++r)
         if (seq_lens[r] < 0 || seq_lens[r] > ld) return SGL_ERR_INVALID_ARG;
@@ -790,6 +791,9 @@ int sgl_groups_from_table(const int32_t* table, int64_t ld, const int32_t* seq_l
     }
     emit(g, segs);
     return SGL_OK;
+} catch (const std::exception&) {   // out of host memory
+    g->clear();
+    return SGL_ERR_INVALID_ARG;
 }
 
 }  // extern "C"

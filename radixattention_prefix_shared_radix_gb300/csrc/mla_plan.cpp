@@ -24,6 +24,7 @@
 #include <algorithm>
 #include <cmath>
 #include <cstring>
+#include <exception>
 #include <functional>
 #include <new>
 #include <queue>
@@ -53,7 +54,7 @@ constexpr double kRowCost = 4096.0 / 6.0e6;
 }  // namespace
 
 extern "C" int sgl_mla_decode_plan(const sgl_mla_params* p, const int32_t* seq_lens, const sgl_prefix_groups* g,
-                                   sgl_plan** plan_out, size_t* workspace_bytes) {
+                                   sgl_plan** plan_out, size_t* workspace_bytes) try {
     if (!p || !g || !plan_out || !workspace_bytes) return SGL_ERR_INVALID_ARG;
     if (p->batch < 0 || p->num_slots < 0 || p->page_size < 1 || !(p->sm_scale >= 0.f) || std::isinf(p->sm_scale))
         return SGL_ERR_INVALID_ARG;
@@ -289,4 +290,6 @@ extern "C" int sgl_mla_decode_plan(const sgl_mla_params* p, const int32_t* seq_l
     *plan_out = plan;
     *workspace_bytes = plan->workspace_bytes;
     return SGL_OK;
+} catch (const std::exception&) {   // out of host memory
+    return SGL_ERR_INVALID_ARG;
 }

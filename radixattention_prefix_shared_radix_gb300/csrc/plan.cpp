@@ -25,6 +25,7 @@
 #include <algorithm>
 #include <cmath>
 #include <cstring>
+#include <exception>
 #include <functional>
 #include <new>
 #include <vector>
@@ -112,7 +113,7 @@ int validate_groups(int32_t B, const int32_t* seq_lens, const sgl_prefix_groups*
 extern "C" {
 
 int sgl_decode_plan(const sgl_attn_params* p, const int32_t* seq_lens, const sgl_prefix_groups* g,
-                    sgl_plan** plan_out, size_t* workspace_bytes) {
+                    sgl_plan** plan_out, size_t* workspace_bytes) try {
     int st = sgl::check_params(p);
     if (st) return st;
     if (!g || !plan_out || !workspace_bytes) return SGL_ERR_INVALID_ARG;
@@ -475,6 +476,8 @@ int sgl_decode_plan(const sgl_attn_params* p, const int32_t* seq_lens, const sgl
     *plan_out = plan;
     *workspace_bytes = plan->workspace_bytes;
     return SGL_OK;
+} catch (const std::exception&) {   // out of host memory
+    return SGL_ERR_INVALID_ARG;
 }
 
 void sgl_plan_destroy(sgl_plan* plan) {
