@@ -354,7 +354,9 @@ int sgl_plan_upload(const sgl_plan* plan, void* workspace, size_t ws_bytes, sgl_
  * (O, LSE) of every chunk are merged per (request, head) by log-sum-exp.
  * A request with seq_len 0 gets O = 0, LSE = -inf.  A NaN score (a NaN in the
  * query or in a key) makes its row's O and LSE NaN, however the plan cut the
- * work; so it does in sgl_extend_attn and sgl_mla_decode_attn. */
+ * work; so it does in sgl_extend_attn and sgl_mla_decode_attn.
+ * The workspace holds the call's partial results: calls that may overlap on
+ * the GPU (other streams, graphs replayed side by side) need one each. */
 int sgl_decode_attn(const void* q, const void* k_pool, const void* v_pool, const int32_t* req_to_token,
                     int64_t ld, const int32_t* seq_lens, const sgl_plan* plan, void* o, float* lse,
                     void* workspace, size_t ws_bytes, sgl_stream_t stream);

@@ -64,3 +64,56 @@ def test_steps_replayed_over_a_shared_prefix(hq, hkv, d, prefix):
         for r in rng.permutation(n)[:6]:
             length = int(start[r]) + 1 + i
             _close(oi[r], li[r], b.ref(r, q=qi[r].cpu(), length=length, kp=K.rows, vp=V.rows))
+
+
+@pytest.mark.parametrize("hq,hkv,d,prefix", [(32, 8, 128, 400), (16, 2, 64, 700), (32, 8, 128, 0)])
+def test_steps_back_to_back_read_what_was_just_written(hq, hkv, d, prefix):
+    """Append and decode again and again over one query buffer, one slot per request and one workspace, with no other
+    kernel in between: each decode sees its own append, not the one before it.  Held to the same calls with a wait after
+    each, bit for bit."""
+    n, steps = 24, 12
+    rng = np.random.default_rng(prefix + 1)
+    b = Batch([([("p", prefix)] if prefix else []) + [(r, int(rng.integers(1, 200)))] for r in range(n)], hq, hkv, d,
+              seed=prefix + 1)
+    plan = b.plan()
+    ws = torch.zeros(plan.workspace_bytes, dtype=torch.uint8, device="cuda")
+    sgl.sgl_plan_upload(plan, ws)
+    kp, vp, table, lens = b.device()
+    gen = torch.Generator().manual_seed(3)
+    q, k, v = (torch.randn(steps, n, h, d, generator=gen).bfloat16().cuda() for h in (hq, hkv, hkv))
+    rope = sgl.sgl_rope_create(d)
+    qr = torch.zeros_like(q[0])
+
+    def run(wait):
+        o, lse = torch.zeros_like(q), torch.zeros(steps, n, hq, device="cuda")
+
+        def calls():
+            for i in range(steps):
+                sgl.sgl_kv_append(rope, b.params(), q[i], k[i], v[i], kp, vp, table, lens, None, qr, ws)
+                sgl.sgl_decode_attn(qr, kp, vp, table, lens, plan, o[i], lse[i], ws)
+                if wait:
+                    torch.cuda.synchronize()
+        if wait:
+            calls()
+            return o, lse
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            calls()
+        for _ in range(10):
+            o.zero_()
+            graph.replay()
+        torch.cuda.synchronize()
+        return o, lse
+    want = run(True)
+    assert not any(torch.equal(want[0][i], want[0][i + 1]) for i in range(steps - 1))
+    got = run(False)
+    sgl.sgl_check(ws)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    # and outside a graph
+    o, lse = torch.zeros_like(q), torch.zeros(steps, n, hq, device="cuda")
+    for i in range(steps):
+        sgl.sgl_kv_append(rope, b.params(), q[i], k[i], v[i], kp, vp, table, lens, None, qr, ws)
+        sgl.sgl_decode_attn(qr, kp, vp, table, lens, plan, o[i], lse[i], ws)
+    sgl.sgl_check(ws)
+    assert torch.equal(o, want[0]) and torch.equal(lse, want[1])
