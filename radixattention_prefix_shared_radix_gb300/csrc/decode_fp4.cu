@@ -290,7 +290,7 @@ __device__ __forceinline__ void fp4_consumer(const Fp4Args& p, int c, uint32_t r
                         *reinterpret_cast<float4*>(dst + 2 * i) =
                             make_float4(o[i][hh] * inv, o[i][2 + hh] * inv, o[i + 1][hh] * inv, o[i + 1][2 + hh] * inv);
                 }
-                if (g == 0) (p.o ? p.lse : p.f.t.plse)[prow] = ll == 0.f ? -INFINITY : (mm + log2f(ll)) * kLn2;
+                if (g == 0) (p.o ? p.lse : p.f.t.plse)[prow] = ll == 0.f ? -INFINITY : (log2f(ll) - (kPShift - mm)) * kLn2;
             }
         }
     };
@@ -426,7 +426,10 @@ __device__ __forceinline__ void fp4_consumer(const Fp4Args& p, int c, uint32_t r
         // ---- softmax (base 2).  The maximum that P is taken against moves
         // only when a score exceeds it by more than 8 (a factor 2^8: P stays
         // within f16), so a step needs no maximum over the lanes, only a vote
-        // that nothing exceeds it.
+        // that nothing exceeds it.  P is taken 2^kPShift times as large (up
+        // to 2^15), so that weights down to 2^-21 of the largest keep all of
+        // f16's bits and smaller ones are off by 2^-32 of it at most: a long
+        // context's many small weights count in full beside a large one.
         if (live != 0xffffffffu) {
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
@@ -460,7 +463,7 @@ __device__ __forceinline__ void fp4_consumer(const Fp4Args& p, int c, uint32_t r
                 o[i][3] *= a1;
             }
         }
-        const float u0 = m0 == -INFINITY ? 0.f : -m0, u1 = m1 == -INFINITY ? 0.f : -m1;
+        const float u0 = m0 == -INFINITY ? 0.f : kPShift - m0, u1 = m1 == -INFINITY ? 0.f : kPShift - m1;
         uint32_t pf[2][2];                      // P^T fragments of the two groups
 #pragma unroll
         for (int u = 0; u < 2; ++u) {

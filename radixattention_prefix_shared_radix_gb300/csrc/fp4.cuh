@@ -18,6 +18,10 @@
 
 namespace sgldev {
 
+// Attention over a 4-bit pool holds the softmax weights as f16: 2^kPShift times
+// exp2(score - maximum), the maximum being up to 8 too low.
+constexpr float kPShift = 7.f;
+
 // bytes of one head's codes and scales, of a block of `n` <= 4 heads, and
 // the offset of head h's block (every block before it is full)
 __host__ __device__ constexpr int fp4_head_bytes(int d) { return d / 2 + d / 16; }

@@ -1022,7 +1022,9 @@ __device__ __forceinline__ void tc_tile_run(const TcArgs& a, const CUtensorMap* 
                         }
                     }
                     if (need) m_used = m_new;
-                    const float nmu = m_used == -INFINITY ? 0.f : -m_used;
+                    // (4-bit pools: P 2^kPShift times as large, within f16's
+                    // range, so that small weights keep their bits)
+                    const float nmu = m_used == -INFINITY ? 0.f : F4 ? kPShift - m_used : -m_used;
                     // p = 2^(s sc - m): one packed FMA per pair, one MUFU op
                     // each, one packed add into the pair sums, one conversion
                     // per pair
@@ -1046,7 +1048,7 @@ __device__ __forceinline__ void tc_tile_run(const TcArgs& a, const CUtensorMap* 
             tc_fence_after();
             const float l = l0 + l1;
             const float inv = l > 0.f ? (F8 ? a.v_scale : 1.f) / l : l;   // (0, or a NaN that is kept)
-            const float lse = l == 0.f ? -INFINITY : (m_used + log2f(l)) * kLn2;
+            const float lse = l == 0.f ? -INFINITY : (F4 ? log2f(l) - (kPShift - m_used) : m_used + log2f(l)) * kLn2;
             // decode: the row goes through shared memory (the K/V stages are
             // idle once every MMA is done; rows padded by 16 bytes, so a
             // warp's 16-byte stores meet no bank twice) and out with one bulk
