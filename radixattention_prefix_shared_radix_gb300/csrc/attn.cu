@@ -461,6 +461,7 @@ static int extend_impl(const void* q_new, const void* k_new, const void* v_new, 
         rows += params->host_extend_lens[r];
     }
     if (rows > 0 && (!q_new || !k_pool || !v_pool || !req_to_token || !o || !lse)) return SGL_ERR_INVALID_ARG;
+    if (rows > 0 && params->dtype == SGL_DTYPE_BF16_FP8KV && params->num_slots == 0) return SGL_ERR_INVALID_ARG;
     if (rows > 0 && k_new && (!v_new || !aligned(k_new, 16) || !aligned(v_new, 16))) return SGL_ERR_INVALID_ARG;
     if (rows * params->num_kv_heads > INT32_MAX) return SGL_ERR_UNSUPPORTED;
     if (!workspace || !aligned(workspace, sgl::kWsAlign) || ws_bytes < sgl::kWsAlign) return SGL_ERR_WORKSPACE;

@@ -181,6 +181,8 @@ int sgl_decode_plan(const sgl_attn_params* p, const int32_t* seq_lens, const sgl
         mem.push_back(r);
         add_units(r, seq_lens[r], seq_lens[r], (int32_t)mem.size() - 1, 1, true);
     }
+    // (the E4M3 tiles read the pool's first row for slots outside the pool)
+    if (max_wide > 0 && p->dtype == SGL_DTYPE_BF16_FP8KV && p->num_slots == 0) return SGL_ERR_INVALID_ARG;
     const int64_t n_ctas = sms;
     // Wide chunks run on tile CTAs whose streaming warps start only when
     // their tiles are done (so the two never compete for an SM's issue slots

@@ -545,7 +545,9 @@ __device__ __forceinline__ void tc_tile_run(const TcArgs& a, const CUtensorMap* 
             // barrier.  A block's slots are looked up one block before its
             // copies are issued and checked only then, so no lookup stalls
             // the conversions.  Positions past the range re-read the range's
-            // last position.
+            // last position, slots outside the pool its first row (so pools
+            // without rows are refused before; zeros in their place, as with
+            // 4-bit pools, cost 1 to 3% however they were made).
             constexpr int CH = D / 16;
             constexpr int NIT = BN * CH;
             constexpr int TPT = (NIT + 32 * NG - 1) / (32 * NG);
@@ -570,11 +572,12 @@ __device__ __forceinline__ void tc_tile_run(const TcArgs& a, const CUtensorMap* 
 #pragma unroll
                 for (int i = 0; i < TPT; ++i) {
                     const int it = t0 + i * 32 * NG;
-                    rw[i] = sl[i] * a_Hkv + kvh;
-                    if (sl[i] < 0 || sl[i] >= a_num_slots) {   // (a row of zeros)
+                    int32_t s1 = sl[i];
+                    if (s1 < 0 || s1 >= a_num_slots) {
                         if (j < nb && it < NIT && it % CH == 0) atomicOr(a_err, 1u);
-                        rw[i] = -1;
+                        s1 = 0;
                     }
+                    rw[i] = s1 * a_Hkv + kvh;
                 }
 #pragma unroll
                 for (int part = 0; part < 2; ++part) {
@@ -584,7 +587,7 @@ __device__ __forceinline__ void tc_tile_run(const TcArgs& a, const CUtensorMap* 
                             const int it = t0 + i * 32 * NG;
                             if (it < NIT)
                                 cp_async16(sb + part * Lay::STG + it * 16,
-                                           (part ? vp8 : kp8) + (int64_t)rw[i] * D + (it % CH) * 16, rw[i] >= 0);
+                                           (part ? vp8 : kp8) + (int64_t)rw[i] * D + (it % CH) * 16, true);
                         }
                     }
                     cp_async_commit();
@@ -1047,7 +1050,7 @@ __device__ __forceinline__ void tc_tile_run(const TcArgs& a, const CUtensorMap* 
             wait(C::DONE, stt.T & 1);
             tc_fence_after();
             const float l = l0 + l1;
-            const float inv = l > 0.f ? (F8 ? a.v_scale : 1.f) / l : l;   // (0, or a NaN that is kept)
+            const float inv = l == 0.f ? 0.f : (F8 ? a.v_scale : 1.f) / l;
             const float lse = l == 0.f ? -INFINITY : (F4 ? log2f(l) - (kPShift - m_used) : m_used + log2f(l)) * kLn2;
             // decode: the row goes through shared memory (the K/V stages are
             // idle once every MMA is done; rows padded by 16 bytes, so a

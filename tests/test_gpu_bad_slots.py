@@ -1,5 +1,5 @@
-"""Slots outside the pool in the tiles of shared prefixes and in extend, over FP8 and 4-bit pools: nothing is read for them
-(the position counts as a zero key and a zero value) and they are reported, in a pool without any rows too."""
+"""Slots outside the pool in the tiles of shared prefixes and in extend, over 4-bit pools: nothing is read for them (the
+position counts as a zero key and a zero value) and they are reported, in a pool without any rows too."""
 
 import numpy as np
 import pytest
@@ -7,7 +7,6 @@ import torch
 
 import radixattention_prefix_shared_radix_gb300 as sgl
 from oracle import fp4
-from oracle.fp8 import e4m3_to_float
 from tests.test_gpu_fp4 import KS, VS, _own, _ref, _star
 from tests.test_gpu_nan import Run
 
@@ -22,9 +21,7 @@ def _built():
 
 def _values(r, pool, scale, slots, bad):
     """Float64 rows of `slots`, zeros where `bad`."""
-    s = np.where(bad, 0, slots)
-    x = (fp4.values(pool.numpy()[s], r.hkv, r.d, scale) if r.kind == "fp4" else e4m3_to_float(pool.numpy()[s]) * scale)
-    return np.where(bad[:, None, None], 0.0, x)
+    return np.where(bad[:, None, None], 0.0, fp4.values(pool.numpy()[np.where(bad, 0, slots)], r.hkv, r.d, scale))
 
 
 def _check(r, table, slots_in_pool, o, lse, q, req, length):
@@ -35,12 +32,11 @@ def _check(r, table, slots_in_pool, o, lse, q, req, length):
     assert (np.abs(o.double().numpy() - O) <= to).all() and (np.abs(lse.double().numpy() - L) <= tl).all()
 
 
-@pytest.mark.parametrize("kind", ["fp8", "fp4"])
 @pytest.mark.parametrize("hq,hkv,d", [(16, 4, 64), (32, 8, 128), (9, 9, 64)])
 @pytest.mark.parametrize("rows", [None, 0])
-def test_extend(kind, hq, hkv, d, rows):
+def test_extend(hq, hkv, d, rows):
     pre, ext = np.array([0, 150, 30]), np.array([140, 70, 1])
-    r = Run(kind, _own(list(pre + ext)), hq, hkv, d, seed=11)
+    r = Run("fp4", _own(list(pre + ext)), hq, hkv, d, seed=11)
     b, n = r.b, int(ext.sum())
     slots = b.slots if rows is None else rows
     b.table[0, 7], b.table[0, 100], b.table[1, 20], b.table[1, 199], b.table[2, 30] = slots, -1, 1 << 30, -7, slots
@@ -61,11 +57,10 @@ def test_extend(kind, hq, hkv, d, rows):
             at += 1
 
 
-@pytest.mark.parametrize("kind", ["fp8", "fp4"])
 @pytest.mark.parametrize("hq,hkv,d", [(16, 4, 64), (32, 8, 128)])
-def test_shared_prefix(kind, hq, hkv, d):
+def test_shared_prefix(hq, hkv, d):
     # (own parts of one token: what is read for the tiles is the prefix alone)
-    r = Run(kind, _star(30, 500, 1, 1), hq, hkv, d, seed=12)
+    r = Run("fp4", _star(30, 500, 1, 1), hq, hkv, d, seed=12)
     b = r.b
     g = sgl.sgl_groups_create()
     sgl.sgl_groups_from_table(b.table, b.lens, g)
