@@ -102,9 +102,7 @@ __device__ __noinline__ void merge_head(const MergeArgs& m, int idx, int j, int 
 #pragma unroll
             for (int u = 0; u < U; ++u) mx = fmaxf(mx, lu[u]);
             if (mx == -INFINITY) {   // nothing yet (the maximum leaves NaN out)
-#pragma unroll
-                for (int u = 0; u < U; ++u)
-                    if (lu[u] != lu[u]) L = lu[u];
+                if (__any_sync(0xffffffffu, ls != ls)) L = __int_as_float(0x7fffffff);
                 continue;
             }
             const float sc = exp2f((M - mx) * kLog2e);   // 0 while nothing was accumulated
