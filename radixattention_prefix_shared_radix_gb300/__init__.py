@@ -633,9 +633,10 @@ def sgl_extend_attn(q_new, k_pool, v_pool, req_to_token, prefix_lens, extend_len
                                workspace.nbytes, _stream(stream)), "sgl_extend_attn")
 
 
-def _row_bytes(params):
-    """Bytes of one pool row (a token's K or V of every head)."""
-    n, kind = params.num_kv_heads * params.head_dim, params.dtype
+def _row_bytes(params, kind=None, n=None):
+    """Bytes of one pool row (a token's K or V of every head); kind and n: params' dtype and elements, where at hand."""
+    if kind is None:
+        kind, n = params.dtype, params.num_kv_heads * params.head_dim
     if kind == SGL_DTYPE_BF16_FP4KV:
         return (n // 2 + n // 16 + 15) // 16 * 16
     return n << (2 if kind == SGL_DTYPE_F32 else 1 if kind == SGL_DTYPE_BF16 else 0)
@@ -787,8 +788,8 @@ def sgl_kv_append(rope, params, q, k_new, v_new, k_pool, v_pool, req_to_token, l
     padded batch) rows ordered by request, row i of request r at position lens[r] + i; None: row r is request r's
     newest token, at position lens[r] - 1."""
     T = _T or _torch()
-    dt = T.float32 if params.dtype == SGL_DTYPE_F32 else T.bfloat16
-    hkv, d, dev = params.num_kv_heads, params.head_dim, T._C._cuda_getDevice()
+    kind, hkv, d, dev = params.dtype, params.num_kv_heads, params.head_dim, T._C._cuda_getDevice()
+    dt = T.float32 if kind == SGL_DTYPE_F32 else T.bfloat16
     pk, sk, n, _ = _rows(k_new, "k_new", hkv, d, dt, None, dev)
     pv, sv, _, _ = _rows(v_new, "v_new", hkv, d, dt, n, dev)
     pq = pqo = None
@@ -801,11 +802,13 @@ def sgl_kv_append(rope, params, q, k_new, v_new, k_pool, v_pool, req_to_token, l
     rows = req_to_token.shape
     if len(rows) != 2 or rows[0] < B[0]:
         raise ValueError("req_to_token must have a row per request")
-    need = params.num_slots * _row_bytes(params)
+    pkp, pvp = _flat(k_pool, "k_pool", dev), _flat(v_pool, "v_pool", dev)
+    need = params.num_slots * _row_bytes(params, kind, hkv * d)
+    if k_pool.nbytes < need or v_pool.nbytes < need:
+        _writable(pkp, k_pool, "k_pool", need)
+        _writable(pvp, v_pool, "v_pool", need)
     st = _lib().sgl_kv_append(None if rope is None else rope.handle, ctypes.byref(params), pq, sq, pk, sk, pv, sv,
-                              _writable(_flat(k_pool, "k_pool", dev), k_pool, "k_pool", need),
-                              _writable(_flat(v_pool, "v_pool", dev), v_pool, "v_pool", need),
-                              _flat(req_to_token, "req_to_token", dev, T.int32), rows[1],
+                              pkp, pvp, _flat(req_to_token, "req_to_token", dev, T.int32), rows[1],
                               _flat(lens, "lens", dev, T.int32, B),
                               None if extend_lens is None else _flat(extend_lens, "extend_lens", dev, T.int32, B), n, pqo,
                               sqo, _flat(workspace, "workspace", dev), workspace.nbytes, _stream(stream))
