@@ -443,8 +443,9 @@ int sgl_extend_workspace_bytes(const sgl_attn_params* params, size_t* bytes);
  * New token i of request r (position p = prefix_lens[r] + i) attends to
  * positions 0..p of row r.  (Over bf16 and E4M3 pools a NaN or an infinity
  * among the values of a chunk's later tokens can still reach its earlier
- * ones, as zero times it; over fp32 and 4-bit pools it cannot.)  workspace: device, >= sgl_extend_workspace_bytes,
- * 256-byte aligned; its error word is cleared by this call.
+ * ones, as zero times it; over fp32 and 4-bit pools it cannot.)
+ * workspace: device, >= sgl_extend_workspace_bytes, 256-byte aligned; its
+ * error word gathers errors until sgl_check clears it.
  * ["SGLang 深度解读" "5. Attention 层": K/V written before attention;
  * "SGLang 深度拆解" §3.2 PagedPrefill: skip the cached prefix's compute] */
 int sgl_extend_attn(const void* q_new, const void* k_pool, const void* v_pool, const int32_t* req_to_token,

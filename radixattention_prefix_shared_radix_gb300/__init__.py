@@ -833,7 +833,8 @@ def sgl_mla_kv_append(rope, params, q, kv_new, kv_pool, req_to_token, lens, exte
         raise ValueError("req_to_token must have a row per request")
     pool = _writable(_flat(kv_pool, "kv_pool", dev), kv_pool, "kv_pool", params.num_slots * d * 2)
     st = _lib().sgl_mla_kv_append(None if rope is None else rope.handle, ctypes.byref(params), pq, sq, pk, sk, pool,
-                                  _flat(req_to_token, "req_to_token", dev, T.int32), rows[1], _flat(lens, "lens", dev, T.int32, B),
+                                  _flat(req_to_token, "req_to_token", dev, T.int32), rows[1],
+                                  _flat(lens, "lens", dev, T.int32, B),
                                   None if extend_lens is None else _flat(extend_lens, "extend_lens", dev, T.int32, B), n,
                                   pqo, sqo, _flat(workspace, "workspace", dev), workspace.nbytes, _stream(stream))
     if st:

@@ -38,10 +38,14 @@
 // conversion and half a packed multiplication (its scale).
 // Conversions, packed multiplications and integer operations each run at 64
 // lanes per clock and SM, mma.sync at one m16n8k16 per two clocks (measured).
-// Measured: 64 requests of 1 to 8192 tokens (273 MB) 57.1 us, of which the
-// merge is 4; an SM's two streams take 0.032 us a position (8 heads of 128),
-// 0.026 being the copy's rate, with 57% of the issue slots and half of the
-// integer pipe busy.  One request of 180 tokens: 7.0 us, 2.6 of them the merge.
+// Measured: 64 requests of 1 to 8192 tokens (273 MB, 40 us at the copy's rate)
+// 57.1 us.  Start and merge take 8 of the 17 above that.  In between an SM's
+// two streams take 0.032 us a position (8 heads of 128) where the copies alone
+// need 0.026, and no unit is full: issue slots 57%, integer pipe 51%, memory
+// 61%, 28% of the warps that an SM can hold.  What is left is the latency of a
+// consumer's chain from load to product: without the multiplications by scales
+// (timing only) it is 4.7 us shorter, without the conversions 0.6.  One request
+// of 180 tokens: 7.0 us, 2.6 of them the merge.
 
 #include <cudaTypedefs.h>
 
