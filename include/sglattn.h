@@ -91,7 +91,8 @@ enum { SGL_DTYPE_F32 = 0, SGL_DTYPE_BF16 = 1, SGL_DTYPE_BF16_FP8KV = 2, SGL_DTYP
  * nearest to max|x| / (6 * scale) (at most 448; NaN where a value is NaN), the
  * codes those of x / (sf * scale), both to nearest even, saturating at 6; all
  * codes are zeros where sf is 0.  The query enters the tensor cores as f16,
- * as with SGL_DTYPE_BF16_FP8KV. */
+ * as with SGL_DTYPE_BF16_FP8KV (elements below 2^-14 keep fewer bits, 2^-25
+ * and less count as zero). */
 
 /* Name of a status code (static string). */
 const char* sgl_status_string(int status);
