@@ -590,6 +590,29 @@ typedef struct sgl_rope_table sgl_rope_table;
  * from it, so it may be destroyed once they have returned, and serves any
  * number of threads and devices). */
 int sgl_rope_create(const sgl_rope_params* params, sgl_rope_table** out);
+
+/* Several axes (time, height, width of a token of an image or a video): each
+ * pair turns by the token's position on one of them.
+ *   BLOCKS  axis 0 has the first sections[0] pairs, axis 1 the next, ..
+ *   TURNS   the axes take one pair each in turn; an axis that has its
+ *           sections[a] pairs is passed over
+ * own_ladder 0: pair j has the frequency it has without axes.  1: the i-th
+ * pair of axis a has that of pair i of a rotation of 2 * sections[a] elements
+ * (for the scalings too: rot_dim above means 2 * sections[a]). */
+enum { SGL_ROPE_AXES_BLOCKS = 0, SGL_ROPE_AXES_TURNS = 1 };
+enum { SGL_ROPE_MAX_AXES = 4 };
+typedef struct {
+    int32_t num_axes;                        /* 1 .. 4 */
+    int32_t sections[SGL_ROPE_MAX_AXES];     /* pairs of each axis, >= 1; their sum is rot_dim / 2 */
+    int32_t arrange;                         /* SGL_ROPE_AXES_* */
+    int32_t own_ladder;                      /* 0 or 1 (NTK: sections of at least 2) */
+} sgl_rope_axes;
+
+/* sgl_rope_create for a rotation with several axes.  sgl_rope and
+ * sgl_kv_append_at take positions on every axis; sgl_kv_append and
+ * sgl_mla_kv_append take a token to stand at its place in the row on all of
+ * them (as text does). */
+int sgl_rope_create_axes(const sgl_rope_params* params, const sgl_rope_axes* axes, sgl_rope_table** out);
 void sgl_rope_destroy(sgl_rope_table* rope);
 
 /* Rotary positions of query and key rows.
@@ -598,7 +621,9 @@ void sgl_rope_destroy(sgl_rope_table* rope);
  *                apart (e.g. columns of a fused projection); either may have
  *                0 heads
  *   positions    device int32 [n_rows], any value up to 2^31 - 1; a row at a
- *                negative position is left as it is in the outputs
+ *                negative position is left as it is in the outputs.  With
+ *                several axes [num_axes, n_rows], axis a's from a * n_rows on
+ *                (negative: on any axis)
  *   q_out, k_out rows as q and k (the part of a head that is not rotated is
  *                copied); may be q and k themselves (same stride), and must
  *                not overlap them in any other way
@@ -644,7 +669,19 @@ int sgl_kv_append(const sgl_rope_table* rope, const sgl_attn_params* params, con
                   int64_t n_rows, void* q_out, int64_t q_out_stride, void* workspace, size_t ws_bytes,
                   sgl_stream_t stream);
 
-/* The same for an MLA pool: kv_new device bf16 [n_rows, 576] (the latent,
+/* sgl_kv_append with the rotation's positions given: device int32
+ * [num_axes, n_rows], row n of axis a at a * n_rows + n (one axis: [n_rows]).
+ * For tokens with positions on several axes, and for requests whose rows no
+ * longer count their tokens (sgl_kv_evict).  Where a row is stored is still
+ * found by lens and extend_lens.  A row at a negative position (on any axis)
+ * is left out: neither rotated nor stored.  rope must be given. */
+int sgl_kv_append_at(const sgl_rope_table* rope, const sgl_attn_params* params, const void* q, int64_t q_stride,
+                     const void* k_new, int64_t k_stride, const void* v_new, int64_t v_stride, void* k_pool,
+                     void* v_pool, const int32_t* req_to_token, int64_t ld, const int32_t* lens,
+                     const int32_t* extend_lens, const int32_t* positions, int64_t n_rows, void* q_out,
+                     int64_t q_out_stride, void* workspace, size_t ws_bytes, sgl_stream_t stream);
+
+/* sgl_kv_append for an MLA pool: kv_new device bf16 [n_rows, 576] (the latent,
  * then the position part), q [n_rows, Hq, 576]; rope with head_dim 576
  * (normally rot_dim 64 at rot_offset 512).
  * [CS349D lecture-16 notes §5.1: one stored row of a latent and a position
@@ -653,6 +690,98 @@ int sgl_mla_kv_append(const sgl_rope_table* rope, const sgl_mla_params* params, 
                       const void* kv_new, int64_t kv_stride, void* kv_pool, const int32_t* req_to_token, int64_t ld,
                       const int32_t* lens, const int32_t* extend_lens, int64_t n_rows, void* q_out,
                       int64_t q_out_stride, void* workspace, size_t ws_bytes, sgl_stream_t stream);
+
+/* ======================================================================== */
+/* Cached tokens by the attention they get                                  */
+/* ======================================================================== */
+
+/* Device workspace that sgl_attn_weights needs (bytes, a multiple of 256): in
+ * the decode form (no host_extend_lens in params) 256; else by the lengths in
+ * params->host_prefix_lens / host_extend_lens and by `window`. */
+int sgl_attn_weights_workspace_bytes(const sgl_attn_params* params, int32_t window, size_t* bytes);
+
+/* The attention weights that each cached token gets from a call's queries,
+ * summed over query rows and heads, added to what it has gathered:
+ *   scores_out[r, p] = decay * scores_in[r, p]
+ *       + sum over asking rows i of request r with p in their context, and
+ *         over query heads h, of exp(sm_scale * <q[i, h], k_p> - lse[i, h])
+ * for every position p of the request's context.  scores_in counts at the
+ * positions that the call before knew: all but the newest token's (decode), all
+ * but the new tokens' (chunks); those begin at 0.
+ *   q, lse       device [N, Hq, d] and fp32 [N, Hq]: the queries of an attention
+ *                call and the log-sum-exp that it gave (a row at -inf adds
+ *                nothing)
+ *   k_pool       as in the attention call (a 4-bit or E4M3 pool's k_scale from
+ *                params; v_scale is not used but checked)
+ *   lens, extend_lens  device int32 [B].  extend_lens NULL (decode): row r is
+ *                request r's newest token and sees positions 0 .. lens[r] - 1
+ *                (N = B; lens[r] = 0: nothing).  Else rows ordered by request,
+ *                row i of request r at position lens[r] + i, seeing positions
+ *                up to its own; params->host_prefix_lens and host_extend_lens
+ *                are host copies of the two, as in sgl_extend_attn
+ *   window       chunks: the last `window` rows of each request ask (0: all)
+ *   scores_in    device fp32 [B, scores_ld], or NULL: as zeros (decay unused);
+ *                scores_out: likewise, may be scores_in itself and must not
+ *                overlap it otherwise.  Positions past a context are neither
+ *                read nor written
+ *   decay        what a gathered score keeps, >= 0 and finite
+ * The products are those of the attention call on the same pool (fp32 sums;
+ * an E4M3 or 4-bit pool takes the query as f16, elements out of its range set
+ * SGL_ERR_BOUNDS for sgl_check); the weights and their sums are fp32, always
+ * added in the same order.  A slot outside the pool gives its token no weight
+ * and sets bit 0 of the workspace's error word; a length outside the table sets
+ * bit 1 and leaves the request's scores as they were.  A prefix that requests
+ * share is read once for each of them.
+ * workspace: device, 256-byte aligned, sgl_attn_weights_workspace_bytes (a
+ * decode plan's serves in the decode form); calls that may overlap on the GPU
+ * need one each.  Can be captured; the decode form follows lens at replay.
+ * ["SGLang 深度解读" "5. Attention 层": attention over req_to_token rows, whose
+ * weights these are] */
+int sgl_attn_weights(const void* q, const float* lse, const void* k_pool, const int32_t* req_to_token, int64_t ld,
+                     const int32_t* lens, const int32_t* extend_lens, const sgl_attn_params* params, int32_t window,
+                     const float* scores_in, float* scores_out, int64_t scores_ld, float decay, void* workspace,
+                     size_t ws_bytes, sgl_stream_t stream);
+
+typedef struct {
+    int32_t batch;          /* B >= 0 */
+    int32_t page_size;      /* P >= 1: pages of P positions, counted from a row's start, stay or go as a whole */
+    int32_t sinks;          /* the first positions, and */
+    int32_t recent;         /* the last ones, that stay whatever their scores (>= 0; their pages) */
+} sgl_evict_params;
+
+/* Tokens with low scores leave their requests' rows.  A request of n = lens[r]
+ * tokens with n > budgets[r] keeps the pages of its first `sinks` and its last
+ * `recent` positions, a last page that is not full, and of the other pages
+ * those of the highest scores (a page's is its highest token's; NaN counts as
+ * -infinity; of equal ones the earlier page stays), as many as budgets[r]
+ * tokens have room for.  (What stays whatever its score may be more than the
+ * budget.)  Other requests keep all.  What is kept closes up, in order:
+ *   scores       device fp32 [B, scores_ld] -> scores_out (0 in the positions
+ *                that the request loses at its end)
+ *   req_to_token device int32 [B, ld] -> table_out (-1 there)
+ *   positions    device int32 [B, ld] -> positions_out (-1 there), or both NULL:
+ *                anything else that a token carries, such as its place in the
+ *                text, which the rotation of new tokens goes by from now on
+ *   lens         device int32 [B] -> lens_out
+ *   budgets      device int32 [B]
+ *   evicted      device int32 [B, evicted_ld], or NULL: the slots that left row
+ *                r, in order, in its first evicted_count[r] entries (device
+ *                int32 [B], or NULL).  Slots past evicted_ld are counted, not
+ *                written, and set bit 1 of the error word.  The caller frees
+ *                those that no other row and no tree node holds
+ * Each output may be its input itself (the rows change in place) and must not
+ * overlap an input otherwise; entries of outputs past lens[r] stay as they
+ * were.  Slots are moved, not looked at.  A length outside [0, ld] or
+ * scores_ld sets bit 1 and counts as the nearest end.  The cached keys stay
+ * where they are and as they were rotated.
+ * workspace: device, 256-byte aligned, its first 256 bytes (the error word;
+ * calls may share it).  Can be captured.
+ * ["SGLang 深度拆解" §2.3: the cache keeps what its budget allows; there whole
+ * sequences by last use, here a sequence's tokens by attention] */
+int sgl_kv_evict(const sgl_evict_params* params, const float* scores, int64_t scores_ld, const int32_t* req_to_token,
+                 int64_t ld, const int32_t* positions, const int32_t* lens, const int32_t* budgets, float* scores_out,
+                 int32_t* table_out, int32_t* positions_out, int32_t* lens_out, int32_t* evicted, int64_t evicted_ld,
+                 int32_t* evicted_count, void* workspace, size_t ws_bytes, sgl_stream_t stream);
 
 /* Wait for `stream`, read the workspace's error word and clear it.
  * SGL_OK, or SGL_ERR_BOUNDS if a kernel skipped an out-of-range slot or a

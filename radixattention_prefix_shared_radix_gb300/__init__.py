@@ -94,7 +94,18 @@ class SglRopeParams(ctypes.Structure):
                 ("high", ctypes.c_double), ("attention_factor", ctypes.c_double)]
 
 
+class SglRopeAxes(ctypes.Structure):
+    _fields_ = [("num_axes", ctypes.c_int32), ("sections", ctypes.c_int32 * 4), ("arrange", ctypes.c_int32),
+                ("own_ladder", ctypes.c_int32)]
+
+
+class SglEvictParams(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int32), ("page_size", ctypes.c_int32), ("sinks", ctypes.c_int32),
+                ("recent", ctypes.c_int32)]
+
+
 SGL_ROPE_HALF, SGL_ROPE_PAIRS = 0, 1
+SGL_ROPE_AXES_BLOCKS, SGL_ROPE_AXES_TURNS = 0, 1
 (SGL_ROPE_SCALE_NONE, SGL_ROPE_SCALE_LINEAR, SGL_ROPE_SCALE_NTK, SGL_ROPE_SCALE_YARN,
  SGL_ROPE_SCALE_BANDED) = range(5)
 
@@ -153,15 +164,27 @@ _SIGS = {
     "sgl_mla_decode_attn": (ctypes.c_int, [_P, _P, _P, ctypes.c_int64, _P, _P, _P, _P, _P, ctypes.c_size_t, _P]),
     "sgl_fp4_row_bytes": (ctypes.c_int, [ctypes.c_int32, ctypes.c_int32, _I64P]),
     "sgl_rope_create": (ctypes.c_int, [ctypes.POINTER(SglRopeParams), ctypes.POINTER(_P)]),
+    "sgl_rope_create_axes": (ctypes.c_int, [ctypes.POINTER(SglRopeParams), ctypes.POINTER(SglRopeAxes),
+                                            ctypes.POINTER(_P)]),
     "sgl_rope_destroy": (None, [_P]),
     "sgl_rope": (ctypes.c_int, [_P, ctypes.c_int32, _P, ctypes.c_int64, ctypes.c_int32, _P, ctypes.c_int64,
                                 ctypes.c_int32, _P, ctypes.c_int64, _P, ctypes.c_int64, _P, ctypes.c_int64, _P]),
     "sgl_kv_append": (ctypes.c_int, [_P, ctypes.POINTER(SglAttnParams), _P, ctypes.c_int64, _P, ctypes.c_int64, _P,
                                      ctypes.c_int64, _P, _P, _P, ctypes.c_int64, _P, _P, ctypes.c_int64, _P,
                                      ctypes.c_int64, _P, ctypes.c_size_t, _P]),
+    "sgl_kv_append_at": (ctypes.c_int, [_P, ctypes.POINTER(SglAttnParams), _P, ctypes.c_int64, _P, ctypes.c_int64, _P,
+                                        ctypes.c_int64, _P, _P, _P, ctypes.c_int64, _P, _P, _P, ctypes.c_int64, _P,
+                                        ctypes.c_int64, _P, ctypes.c_size_t, _P]),
     "sgl_mla_kv_append": (ctypes.c_int, [_P, ctypes.POINTER(SglMlaParams), _P, ctypes.c_int64, _P, ctypes.c_int64, _P,
                                          _P, ctypes.c_int64, _P, _P, ctypes.c_int64, _P, ctypes.c_int64, _P,
                                          ctypes.c_size_t, _P]),
+    "sgl_attn_weights_workspace_bytes": (ctypes.c_int, [ctypes.POINTER(SglAttnParams), ctypes.c_int32,
+                                                        ctypes.POINTER(ctypes.c_size_t)]),
+    "sgl_attn_weights": (ctypes.c_int, [_P, _P, _P, _P, ctypes.c_int64, _P, _P, ctypes.POINTER(SglAttnParams),
+                                        ctypes.c_int32, _P, _P, ctypes.c_int64, ctypes.c_float, _P, ctypes.c_size_t,
+                                        _P]),
+    "sgl_kv_evict": (ctypes.c_int, [ctypes.POINTER(SglEvictParams), _P, ctypes.c_int64, _P, ctypes.c_int64, _P, _P, _P,
+                                    _P, _P, _P, _P, _P, ctypes.c_int64, _P, _P, ctypes.c_size_t, _P]),
 }
 
 _LIB = None
@@ -684,12 +707,13 @@ def sgl_fp4_row_bytes(num_kv_heads, head_dim):
 
 
 class Rope:
-    """Owns an sgl_rope_table handle; head_dim and rot_dim as given."""
+    """Owns an sgl_rope_table handle; head_dim, rot_dim and the number of axes as given."""
 
-    def __init__(self, handle, head_dim, rot_dim):
+    def __init__(self, handle, head_dim, rot_dim, axes=1):
         self.handle = handle
         self.head_dim = head_dim
         self.rot_dim = rot_dim
+        self.axes = axes
 
     def __del__(self):
         if self.handle and _LIB is not None:
@@ -698,13 +722,21 @@ class Rope:
 
 
 def sgl_rope_create(head_dim, rot_dim=0, rot_offset=0, layout=SGL_ROPE_HALF, scaling=SGL_ROPE_SCALE_NONE, theta=10000.0,
-                    factor=1.0, original_positions=0, low=0.0, high=0.0, attention_factor=0.0):
-    """The frequencies of a rotation (rot_dim 0: the whole head from rot_offset on)."""
+                    factor=1.0, original_positions=0, low=0.0, high=0.0, attention_factor=0.0, axes=None,
+                    arrange=SGL_ROPE_AXES_BLOCKS, own_ladder=False):
+    """The frequencies of a rotation (rot_dim 0: the whole head from rot_offset on).  axes: pairs of each axis, where a
+    token has positions on several (their sum is rot_dim / 2)."""
     p = SglRopeParams(head_dim, rot_dim or head_dim - rot_offset, rot_offset, layout, scaling, theta, factor,
                       original_positions, low, high, attention_factor)
     h = _P()
-    _ok(_lib().sgl_rope_create(ctypes.byref(p), ctypes.byref(h)), "sgl_rope_create")
-    return Rope(h, p.head_dim, p.rot_dim)
+    if axes is None:
+        _ok(_lib().sgl_rope_create(ctypes.byref(p), ctypes.byref(h)), "sgl_rope_create")
+        return Rope(h, p.head_dim, p.rot_dim)
+    if not 1 <= len(axes) <= 4:
+        raise ValueError("axes must have one to four sections")
+    a = SglRopeAxes(len(axes), (ctypes.c_int32 * 4)(*axes), arrange, int(own_ladder))
+    _ok(_lib().sgl_rope_create_axes(ctypes.byref(p), ctypes.byref(a), ctypes.byref(h)), "sgl_rope_create_axes")
+    return Rope(h, p.head_dim, p.rot_dim, len(axes))
 
 
 def _rows(t, what, heads, dim, dtype, n, dev):
@@ -745,9 +777,15 @@ def _refuse(t, what, dtype, shape, dev, layout):
     raise ValueError("%s must %s" % (what, layout))
 
 
+def _positions(rope, t, n, dev):
+    """The address of a rotation's positions: int32 [axes, n] (one axis: [n] or [1, n])."""
+    shape = (n,) if rope.axes == 1 and t.dim() == 1 else (rope.axes, n)
+    return _flat(t, "positions", dev, _T.int32, shape)
+
+
 def sgl_rope(rope, q, k, positions, q_out=None, k_out=None, stream=None):
     """Rotary positions of q [N, Hq, head_dim] and k [N, Hk, head_dim] (either may be None; rows may be strided, as
-    columns of a fused projection are) into q_out and k_out (None: in place).  positions: int32 [N]."""
+    columns of a fused projection are) into q_out and k_out (None: in place).  positions: int32 [N], or [axes, N]."""
     T = _T or _torch()
     some = q if q is not None else k
     if not isinstance(some, T.Tensor):
@@ -775,18 +813,14 @@ def sgl_rope(rope, q, k, positions, q_out=None, k_out=None, stream=None):
         pko, sko = pk, sk
         if k_out is not None:
             pko, sko, _, _ = _rows(k_out, "k_out", hk, d, dt, n, dev)
-    st = _lib().sgl_rope(rope.handle, kind, pq, sq, hq, pk, sk, hk, _flat(positions, "positions", dev, T.int32, (n,)), n,
+    st = _lib().sgl_rope(rope.handle, kind, pq, sq, hq, pk, sk, hk, _positions(rope, positions, n, dev), n,
                          pqo, sqo, pko, sko, _stream(stream))
     if st:
         raise SglError(st, "sgl_rope")
 
 
-def sgl_kv_append(rope, params, q, k_new, v_new, k_pool, v_pool, req_to_token, lens, extend_lens, q_out, workspace,
-                  stream=None):
-    """New keys and values [N, Hkv, d] into the paged pools, keys and queries rotated on the way (rope None: not
-    rotated; q and q_out None: keys and values only).  extend_lens given: N = the sum of extend_lens (or more, in a
-    padded batch) rows ordered by request, row i of request r at position lens[r] + i; None: row r is request r's
-    newest token, at position lens[r] - 1."""
+def _append(where, rope, params, q, k_new, v_new, k_pool, v_pool, req_to_token, lens, extend_lens, positions, q_out,
+            workspace, stream):
     T = _T or _torch()
     kind, hkv, d, dev = params.dtype, params.num_kv_heads, params.head_dim, T._C._cuda_getDevice()
     dt = T.float32 if kind == SGL_DTYPE_F32 else T.bfloat16
@@ -807,13 +841,34 @@ def sgl_kv_append(rope, params, q, k_new, v_new, k_pool, v_pool, req_to_token, l
     if k_pool.nbytes < need or v_pool.nbytes < need:
         _writable(pkp, k_pool, "k_pool", need)
         _writable(pvp, v_pool, "v_pool", need)
-    st = _lib().sgl_kv_append(None if rope is None else rope.handle, ctypes.byref(params), pq, sq, pk, sk, pv, sv,
-                              pkp, pvp, _flat(req_to_token, "req_to_token", dev, T.int32), rows[1],
-                              _flat(lens, "lens", dev, T.int32, B),
-                              None if extend_lens is None else _flat(extend_lens, "extend_lens", dev, T.int32, B), n, pqo,
-                              sqo, _flat(workspace, "workspace", dev), workspace.nbytes, _stream(stream))
+    at = () if positions is None else (_positions(rope, positions, n, dev),)
+    st = getattr(_lib(), where)(None if rope is None else rope.handle, ctypes.byref(params), pq, sq, pk, sk, pv, sv,
+                                pkp, pvp, _flat(req_to_token, "req_to_token", dev, T.int32), rows[1],
+                                _flat(lens, "lens", dev, T.int32, B),
+                                None if extend_lens is None else _flat(extend_lens, "extend_lens", dev, T.int32, B),
+                                *at, n, pqo, sqo, _flat(workspace, "workspace", dev), workspace.nbytes, _stream(stream))
     if st:
-        raise SglError(st, "sgl_kv_append")
+        raise SglError(st, where)
+
+
+def sgl_kv_append(rope, params, q, k_new, v_new, k_pool, v_pool, req_to_token, lens, extend_lens, q_out, workspace,
+                  stream=None):
+    """New keys and values [N, Hkv, d] into the paged pools, keys and queries rotated on the way (rope None: not
+    rotated; q and q_out None: keys and values only).  extend_lens given: N = the sum of extend_lens (or more, in a
+    padded batch) rows ordered by request, row i of request r at position lens[r] + i; None: row r is request r's
+    newest token, at position lens[r] - 1."""
+    _append("sgl_kv_append", rope, params, q, k_new, v_new, k_pool, v_pool, req_to_token, lens, extend_lens, None, q_out,
+            workspace, stream)
+
+
+def sgl_kv_append_at(rope, params, q, k_new, v_new, k_pool, v_pool, req_to_token, lens, extend_lens, positions, q_out,
+                     workspace, stream=None):
+    """sgl_kv_append with the rotation's positions given: int32 [axes, N] (one axis: [N] too).  A row at a negative
+    position is neither rotated nor stored."""
+    if rope is None or positions is None:
+        raise TypeError("rope and positions must be given")
+    _append("sgl_kv_append_at", rope, params, q, k_new, v_new, k_pool, v_pool, req_to_token, lens, extend_lens, positions,
+            q_out, workspace, stream)
 
 
 def sgl_mla_kv_append(rope, params, q, kv_new, kv_pool, req_to_token, lens, extend_lens, q_out, workspace, stream=None):
@@ -839,3 +894,88 @@ def sgl_mla_kv_append(rope, params, q, kv_new, kv_pool, req_to_token, lens, exte
                                   pqo, sqo, _flat(workspace, "workspace", dev), workspace.nbytes, _stream(stream))
     if st:
         raise SglError(st, "sgl_mla_kv_append")
+
+
+# ------------------------------- cached tokens by the attention they get
+def sgl_attn_weights_workspace_bytes(params, window=0):
+    """Device workspace of sgl_attn_weights (params with host_prefix_lens and host_extend_lens: of its chunk form)."""
+    b = ctypes.c_size_t()
+    _ok(_lib().sgl_attn_weights_workspace_bytes(ctypes.byref(params), window, ctypes.byref(b)),
+        "sgl_attn_weights_workspace_bytes")
+    return b.value
+
+
+def _table_rows(t, what, batch, dev, dtype):
+    """A contiguous tensor with a row for each of `batch` requests: (address, row length)."""
+    p = _flat(t, what, dev, dtype)
+    if t.dim() != 2 or t.shape[0] < batch:
+        raise ValueError("%s must have a row per request" % what)
+    return p, t.shape[1]
+
+
+def sgl_attn_weights(q, lse, k_pool, req_to_token, lens, extend_lens, params, scores_in, scores_out, workspace, decay=1.0,
+                     window=0, stream=None):
+    """The attention weights that each cached token gets from the queries q [N, Hq, d] of an attention call with its
+    log-sum-exp lse [N, Hq], added to decay times scores_in [B, L] (None: zeros), into scores_out (may be scores_in).
+    extend_lens None: a decode batch, lens its contexts; else chunks behind lens cached tokens, of which the last
+    `window` rows of each request ask (0: all)."""
+    T = _T or _torch()
+    kind, d, dev = params.dtype, params.head_dim, T._C._cuda_getDevice()
+    pq, sq, n, hq = _rows(q, "q", params.num_qo_heads, d, T.float32 if kind == SGL_DTYPE_F32 else T.bfloat16, None, dev)
+    if sq != hq * d:
+        raise ValueError("q must be contiguous")
+    B = (params.batch,)
+    if extend_lens is None:
+        if n != params.batch:
+            raise ValueError("q must have a row per request")
+    elif params.batch and not (params.host_prefix_lens and params.host_extend_lens):
+        raise ValueError("params must have host_prefix_lens and host_extend_lens")
+    elif sum(params.host_extend_lens[:params.batch]) > n:
+        raise ValueError("q must hold the rows of extend_lens")
+    pt, ld = _table_rows(req_to_token, "req_to_token", params.batch, dev, T.int32)
+    po, sld = _table_rows(scores_out, "scores_out", params.batch, dev, T.float32)
+    pi = None
+    if scores_in is not None:
+        pi, ild = _table_rows(scores_in, "scores_in", params.batch, dev, T.float32)
+        if ild != sld:
+            raise ValueError("scores_in and scores_out must have rows of one length")
+    st = _lib().sgl_attn_weights(pq, _flat(lse, "lse", dev, T.float32, (n, hq)),
+                                 _writable(_flat(k_pool, "k_pool", dev), k_pool, "k_pool",
+                                           params.num_slots * _row_bytes(params)),
+                                 pt, ld, _flat(lens, "lens", dev, T.int32, B),
+                                 None if extend_lens is None else _flat(extend_lens, "extend_lens", dev, T.int32, B),
+                                 ctypes.byref(params), window, pi, po, sld, decay, _flat(workspace, "workspace", dev),
+                                 workspace.nbytes, _stream(stream))
+    if st:
+        raise SglError(st, "sgl_attn_weights")
+
+
+def sgl_kv_evict(scores, req_to_token, lens, budgets, scores_out, table_out, lens_out, workspace, evicted=None,
+                 evicted_count=None, positions=None, positions_out=None, page_size=1, sinks=0, recent=0, stream=None):
+    """The tokens (pages) with the lowest scores leave the rows of requests over their budgets, which close up: scores
+    [B, L], req_to_token and positions [B, ld] into their outputs (each may be its input), lens [B] into lens_out; the
+    slots that left into evicted [B, any] and their number into evicted_count [B]."""
+    T = _T or _torch()
+    dev, B = T._C._cuda_getDevice(), len(lens)
+    ps, sld = _table_rows(scores, "scores", B, dev, T.float32)
+    pt, ld = _table_rows(req_to_token, "req_to_token", B, dev, T.int32)
+    pp = ppo = pe = pc = None
+    eld = 0
+    if (positions is None) != (positions_out is None):
+        raise ValueError("positions and positions_out go together")
+    if positions is not None:
+        pp = _flat(positions, "positions", dev, T.int32, req_to_token.shape)
+        ppo = _flat(positions_out, "positions_out", dev, T.int32, req_to_token.shape)
+    if evicted is not None:
+        pe, eld = _table_rows(evicted, "evicted", B, dev, T.int32)
+    if evicted_count is not None:
+        pc = _flat(evicted_count, "evicted_count", dev, T.int32, (B,))
+    p = SglEvictParams(B, page_size, sinks, recent)
+    st = _lib().sgl_kv_evict(ctypes.byref(p), ps, sld, pt, ld, pp, _flat(lens, "lens", dev, T.int32, (B,)),
+                             _flat(budgets, "budgets", dev, T.int32, (B,)),
+                             _flat(scores_out, "scores_out", dev, T.float32, scores.shape),
+                             _flat(table_out, "table_out", dev, T.int32, req_to_token.shape), ppo,
+                             _flat(lens_out, "lens_out", dev, T.int32, (B,)), pe, eld, pc,
+                             _flat(workspace, "workspace", dev), workspace.nbytes, _stream(stream))
+    if st:
+        raise SglError(st, "sgl_kv_evict")

@@ -1,0 +1,341 @@
+// Tokens leave a cache by their scores: for each request the pages that stay
+// are found, and its rows of slots, scores and positions close up.
+//
+// A row's pages of P positions [0, n): those before `head` (sinks) and from
+// `first` on (recent ones, and a last page that is not full) stay; of the
+// others, whose score is their highest token's, the `more` highest stay, the
+// earlier of equal ones.  Which score is the lowest that stays is found digit
+// by digit (radix selection): scores become whole numbers of the same order,
+// and four rounds each count the 256 values of the next eight bits among the
+// pages that agree with the digits found so far.
+//
+// Work: a cluster of CTAs per request.  Each holds the scores of its share of
+// the pages in shared memory, so that the rounds read no memory; their counts
+// are joined through distributed shared memory.  Kept pages are then numbered
+// in order (ballots, and one exchange of the CTAs' totals), which gives every
+// page its place, kept in place of its score.  The row is moved front to back
+// in rounds of the whole cluster that read before any of them writes: places
+// only get smaller, so a row may be moved onto itself.
+//
+// ["SGLang 深度拆解" §2.3: the cache keeps what its budget allows]
+
+#include <cooperative_groups.h>
+
+#include <algorithm>
+
+#include "common.h"
+#include "device_common.cuh"
+
+namespace {
+
+using namespace sgldev;
+namespace cg = cooperative_groups;
+
+constexpr int kThreads = 1024;
+constexpr int kWarps = kThreads / 32;
+constexpr int kMaxCluster = 16;
+constexpr int kEach = 4;                 // positions of a thread per round of moves
+constexpr int kMaxShare = 49152;         // pages of a CTA's share (shared memory)
+
+struct EvictArgs {
+    const float* scores;
+    const int32_t *table, *positions, *lens, *budgets;
+    float* scores_out;
+    int32_t *table_out, *positions_out, *lens_out, *evicted, *count;
+    int64_t scores_ld, ld, evicted_ld;
+    uint32_t* err;
+    int page, lg_page;                   // lg_page < 0: not a power of two
+    int sinks, recent;
+    int lim;                             // positions of a row: the shorter of ld and scores_ld
+    bool in_place;                       // some output is its input
+};
+
+// A score as a whole number of the same order; NaN as -infinity, -0 as 0.
+__device__ __forceinline__ uint32_t order_of(float x) {
+    const uint32_t u = x == x ? __float_as_uint(x + 0.f) : 0xff800000u;
+    return u & 0x80000000u ? ~u : u | 0x80000000u;
+}
+
+__global__ void __launch_bounds__(kThreads, 1) evict_kernel(const __grid_constant__ EvictArgs a) {
+    extern __shared__ uint32_t share[];          // a page's score; then its place, or ~(kept pages before it) if it leaves
+    __shared__ uint32_t hist[2][256], sums[256];
+    __shared__ uint2 warp_counts[kWarps], cta_counts;      // (pages that surely stay, pages at the lowest kept score)
+    cg::cluster_group cl = cg::this_cluster();
+    const int C = (int)cl.num_blocks(), c = (int)cl.block_rank();
+    const int r = blockIdx.x / C, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    auto sync_all = [&] {
+        if (C > 1)
+            cl.sync();
+        else
+            __syncthreads();
+    };
+    grid_dep_wait();
+    grid_dep_launch();
+    int n = a.lens[r];                       // (lens_out may be lens)
+    const int budget = max(__ldg(a.budgets + r), 0);
+    if (n < 0 || n > a.lim) {
+        if (c == 0 && tid == 0) atomicOr(a.err, 2u);
+        n = max(0, min(n, a.lim));
+    }
+    const int P = a.page;
+    auto page_of = [&](int p) { return a.lg_page >= 0 ? p >> a.lg_page : p / P; };
+    const int pages = n > 0 ? page_of(n - 1) + 1 : 0;
+    const int first = page_of(max(n - a.recent, 0));       // (recent 0: a last page that is not full stays)
+    const int head = min(page_of(a.sinks) + (a.sinks - page_of(a.sinks) * P > 0), first);
+    const int fixed = head * P + (n - first * P);
+    const int more = min(max(page_of(max(budget - fixed, 0)), 0), first - head);
+    const bool some = n > budget && more < first - head;   // some pages leave
+
+    const float* const scores = a.scores + (int64_t)r * a.scores_ld;
+    const int32_t* const table = a.table + (int64_t)r * a.ld;
+    const int32_t* const positions = a.positions ? a.positions + (int64_t)r * a.ld : nullptr;
+    float* const scores_out = a.scores_out + (int64_t)r * a.scores_ld;
+    int32_t* const table_out = a.table_out + (int64_t)r * a.ld;
+    int32_t* const positions_out = a.positions ? a.positions_out + (int64_t)r * a.ld : nullptr;
+
+    const int S = (pages + C - 1) / C;                     // pages of a share
+    const int p0 = c * S, np = max(0, min(S, pages - p0)); // this CTA's
+    if (some) {
+        if (P > 1) {
+            for (int i = tid; i < np; i += kThreads) share[i] = 0;
+            __syncthreads();
+        }
+        const int t1 = min(n, (p0 + np) * P);
+#pragma unroll 4
+        for (int t = p0 * P + tid; t < t1; t += kThreads) {
+            const uint32_t k = order_of(scores[t]);
+            if (P == 1)
+                share[t - p0] = k;
+            else
+                atomicMax(&share[page_of(t) - p0], k);
+        }
+        if (tid < 256) hist[0][tid] = 0;
+        __syncthreads();
+        // lowest score that stays, and how many of those at it
+        uint32_t low = 0xffffffffu, mask = 0, found = 0;
+        int need = 0;
+        if (more > 0) {
+            int k = more;
+            const int m0 = max(head - p0, 0), m1 = min(first - p0, np);
+            for (int pass = 0; pass < 4; ++pass) {
+                const int shift = 24 - 8 * pass;
+                uint32_t* const h = hist[pass & 1];
+                for (int i = m0 + tid; i < m1; i += kThreads) {
+                    const uint32_t x = share[i];
+                    if ((x & mask) == found) atomicAdd(&h[(x >> shift) & 255u], 1u);
+                }
+                sync_all();
+                if (tid < 256) {
+                    uint32_t s = 0;
+                    for (int b = 0; b < C; ++b) s += cl.map_shared_rank(h, b)[tid];
+                    sums[tid] = s;
+                    hist[(pass + 1) & 1][tid] = 0;
+                }
+                __syncthreads();
+                // lane l has digits 255 - 8 l .. 248 - 8 l: the digit with fewer
+                // than k pages above it and at least k from it on (every warp)
+                uint32_t v[8], mine = 0;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) mine += v[i] = sums[255 - 8 * lane - i];
+                uint32_t upto = mine;
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const uint32_t y = __shfl_up_sync(0xffffffffu, upto, o);
+                    if (lane >= o) upto += y;
+                }
+                const int l = __ffs(__ballot_sync(0xffffffffu, upto >= (uint32_t)k)) - 1;
+                uint32_t above = upto - mine, digit = 0, size = 0;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    if (size == 0 && above + v[i] >= (uint32_t)k) {
+                        digit = 255 - 8 * lane - i;
+                        size = v[i];
+                    }
+                    if (size == 0) above += v[i];
+                }
+                above = __shfl_sync(0xffffffffu, above, l);
+                digit = __shfl_sync(0xffffffffu, digit, l);
+                size = __shfl_sync(0xffffffffu, size, l);
+                k -= (int)above;
+                found |= digit << shift;
+                mask |= 255u << shift;
+                low = found;
+                need = k;
+                if (size == (uint32_t)k && found > 0) {    // all of these stay: no further digit matters
+                    low = found - 1;
+                    need = 0;
+                    break;
+                }
+            }
+        }
+        // number the kept pages: warps take runs of their CTA's share
+        const int run = ((np + kWarps - 1) / kWarps + 31) & ~31;
+        const int r0 = min(warp * run, np), r1 = min(r0 + run, np);
+        auto sure = [&](int i) { return i < r1 && (p0 + i < head || p0 + i >= first || share[i] > low); };
+        auto equal = [&](int i) { return i < r1 && p0 + i >= head && p0 + i < first && share[i] == low; };
+        uint2 mine = make_uint2(0, 0);
+        for (int i = r0; i < r1; i += 32) {
+            mine.x += __popc(__ballot_sync(0xffffffffu, sure(i + lane)));
+            mine.y += __popc(__ballot_sync(0xffffffffu, equal(i + lane)));
+        }
+        if (lane == 0) warp_counts[warp] = mine;
+        __syncthreads();
+        uint2 w = warp_counts[lane];
+        const uint2 own = w;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const uint32_t x = __shfl_up_sync(0xffffffffu, w.x, o), y = __shfl_up_sync(0xffffffffu, w.y, o);
+            if (lane >= o) {
+                w.x += x;
+                w.y += y;
+            }
+        }
+        if (tid == 31) cta_counts = w;
+        uint32_t surely = __shfl_sync(0xffffffffu, w.x - own.x, warp), equals = __shfl_sync(0xffffffffu, w.y - own.y, warp);
+        if (C > 1) {
+            cl.sync();
+            for (int b = 0; b < c; ++b) {
+                const uint2 o = *cl.map_shared_rank(&cta_counts, b);
+                surely += o.x;
+                equals += o.y;
+            }
+        }
+        const uint32_t below = (1u << lane) - 1u;
+        for (int i = r0; i < r1; i += 32) {
+            const bool s = sure(i + lane), e = equal(i + lane);
+            const uint32_t bs = __ballot_sync(0xffffffffu, s), be = __ballot_sync(0xffffffffu, e);
+            const uint32_t before = equals + __popc(be & below);       // pages at the lowest score before this one
+            const int place = (int)(surely + __popc(bs & below) + min(before, (uint32_t)need));
+            __syncwarp();
+            if (i + lane < r1) share[i + lane] = s || (e && before < (uint32_t)need) ? (uint32_t)place : ~(uint32_t)place;
+            surely += __popc(bs);
+            equals += __popc(be);
+        }
+        sync_all();
+    }
+    const int left = some ? n - (first - head - more) * P : n;
+    if (c == 0 && tid == 0) {
+        a.lens_out[r] = left;
+        if (a.count) a.count[r] = n - left;
+        if (a.evicted && n - left > a.evicted_ld) atomicOr(a.err, 2u);
+    }
+    if (!some && a.in_place && scores == scores_out && table == table_out && positions == positions_out) return;
+    // page / S, exactly: pages and S below 2^20
+    const uint64_t inv = S > 0 ? ((1ull << 40) + S - 1) / S : 0;
+    for (int64_t base = 0; base < n; base += (int64_t)C * kThreads * kEach) {
+        float x[kEach];
+        int slot[kEach], at[kEach], to[kEach];
+        const int64_t q0 = base + (int64_t)c * kThreads * kEach + tid;
+#pragma unroll
+        for (int e = 0; e < kEach; ++e) {
+            const int64_t p = q0 + e * kThreads;
+            to[e] = (int)p;
+            if (p >= n) continue;
+            x[e] = scores[p];
+            slot[e] = table[p];
+            if (positions) at[e] = positions[p];
+            if (some) {
+                const int page = page_of((int)p), owner = (int)((page * inv) >> 40);
+                const int place = (int)cl.map_shared_rank(share, owner)[page - owner * S];
+                const int rest = (int)p - page * P;
+                // (a page that leaves: its place among those, from the end of the ints on)
+                to[e] = place >= 0 ? place * P + rest : ~((page - ~place) * P + rest);
+            }
+        }
+        if (some && a.in_place) sync_all();
+#pragma unroll
+        for (int e = 0; e < kEach; ++e) {
+            const int64_t p = q0 + e * kThreads;
+            if (p >= n) continue;
+            if (to[e] >= 0) {
+                scores_out[to[e]] = x[e];
+                table_out[to[e]] = slot[e];
+                if (positions) positions_out[to[e]] = at[e];
+            } else if (a.evicted && ~to[e] < a.evicted_ld) {
+                a.evicted[(int64_t)r * a.evicted_ld + ~to[e]] = slot[e];
+            }
+            if (p >= left) {
+                scores_out[p] = 0.f;
+                table_out[p] = -1;
+                if (positions) positions_out[p] = -1;
+            }
+        }
+    }
+    if (C > 1 && some) cl.sync();      // (others may still read this CTA's share)
+}
+
+int cuda_status(cudaError_t e) {
+    if (e == cudaSuccess) return SGL_OK;
+    sgl::set_cuda_error(static_cast<int>(e));
+    return SGL_ERR_CUDA;
+}
+
+}  // namespace
+
+extern "C" {
+
+int sgl_kv_evict(const sgl_evict_params* params, const float* scores, int64_t scores_ld, const int32_t* req_to_token,
+                 int64_t ld, const int32_t* positions, const int32_t* lens, const int32_t* budgets, float* scores_out,
+                 int32_t* table_out, int32_t* positions_out, int32_t* lens_out, int32_t* evicted, int64_t evicted_ld,
+                 int32_t* evicted_count, void* workspace, size_t ws_bytes, sgl_stream_t stream) {
+    if (!params || params->batch < 0 || params->page_size < 1 || params->sinks < 0 || params->recent < 0)
+        return SGL_ERR_INVALID_ARG;
+    if (ld < 0 || scores_ld < 0 || evicted_ld < 0) return SGL_ERR_INVALID_ARG;
+    if (!workspace || (reinterpret_cast<uintptr_t>(workspace) % sgl::kWsAlign) != 0 || ws_bytes < sgl::kWsAlign)
+        return SGL_ERR_WORKSPACE;
+    if (params->batch == 0) return SGL_OK;
+    if (!lens || !budgets || !lens_out || !positions != !positions_out) return SGL_ERR_INVALID_ARG;
+    const int64_t lim = std::min(ld, scores_ld);
+    if (lim > 0 && (!scores || !req_to_token || !scores_out || !table_out)) return SGL_ERR_INVALID_ARG;
+    const int P = params->page_size;
+    const int64_t pages = (lim + P - 1) / P;
+    if (lim > INT32_MAX / 2 || P > INT32_MAX / 2 || pages > (int64_t)kMaxCluster * kMaxShare) return SGL_ERR_UNSUPPORTED;
+    EvictArgs a{};
+    a.scores = scores;
+    a.table = req_to_token;
+    a.positions = positions;
+    a.lens = lens;
+    a.budgets = budgets;
+    a.scores_out = scores_out;
+    a.table_out = table_out;
+    a.positions_out = positions_out;
+    a.lens_out = lens_out;
+    a.evicted = evicted;
+    a.count = evicted_count;
+    a.scores_ld = scores_ld;
+    a.ld = ld;
+    a.evicted_ld = evicted_ld;
+    a.err = static_cast<uint32_t*>(workspace);
+    a.page = P;
+    a.lg_page = (P & (P - 1)) == 0 ? 31 - __builtin_clz(P) : -1;
+    a.sinks = std::min<int32_t>(params->sinks, INT32_MAX / 2);
+    a.recent = std::min<int32_t>(params->recent, INT32_MAX / 2);
+    a.lim = (int)lim;
+    a.in_place = scores == scores_out || req_to_token == table_out || (positions && positions == positions_out);
+    int C = 1;
+    while (C < kMaxCluster && lim > (int64_t)C * 8192) C *= 2;
+    while (pages > (int64_t)C * kMaxShare) C *= 2;
+    if ((int64_t)params->batch * C > INT32_MAX) return SGL_ERR_UNSUPPORTED;
+    static sgl::PerDevice ready;
+    if (const int e = ready_here(ready, [] {
+            if (const int e2 = large_smem(evict_kernel, kMaxShare * 4)) return e2;
+            return (int)cudaFuncSetAttribute(evict_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+        }))
+        return cuda_status(static_cast<cudaError_t>(e));
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = (unsigned)C;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)(params->batch * C));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = (size_t)((pages + C - 1) / C) * 4;
+    cfg.stream = reinterpret_cast<cudaStream_t>(stream);
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cuda_status(cudaLaunchKernelEx(&cfg, evict_kernel, a));
+}
+
+}  // extern "C"

@@ -54,6 +54,8 @@ struct sgl_rope_table {
     sgl_rope_params p;
     double amplitude;                // multiplies cos and sin
     uint64_t turn[SGL_ROPE_MAX_DIM / 2];   // f_j 2^64 / (2 pi): fractions of a turn per position
+    int axes;                        // axes that a token has positions on
+    uint64_t axis[4];                // pair j's axis: bits 2 (j % 32) and the next of word j / 32
 };
 
 namespace {
@@ -73,7 +75,11 @@ struct RopeArgs {
     void *qo, *ko;                   // rotated rows (ko: without pools)
     int64_t qos, kos;
     uint8_t *kp, *vp;                // pools
-    const int32_t* positions;        // rotation only
+    // the rotation's positions, [axes, n_rows]; null (appends): the token's
+    // place in its row, on every axis
+    const int32_t* positions;
+    int axes;                        // 1 with positions null
+    uint64_t axis[4];                // each pair's axis (as in the table)
     const int32_t* r2t;
     int64_t ld;
     const int32_t *lens, *ext;       // ext null: one token per request at lens[r] - 1
@@ -300,7 +306,9 @@ struct Part {
     static constexpr int value = N;
 };
 
-template <typename T, int POOL, bool POW2>
+// AT: the rotation's positions are given (always without a pool); an instance of
+// its own for the appends, which otherwise spill more
+template <typename T, int POOL, bool POW2, bool AT>
 __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 9 : 6) rope_kernel(const __grid_constant__ RopeArgs a) {
     __shared__ __align__(16) float cs[kWarps][2][kMaxHalf];    // cosines, sines of a warp's token
     const int lane = threadIdx.x & 31;
@@ -349,9 +357,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 9 : 6) rope_kernel(
     fetch(id0);
     // position and slot: -1 where there is nothing to do
     int pos = -1, slot = -1;
-    if constexpr (POOL == kPoolNone) {
-        pos = __ldg(a.positions + n);
-    } else {
+    if constexpr (POOL != kPoolNone) {
         int r = (int)n, i = 0;
         if (!a.ext || find_request(a.ext, a.B, (int)n, lane, &r, &i)) {
             const int64_t p = a.ext ? (int64_t)__ldg(a.lens + r) + i : (int64_t)__ldg(a.lens + r) - 1;
@@ -368,6 +374,12 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 9 : 6) rope_kernel(
             }
         }
     }
+    if (AT && (POOL == kPoolNone || pos >= 0)) {
+        // (the further axes' are read again below, from L1)
+        pos = __ldg(a.positions + n);
+        for (int x = 1; x < a.axes; ++x)
+            if (__ldg(a.positions + x * a.n_rows + n) < 0) pos = -1;
+    }
     if (pos < 0) return;
     const int half = a.rot >> 1;
     for (int j = lane; j < half; j += 32) {
@@ -375,7 +387,13 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 9 : 6) rope_kernel(
         // cache would serve one by one)
         uint64_t turn;
         asm("ld.b64 %0, [%1];" : "=l"(turn) : "l"(&a.turn[j]));
-        const float2 v = cos_sin_turn((uint64_t)(uint32_t)pos * turn, a.amp_hi, a.amp_lo);
+        int at = pos;
+        if (AT && a.axes > 1) {
+            // (lanes of one trip share a word)
+            const uint32_t x = (uint32_t)(a.axis[j >> 5] >> (2 * lane)) & 3u;
+            at = __ldg(a.positions + x * a.n_rows + n);
+        }
+        const float2 v = cos_sin_turn((uint64_t)(uint32_t)at * turn, a.amp_hi, a.amp_lo);
         cs[warp][0][j] = v.x;
         cs[warp][1][j] = v.y;
     }
@@ -518,7 +536,7 @@ bool rows_ok(const void* p, int64_t stride, int heads, int d, int es) {
     return p && aligned16(p) && stride >= (int64_t)heads * d && stride * es % 16 == 0;
 }
 
-template <typename T, int POOL, bool POW2>
+template <typename T, int POOL, bool POW2, bool AT>
 int launch_as(RopeArgs& a, cudaStream_t s) {
     // Two tokens share a CTA (two warps each) once every SM has one; below one
     // token per SM a token's groups are spread over several CTAs.  Measured
@@ -553,15 +571,19 @@ int launch_as(RopeArgs& a, cudaStream_t s) {
     cfg.stream = s;
     cfg.attrs = pdl;
     cfg.numAttrs = 1;
-    return cuda_status(cudaLaunchKernelEx(&cfg, rope_kernel<T, POOL, POW2>, a));
+    return cuda_status(cudaLaunchKernelEx(&cfg, rope_kernel<T, POOL, POW2, AT>, a));
 }
 
 template <typename T, int POOL>
 int launch(RopeArgs& a, cudaStream_t s) {
     if (a.n_rows == 0 || a.Hq + a.Hk + a.Hv == 0) return SGL_OK;
-    if ((a.d & (a.d - 1)) == 0 && a.d <= 512) return launch_as<T, POOL, true>(a, s);
+    if ((a.d & (a.d - 1)) == 0 && a.d <= 512) {
+        if (POOL == kPoolNone || a.positions) return launch_as<T, POOL, true, true>(a, s);
+        return launch_as<T, POOL, true, POOL == kPoolNone>(a, s);
+    }
     // other widths: rotation alone and MLA rows (the pools' heads are 64 or 128 wide)
-    if constexpr (POOL == kPoolNone || (POOL == kPoolSame && sizeof(T) == 2)) return launch_as<T, POOL, false>(a, s);
+    if constexpr (POOL == kPoolNone || (POOL == kPoolSame && sizeof(T) == 2))
+        return launch_as<T, POOL, false, POOL == kPoolNone>(a, s);
     return SGL_ERR_UNSUPPORTED;
 }
 
@@ -575,6 +597,13 @@ void set_table(RopeArgs& a, const sgl_rope_table* t) {
     std::memcpy(a.turn, t->turn, sizeof(uint64_t) * (size_t)(t->p.rot_dim / 2));
 }
 
+// the rotation's positions as given, on each of the table's axes
+void set_positions(RopeArgs& a, const sgl_rope_table* t, const int32_t* positions) {
+    a.positions = positions;
+    a.axes = t->axes;
+    std::memcpy(a.axis, t->axis, sizeof(a.axis));
+}
+
 // 2^64 f / (2 pi) as a whole number, within one: f times 1 / (2 pi) as the sum
 // of two doubles (a quotient in doubles is off by 2^-53 of itself, which the
 // position multiplies: a millionth of a radian at positions near 2^31).  f <= 1
@@ -584,6 +613,37 @@ uint64_t turn_of(double f) {
     const double p = f * kHi, e = std::fma(f, kHi, -p) + f * kLo;
     const double whole = std::floor(std::ldexp(p, 64));
     return (uint64_t)whole + (uint64_t)(int64_t)std::nearbyint((std::ldexp(p, 64) - whole) + std::ldexp(e, 64));
+}
+
+// fractions of a turn per position of the pairs of a rotation of n elements
+void frequencies(const sgl_rope_params& p, int n, uint64_t* turn) {
+    const int kind = p.scaling;
+    const double by = p.factor;
+    const double two_pi = 6.283185307179586476925286766559;
+    const double orig = (double)p.original_positions;
+    double theta = p.theta;
+    if (kind == SGL_ROPE_SCALE_NTK) theta *= std::pow(by, (double)n / (n - 2));
+    double lo = 0.0, hi = 1.0;
+    if (kind == SGL_ROPE_SCALE_YARN) {
+        // the pair index at which a pair makes `turns` turns over the original positions
+        auto index = [&](double turns) { return n * std::log(orig / (turns * two_pi)) / (2.0 * std::log(p.theta)); };
+        lo = std::fmax(std::floor(index(p.high)), 0.0);
+        hi = std::fmin(std::ceil(index(p.low)), n - 1.0);
+        if (hi <= lo) hi = lo + 0.001;
+    }
+    for (int j = 0; j < n / 2; ++j) {
+        double f = std::pow(theta, -2.0 * j / n);
+        if (kind == SGL_ROPE_SCALE_LINEAR) {
+            f /= by;
+        } else if (kind == SGL_ROPE_SCALE_YARN) {
+            const double w = std::fmin(std::fmax((j - lo) / (hi - lo), 0.0), 1.0);
+            f = f / by * w + f * (1.0 - w);
+        } else if (kind == SGL_ROPE_SCALE_BANDED) {
+            const double w = std::fmin(std::fmax((orig * f / two_pi - p.low) / (p.high - p.low), 0.0), 1.0);
+            f = f / by * (1.0 - w) + f * w;
+        }
+        turn[j] = turn_of(f);
+    }
 }
 
 // the arguments that both appends share, checked
@@ -601,6 +661,7 @@ int append_rows(RopeArgs& a, const sgl_rope_table* rope, int es, int64_t n_rows,
         return SGL_ERR_INVALID_ARG;
     if (q && q == q_out && q_stride != q_out_stride) return SGL_ERR_INVALID_ARG;
     set_table(a, rope);
+    a.axes = 1;
     a.q = q;
     a.qs = q_stride;
     a.qo = q_out;
@@ -654,34 +715,51 @@ int sgl_rope_create(const sgl_rope_params* p, sgl_rope_table** out) {
     auto* t = new (std::nothrow) sgl_rope_table();
     if (!t) return SGL_ERR_INVALID_ARG;
     t->p = *p;
-    const double two_pi = 6.283185307179586476925286766559;
-    const double orig = (double)p->original_positions;
-    double theta = p->theta;
-    if (kind == SGL_ROPE_SCALE_NTK) theta *= std::pow(by, (double)n / (n - 2));
-    double lo = 0.0, hi = 1.0;
-    if (kind == SGL_ROPE_SCALE_YARN) {
-        // the pair index at which a pair makes `turns` turns over the original positions
-        auto index = [&](double turns) { return n * std::log(orig / (turns * two_pi)) / (2.0 * std::log(p->theta)); };
-        lo = std::fmax(std::floor(index(p->high)), 0.0);
-        hi = std::fmin(std::ceil(index(p->low)), n - 1.0);
-        if (hi <= lo) hi = lo + 0.001;
-    }
-    for (int j = 0; j < n / 2; ++j) {
-        double f = std::pow(theta, -2.0 * j / n);
-        if (kind == SGL_ROPE_SCALE_LINEAR) {
-            f /= by;
-        } else if (kind == SGL_ROPE_SCALE_YARN) {
-            const double w = std::fmin(std::fmax((j - lo) / (hi - lo), 0.0), 1.0);
-            f = f / by * w + f * (1.0 - w);
-        } else if (kind == SGL_ROPE_SCALE_BANDED) {
-            const double w = std::fmin(std::fmax((orig * f / two_pi - p->low) / (p->high - p->low), 0.0), 1.0);
-            f = f / by * (1.0 - w) + f * w;
-        }
-        t->turn[j] = turn_of(f);
-    }
+    frequencies(*p, n, t->turn);
     double amp = p->attention_factor;
     if (amp == 0.0) amp = kind == SGL_ROPE_SCALE_YARN ? 0.1 * std::log(by) + 1.0 : 1.0;
     t->amplitude = amp;
+    t->axes = 1;
+    *out = t;
+    return SGL_OK;
+}
+
+int sgl_rope_create_axes(const sgl_rope_params* params, const sgl_rope_axes* axes, sgl_rope_table** out) {
+    if (!params || !axes || !out) return SGL_ERR_INVALID_ARG;
+    if (axes->num_axes < 1 || axes->num_axes > SGL_ROPE_MAX_AXES) return SGL_ERR_INVALID_ARG;
+    if (axes->arrange != SGL_ROPE_AXES_BLOCKS && axes->arrange != SGL_ROPE_AXES_TURNS) return SGL_ERR_UNSUPPORTED;
+    if (axes->own_ladder != 0 && axes->own_ladder != 1) return SGL_ERR_INVALID_ARG;
+    int64_t sum = 0;
+    for (int x = 0; x < axes->num_axes; ++x) {
+        if (axes->sections[x] < 1) return SGL_ERR_INVALID_ARG;
+        // (a ladder of one pair has no base to scale)
+        if (axes->own_ladder && params->scaling == SGL_ROPE_SCALE_NTK && axes->sections[x] < 2) return SGL_ERR_INVALID_ARG;
+        sum += axes->sections[x];
+    }
+    if (sum * 2 != params->rot_dim) return SGL_ERR_INVALID_ARG;
+    sgl_rope_table* t = nullptr;
+    if (const int st = sgl_rope_create(params, &t)) return st;
+    t->axes = axes->num_axes;
+    int index[kMaxHalf], axis[kMaxHalf], left[SGL_ROPE_MAX_AXES];     // each pair's place within its axis, its axis
+    for (int x = 0; x < axes->num_axes; ++x) left[x] = axes->sections[x];
+    for (int j = 0; j < (int)sum;) {
+        for (int x = 0; x < axes->num_axes; ++x) {
+            const int take = axes->arrange == SGL_ROPE_AXES_BLOCKS ? left[x] : left[x] > 0 ? 1 : 0;
+            for (int i = 0; i < take; ++i, ++j) {
+                axis[j] = x;
+                index[j] = axes->sections[x] - left[x]--;
+            }
+        }
+    }
+    if (axes->own_ladder) {
+        for (int x = 0; x < axes->num_axes; ++x) {
+            uint64_t own[kMaxHalf];
+            frequencies(*params, 2 * axes->sections[x], own);
+            for (int j = 0; j < (int)sum; ++j)
+                if (axis[j] == x) t->turn[j] = own[index[j]];
+        }
+    }
+    for (int j = 0; j < (int)sum; ++j) t->axis[j >> 5] |= (uint64_t)axis[j] << (2 * (j & 31));
     *out = t;
     return SGL_OK;
 }
@@ -714,7 +792,7 @@ int sgl_rope(const sgl_rope_table* rope, int32_t dtype, const void* q, int64_t q
     a.ko = k_out;
     a.qos = q_out_stride;
     a.kos = k_out_stride;
-    a.positions = positions;
+    set_positions(a, rope, positions);
     a.n_rows = n_rows;
     a.Hq = num_q_heads;
     a.Hk = num_k_heads;
@@ -724,11 +802,11 @@ int sgl_rope(const sgl_rope_table* rope, int32_t dtype, const void* q, int64_t q
     return es == 4 ? launch<float, kPoolNone>(a, s) : launch<bf16, kPoolNone>(a, s);
 }
 
-int sgl_kv_append(const sgl_rope_table* rope, const sgl_attn_params* params, const void* q, int64_t q_stride,
-                  const void* k_new, int64_t k_stride, const void* v_new, int64_t v_stride, void* k_pool, void* v_pool,
-                  const int32_t* req_to_token, int64_t ld, const int32_t* lens, const int32_t* extend_lens,
-                  int64_t n_rows, void* q_out, int64_t q_out_stride, void* workspace, size_t ws_bytes,
-                  sgl_stream_t stream) {
+static int append_impl(const sgl_rope_table* rope, const sgl_attn_params* params, const void* q, int64_t q_stride,
+                       const void* k_new, int64_t k_stride, const void* v_new, int64_t v_stride, void* k_pool,
+                       void* v_pool, const int32_t* req_to_token, int64_t ld, const int32_t* lens,
+                       const int32_t* extend_lens, const int32_t* positions, int64_t n_rows, void* q_out,
+                       int64_t q_out_stride, void* workspace, size_t ws_bytes, sgl_stream_t stream) {
     const int st = sgl::check_params(params);
     if (st) return st;
     const int d = params->head_dim, Hkv = params->num_kv_heads, es = params->dtype == SGL_DTYPE_F32 ? 4 : 2;
@@ -737,6 +815,7 @@ int sgl_kv_append(const sgl_rope_table* rope, const sgl_attn_params* params, con
     if (const int e = append_rows(a, rope, es, n_rows, req_to_token, ld, lens, extend_lens, params->batch, q, q_stride,
                                   q_out, q_out_stride, params->num_qo_heads, d, workspace, ws_bytes))
         return e;
+    if (positions) set_positions(a, rope, positions);
     if (n_rows == 0) return SGL_OK;
     if (!rows_ok(k_new, k_stride, Hkv, d, es) || !rows_ok(v_new, v_stride, Hkv, d, es)) return SGL_ERR_INVALID_ARG;
     if (!k_pool || !v_pool || !aligned16(k_pool) || !aligned16(v_pool)) return SGL_ERR_INVALID_ARG;
@@ -761,6 +840,25 @@ int sgl_kv_append(const sgl_rope_table* rope, const sgl_attn_params* params, con
         case SGL_DTYPE_BF16_FP8KV: a.row_bytes = Hkv * d; return launch<bf16, kPoolE4m3>(a, s);
         default: a.row_bytes = fp4_row_bytes(Hkv, d); return launch<bf16, kPoolFp4>(a, s);
     }
+}
+
+int sgl_kv_append(const sgl_rope_table* rope, const sgl_attn_params* params, const void* q, int64_t q_stride,
+                  const void* k_new, int64_t k_stride, const void* v_new, int64_t v_stride, void* k_pool, void* v_pool,
+                  const int32_t* req_to_token, int64_t ld, const int32_t* lens, const int32_t* extend_lens,
+                  int64_t n_rows, void* q_out, int64_t q_out_stride, void* workspace, size_t ws_bytes,
+                  sgl_stream_t stream) {
+    return append_impl(rope, params, q, q_stride, k_new, k_stride, v_new, v_stride, k_pool, v_pool, req_to_token, ld, lens,
+                       extend_lens, nullptr, n_rows, q_out, q_out_stride, workspace, ws_bytes, stream);
+}
+
+int sgl_kv_append_at(const sgl_rope_table* rope, const sgl_attn_params* params, const void* q, int64_t q_stride,
+                     const void* k_new, int64_t k_stride, const void* v_new, int64_t v_stride, void* k_pool,
+                     void* v_pool, const int32_t* req_to_token, int64_t ld, const int32_t* lens,
+                     const int32_t* extend_lens, const int32_t* positions, int64_t n_rows, void* q_out,
+                     int64_t q_out_stride, void* workspace, size_t ws_bytes, sgl_stream_t stream) {
+    if (!rope || (n_rows > 0 && !positions)) return SGL_ERR_INVALID_ARG;
+    return append_impl(rope, params, q, q_stride, k_new, k_stride, v_new, v_stride, k_pool, v_pool, req_to_token, ld, lens,
+                       extend_lens, positions, n_rows, q_out, q_out_stride, workspace, ws_bytes, stream);
 }
 
 int sgl_mla_kv_append(const sgl_rope_table* rope, const sgl_mla_params* params, const void* q, int64_t q_stride,
