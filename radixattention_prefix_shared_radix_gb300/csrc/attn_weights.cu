@@ -186,6 +186,296 @@ __global__ void __launch_bounds__(256) weights_plain(const __grid_constant__ Wei
 }
 
 // ---------------------------------------------------------------------------
+// Decode: the keys are streamed once, straight into the fragments of a matrix
+// instruction.  A warp takes one KV head of 8 NR positions at a time: lane
+// 4 g + t holds, of each row 8 n + g, every fourth 16-byte piece from piece t
+// on.  A dot product does not ask in which order its terms come, so these
+// pieces are the A operand of m16n8k16 as they are (words 2 j and 2 j + 1 of a
+// piece are an instruction's two k pairs), with the query's pieces of the same
+// places as B.  No shared memory and no ldmatrix lie between HBM and the
+// multiplier; FP8 and 4-bit pieces become f16 on the way (exact).  fp32 keys are
+// multiplied on CUDA cores, the query from shared memory.
+//
+// A tile of positions is shared by the CTA's warps, one per KV head (heads
+// beyond eight in turns), or, with fewer heads, several per head over
+// neighbouring positions; their sums meet in shared memory and are added in the
+// heads' order.  Each CTA takes an equal, contiguous run of the batch's tiles, so
+// a request's query stays in registers over its tiles.
+// Memory-bound; what counts is the bytes in flight.
+// ---------------------------------------------------------------------------
+template <int D, int KV>
+struct Stream {
+    static constexpr int RW = D * (KV == kKvF32 ? 32 : KV == 0 ? 16 : KV == 1 ? 8 : 4) / 8 / 16;   // a lane's words of a row
+    static constexpr int NR = KV == kKvF32 ? (D == 128 ? 1 : 2) : KV == 2 ? 8 : 32 / RW;            // rows of a lane
+    static constexpr int PU = 8 * NR;                                                               // positions of a warp
+};
+constexpr int kStreamThreads = 256;
+
+// 16 (8) bytes that are read once
+__device__ __forceinline__ uint4 ldg_once(const void* p) {
+    uint4 v;
+    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "l"(p));
+    return v;
+}
+__device__ __forceinline__ uint2 ldg_once8(const void* p) {
+    uint2 v;
+    asm volatile("ld.global.nc.L1::no_allocate.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p));
+    return v;
+}
+// D[16x8] += A[16x16] * B[16x8], f16 inputs, fp32 accumulate.
+__device__ __forceinline__ void mma16816_f16(float* c, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                             uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+template <int D, int KV>
+__global__ void __launch_bounds__(kStreamThreads, 3) weights_decode(const __grid_constant__ WeightArgs a, int hw, int nsub) {
+    using U = Stream<D, KV>;
+    constexpr int NR = U::NR, RW = U::RW, PU = U::PU;
+    constexpr bool F32 = KV == kKvF32;
+    constexpr int QW = D / 8;                        // a lane's words of the query (16 bits)
+    __shared__ float sums[2][8 * PU];                // [head warp][position of the tile]
+    __shared__ __align__(16) float sq[F32 ? 8 * 8 * D : 4];
+    const int tid = threadIdx.x, lane = tid & 31, g = lane >> 2, t = lane & 3;
+    const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
+    const int wh = warp % hw, sub = warp / hw, TP = PU * nsub;
+    grid_dep_wait();
+    grid_dep_launch();
+    // this CTA's tiles [at, end) of all requests', in order
+    auto tiles_of = [&](int len) { return len > 0 && len <= a.lim ? (len + TP - 1) / TP : 0; };
+    int64_t total = 0;
+    for (int b = lane; b < a.B; b += 32) {
+        const int len = __ldg(a.lens + b);
+        if ((len < 0 || len > a.lim) && blockIdx.x == 0 && warp == 0) atomicOr(a.err, 2u);
+        total += tiles_of(len);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+    int64_t at = total * blockIdx.x / gridDim.x;
+    const int64_t end = total * (blockIdx.x + 1) / gridDim.x;
+    if (at >= end) return;
+    int r = 0, tile = 0, len = 0;                    // request, tile of it, its length
+    {
+        int64_t acc = 0;
+        for (int b = 0; b < a.B; b += 32) {
+            const int l = b + lane < a.B ? __ldg(a.lens + b + lane) : 0, n = tiles_of(l);
+            int s = n;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int y = __shfl_up_sync(0xffffffffu, s, o);
+                if (lane >= o) s += y;
+            }
+            const uint32_t hit = __ballot_sync(0xffffffffu, acc + s > at);
+            if (hit) {
+                const int w = __ffs(hit) - 1;
+                r = b + w;
+                tile = (int)(at - acc) - __shfl_sync(0xffffffffu, s - n, w);
+                len = __shfl_sync(0xffffffffu, l, w);
+                break;
+            }
+            acc += __shfl_sync(0xffffffffu, s, 31);
+        }
+    }
+    auto next_tile = [&](int& r2, int& tile2, int& len2) {
+        if (++tile2 >= tiles_of(len2)) {
+            tile2 = 0;
+            do len2 = __ldg(a.lens + ++r2);
+            while (tiles_of(len2) == 0);             // (there is a next one: the caller counts)
+        }
+    };
+    int slot[NR];
+    auto load_slots = [&](int r2, int tile2, int len2) {
+        const int32_t* row = a.r2t + (int64_t)r2 * a.ld;
+#pragma unroll
+        for (int n = 0; n < NR; ++n) {
+            const int p = tile2 * TP + sub * PU + 8 * n + g;
+            slot[n] = p < len2 ? __ldg(row + p) : -1;
+        }
+    };
+    uint32_t raw[NR][RW], scale[KV == 2 ? NR : 1];
+    uint32_t live = 0;                               // rows of the lane that a slot in the pool holds
+    auto load_keys = [&](int h, int tile2, int len2) {
+        live = 0;
+#pragma unroll
+        for (int n = 0; n < NR; ++n) {
+            const bool ok = slot[n] >= 0 && slot[n] < a.num_slots;
+            if (ok)
+                live |= 1u << n;
+            else if (tile2 * TP + sub * PU + 8 * n + g < len2)
+                atomicOr(a.err, 1u);
+            const uint8_t* row = a.kp + (int64_t)(ok ? slot[n] : 0) * a.row_bytes;
+            if constexpr (KV == 2) {
+                const uint8_t* codes = row + fp4_code_off(h, D);
+                const uint8_t* sf = row + fp4_scale_off(h, a.Hkv, D);
+                if constexpr (D == 128) {
+                    const uint4 v = ok ? ldg_once(codes + 16 * t) : make_uint4(0, 0, 0, 0);
+                    raw[n][0] = v.x; raw[n][1] = v.y; raw[n][2] = v.z; raw[n][3] = v.w;
+                    scale[n] = ok ? *reinterpret_cast<const uint16_t*>(sf + 2 * t) : 0;
+                } else {
+                    const uint2 v = ok ? ldg_once8(codes + 8 * t) : make_uint2(0, 0);
+                    raw[n][0] = v.x; raw[n][1] = v.y;
+                    scale[n] = ok ? sf[t] : 0;
+                }
+            } else {
+                const uint8_t* piece = row + h * (RW * 16) + 16 * t;
+#pragma unroll
+                for (int i = 0; i < RW / 4; ++i) {
+                    const uint4 v = ok ? ldg_once(piece + 64 * i) : make_uint4(0, 0, 0, 0);
+                    raw[n][4 * i] = v.x; raw[n][4 * i + 1] = v.y; raw[n][4 * i + 2] = v.z; raw[n][4 * i + 3] = v.w;
+                }
+            }
+        }
+    };
+    // the query rows of KV head h: B fragments (row g of eight) of the same
+    // pieces that the keys come in, and the log-sum-exps of columns 2 t, 2 t + 1
+    uint32_t qf[F32 ? 1 : QW];
+    float2 l0, l1;
+    auto load_query = [&](int r2, int h) {
+        const int64_t row = (int64_t)r2 * a.Hq + h * a.G;
+        if constexpr (F32) {
+            __syncwarp();
+            for (int i = lane; i < a.G * (D / 4); i += 32)
+                reinterpret_cast<float4*>(&sq[warp * 8 * D])[i] = __ldg(reinterpret_cast<const float4*>(a.q) + row * (D / 4) + i);
+            __syncwarp();
+            l0 = t < a.G ? lse_parts(__ldg(a.lse + row + t)) : make_float2(0.f, 0.f);
+            l1 = t + 4 < a.G ? lse_parts(__ldg(a.lse + row + t + 4)) : make_float2(0.f, 0.f);
+        } else {
+            const uint4* q = reinterpret_cast<const uint4*>(static_cast<const bf16*>(a.q) + (row + min(g, a.G - 1)) * D);
+            uint32_t bad = 0;
+#pragma unroll
+            for (int i = 0; i < QW / 4; ++i) {
+                // bf16: piece 4 i + t; codes: a key piece's 16 or 32 elements are consecutive ones
+                const uint4 v = __ldg(q + (KV == 0 ? 4 * i + t : KV == 1 ? 8 * (i >> 1) + 2 * t + (i & 1) : (QW / 4) * t + i));
+                const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                for (int j = 0; j < 4; ++j) qf[4 * i + j] = KV == 0 ? w[j] : bf16x2_to_f16x2_chk(w[j], bad);
+            }
+            if (bad && g < a.G) atomicOr(a.err, kErrQRange);
+            l0 = 2 * t < a.G ? lse_parts(__ldg(a.lse + row + 2 * t)) : make_float2(0.f, 0.f);
+            l1 = 2 * t + 1 < a.G ? lse_parts(__ldg(a.lse + row + 2 * t + 1)) : make_float2(0.f, 0.f);
+        }
+    };
+    load_slots(r, tile, len);
+    load_keys(wh, tile, len);
+    int q_r = -1, q_h = -1;
+    for (int buf = 0; at < end; ++at, buf ^= 1) {
+        const int p0 = tile * TP;
+        float old = 0.f;
+        const int64_t score0 = (int64_t)r * a.scores_ld + p0;
+        // (all but the newest token had a score)
+        if (a.in && tid < TP && p0 + tid < len - 1) old = a.in[score0 + tid];
+        int r2 = r, tile2 = tile, len2 = len;
+        if (at + 1 < end) next_tile(r2, tile2, len2);
+        float sum[NR];
+#pragma unroll
+        for (int n = 0; n < NR; ++n) sum[n] = 0.f;
+        for (int h = wh; h < a.Hkv; h += hw) {
+            const bool last = h + hw >= a.Hkv;
+            if (last && at + 1 < end) load_slots(r2, tile2, len2);
+            if (q_r != r || q_h != h) load_query(r, h);
+            q_r = r;
+            q_h = h;
+            const uint32_t now = live;
+            float c[F32 ? NR * 2 : NR / 2][4];
+            if constexpr (F32) {
+#pragma unroll
+                for (int n = 0; n < NR; ++n) {
+                    // (lane t keeps the products of rows t and t + 4)
+                    float mine[2] = {0.f, 0.f};
+                    for (int j = 0; j < a.G; ++j) {
+                        const float4* q = reinterpret_cast<const float4*>(&sq[(warp * 8 + j) * D]);
+                        float dot = 0.f;
+#pragma unroll
+                        for (int i = 0; i < RW / 4; ++i) {
+                            const float4 y = q[4 * i + t];
+                            dot = fmaf(__uint_as_float(raw[n][4 * i]), y.x, dot);
+                            dot = fmaf(__uint_as_float(raw[n][4 * i + 1]), y.y, dot);
+                            dot = fmaf(__uint_as_float(raw[n][4 * i + 2]), y.z, dot);
+                            dot = fmaf(__uint_as_float(raw[n][4 * i + 3]), y.w, dot);
+                        }
+                        dot = quad_sum(dot);
+                        if ((j & 3) == t) mine[j >> 2] = dot;
+                    }
+                    c[n][0] = mine[0];
+                    c[n][1] = mine[1];
+                }
+            } else {
+#pragma unroll
+                for (int m = 0; m < NR / 2; ++m) {
+                    c[m][0] = c[m][1] = c[m][2] = c[m][3] = 0.f;
+                    const uint32_t* x = raw[2 * m];
+                    const uint32_t* y = raw[2 * m + 1];
+                    if constexpr (KV == 0) {
+#pragma unroll
+                        for (int i = 0; i < RW; i += 2) {
+                            const uint32_t f[4] = {x[i], y[i], x[i + 1], y[i + 1]};
+                            mma16816(c[m], f, qf[i], qf[i + 1]);
+                        }
+                    } else if constexpr (KV == 1) {
+#pragma unroll
+                        for (int i = 0; i < RW; ++i) {
+                            uint32_t x0, x1, y0, y1;
+                            e4m3x4_to_f16(x[i], x0, x1);
+                            e4m3x4_to_f16(y[i], y0, y1);
+                            mma16816_f16(c[m], x0, y0, x1, y1, qf[2 * i], qf[2 * i + 1]);
+                        }
+                    } else {
+                        const uint32_t xs = e4m3x2_to_f16(scale[2 * m]), ys = e4m3x2_to_f16(scale[2 * m + 1]);
+#pragma unroll
+                        for (int i = 0; i < RW; ++i) {
+                            // (a word is half a block of 16)
+                            const uint32_t sel = i < 2 ? 0x1010u : 0x3232u;
+                            const uint32_t xf = __byte_perm(xs, 0, sel), yf = __byte_perm(ys, 0, sel);
+                            uint32_t u[4], w[4];
+                            e2m1x8_to_f16(x[i], u);
+                            e2m1x8_to_f16(y[i], w);
+#pragma unroll
+                            for (int j = 0; j < 4; j += 2)
+                                mma16816_f16(c[m], hmul2_u(u[j], xf), hmul2_u(w[j], yf), hmul2_u(u[j + 1], xf),
+                                             hmul2_u(w[j + 1], yf), qf[4 * i + j], qf[4 * i + j + 1]);
+                        }
+                    }
+                }
+            }
+            // the next keys are on their way while this unit is finished
+            if (!last)
+                load_keys(h + hw, tile, len);
+            else if (at + 1 < end)
+                load_keys(wh, tile2, len2);
+            // (columns that are no query rows may hold 0 times an infinity)
+            const bool v0 = F32 ? t < a.G : 2 * t < a.G, v1 = F32 ? t + 4 < a.G : 2 * t + 1 < a.G;
+#pragma unroll
+            for (int n = 0; n < NR; ++n) {
+                const float x0 = F32 ? c[n][0] : c[n / 2][2 * (n & 1)], x1 = F32 ? c[n][1] : c[n / 2][2 * (n & 1) + 1];
+                const float w0 = ex2_ftz(fmaf(x0, a.scale, -l0.x)) * l0.y, w1 = ex2_ftz(fmaf(x1, a.scale, -l1.x)) * l1.y;
+                if (now >> n & 1u) sum[n] += (v0 ? w0 : 0.f) + (v1 ? w1 : 0.f);
+            }
+        }
+        float* const out = sums[buf] + wh * TP + sub * PU + g;
+#pragma unroll
+        for (int n = 0; n < NR; ++n) {
+            const float s = quad_sum(sum[n]);
+            if (t == 0) out[8 * n] = s;
+        }
+        __syncthreads();
+        for (int i = tid; i < TP && p0 + i < len; i += hw * nsub * 32) {
+            float s = 0.f;
+            for (int h = 0; h < hw; ++h) s += sums[buf][h * TP + i];
+            if (i != tid && a.in && p0 + i < len - 1) old = a.in[score0 + i];
+            a.out[score0 + i] = a.in && p0 + i < len - 1 ? fmaf(a.decay, old, s) : s;
+        }
+        r = r2;
+        tile = tile2;
+        len = len2;
+    }
+}
+
+// ---------------------------------------------------------------------------
 // Host side
 // ---------------------------------------------------------------------------
 int cuda_status(cudaError_t e) {
@@ -193,6 +483,34 @@ int cuda_status(cudaError_t e) {
     sgl::set_cuda_error(static_cast<int>(e));
     return SGL_ERR_CUDA;
 }
+
+// [head_dim 128][dtype]: the kernel, positions of a warp
+struct DecodeKernel {
+    void (*run)(WeightArgs, int, int);
+    int positions;
+};
+constexpr DecodeKernel decode_kernels[2][4] = {
+    {{weights_decode<64, kKvF32>, Stream<64, kKvF32>::PU}, {weights_decode<64, 0>, Stream<64, 0>::PU},
+     {weights_decode<64, 1>, Stream<64, 1>::PU}, {weights_decode<64, 2>, Stream<64, 2>::PU}},
+    {{weights_decode<128, kKvF32>, Stream<128, kKvF32>::PU}, {weights_decode<128, 0>, Stream<128, 0>::PU},
+     {weights_decode<128, 1>, Stream<128, 1>::PU}, {weights_decode<128, 2>, Stream<128, 2>::PU}}};
+
+cudaError_t launch_decode(const DecodeKernel& k, const WeightArgs& a, cudaStream_t s) {
+    // a warp per KV head up to eight, else several per head
+    const int hw = std::min(a.Hkv, 8), nsub = 8 / hw, tp = k.positions * nsub;
+    constexpr int kCtas = 152 * 3;
+    cudaLaunchAttribute pdl[1];
+    pdl[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    pdl[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)std::min<int64_t>(kCtas, a.B * (((int64_t)a.lim + tp - 1) / tp)));
+    cfg.blockDim = dim3((unsigned)(hw * nsub * 32));
+    cfg.stream = s;
+    cfg.attrs = pdl;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, k.run, a, hw, nsub);
+}
+
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
 }  // namespace
@@ -270,6 +588,10 @@ int sgl_attn_weights(const void* q, const float* lse, const void* k_pool, const 
     if (kind == SGL_DTYPE_BF16_FP8KV || kind == SGL_DTYPE_BF16_FP4KV) a.scale *= params->k_scale;
     a.decay = decay;
     auto s = reinterpret_cast<cudaStream_t>(stream);
+    if (!extend_lens) {
+        const auto* kernel = &decode_kernels[d == 128][kind];
+        return cuda_status(launch_decode(*kernel, a, s));
+    }
     const dim3 grid((unsigned)((most + 31) / 32), (unsigned)B);
     if (B > 65535) return SGL_ERR_UNSUPPORTED;
     auto go = [&](auto kernel) { kernel<<<grid, 256, 0, s>>>(a); };
