@@ -726,9 +726,9 @@ int sgl_attn_weights_workspace_bytes(const sgl_attn_params* params, int32_t wind
  *                read nor written
  *   decay        what a gathered score keeps, >= 0 and finite
  * The products are those of the attention call on the same pool (fp32 sums;
- * an E4M3 or 4-bit pool takes the query as f16, elements out of its range set
- * SGL_ERR_BOUNDS for sgl_check); the weights and their sums are fp32, always
- * added in the same order.  A slot outside the pool gives its token no weight
+ * the decode form takes the query of an E4M3 or 4-bit pool as f16, elements out
+ * of its range set SGL_ERR_BOUNDS for sgl_check, chunks take it as it is); the
+ * weights and their sums are fp32, always added in the same order.  A slot outside the pool gives its token no weight
  * and sets bit 0 of the workspace's error word; a length outside the table sets
  * bit 1 and leaves the request's scores as they were.  A prefix that requests
  * share is read once for each of them.

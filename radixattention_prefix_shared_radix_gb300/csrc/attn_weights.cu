@@ -13,95 +13,19 @@
 #include <cmath>
 
 #include "common.h"
-#include "device_common.cuh"
-#include "fp4.cuh"
+#include "weights.cuh"
 
 namespace {
 
 using namespace sgldev;
-
-constexpr int kKvF32 = 3;                // pools by dtype, as elsewhere: 0 bf16, 1 E4M3, 2 4-bit rows
-
-struct WeightArgs {
-    const void* q;
-    const float* lse;
-    const uint8_t* kp;
-    const int32_t* r2t;
-    const int32_t *lens, *ext;           // ext null: decode
-    const float* in;                     // null: zeros
-    float* out;
-    int64_t ld, scores_ld, num_slots, n_rows;
-    uint32_t* err;
-    int B, Hq, Hkv, G, window, lim, row_bytes;
-    float scale, decay;                  // scale: of a product, to a power of 2
-};
-
-// What request r asks: rows [row, row + ask) of the queries, row i of which sees
-// positions 0 .. p0 + i; its scores [0, total), those from `fresh` on beginning
-// at 0.  ask 0: nothing to do (or lengths that the tables do not hold).
-struct Asked {
-    int total, ask, p0, fresh;
-    int64_t row;
-};
-__device__ __forceinline__ Asked asked(const WeightArgs& a, int r, int64_t before, bool flag) {
-    Asked x{0, 0, 0, 0, 0};
-    const int len = __ldg(a.lens + r);
-    if (!a.ext) {
-        if (len < 0 || len > a.lim) {
-            if (flag) atomicOr(a.err, 2u);
-            return x;
-        }
-        return Asked{len, len > 0 ? 1 : 0, len - 1, len - 1, r};
-    }
-    const int e = __ldg(a.ext + r);
-    if (len < 0 || e < 0 || (int64_t)len + e > a.lim || before + e > a.n_rows) {
-        if (flag) atomicOr(a.err, 2u);
-        return x;
-    }
-    const int ask = a.window > 0 ? min(a.window, e) : e;
-    return Asked{len + e, ask, len + e - ask, len, before + e - ask};
-}
-
-// hi and 2^(-lo) of a row's log-sum-exp L: hi + lo = L log2 e, log2 e as the sum of two floats
-__device__ __forceinline__ float2 lse_parts(float l) {
-    constexpr float kLow = 1.92596299e-8f;
-    if (l == -INFINITY) return make_float2(0.f, 0.f);
-    const float hi = l * kLog2e;
-    return make_float2(hi, ex2_ftz(-fmaf(l, kLow, fmaf(l, kLog2e, -hi))));
-}
+using namespace sgl::wts;
 
 // ---------------------------------------------------------------------------
-// Chunks, on CUDA cores: a CTA per (tile of 32 positions, request) takes every KV
+// Chunks over fp32 pools, on CUDA cores: a CTA per (tile of 32 positions, request) takes every KV
 // head and asking row, 32 rows at a time; a thread has one position and four
 // rows of each 32.
 // ---------------------------------------------------------------------------
-template <int D, int KV>
-__device__ __forceinline__ float4 key4(const WeightArgs& a, int64_t slot, int h, int c) {
-    const uint8_t* row = a.kp + slot * a.row_bytes;
-    float4 v;
-    if constexpr (KV == kKvF32) {
-        v = reinterpret_cast<const float4*>(row)[h * (D / 4) + c];
-    } else if constexpr (KV == 0) {
-        const uint2 w = reinterpret_cast<const uint2*>(row)[h * (D / 4) + c];
-        v = make_float4(__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xffff0000u), __uint_as_float(w.y << 16),
-                        __uint_as_float(w.y & 0xffff0000u));
-    } else if constexpr (KV == 1) {
-        uint32_t lo, hi;
-        e4m3x4_to_f16(reinterpret_cast<const uint32_t*>(row)[h * (D / 4) + c], lo, hi);
-        const float2 x = __half22float2(*reinterpret_cast<__half2*>(&lo)), y = __half22float2(*reinterpret_cast<__half2*>(&hi));
-        v = make_float4(x.x, x.y, y.x, y.y);
-    } else {
-        const uint32_t w = *reinterpret_cast<const uint16_t*>(row + fp4_code_off(h, D) + 2 * c);
-        uint32_t y[4];
-        e2m1x8_to_f16(w, y);
-        const float f = e4m3_value(row[fp4_scale_off(h, a.Hkv, D) + c / 4]);
-        const float2 p = __half22float2(*reinterpret_cast<__half2*>(&y[0])), s = __half22float2(*reinterpret_cast<__half2*>(&y[1]));
-        v = make_float4(p.x * f, p.y * f, s.x * f, s.y * f);
-    }
-    return v;
-}
-
-template <int D, int KV>
+template <int D>
 __global__ void __launch_bounds__(256) weights_plain(const __grid_constant__ WeightArgs a) {
     constexpr int RS = D + 4;            // (rows of 32 in distinct banks)
     __shared__ __align__(16) float sk[32 * RS], sq[32 * RS];
@@ -134,7 +58,8 @@ __global__ void __launch_bounds__(256) weights_plain(const __grid_constant__ Wei
     for (int h = 0; h < a.Hkv; ++h) {
         __syncthreads();
         for (int c = sub; c < D / 4; c += 8) {
-            const float4 v = slot >= 0 ? key4<D, KV>(a, slot, h, c) : make_float4(0.f, 0.f, 0.f, 0.f);
+            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (slot >= 0) v = reinterpret_cast<const float4*>(a.kp + slot * a.row_bytes)[h * (D / 4) + c];
             *reinterpret_cast<float4*>(&sk[(tid >> 3) * RS + 4 * c]) = v;
         }
         for (int b = row0; b < rows; b += 32) {
@@ -143,15 +68,7 @@ __global__ void __launch_bounds__(256) weights_plain(const __grid_constant__ Wei
             const int64_t qrow = (x.row + mine / a.G) * a.Hq + h * a.G + mine % a.G;
             for (int c = sub; c < D / 4; c += 8) {
                 float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-                if (mine < rows) {
-                    if constexpr (KV == kKvF32) {
-                        v = reinterpret_cast<const float4*>(a.q)[qrow * (D / 4) + c];
-                    } else {
-                        const uint2 w = reinterpret_cast<const uint2*>(a.q)[qrow * (D / 4) + c];
-                        v = make_float4(__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xffff0000u),
-                                        __uint_as_float(w.y << 16), __uint_as_float(w.y & 0xffff0000u));
-                    }
-                }
+                if (mine < rows) v = reinterpret_cast<const float4*>(a.q)[qrow * (D / 4) + c];
                 *reinterpret_cast<float4*>(&sq[(tid >> 3) * RS + 4 * c]) = v;
             }
             if (sub == 0) sl[tid >> 3] = mine < rows ? lse_parts(a.lse[qrow]) : make_float2(0.f, 0.f);
@@ -531,6 +448,7 @@ int sgl_attn_weights_workspace_bytes(const sgl_attn_params* params, int32_t wind
             if (params->host_prefix_lens[r] < 0 || params->host_extend_lens[r] < 0) return SGL_ERR_INVALID_ARG;
     }
     *bytes = sgl::kWsAlign;
+    if (params->host_extend_lens && params->dtype != SGL_DTYPE_F32) *bytes += (size_t)tc_plan(params, window).items * 1024;
     return SGL_OK;
 }
 
@@ -584,23 +502,30 @@ int sgl_attn_weights(const void* q, const float* lse, const void* k_pool, const 
     a.lim = (int)lim;
     a.row_bytes = kind == SGL_DTYPE_BF16_FP4KV ? fp4_row_bytes(a.Hkv, d)
                                                : a.Hkv * d * (kind == SGL_DTYPE_F32 ? 4 : kind == SGL_DTYPE_BF16 ? 2 : 1);
-    a.scale = (params->sm_scale > 0.f ? params->sm_scale : 1.0f / std::sqrt(static_cast<float>(d))) * kLog2e;
-    if (kind == SGL_DTYPE_BF16_FP8KV || kind == SGL_DTYPE_BF16_FP4KV) a.scale *= params->k_scale;
+    // (rounded once: what it is off by moves every weight the same way)
+    double scale = (params->sm_scale > 0.f ? params->sm_scale : 1.0 / std::sqrt(static_cast<double>(d))) * 1.4426950408889634;
+    if (kind == SGL_DTYPE_BF16_FP8KV || kind == SGL_DTYPE_BF16_FP4KV) scale *= params->k_scale;
+    a.scale = static_cast<float>(scale);
     a.decay = decay;
     auto s = reinterpret_cast<cudaStream_t>(stream);
     if (!extend_lens) {
         const auto* kernel = &decode_kernels[d == 128][kind];
         return cuda_status(launch_decode(*kernel, a, s));
     }
+    if (kind != SGL_DTYPE_F32) {
+        const TcPlan plan = tc_plan(params, window);
+        if (ws_bytes < sgl::kWsAlign + (size_t)plan.items * 1024) return SGL_ERR_WORKSPACE;
+        auto* partial = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + sgl::kWsAlign);
+        const int kv = kind == SGL_DTYPE_BF16 ? 0 : kind == SGL_DTYPE_BF16_FP8KV ? 1 : 2;
+        const int e = launch_weights_tc(a, kv, d, plan, partial, s);
+        return e < 0 ? SGL_ERR_UNSUPPORTED : cuda_status(static_cast<cudaError_t>(e));
+    }
     const dim3 grid((unsigned)((most + 31) / 32), (unsigned)B);
     if (B > 65535) return SGL_ERR_UNSUPPORTED;
-    auto go = [&](auto kernel) { kernel<<<grid, 256, 0, s>>>(a); };
-    switch (kind) {
-        case SGL_DTYPE_F32: d == 64 ? go(weights_plain<64, kKvF32>) : go(weights_plain<128, kKvF32>); break;
-        case SGL_DTYPE_BF16: d == 64 ? go(weights_plain<64, 0>) : go(weights_plain<128, 0>); break;
-        case SGL_DTYPE_BF16_FP8KV: d == 64 ? go(weights_plain<64, 1>) : go(weights_plain<128, 1>); break;
-        default: d == 64 ? go(weights_plain<64, 2>) : go(weights_plain<128, 2>); break;
-    }
+    if (d == 64)
+        weights_plain<64><<<grid, 256, 0, s>>>(a);
+    else
+        weights_plain<128><<<grid, 256, 0, s>>>(a);
     return cuda_status(cudaGetLastError());
 }
 

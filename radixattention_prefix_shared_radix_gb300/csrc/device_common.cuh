@@ -424,6 +424,14 @@ __device__ __forceinline__ void tma_load_row(uint32_t dst, const void* tmap, int
 __device__ __forceinline__ void tma_load_box(uint32_t dst, const void* tmap, int x, int y, uint32_t bar) {
     tma_load_row(dst, tmap, x, y, bar);
 }
+// The same of a 3-D tensor: column x, rows from (y, z) on.
+__device__ __forceinline__ void tma_load_box3(uint32_t dst, const void* tmap, int x, int y, int z, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], "
+        "[%5];\n" ::"r"(dst),
+        "l"(tmap), "r"(x), "r"(y), "r"(z), "r"(bar)
+        : "memory");
+}
 // Arrive on `bar` once every cp.async this thread issued so far has landed
 // (the barrier's expected count includes this arrival).
 __device__ __forceinline__ void cp_async_arrive_noinc(uint32_t bar) {

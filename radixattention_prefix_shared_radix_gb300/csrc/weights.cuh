@@ -1,0 +1,76 @@
+// What the kernels that sum attention weights (attn_weights.cu, weights_tc.cu)
+// share: their arguments, what a request asks, and a row's log-sum-exp in two
+// parts.
+#pragma once
+
+#include "device_common.cuh"
+#include "fp4.cuh"
+
+namespace sgl {
+namespace wts {
+
+using namespace sgldev;
+
+constexpr int kKvF32 = 3;                // pools by dtype, as elsewhere: 0 bf16, 1 E4M3, 2 4-bit rows
+
+struct WeightArgs {
+    const void* q;
+    const float* lse;
+    const uint8_t* kp;
+    const int32_t* r2t;
+    const int32_t *lens, *ext;           // ext null: decode
+    const float* in;                     // null: zeros
+    float* out;
+    int64_t ld, scores_ld, num_slots, n_rows;
+    uint32_t* err;
+    int B, Hq, Hkv, G, window, lim, row_bytes;
+    float scale, decay;                  // scale: of a product, to a power of 2
+};
+
+// What request r asks: rows [row, row + ask) of the queries, row i of which sees
+// positions 0 .. p0 + i; its scores [0, total), those from `fresh` on beginning
+// at 0.  ask 0: nothing to do (or lengths that the tables do not hold).
+struct Asked {
+    int total, ask, p0, fresh;
+    int64_t row;
+};
+__device__ __forceinline__ Asked asked(const WeightArgs& a, int r, int64_t before, bool flag) {
+    Asked x{0, 0, 0, 0, 0};
+    const int len = __ldg(a.lens + r);
+    if (!a.ext) {
+        if (len < 0 || len > a.lim) {
+            if (flag) atomicOr(a.err, 2u);
+            return x;
+        }
+        return Asked{len, len > 0 ? 1 : 0, len - 1, len - 1, r};
+    }
+    const int e = __ldg(a.ext + r);
+    if (len < 0 || e < 0 || (int64_t)len + e > a.lim || before + e > a.n_rows) {
+        if (flag) atomicOr(a.err, 2u);
+        return x;
+    }
+    const int ask = a.window > 0 ? min(a.window, e) : e;
+    return Asked{len + e, ask, len + e - ask, len, before + e - ask};
+}
+
+// hi and 2^(-lo) of a row's log-sum-exp L: hi + lo = L log2 e, log2 e as the sum of two floats
+__device__ __forceinline__ float2 lse_parts(float l) {
+    constexpr float kLow = 1.92596299e-8f;
+    if (l == -INFINITY) return make_float2(0.f, 0.f);
+    if (!(l < INFINITY)) return make_float2(l, 1.f);     // (a NaN in the exponent, where a mask still takes it out)
+    const float hi = l * kLog2e;
+    return make_float2(hi, ex2_ftz(-fmaf(l, kLow, fmaf(l, kLog2e, -hi))));
+}
+
+// Chunks on the tensor cores (weights_tc.cu): what a call needs of its
+// workspace is 1024 bytes an item.
+struct TcPlan {
+    int64_t items, tiles;                // work items; tiles of 256 positions
+    int run;                             // query blocks of an item
+};
+TcPlan tc_plan(const sgl_attn_params* params, int window);
+// 0, a cudaError_t, or -1: beyond what the kernels count
+int launch_weights_tc(const WeightArgs& args, int kv, int head_dim, const TcPlan& plan, float* partial, cudaStream_t s);
+
+}  // namespace wts
+}  // namespace sgl

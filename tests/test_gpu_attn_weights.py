@@ -320,17 +320,19 @@ def test_bad_slots_and_lengths_are_reported(kind, decode):
 
 
 @pytest.mark.parametrize("kind", ["fp8", "fp4"])
-@pytest.mark.parametrize("decode", [False, True])
-def test_a_query_beyond_f16_is_reported(kind, decode):
-    ext = np.array([1, 1]) if decode else np.array([70, 30])
-    pre = np.array([150, 20])
+def test_a_query_beyond_f16(kind):
+    """A decode batch over FP8 or 4-bit keys reports it; chunks multiply in bf16 and take it as it is."""
+    pre, ext = np.array([150, 20]), np.array([1, 1])
     c = Cache(kind, pre + ext, 8, 4, 64, seed=7)
-    q = c.queries(int(ext.sum()))
-    lse = c.lse(q, pre, ext, 0.125)
+    q = c.queries(2)
     q[-1, 3, 17] = 70000.0
+    lse = c.lse(q, pre, ext, 0.125)
     with pytest.raises(sgl.SglError) as e:
-        _run(c, q, lse, pre, ext, 0, None, 1.0, decode)
+        _run(c, q, lse, pre, ext, 0, None, 1.0, True)
     assert e.value.status == -5
+    got = _run(c, q, lse, pre, ext, 0, None, 1.0, False)
+    want, tol = c.expect(q, lse, pre, ext, 0, np.zeros(got.shape, dtype=np.float32), 0.0, False, 0.125)
+    assert (np.abs(got - want) <= tol).all()
 
 
 @pytest.mark.parametrize("kind", list(KINDS))
