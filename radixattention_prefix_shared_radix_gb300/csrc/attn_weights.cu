@@ -3,11 +3,7 @@
 //
 // With s = sm_scale <q, k_p> and the row's log-sum-exp L from the attention
 // call, a weight is exp(s - L): no second softmax, one product Q K^T and one
-// exponential per (row, head, position), and a sum over rows.  In base 2,
-// 2^(s log2 e - hi) times the row's factor 2^(-lo), hi + lo = L log2 e: hi alone
-// is off by up to half a unit of its last place (2^-20 at L near 10), and the
-// factor costs nothing, since the sum over rows takes it as the multiplier of a
-// fused multiply-add (0 for a row that saw nothing).
+// exponential per (row, head, position), and a sum over rows.
 
 #include <algorithm>
 #include <cmath>
@@ -29,7 +25,7 @@ template <int D>
 __global__ void __launch_bounds__(256) weights_plain(const __grid_constant__ WeightArgs a) {
     constexpr int RS = D + 4;            // (rows of 32 in distinct banks)
     __shared__ __align__(16) float sk[32 * RS], sq[32 * RS];
-    __shared__ float2 sl[32];
+    __shared__ float sl[32];
     __shared__ int64_t before_s;
     const int r = blockIdx.y, tid = threadIdx.x, t0 = blockIdx.x * 32;
     if (tid < 32) {
@@ -71,7 +67,7 @@ __global__ void __launch_bounds__(256) weights_plain(const __grid_constant__ Wei
                 if (mine < rows) v = reinterpret_cast<const float4*>(a.q)[qrow * (D / 4) + c];
                 *reinterpret_cast<float4*>(&sq[(tid >> 3) * RS + 4 * c]) = v;
             }
-            if (sub == 0) sl[tid >> 3] = mine < rows ? lse_parts(a.lse[qrow]) : make_float2(0.f, 0.f);
+            if (sub == 0) sl[tid >> 3] = mine < rows ? minus_lse(a.lse[qrow]) : 0.f;
             __syncthreads();
             float dot[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll 8
@@ -86,10 +82,9 @@ __global__ void __launch_bounds__(256) weights_plain(const __grid_constant__ Wei
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const int row = 4 * i + (sub & 3) + 16 * (sub >> 2);
-                const float2 l = sl[row];
                 // a row sees positions up to its own
                 if (b + row < rows && pos <= x.p0 + (b + row) / a.G)
-                    sum = fmaf(ex2_ftz(fmaf(dot[i], a.scale, -l.x)), l.y, sum);
+                    sum += weight_of(dot[i], a.scale, sl[row]);
             }
         }
     }
@@ -251,7 +246,7 @@ __global__ void __launch_bounds__(kStreamThreads, 3) weights_decode(const __grid
     // the query rows of KV head h: B fragments (row g of eight) of the same
     // pieces that the keys come in, and the log-sum-exps of columns 2 t, 2 t + 1
     uint32_t qf[F32 ? 1 : QW];
-    float2 l0, l1;
+    float l0, l1;
     auto load_query = [&](int r2, int h) {
         const int64_t row = (int64_t)r2 * a.Hq + h * a.G;
         if constexpr (F32) {
@@ -259,8 +254,8 @@ __global__ void __launch_bounds__(kStreamThreads, 3) weights_decode(const __grid
             for (int i = lane; i < a.G * (D / 4); i += 32)
                 reinterpret_cast<float4*>(&sq[warp * 8 * D])[i] = __ldg(reinterpret_cast<const float4*>(a.q) + row * (D / 4) + i);
             __syncwarp();
-            l0 = t < a.G ? lse_parts(__ldg(a.lse + row + t)) : make_float2(0.f, 0.f);
-            l1 = t + 4 < a.G ? lse_parts(__ldg(a.lse + row + t + 4)) : make_float2(0.f, 0.f);
+            l0 = t < a.G ? minus_lse(__ldg(a.lse + row + t)) : 0.f;
+            l1 = t + 4 < a.G ? minus_lse(__ldg(a.lse + row + t + 4)) : 0.f;
         } else {
             const uint4* q = reinterpret_cast<const uint4*>(static_cast<const bf16*>(a.q) + (row + min(g, a.G - 1)) * D);
             uint32_t bad = 0;
@@ -273,8 +268,8 @@ __global__ void __launch_bounds__(kStreamThreads, 3) weights_decode(const __grid
                 for (int j = 0; j < 4; ++j) qf[4 * i + j] = KV == 0 ? w[j] : bf16x2_to_f16x2_chk(w[j], bad);
             }
             if (bad && g < a.G) atomicOr(a.err, kErrQRange);
-            l0 = 2 * t < a.G ? lse_parts(__ldg(a.lse + row + 2 * t)) : make_float2(0.f, 0.f);
-            l1 = 2 * t + 1 < a.G ? lse_parts(__ldg(a.lse + row + 2 * t + 1)) : make_float2(0.f, 0.f);
+            l0 = 2 * t < a.G ? minus_lse(__ldg(a.lse + row + 2 * t)) : 0.f;
+            l1 = 2 * t + 1 < a.G ? minus_lse(__ldg(a.lse + row + 2 * t + 1)) : 0.f;
         }
     };
     load_slots(r, tile, len);
@@ -369,7 +364,7 @@ __global__ void __launch_bounds__(kStreamThreads, 3) weights_decode(const __grid
 #pragma unroll
             for (int n = 0; n < NR; ++n) {
                 const float x0 = F32 ? c[n][0] : c[n / 2][2 * (n & 1)], x1 = F32 ? c[n][1] : c[n / 2][2 * (n & 1) + 1];
-                const float w0 = ex2_ftz(fmaf(x0, a.scale, -l0.x)) * l0.y, w1 = ex2_ftz(fmaf(x1, a.scale, -l1.x)) * l1.y;
+                const float w0 = weight_of(x0, a.scale, l0), w1 = weight_of(x1, a.scale, l1);
                 if (now >> n & 1u) sum[n] += (v0 ? w0 : 0.f) + (v1 ? w1 : 0.f);
             }
         }
@@ -448,7 +443,7 @@ int sgl_attn_weights_workspace_bytes(const sgl_attn_params* params, int32_t wind
             if (params->host_prefix_lens[r] < 0 || params->host_extend_lens[r] < 0) return SGL_ERR_INVALID_ARG;
     }
     *bytes = sgl::kWsAlign;
-    if (params->host_extend_lens && params->dtype != SGL_DTYPE_F32) *bytes += (size_t)tc_plan(params, window).items * 1024;
+    if (params->host_extend_lens && params->dtype != SGL_DTYPE_F32) *bytes += (size_t)tc_plan(params, window).items * 2048;
     return SGL_OK;
 }
 
@@ -502,10 +497,8 @@ int sgl_attn_weights(const void* q, const float* lse, const void* k_pool, const 
     a.lim = (int)lim;
     a.row_bytes = kind == SGL_DTYPE_BF16_FP4KV ? fp4_row_bytes(a.Hkv, d)
                                                : a.Hkv * d * (kind == SGL_DTYPE_F32 ? 4 : kind == SGL_DTYPE_BF16 ? 2 : 1);
-    // (rounded once: what it is off by moves every weight the same way)
-    double scale = (params->sm_scale > 0.f ? params->sm_scale : 1.0 / std::sqrt(static_cast<double>(d))) * 1.4426950408889634;
-    if (kind == SGL_DTYPE_BF16_FP8KV || kind == SGL_DTYPE_BF16_FP4KV) scale *= params->k_scale;
-    a.scale = static_cast<float>(scale);
+    a.scale = params->sm_scale > 0.f ? params->sm_scale : 1.0f / std::sqrt(static_cast<float>(d));
+    if (kind == SGL_DTYPE_BF16_FP8KV || kind == SGL_DTYPE_BF16_FP4KV) a.scale *= params->k_scale;
     a.decay = decay;
     auto s = reinterpret_cast<cudaStream_t>(stream);
     if (!extend_lens) {
@@ -514,7 +507,7 @@ int sgl_attn_weights(const void* q, const float* lse, const void* k_pool, const 
     }
     if (kind != SGL_DTYPE_F32) {
         const TcPlan plan = tc_plan(params, window);
-        if (ws_bytes < sgl::kWsAlign + (size_t)plan.items * 1024) return SGL_ERR_WORKSPACE;
+        if (ws_bytes < sgl::kWsAlign + (size_t)plan.items * 2048) return SGL_ERR_WORKSPACE;
         auto* partial = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + sgl::kWsAlign);
         const int kv = kind == SGL_DTYPE_BF16 ? 0 : kind == SGL_DTYPE_BF16_FP8KV ? 1 : 2;
         const int e = launch_weights_tc(a, kv, d, plan, partial, s);

@@ -1,6 +1,5 @@
 // What the kernels that sum attention weights (attn_weights.cu, weights_tc.cu)
-// share: their arguments, what a request asks, and a row's log-sum-exp in two
-// parts.
+// share: their arguments, what a request asks, and a weight.
 #pragma once
 
 #include "device_common.cuh"
@@ -24,7 +23,7 @@ struct WeightArgs {
     int64_t ld, scores_ld, num_slots, n_rows;
     uint32_t* err;
     int B, Hq, Hkv, G, window, lim, row_bytes;
-    float scale, decay;                  // scale: of a product, to a power of 2
+    float scale, decay;                  // scale: of a product
 };
 
 // What request r asks: rows [row, row + ask) of the queries, row i of which sees
@@ -53,17 +52,17 @@ __device__ __forceinline__ Asked asked(const WeightArgs& a, int r, int64_t befor
     return Asked{len + e, ask, len + e - ask, len, before + e - ask};
 }
 
-// hi and 2^(-lo) of a row's log-sum-exp L: hi + lo = L log2 e, log2 e as the sum of two floats
-__device__ __forceinline__ float2 lse_parts(float l) {
-    constexpr float kLow = 1.92596299e-8f;
-    if (l == -INFINITY) return make_float2(0.f, 0.f);
-    if (!(l < INFINITY)) return make_float2(l, 1.f);     // (a NaN in the exponent, where a mask still takes it out)
-    const float hi = l * kLog2e;
-    return make_float2(hi, ex2_ftz(-fmaf(l, kLow, fmaf(l, kLog2e, -hi))));
+// What a row adds to its products' scale before the exponential: minus its
+// log-sum-exp, and -infinity for a row that saw nothing (it adds no weight).
+__device__ __forceinline__ float minus_lse(float l) { return l == -INFINITY ? l : -l; }
+// exp(s + m): the difference first, rounded once, then to base 2 (in base 2
+// from the start the log-sum-exp itself would be rounded, by up to 2^-20)
+__device__ __forceinline__ float weight_of(float product, float scale, float m) {
+    return ex2_ftz(fmaf(product, scale, m) * kLog2e);
 }
 
 // Chunks on the tensor cores (weights_tc.cu): what a call needs of its
-// workspace is 1024 bytes an item.
+// workspace is 2048 bytes an item.
 struct TcPlan {
     int64_t items, tiles;                // work items; tiles of 256 positions
     int run;                             // query blocks of an item

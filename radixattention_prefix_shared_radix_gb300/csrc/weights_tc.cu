@@ -16,16 +16,23 @@
 // that an MMA reads from shared memory only its N rows.
 //
 // An item is 256 positions (two tiles of 128 rows) of one request and KV head
-// against a run of its query blocks of 128 rows; it writes 256 partial sums.
-// CTAs (one per SM) take items in turn; a second launch adds the partial sums of
-// a request's heads and runs in order and puts them into the scores.
-//   warps 0 .. 7    softmax: tile w / 4, thread = position = TMEM lane
-//   warps 8 .. 15   K: a thread takes half of a position's row of either tile
-//                   from the pool (looked up an item ahead, loaded while the item
-//                   before is multiplied) into TMEM, two items' rows in turn
-//   warp 16         issues the MMAs (and owns TMEM)
-//   warp 17         Q blocks by TMA (four stages), and the rows' log-sum-exps,
-//                   in two parts, beside them (eight stages)
+// against a run of its query blocks of 128 rows; CTAs (one per SM) take items in
+// turn.  Two warpgroups share a block's columns, 64 each, for both tiles: a
+// column's log-sum-exp, which every position needs, comes from shared memory as a
+// broadcast, and a warp's broadcast costs the same 512 bytes of bandwidth
+// whatever it is worth, so it is used for two positions at once.  A whole half
+// block (128 scores of a thread) goes to registers before any exponential, which
+// hands the accumulators back to the MMAs; the warpgroups have 176 registers a
+// thread for it, taken from the others.  The two warpgroups' sums, 256 each, go
+// to memory; a second launch adds those of a request's heads and runs in order
+// and puts them into the scores.
+//   warps 0 .. 7    softmax: columns 64 (w / 4) on, thread = TMEM lane
+//   warps 8 .. 11   K: rows 32 (w % 4) on of both tiles, copied to shared memory
+//                   some tiles ahead, and from there, converted, to TMEM, where two
+//                   items' rows take turns
+//   warp 12         issues the MMAs (and owns TMEM)
+//   warp 13         Q blocks by TMA, and beside them the rows' log-sum-exps, which
+//                   it loads a block ahead
 // All waits are bounded: one that gives up sets bit 2 of the error word, and the
 // code runs to its end without hanging.
 
@@ -43,16 +50,24 @@ namespace {
 
 using namespace tc;
 
-constexpr int kThreads = 18 * 32;
-constexpr int kLoadWarp = 8, kMmaWarp = 16, kQueryWarp = 17;
-constexpr int kQStages = 4, kLStages = 8;
+constexpr int kThreads = 512;
+constexpr int kLoadWarp = 8, kMmaWarp = 12, kQueryWarp = 13;
+constexpr int kLStages = 8;
 constexpr int kMaxRows = 1 << 24;        // query rows of a call
+// registers of a thread: 2 x 128 x 176 + 128 x 96 + 128 x 64 = the launch's 512 x 128
+constexpr int kSoftmaxRegs = 176, kLoadRegs = 96, kOtherRegs = 64;
 
-template <int D>
+template <int D, int KV>
 struct Lay {
+    // a pool row of one head as staged: its bytes (4-bit rows: codes, then scales) and the stride, an odd number of 16 bytes
+    static constexpr int ROW = KV == 0 ? D * 2 : KV == 1 ? D : D / 2;
+    static constexpr int STRIDE = KV == 2 ? D / 2 + 16 : ROW + 16;
+    static constexpr int KTILES = KV == 0 && D == 128 ? 3 : 4;   // staged tiles
+    static constexpr int QSTAGES = KV == 0 && D == 128 ? 3 : 4;
     static constexpr int QTILE = 128 * D * 2;
-    static constexpr int OFF_L = kQStages * QTILE;               // (-hi, -hi, factor, factor) of column pairs
-    static constexpr int OFF_BAR = OFF_L + kLStages * 1024;
+    static constexpr int OFF_K = QSTAGES * QTILE;
+    static constexpr int OFF_L = OFF_K + KTILES * 128 * STRIDE;  // minus the log-sum-exps of a block's columns
+    static constexpr int OFF_BAR = OFF_L + kLStages * 512;
     static constexpr int OFF_TMEM = OFF_BAR + 40 * 8;
     static constexpr int END = OFF_TMEM + 16;
     // barriers
@@ -62,7 +77,7 @@ struct Lay {
 
 struct TcWeightArgs {
     WeightArgs w;
-    float* partial;                      // [items, 256]
+    float* partial;                      // [items, 2, 256]
     int items, run;                      // items of the call; query blocks of an item
 };
 
@@ -154,6 +169,7 @@ struct Item {
 
 // The next item from `at` on, or false; warps of every role go through the same ones.
 __device__ __forceinline__ bool item_at(const TcWeightArgs& a, Walk& w, int at, Item& it) {
+    __syncwarp();        // (after what single lanes did: the search needs the whole warp)
     if (at >= a.items || !w.find(a.w, a.run, at, false, it.q)) return false;
     const int k = at - it.q.first, tile = k % it.q.tiles, hs = k / it.q.tiles, s = hs % it.q.runs;
     it.at = at;
@@ -169,7 +185,7 @@ __device__ __forceinline__ bool item_at(const TcWeightArgs& a, Walk& w, int at, 
     return true;
 }
 
-// (y0, y1) = (a0, a1) * (b0, b1) + (c0, c1), packed
+// packed pairs
 __device__ __forceinline__ uint64_t pack2(float x, float y) {
     uint64_t r;
     asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
@@ -183,6 +199,16 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
     asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
     return r;
 }
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
 
 // 16 consecutive TMEM columns of this thread's lane
 __device__ __forceinline__ void tst16u_nw(uint32_t taddr, const uint32_t* r) {
@@ -192,76 +218,48 @@ __device__ __forceinline__ void tst16u_nw(uint32_t taddr, const uint32_t* r) {
         "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
         : "memory");
 }
-// an f16 pair as bf16 pairs (exact for the pools' values; NaN kept)
+// an f16 pair as a bf16 pair (exact for the pools' values; NaN kept)
 __device__ __forceinline__ uint32_t bf16x2_of_f16x2(uint32_t h) {
     const float2 f = __half22float2(*reinterpret_cast<__half2*>(&h));
     return pack_bf16(f.x, f.y);
 }
 
-// Half a pool row of KV head h: as loaded, and as D / 4 TMEM columns (bf16 pairs).
+// 32 elements of a staged row (a quarter of 128, half of 64) as 16 TMEM columns (bf16 pairs)
 template <int D, int KV>
-struct HalfRow {
-    static constexpr int RW = D * (KV == 0 ? 16 : KV == 1 ? 8 : 4) / 2 / 32;     // words
-    uint32_t raw[RW], scale;
-    __device__ __forceinline__ void load(const WeightArgs& a, int slot, int h, int half) {
-        if (slot < 0) {
+__device__ __forceinline__ void convert32(uint32_t row, int c, uint32_t* y) {
+    if constexpr (KV == 0) {
 #pragma unroll
-            for (int i = 0; i < RW; ++i) raw[i] = 0;
-            scale = 0;
-            return;
-        }
-        const uint8_t* row = a.kp + (int64_t)slot * a.row_bytes;
-        const uint8_t* p;
-        if constexpr (KV == 2) {
-            p = row + fp4_code_off(h, D) + half * (RW * 4);
-            const uint8_t* sf = row + fp4_scale_off(h, a.Hkv, D) + half * (D / 32);
-            if constexpr (D == 128)
-                scale = __ldg(reinterpret_cast<const uint32_t*>(sf));
-            else
-                scale = __ldg(reinterpret_cast<const uint16_t*>(sf));
-        } else {
-            p = row + (h * 2 + half) * (RW * 4);
-        }
+        for (int i = 0; i < 4; ++i) lds128(row + 64 * c + 16 * i, y + 4 * i);
+    } else if constexpr (KV == 1) {
+        uint32_t w[8];
+        lds128(row + 32 * c, w);
+        lds128(row + 32 * c + 16, w + 4);
 #pragma unroll
-        for (int i = 0; i < RW / 4; ++i) {
-            const uint4 v = __ldg(reinterpret_cast<const uint4*>(p) + i);
-            raw[4 * i] = v.x; raw[4 * i + 1] = v.y; raw[4 * i + 2] = v.z; raw[4 * i + 3] = v.w;
+        for (int i = 0; i < 8; ++i) {
+            uint32_t lo, hi;
+            e4m3x4_to_f16(w[i], lo, hi);
+            y[2 * i] = bf16x2_of_f16x2(lo);
+            y[2 * i + 1] = bf16x2_of_f16x2(hi);
+        }
+    } else {
+        uint32_t w[4];
+        lds128(row + 16 * c, w);
+        const uint32_t sf = e4m3x2_to_f16(ld_shared_u16(row + D / 2 + 2 * c));
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {                // a word is half a block of 16
+            const uint32_t s2 = __byte_perm(sf, sf, i < 2 ? 0x1010 : 0x3232);
+            uint32_t f[4];
+            e2m1x8_to_f16(w[i], f);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) y[4 * i + j] = bf16x2_of_f16x2(hmul2_u(f[j], s2));
         }
     }
-    __device__ __forceinline__ void store(uint32_t taddr) const {
-        uint32_t y[D / 4];
-        if constexpr (KV == 0) {
-#pragma unroll
-            for (int i = 0; i < D / 4; ++i) y[i] = raw[i];
-        } else if constexpr (KV == 1) {
-#pragma unroll
-            for (int i = 0; i < RW; ++i) {
-                uint32_t lo, hi;
-                e4m3x4_to_f16(raw[i], lo, hi);
-                y[2 * i] = bf16x2_of_f16x2(lo);
-                y[2 * i + 1] = bf16x2_of_f16x2(hi);
-            }
-        } else {
-#pragma unroll
-            for (int i = 0; i < RW; ++i) {           // a word is half a block of 16
-                const uint32_t sf = e4m3x2_to_f16(scale >> (8 * (i / 2)) & 0xffu), s2 = __byte_perm(sf, sf, 0x1010);
-                uint32_t f[4];
-                e2m1x8_to_f16(raw[i], f);
-#pragma unroll
-                for (int j = 0; j < 4; ++j) y[4 * i + j] = bf16x2_of_f16x2(hmul2_u(f[j], s2));
-            }
-        }
-        if constexpr (D == 128)
-            tst32u_nw(taddr, y);
-        else
-            tst16u_nw(taddr, y);
-    }
-};
+}
 
 template <int D, int KV>
 __global__ void __launch_bounds__(kThreads, 1) weights_tc_kernel(const __grid_constant__ TcWeightArgs a,
                                                                  const __grid_constant__ CUtensorMap tmq) {
-    using L = Lay<D>;
+    using L = Lay<D, KV>;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t* sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     const uint32_t sq = smem_u32(sm), sl = sq + L::OFF_L, bar0 = sq + L::OFF_BAR;
@@ -271,12 +269,12 @@ __global__ void __launch_bounds__(kThreads, 1) weights_tc_kernel(const __grid_co
     const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
     if (tid == 0) {
         for (int i = 0; i < 2; ++i) {
-            mbar_init(bar(L::AFULL + i), 8);
+            mbar_init(bar(L::AFULL + i), 4);
             mbar_init(bar(L::AEMPTY + i), 1);
             mbar_init(bar(L::SFULL + i), 1);
-            mbar_init(bar(L::SEMPTY + i), 4);
+            mbar_init(bar(L::SEMPTY + i), 8);
         }
-        for (int i = 0; i < kQStages; ++i) {
+        for (int i = 0; i < L::QSTAGES; ++i) {
             mbar_init(bar(L::QFULL + i), 1);
             mbar_init(bar(L::QEMPTY + i), 1);
         }
@@ -300,7 +298,9 @@ __global__ void __launch_bounds__(kThreads, 1) weights_tc_kernel(const __grid_co
     bool gave_up = false;
     auto wait = [&](int b, uint32_t parity) {
         if (gave_up) return;
-        // (decided for the whole warp)
+        // the warp polls together and decides together: lanes that polled while
+        // lane 0 still had an MMA or a copy to issue could keep it from doing so
+        __syncwarp();
         if (!__all_sync(0xffffffffu, mbar_wait(bar(b), parity))) {
             atomicOr(a.w.err, 4u);
             gave_up = true;
@@ -308,24 +308,102 @@ __global__ void __launch_bounds__(kThreads, 1) weights_tc_kernel(const __grid_co
     };
     Walk walk;
     Item it;
-    if (warp >= kLoadWarp && warp < kMmaWarp) {
-        // ------------------------------------------------------------ K
-        const int row = 32 * (warp & 3) + lane, half = (warp - kLoadWarp) >> 2;
-        const uint32_t tl = tbase + ((uint32_t)(32 * (warp & 3)) << 16) + half * (D / 4);
-        int slot[2];
-        HalfRow<D, KV> k[2];
-        auto lookup = [&] {
-#pragma unroll
-            for (int t = 0; t < 2; ++t) {
-                const int p = it.t0 + 128 * t + row;
-                slot[t] = p < it.q.x.total ? __ldg(a.w.r2t + (int64_t)it.q.r * a.w.ld + p) : 0;
-                if (p >= it.q.x.total) slot[t] = -1;
-                else if (slot[t] < 0 || slot[t] >= a.w.num_slots) {
-                    if (half == 0) atomicOr(a.w.err, 1u);
-                    slot[t] = -1;
+    if (warp < kLoadWarp) {
+        // ------------------------------------------------------------ softmax
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(kSoftmaxRegs));
+        const int wg = warp >> 2, row = tid & 127, lg = 31 - __clz(a.w.G);
+        const uint32_t ts = tbase + 256 + 64 * wg + ((uint32_t)(32 * (warp & 3)) << 16);
+        const uint64_t scale2 = pack2(a.w.scale, a.w.scale), log2e2 = pack2(kLog2e, kLog2e);
+        uint32_t qn = 0, sn0 = 0, sn1 = 0;
+        for (int at = blockIdx.x; item_at(a, walk, at, it); at += gridDim.x) {
+            float sum0 = 0.f, sum1 = 0.f;
+            for (int b = it.b0; b < it.b1; ++b, ++qn) {
+                const uint32_t ls = qn % kLStages;
+                const bool both = b >= it.b0_1;
+                // of this warpgroup's columns, those that a position is seen by: of rows that ask, from the first that
+                // stands at it or behind
+                const int from = 128 * b + 64 * wg;
+                const int lo = ((it.t0 + row - it.q.x.p0) << lg) - from, hi = min((it.q.x.ask << lg) - from, 64);
+                const bool all = __all_sync(0xffffffffu, lo + (both ? 128 << lg : 0) <= 0) && hi == 64;
+                float v0[64], v1[64];
+                wait(L::SFULL, sn0 & 1u);
+                ++sn0;
+                if (gave_up) break;
+                tc_fence_after();
+                tld64_nw(ts, v0);
+                tld_wait();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(L::SEMPTY));
+                if (both) {
+                    wait(L::SFULL + 1, sn1 & 1u);
+                    ++sn1;
+                    if (gave_up) break;
+                    tc_fence_after();
+                    tld64_nw(ts + 128, v1);
+                    tld_wait();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bar(L::SEMPTY + 1));
                 }
+                wait(L::LFULL + ls, (qn / kLStages) & 1u);
+                if (gave_up) break;
+                const uint32_t lp = sl + ls * 512 + 256 * wg;
+                uint64_t acc0 = 0, acc1 = 0;
+                // weights of two columns of a position, added to acc
+                auto add = [&](float s0, float s1, uint64_t m, uint64_t& acc, int c, int first, auto masked) {
+                    float x0, x1;
+                    unpack2(mul2(fma2(pack2(s0, s1), scale2, m), log2e2), x0, x1);
+                    x0 = ex2_ftz(x0);
+                    x1 = ex2_ftz(x1);
+                    if constexpr (decltype(masked)::value) {
+                        x0 = c >= first && c < hi ? x0 : 0.f;
+                        x1 = c + 1 >= first && c + 1 < hi ? x1 : 0.f;
+                    }
+                    acc = add2(pack2(x0, x1), acc);
+                };
+                auto terms = [&](auto masked, auto two) {
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) {
+                        uint32_t w[4];
+                        lds128(lp + 16 * j, w);
+                        const uint64_t m0 = pack2(__uint_as_float(w[0]), __uint_as_float(w[1]));
+                        const uint64_t m1 = pack2(__uint_as_float(w[2]), __uint_as_float(w[3]));
+                        add(v0[4 * j], v0[4 * j + 1], m0, acc0, 4 * j, lo, masked);
+                        add(v0[4 * j + 2], v0[4 * j + 3], m1, acc0, 4 * j + 2, lo, masked);
+                        if constexpr (decltype(two)::value) {
+                            add(v1[4 * j], v1[4 * j + 1], m0, acc1, 4 * j, lo + (128 << lg), masked);
+                            add(v1[4 * j + 2], v1[4 * j + 3], m1, acc1, 4 * j + 2, lo + (128 << lg), masked);
+                        }
+                    }
+                };
+                if (!both)
+                    terms(std::true_type{}, std::false_type{});
+                else if (all)
+                    terms(std::false_type{}, std::true_type{});
+                else
+                    terms(std::true_type{}, std::true_type{});
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(L::LEMPTY + ls));
+                // (a block's sum by itself: long chains round more)
+                float x, y;
+                unpack2(acc0, x, y);
+                sum0 += x + y;
+                unpack2(acc1, x, y);
+                sum1 += x + y;
             }
-        };
+            if (gave_up) break;
+            float* out = a.partial + (int64_t)at * 512 + 256 * wg + row;
+            out[0] = sum0;
+            out[128] = sum1;
+        }
+    } else if (warp < kMmaWarp) {
+        // ------------------------------------------------------------ K
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(kLoadRegs));
+        const int q = warp & 3;
+        const uint32_t tl = tbase + ((uint32_t)(32 * q) << 16);
+        const uint32_t stage = sq + L::OFF_K + 32 * q * L::STRIDE;       // this warp's rows of the first staged tile
+        int t = 0, slot = -1;                        // the next tile to copy: of item `it`
         auto next = [&](int at) {                    // the next item with query blocks
             while (item_at(a, walk, at, it)) {
                 if (it.b0 < it.b1) return true;
@@ -333,75 +411,145 @@ __global__ void __launch_bounds__(kThreads, 1) weights_tc_kernel(const __grid_co
             }
             return false;
         };
-        bool have = next((int)blockIdx.x);
-        if (have) lookup();
-        for (uint32_t n = 0; have; ++n) {
-            const bool two = it.two;
-            k[0].load(a.w, slot[0], it.h, half);
-            if (two) k[1].load(a.w, slot[1], it.h, half);
-            have = next(it.at + (int)gridDim.x);
-            if (have) lookup();
+        bool more = next((int)blockIdx.x);
+        auto lookup = [&] {                          // lane: the slot of its row of that tile
+            const int p = it.t0 + 128 * t + 32 * q + lane;
+            slot = -1;
+            if (p < it.q.x.total) slot = __ldg(a.w.r2t + (int64_t)it.q.r * a.w.ld + p);
+            if (slot >= a.w.num_slots) slot = -1;    // (the join reports it)
+        };
+        if (more) lookup();
+        uint32_t copied = 0, ends = 0;               // tiles copied; those that are their item's last, by their number's low bits
+        auto copy = [&] {                            // the next tile, as one group (empty past the last)
+            if (more) {
+                const uint32_t to = stage + (copied % L::KTILES) * 128 * L::STRIDE;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    // four lanes copy a row's neighbouring pieces
+                    const int r = 8 * k + (lane >> 2), s = __shfl_sync(0xffffffffu, slot, r);
+                    const bool ok = s >= 0;
+                    const uint8_t* src = a.w.kp + (int64_t)(ok ? s : 0) * a.w.row_bytes
+                                         + (KV == 2 ? fp4_code_off(it.h, D) : it.h * L::ROW);
+                    const uint32_t dst = to + r * L::STRIDE;
+#pragma unroll
+                    for (int i = 0; i < (L::ROW + 63) / 64; ++i) {
+                        const int piece = 4 * i + (lane & 3);
+                        if (16 * piece < L::ROW) cp_async16(dst + 16 * piece, src + 16 * piece, ok);
+                    }
+                    if (KV == 2 && (lane & 3) == 0)
+                        cp_async_small<D / 16>(dst + D / 2, a.w.kp + (int64_t)(ok ? s : 0) * a.w.row_bytes
+                                               + fp4_scale_off(it.h, a.w.Hkv, D), ok);
+                }
+                const bool last = t == 1 || !it.two;
+                ends = (ends & ~(1u << (copied & 31u))) | (uint32_t)last << (copied & 31u);
+                ++copied;
+                t = last ? 0 : 1;
+                if (last) more = next(it.at + (int)gridDim.x);
+                if (more) lookup();
+            }
+            cp_async_commit();
+        };
+#pragma unroll 1
+        for (int i = 0; i < L::KTILES; ++i) copy();
+        uint32_t n = 0, col = 0;                     // items put into TMEM; the tile's place in its item's columns
+#pragma unroll 1
+        for (uint32_t tn = 0; tn < copied; ++tn) {
             const uint32_t ab = n & 1u;
-            wait(L::AEMPTY + ab, ((n >> 1) & 1u) ^ 1u);
-            if (gave_up) break;
-            tc_fence_after();
-            k[0].store(tl + ab * 128);
-            if (two) k[1].store(tl + ab * 128 + 64);
+            if (col == 0) {
+                wait(L::AEMPTY + ab, ((n >> 1) & 1u) ^ 1u);
+                if (gave_up) break;
+                tc_fence_after();
+            }
+            cp_async_wait<L::KTILES - 1>();
+            __syncwarp();
+            const uint32_t from = stage + (tn % L::KTILES) * 128 * L::STRIDE + lane * L::STRIDE;
+#pragma unroll
+            for (int c = 0; c < D / 32; ++c) {
+                uint32_t y[16];
+                convert32<D, KV>(from, c, y);
+                tst16u_nw(tl + ab * 128 + col + 16 * c, y);
+            }
             tst_wait();
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(bar(L::AFULL + ab));
+            col = 64;
+            if (ends >> (tn & 31u) & 1u) {
+                if (lane == 0) mbar_arrive(bar(L::AFULL + ab));
+                ++n;
+                col = 0;
+            }
+            __syncwarp();
+            copy();                                  // (into the tile just read)
         }
-    } else if (warp == kMmaWarp) {
-        // ------------------------------------------------------------ MMA
-        constexpr uint32_t I = idesc_bf16(128, 128, false);
-        uint32_t n = 0, qn = 0, sn[2] = {0, 0};
-        for (int at = blockIdx.x; item_at(a, walk, at, it); at += gridDim.x) {
-            if (it.b0 >= it.b1) continue;
-            const uint32_t ab = n & 1u;
-            wait(L::AFULL + ab, (n >> 1) & 1u);
-            ++n;
-            for (int b = it.b0; b < it.b1; ++b, ++qn) {
-                const uint32_t st = qn % kQStages;
-                wait(L::QFULL + st, (qn / kQStages) & 1u);
-                if (gave_up) break;
+        asm volatile("cp.async.wait_all;\n" ::: "memory");
+    } else {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(kOtherRegs));
+        if (warp == kMmaWarp) {
+            // -------------------------------------------------------- MMA
+            constexpr uint32_t I = idesc_bf16(128, 128, false);
+            const uint64_t desc0 = sdesc(sq, 16, 1024);
+            uint32_t n = 0, st = 0, qpar = 0, sn0 = 0, sn1 = 0;
+            for (int at = blockIdx.x; item_at(a, walk, at, it); at += gridDim.x) {
+                if (it.b0 >= it.b1) continue;
+                const uint32_t ta = tbase + (n & 1u) * 128;
+                wait(L::AFULL + (n & 1u), (n >> 1) & 1u);
+                for (int b = it.b0; b < it.b1; ++b) {
+                    wait(L::QFULL + st, qpar);
+                    const uint64_t desc = desc0 + (uint64_t)(st * (L::QTILE >> 4));
 #pragma unroll
-                for (int t = 0; t < 2; ++t) {
-                    if (t == 1 && b < it.b0_1) continue;
-                    wait(L::SEMPTY + t, (sn[t] & 1u) ^ 1u);
-                    ++sn[t];
+                    for (int t = 0; t < 2; ++t) {
+                        if (t == 1 && b < it.b0_1) continue;
+                        wait(L::SEMPTY + t, ((t ? sn1 : sn0) & 1u) ^ 1u);
+                        ++(t ? sn1 : sn0);
+                        if (gave_up) break;
+                        tc_fence_after();
+                        if (lane == 0) {
+#pragma unroll
+                            for (int ks = 0; ks < D / 16; ++ks)
+                                tc_mma_tmem_a(tbase + 256 + 128 * t, ta + t * 64 + ks * 8,
+                                              desc + (uint64_t)(((ks >> 2) * kQRegion + (ks & 3) * 32) >> 4), I, ks > 0);
+                            tc_commit(bar(L::SFULL + t));
+                        }
+                        __syncwarp();
+                    }
                     if (gave_up) break;
-                    tc_fence_after();
                     if (lane == 0) {
-#pragma unroll
-                        for (int ks = 0; ks < D / 16; ++ks)
-                            tc_mma_tmem_a(tbase + 256 + 128 * t, tbase + ab * 128 + t * 64 + ks * 8,
-                                          sdesc(sq + st * L::QTILE + (ks >> 2) * kQRegion + (ks & 3) * 32, 16, 1024), I, ks > 0);
-                        tc_commit(bar(L::SFULL + t));
+                        tc_commit(bar(L::QEMPTY + st));
+                        if (b + 1 == it.b1) tc_commit(bar(L::AEMPTY + (n & 1u)));
                     }
                     __syncwarp();
+                    if (++st == L::QSTAGES) {
+                        st = 0;
+                        qpar ^= 1u;
+                    }
                 }
                 if (gave_up) break;
-                if (lane == 0) {
-                    tc_commit(bar(L::QEMPTY + st));
-                    if (b + 1 == it.b1) tc_commit(bar(L::AEMPTY + ab));
-                }
-                __syncwarp();
+                ++n;
             }
-            if (gave_up) break;
-        }
-        // every MMA and commit has finished before this warp goes on
-        if (lane == 0) tc_commit(bar(L::DONE));
-        if (!mbar_wait(bar(L::DONE), 0)) atomicOr(a.w.err, 4u);
-        __syncwarp();
-    } else if (warp == kQueryWarp) {
-        // ------------------------------------------------------------ Q and log-sum-exps
-        const int lg = 31 - __clz(a.w.G);
-        uint32_t qn = 0;
-        for (int at = blockIdx.x; item_at(a, walk, at, it); at += gridDim.x) {
+            // every MMA and commit has finished before this warp goes on
+            __syncwarp();
+            if (lane == 0) tc_commit(bar(L::DONE));
+            __syncwarp();
+            if (!mbar_wait(bar(L::DONE), 0)) atomicOr(a.w.err, 4u);
+            __syncwarp();
+        } else if (warp == kQueryWarp) {
+            // -------------------------------------------------------- Q and log-sum-exps
+            const int lg = 31 - __clz(a.w.G);
+            uint32_t qn = 0;
+            int b = 0;
+            bool have = false;
             float nx[4];
-            // columns 4 lane .. 4 lane + 3 of block b
-            auto fetch = [&](int b) {
+            // block b of item `it`, or the first of the next item that has one; its columns 4 lane .. 4 lane + 3
+            auto fetch = [&](int at) {
+                have = true;
+                while (b >= it.b1) {
+                    if (!item_at(a, walk, at, it)) {
+                        have = false;
+                        return;
+                    }
+                    b = it.b0;
+                    at += gridDim.x;
+                }
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const int rho = 128 * b + 4 * lane + i;
@@ -410,102 +558,35 @@ __global__ void __launch_bounds__(kThreads, 1) weights_tc_kernel(const __grid_co
                         nx[i] = __ldg(a.w.lse + (it.q.x.row + (rho >> lg)) * a.w.Hq + (it.h << lg) + (rho & (a.w.G - 1)));
                 }
             };
-            if (it.b0 < it.b1) fetch(it.b0);
-            for (int b = it.b0; b < it.b1; ++b, ++qn) {
-                const uint32_t st = qn % kQStages, ls = qn % kLStages;
-                wait(L::QEMPTY + st, ((qn / kQStages) & 1u) ^ 1u);
+            it.b1 = 0;
+            fetch((int)blockIdx.x);
+            for (; have; ++qn) {
+                const uint32_t st = qn % L::QSTAGES, ls = qn % kLStages;
+                const float y[4] = {nx[0], nx[1], nx[2], nx[3]};
+                const int head = it.h << lg, token = (int)it.q.x.row + (b << 7 >> lg);
+                ++b;
+                fetch(it.at + (int)gridDim.x);
+                wait(L::QEMPTY + st, ((qn / L::QSTAGES) & 1u) ^ 1u);
                 if (gave_up) break;
                 if (lane == 0) {
                     mbar_expect_tx(bar(L::QFULL + st), L::QTILE);
 #pragma unroll
                     for (int x = 0; x < D / 64; ++x)
-                        tma_load_box3(sq + st * L::QTILE + x * kQRegion, &tmq, 64 * x, it.h << lg,
-                                      (int)it.q.x.row + (b << 7 >> lg), bar(L::QFULL + st));
+                        tma_load_box3(sq + st * L::QTILE + x * kQRegion, &tmq, 64 * x, head, token, bar(L::QFULL + st));
                 }
-                float2 y[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) y[i] = lse_parts(nx[i]);
-                if (b + 1 < it.b1) fetch(b + 1);
                 wait(L::LEMPTY + ls, ((qn / kLStages) & 1u) ^ 1u);
-                if (gave_up) break;
-                const uint32_t to = sl + ls * 1024 + 32 * lane;
-#pragma unroll
-                for (int i = 0; i < 4; i += 2)
-                    st_shared_v4(to + 8 * i, __float_as_uint(-y[i].x), __float_as_uint(-y[i + 1].x), __float_as_uint(y[i].y),
-                                 __float_as_uint(y[i + 1].y));
+                if (gave_up) {
+                    ++qn;
+                    break;
+                }
+                st_shared_v4(sl + ls * 512 + 16 * lane, __float_as_uint(minus_lse(y[0])), __float_as_uint(minus_lse(y[1])),
+                             __float_as_uint(minus_lse(y[2])), __float_as_uint(minus_lse(y[3])));
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar(L::LFULL + ls));
             }
-            if (gave_up) break;
-        }
-        // (no copy in flight when the CTA ends, also where a wait gave up)
-        for (uint32_t i = qn > kQStages ? qn - kQStages : 0; gave_up && i < qn; ++i)
-            mbar_wait(bar(L::QFULL + i % kQStages), (i / kQStages) & 1u);
-    } else {
-        // ------------------------------------------------------------ softmax
-        const int t = warp >> 2, row = tid & 127, lg = 31 - __clz(a.w.G);
-        const uint32_t ts = tbase + 256 + 128 * t + ((uint32_t)(32 * (warp & 3)) << 16);
-        const uint64_t scale2 = pack2(a.w.scale, a.w.scale);
-        uint32_t qn = 0, sn = 0;
-        for (int at = blockIdx.x; item_at(a, walk, at, it); at += gridDim.x) {
-            const int pos = it.t0 + 128 * t + row;
-            float sum = 0.f;
-            for (int b = it.b0; b < it.b1; ++b, ++qn) {
-                const uint32_t ls = qn % kLStages;
-                if (t == 0 || b >= it.b0_1) {
-                    // columns that this position is seen by: of rows that ask, from the first that stands at it or behind
-                    const int lo = max(((pos - it.q.x.p0) << lg) - 128 * b, 0), hi = min((it.q.x.ask << lg) - 128 * b, 128);
-                    const bool all = __all_sync(0xffffffffu, lo <= 0) && hi == 128;
-                    wait(L::LFULL + ls, (qn / kLStages) & 1u);
-                    wait(L::SFULL + t, sn & 1u);
-                    ++sn;
-                    if (gave_up) break;
-                    tc_fence_after();
-                    uint64_t acc[2] = {0, 0};
-#pragma unroll
-                    for (int half = 0; half < 2; ++half) {
-                        float v[64];
-                        tld64_nw(ts + 64 * half, v);
-                        tld_wait();
-                        if (half == 1) {
-                            tc_fence_before();
-                            __syncwarp();
-                            if (lane == 0) mbar_arrive(bar(L::SEMPTY + t));
-                        }
-                        const uint32_t lp = sl + ls * 1024 + 512 * half;
-                        auto terms = [&](auto masked) {
-#pragma unroll
-                            for (int j = 0; j < 32; ++j) {
-                                uint32_t w[4];
-                                lds128(lp + 16 * j, w);
-                                float x0, x1;
-                                unpack2(fma2(pack2(v[2 * j], v[2 * j + 1]), scale2,
-                                             pack2(__uint_as_float(w[0]), __uint_as_float(w[1]))), x0, x1);
-                                x0 = ex2_ftz(x0);
-                                x1 = ex2_ftz(x1);
-                                if constexpr (decltype(masked)::value) {
-                                    const int c = 64 * half + 2 * j;
-                                    x0 = c >= lo && c < hi ? x0 : 0.f;
-                                    x1 = c + 1 >= lo && c + 1 < hi ? x1 : 0.f;
-                                }
-                                acc[j & 1] = fma2(pack2(x0, x1), pack2(__uint_as_float(w[2]), __uint_as_float(w[3])), acc[j & 1]);
-                            }
-                        };
-                        if (all)
-                            terms(std::false_type{});
-                        else
-                            terms(std::true_type{});
-                    }
-                    float p0, p1, p2, p3;
-                    unpack2(acc[0], p0, p1);
-                    unpack2(acc[1], p2, p3);
-                    sum += (p0 + p1) + (p2 + p3);        // (a block's sum by itself: long chains round more)
-                }
-                __syncwarp();
-                if (lane == 0) mbar_arrive(bar(L::LEMPTY + ls));
-            }
-            if (gave_up) break;
-            a.partial[(int64_t)at * 256 + 128 * t + row] = sum;
+            // (no copy in flight when the CTA ends, also where a wait gave up)
+            for (uint32_t i = qn > L::QSTAGES ? qn - L::QSTAGES : 0; gave_up && i < qn; ++i)
+                mbar_wait(bar(L::QFULL + i % L::QSTAGES), (i / L::QSTAGES) & 1u);
         }
     }
     tc_fence_before();
@@ -557,7 +638,10 @@ __global__ void __launch_bounds__(256) weights_join(const __grid_constant__ TcWe
     float s = 0.f;
     const int n = q.runs * a.w.Hkv;
     if (q.first + n * q.tiles <= a.items)
-        for (int i = 0; i < n; ++i) s += a.partial[((int64_t)q.first + i * q.tiles + tile) * 256 + tid];
+        for (int i = 0; i < n; ++i) {
+            const float* p = a.partial + ((int64_t)q.first + i * q.tiles + tile) * 512 + tid;
+            s += p[0] + p[256];
+        }
     if (slot < 0 || slot >= a.w.num_slots) {
         s = 0.f;
         atomicOr(a.w.err, 1u);
@@ -567,7 +651,8 @@ __global__ void __launch_bounds__(256) weights_join(const __grid_constant__ TcWe
 
 template <int D, int KV>
 cudaError_t run(const TcWeightArgs& a, const CUtensorMap& tmq, int ctas, cudaStream_t s) {
-    constexpr int smem = Lay<D>::END + 1024;
+    constexpr int smem = Lay<D, KV>::END + 1024;
+    static_assert(smem <= 232448, "shared memory of an SM");
     static PerDevice ready;
     if (const int e = ready_here(ready, [] { return large_smem(weights_tc_kernel<D, KV>, smem); })) return (cudaError_t)e;
     cudaLaunchAttribute pdl[1];
