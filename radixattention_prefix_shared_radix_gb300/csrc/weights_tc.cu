@@ -33,6 +33,7 @@
 //   warp 12         issues the MMAs (and owns TMEM)
 //   warp 13         Q blocks by TMA, and beside them the rows' log-sum-exps, which
 //                   it loads a block ahead
+//   warp 14         finds the items and puts them where the others read them
 // All waits are bounded: one that gives up sets bit 2 of the error word, and the
 // code runs to its end without hanging.
 
@@ -52,7 +53,9 @@ using namespace tc;
 
 constexpr int kThreads = 512;
 constexpr int kLoadWarp = 8, kMmaWarp = 12, kQueryWarp = 13;
+constexpr int kItemWarp = 14;
 constexpr int kLStages = 8;
+constexpr int kItems = 8;                // items found ahead
 constexpr int kMaxRows = 1 << 24;        // query rows of a call
 // registers of a thread: 2 x 128 x 176 + 128 x 96 + 128 x 64 = the launch's 512 x 128
 constexpr int kSoftmaxRegs = 176, kLoadRegs = 96, kOtherRegs = 64;
@@ -67,12 +70,13 @@ struct Lay {
     static constexpr int QTILE = 128 * D * 2;
     static constexpr int OFF_K = QSTAGES * QTILE;
     static constexpr int OFF_L = OFF_K + KTILES * 128 * STRIDE;  // minus the log-sum-exps of a block's columns
-    static constexpr int OFF_BAR = OFF_L + kLStages * 512;
+    static constexpr int OFF_ITEM = OFF_L + kLStages * 512;
+    static constexpr int OFF_BAR = OFF_ITEM + kItems * 64;
     static constexpr int OFF_TMEM = OFF_BAR + 40 * 8;
     static constexpr int END = OFF_TMEM + 16;
     // barriers
-    static constexpr int AFULL = 0, AEMPTY = 2, SFULL = 4, SEMPTY = 6, QFULL = 8, QEMPTY = 12, LFULL = 16, LEMPTY = 24,
-                         DONE = 32;
+    static constexpr int AFULL = 0, AEMPTY = 2, SFULL = 4, SEMPTY = 5, QFULL = 6, QEMPTY = 10, IFULL = 14,
+                         IEMPTY = IFULL + kItems, DONE = IEMPTY + kItems;
 };
 
 struct TcWeightArgs {
@@ -161,28 +165,41 @@ struct Walk {
     }
 };
 
-struct Item {
-    int at, t0, h, b0, b1, b0_1;         // first position, KV head, query blocks [b0, b1), the second tile's first
-    bool two;                            // there is a second tile
-    Request q;
+// An item as its warps see it (64 bytes of shared memory).
+struct alignas(16) Item {
+    int at, t0, two, h;                  // -1: there are no more; first position; there is a second tile; KV head
+    int b0, b1, b0_1, p0;                // query blocks [b0, b1), the second tile's first; (as in Asked) p0, ..
+    int total, rows, row, r;             // .. total, query rows of a head, first query token; request
 };
 
-// The next item from `at` on, or false; warps of every role go through the same ones.
-__device__ __forceinline__ bool item_at(const TcWeightArgs& a, Walk& w, int at, Item& it) {
-    __syncwarp();        // (after what single lanes did: the search needs the whole warp)
-    if (at >= a.items || !w.find(a.w, a.run, at, false, it.q)) return false;
-    const int k = at - it.q.first, tile = k % it.q.tiles, hs = k / it.q.tiles, s = hs % it.q.runs;
-    it.at = at;
-    it.h = hs / it.q.runs;
-    it.t0 = 256 * tile;
-    it.two = it.t0 + 128 < it.q.x.total;
-    // a tile's rows begin with the first that sees its first position
+// Query blocks pass a tile over until one has a row that sees its first position.
+__device__ __forceinline__ int first_block(const Asked& x, int t0, int lg) { return max(t0 - x.p0, 0) << lg >> 7; }
+
+// The next item from `at` on, `step` apart, that has query blocks; at -1: none.
+__device__ __forceinline__ Item next_item(const TcWeightArgs& a, Walk& w, int at, int step) {
+    Request q;
+    Item it{};
     const int lg = 31 - __clz(a.w.G);
-    auto from = [&](int t0) { return max(t0 - it.q.x.p0, 0) << lg >> 7; };
-    it.b0 = max(s * a.run, from(it.t0));
-    it.b1 = min((s + 1) * a.run, it.q.blocks);
-    it.b0_1 = it.two ? max(it.b0, from(it.t0 + 128)) : it.b1;
-    return true;
+    for (;; at += step) {
+        it.at = -1;
+        if (at >= a.items || !w.find(a.w, a.run, at, false, q)) return it;
+        const int k = at - q.first, hs = k / q.tiles, tile = k - hs * q.tiles, h = hs / q.runs, s = hs - h * q.runs;
+        const int t0 = 256 * tile;
+        it.b0 = max(s * a.run, first_block(q.x, t0, lg));
+        it.b1 = min((s + 1) * a.run, q.blocks);
+        if (it.b0 >= it.b1) continue;    // (the join passes over it too)
+        it.at = at;
+        it.t0 = t0;
+        it.two = t0 + 128 < q.x.total;
+        it.h = h;
+        it.b0_1 = it.two ? max(it.b0, first_block(q.x, t0 + 128, lg)) : it.b1;
+        it.p0 = q.x.p0;
+        it.total = q.x.total;
+        it.rows = q.x.ask << lg;
+        it.row = (int)q.x.row;
+        it.r = q.r;
+        return it;
+    }
 }
 
 // packed pairs
@@ -271,16 +288,16 @@ __global__ void __launch_bounds__(kThreads, 1) weights_tc_kernel(const __grid_co
         for (int i = 0; i < 2; ++i) {
             mbar_init(bar(L::AFULL + i), 4);
             mbar_init(bar(L::AEMPTY + i), 1);
-            mbar_init(bar(L::SFULL + i), 1);
-            mbar_init(bar(L::SEMPTY + i), 8);
         }
+        mbar_init(bar(L::SFULL), 1);
+        mbar_init(bar(L::SEMPTY), 8);
         for (int i = 0; i < L::QSTAGES; ++i) {
-            mbar_init(bar(L::QFULL + i), 1);
+            mbar_init(bar(L::QFULL + i), 2);
             mbar_init(bar(L::QEMPTY + i), 1);
         }
-        for (int i = 0; i < kLStages; ++i) {
-            mbar_init(bar(L::LFULL + i), 1);
-            mbar_init(bar(L::LEMPTY + i), 8);
+        for (int i = 0; i < kItems; ++i) {
+            mbar_init(bar(L::IFULL + i), 1);
+            mbar_init(bar(L::IEMPTY + i), 14);
         }
         mbar_init(bar(L::DONE), 1);
         mbar_fence_init();
@@ -306,49 +323,50 @@ __global__ void __launch_bounds__(kThreads, 1) weights_tc_kernel(const __grid_co
             gave_up = true;
         }
     };
-    Walk walk;
+    // the items in turn, from the warp that finds them; false past the last
+    uint32_t items_seen = 0;
     Item it;
+    auto next = [&] {
+        const uint32_t i = items_seen % kItems;
+        wait(L::IFULL + i, (items_seen / kItems) & 1u);
+        if (gave_up) return false;
+        const uint32_t from = sq + L::OFF_ITEM + i * 64;
+        uint32_t* w = reinterpret_cast<uint32_t*>(&it);
+        lds128(from, w);
+        lds128(from + 16, w + 4);
+        lds128(from + 32, w + 8);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(L::IEMPTY + i));
+        ++items_seen;
+        return it.at >= 0;
+    };
     if (warp < kLoadWarp) {
         // ------------------------------------------------------------ softmax
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(kSoftmaxRegs));
         const int wg = warp >> 2, row = tid & 127, lg = 31 - __clz(a.w.G);
         const uint32_t ts = tbase + 256 + 64 * wg + ((uint32_t)(32 * (warp & 3)) << 16);
         const uint64_t scale2 = pack2(a.w.scale, a.w.scale), log2e2 = pack2(kLog2e, kLog2e);
-        uint32_t qn = 0, sn0 = 0, sn1 = 0;
-        for (int at = blockIdx.x; item_at(a, walk, at, it); at += gridDim.x) {
+        uint32_t qn = 0;
+        while (next()) {
             float sum0 = 0.f, sum1 = 0.f;
             for (int b = it.b0; b < it.b1; ++b, ++qn) {
-                const uint32_t ls = qn % kLStages;
                 const bool both = b >= it.b0_1;
                 // of this warpgroup's columns, those that a position is seen by: of rows that ask, from the first that
                 // stands at it or behind
                 const int from = 128 * b + 64 * wg;
-                const int lo = ((it.t0 + row - it.q.x.p0) << lg) - from, hi = min((it.q.x.ask << lg) - from, 64);
+                const int lo = ((it.t0 + row - it.p0) << lg) - from, hi = min(it.rows - from, 64);
                 const bool all = __all_sync(0xffffffffu, lo + (both ? 128 << lg : 0) <= 0) && hi == 64;
                 float v0[64], v1[64];
-                wait(L::SFULL, sn0 & 1u);
-                ++sn0;
+                wait(L::SFULL, qn & 1u);
                 if (gave_up) break;
                 tc_fence_after();
                 tld64_nw(ts, v0);
+                if (both) tld64_nw(ts + 128, v1);
                 tld_wait();
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar(L::SEMPTY));
-                if (both) {
-                    wait(L::SFULL + 1, sn1 & 1u);
-                    ++sn1;
-                    if (gave_up) break;
-                    tc_fence_after();
-                    tld64_nw(ts + 128, v1);
-                    tld_wait();
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(bar(L::SEMPTY + 1));
-                }
-                wait(L::LFULL + ls, (qn / kLStages) & 1u);
-                if (gave_up) break;
-                const uint32_t lp = sl + ls * 512 + 256 * wg;
+                const uint32_t lp = sl + qn % kLStages * 512 + 256 * wg;
                 uint64_t acc0 = 0, acc1 = 0;
                 // weights of two columns of a position, added to acc
                 auto add = [&](float s0, float s1, uint64_t m, uint64_t& acc, int c, int first, auto masked) {
@@ -383,8 +401,6 @@ __global__ void __launch_bounds__(kThreads, 1) weights_tc_kernel(const __grid_co
                     terms(std::false_type{}, std::true_type{});
                 else
                     terms(std::true_type{}, std::true_type{});
-                __syncwarp();
-                if (lane == 0) mbar_arrive(bar(L::LEMPTY + ls));
                 // (a block's sum by itself: long chains round more)
                 float x, y;
                 unpack2(acc0, x, y);
@@ -393,7 +409,7 @@ __global__ void __launch_bounds__(kThreads, 1) weights_tc_kernel(const __grid_co
                 sum1 += x + y;
             }
             if (gave_up) break;
-            float* out = a.partial + (int64_t)at * 512 + 256 * wg + row;
+            float* out = a.partial + (int64_t)it.at * 512 + 256 * wg + row;
             out[0] = sum0;
             out[128] = sum1;
         }
@@ -404,18 +420,11 @@ __global__ void __launch_bounds__(kThreads, 1) weights_tc_kernel(const __grid_co
         const uint32_t tl = tbase + ((uint32_t)(32 * q) << 16);
         const uint32_t stage = sq + L::OFF_K + 32 * q * L::STRIDE;       // this warp's rows of the first staged tile
         int t = 0, slot = -1;                        // the next tile to copy: of item `it`
-        auto next = [&](int at) {                    // the next item with query blocks
-            while (item_at(a, walk, at, it)) {
-                if (it.b0 < it.b1) return true;
-                at += (int)gridDim.x;
-            }
-            return false;
-        };
-        bool more = next((int)blockIdx.x);
+        bool more = next();
         auto lookup = [&] {                          // lane: the slot of its row of that tile
             const int p = it.t0 + 128 * t + 32 * q + lane;
             slot = -1;
-            if (p < it.q.x.total) slot = __ldg(a.w.r2t + (int64_t)it.q.r * a.w.ld + p);
+            if (p < it.total) slot = __ldg(a.w.r2t + (int64_t)it.r * a.w.ld + p);
             if (slot >= a.w.num_slots) slot = -1;    // (the join reports it)
         };
         if (more) lookup();
@@ -444,7 +453,7 @@ __global__ void __launch_bounds__(kThreads, 1) weights_tc_kernel(const __grid_co
                 ends = (ends & ~(1u << (copied & 31u))) | (uint32_t)last << (copied & 31u);
                 ++copied;
                 t = last ? 0 : 1;
-                if (last) more = next(it.at + (int)gridDim.x);
+                if (last) more = next();
                 if (more) lookup();
             }
             cp_async_commit();
@@ -488,32 +497,24 @@ __global__ void __launch_bounds__(kThreads, 1) weights_tc_kernel(const __grid_co
             // -------------------------------------------------------- MMA
             constexpr uint32_t I = idesc_bf16(128, 128, false);
             const uint64_t desc0 = sdesc(sq, 16, 1024);
-            uint32_t n = 0, st = 0, qpar = 0, sn0 = 0, sn1 = 0;
-            for (int at = blockIdx.x; item_at(a, walk, at, it); at += gridDim.x) {
-                if (it.b0 >= it.b1) continue;
+            uint32_t n = 0, st = 0, qpar = 0, sn = 0;
+            for (; next(); ++n) {
                 const uint32_t ta = tbase + (n & 1u) * 128;
                 wait(L::AFULL + (n & 1u), (n >> 1) & 1u);
-                for (int b = it.b0; b < it.b1; ++b) {
+                for (int b = it.b0; b < it.b1; ++b, ++sn) {
                     wait(L::QFULL + st, qpar);
-                    const uint64_t desc = desc0 + (uint64_t)(st * (L::QTILE >> 4));
-#pragma unroll
-                    for (int t = 0; t < 2; ++t) {
-                        if (t == 1 && b < it.b0_1) continue;
-                        wait(L::SEMPTY + t, ((t ? sn1 : sn0) & 1u) ^ 1u);
-                        ++(t ? sn1 : sn0);
-                        if (gave_up) break;
-                        tc_fence_after();
-                        if (lane == 0) {
+                    wait(L::SEMPTY, (sn & 1u) ^ 1u);
+                    if (gave_up) break;
+                    tc_fence_after();
+                    if (lane == 0) {
+                        const uint64_t desc = desc0 + (uint64_t)(st * (L::QTILE >> 4));
+                        for (int t = 0; t < (b >= it.b0_1 ? 2 : 1); ++t) {
 #pragma unroll
                             for (int ks = 0; ks < D / 16; ++ks)
                                 tc_mma_tmem_a(tbase + 256 + 128 * t, ta + t * 64 + ks * 8,
                                               desc + (uint64_t)(((ks >> 2) * kQRegion + (ks & 3) * 32) >> 4), I, ks > 0);
-                            tc_commit(bar(L::SFULL + t));
                         }
-                        __syncwarp();
-                    }
-                    if (gave_up) break;
-                    if (lane == 0) {
+                        tc_commit(bar(L::SFULL));
                         tc_commit(bar(L::QEMPTY + st));
                         if (b + 1 == it.b1) tc_commit(bar(L::AEMPTY + (n & 1u)));
                     }
@@ -524,7 +525,6 @@ __global__ void __launch_bounds__(kThreads, 1) weights_tc_kernel(const __grid_co
                     }
                 }
                 if (gave_up) break;
-                ++n;
             }
             // every MMA and commit has finished before this warp goes on
             __syncwarp();
@@ -536,36 +536,29 @@ __global__ void __launch_bounds__(kThreads, 1) weights_tc_kernel(const __grid_co
             // -------------------------------------------------------- Q and log-sum-exps
             const int lg = 31 - __clz(a.w.G);
             uint32_t qn = 0;
-            int b = 0;
-            bool have = false;
             float nx[4];
-            // block b of item `it`, or the first of the next item that has one; its columns 4 lane .. 4 lane + 3
-            auto fetch = [&](int at) {
-                have = true;
-                while (b >= it.b1) {
-                    if (!item_at(a, walk, at, it)) {
-                        have = false;
-                        return;
-                    }
-                    b = it.b0;
-                    at += gridDim.x;
-                }
+            int b = 0;
+            bool have = next();
+            if (have) b = it.b0;
+            auto fetch = [&] {                       // block b's columns 4 lane .. 4 lane + 3
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const int rho = 128 * b + 4 * lane + i;
                     nx[i] = -INFINITY;
-                    if (rho < it.q.x.ask << lg)
-                        nx[i] = __ldg(a.w.lse + (it.q.x.row + (rho >> lg)) * a.w.Hq + (it.h << lg) + (rho & (a.w.G - 1)));
+                    if (rho < it.rows)
+                        nx[i] = __ldg(a.w.lse + ((int64_t)it.row + (rho >> lg)) * a.w.Hq + (it.h << lg) + (rho & (a.w.G - 1)));
                 }
             };
-            it.b1 = 0;
-            fetch((int)blockIdx.x);
+            if (have) fetch();
             for (; have; ++qn) {
-                const uint32_t st = qn % L::QSTAGES, ls = qn % kLStages;
+                const uint32_t st = qn % L::QSTAGES;
                 const float y[4] = {nx[0], nx[1], nx[2], nx[3]};
-                const int head = it.h << lg, token = (int)it.q.x.row + (b << 7 >> lg);
-                ++b;
-                fetch(it.at + (int)gridDim.x);
+                const int head = it.h << lg, token = it.row + (b << 7 >> lg);
+                if (++b >= it.b1) {
+                    have = next();
+                    b = it.b0;
+                }
+                if (have) fetch();
                 wait(L::QEMPTY + st, ((qn / L::QSTAGES) & 1u) ^ 1u);
                 if (gave_up) break;
                 if (lane == 0) {
@@ -574,19 +567,38 @@ __global__ void __launch_bounds__(kThreads, 1) weights_tc_kernel(const __grid_co
                     for (int x = 0; x < D / 64; ++x)
                         tma_load_box3(sq + st * L::QTILE + x * kQRegion, &tmq, 64 * x, head, token, bar(L::QFULL + st));
                 }
-                wait(L::LEMPTY + ls, ((qn / kLStages) & 1u) ^ 1u);
-                if (gave_up) {
-                    ++qn;
-                    break;
-                }
-                st_shared_v4(sl + ls * 512 + 16 * lane, __float_as_uint(minus_lse(y[0])), __float_as_uint(minus_lse(y[1])),
-                             __float_as_uint(minus_lse(y[2])), __float_as_uint(minus_lse(y[3])));
+                // A stage of log-sum-exps is free without a barrier of its own: block
+                // qn - QSTAGES has been multiplied, so the scores of the block before
+                // it have been taken, by warps that had finished the one before that,
+                // and qn - kLStages lies behind.
+                static_assert(kLStages >= L::QSTAGES + 2, "log-sum-exp stages");
+                st_shared_v4(sl + qn % kLStages * 512 + 16 * lane, __float_as_uint(minus_lse(y[0])),
+                             __float_as_uint(minus_lse(y[1])), __float_as_uint(minus_lse(y[2])), __float_as_uint(minus_lse(y[3])));
                 __syncwarp();
-                if (lane == 0) mbar_arrive(bar(L::LFULL + ls));
+                if (lane == 0) mbar_arrive(bar(L::QFULL + st));
             }
             // (no copy in flight when the CTA ends, also where a wait gave up)
             for (uint32_t i = qn > L::QSTAGES ? qn - L::QSTAGES : 0; gave_up && i < qn; ++i)
                 mbar_wait(bar(L::QFULL + i % L::QSTAGES), (i / L::QSTAGES) & 1u);
+        } else if (warp == kItemWarp) {
+            // -------------------------------------------------------- items
+            Walk walk;
+            int at = blockIdx.x;
+            for (uint32_t n = 0; at >= 0; ++n) {
+                const Item x = next_item(a, walk, at, (int)gridDim.x);
+                const uint32_t i = n % kItems;
+                wait(L::IEMPTY + i, ((n / kItems) & 1u) ^ 1u);
+                if (gave_up) break;
+                if (lane == 0) {
+                    const uint32_t to = sq + L::OFF_ITEM + i * 64;
+                    st_shared_v4(to, x.at, x.t0, x.two, x.h);
+                    st_shared_v4(to + 16, x.b0, x.b1, x.b0_1, x.p0);
+                    st_shared_v4(to + 32, x.total, x.rows, x.row, x.r);
+                    mbar_arrive(bar(L::IFULL + i));
+                }
+                __syncwarp();
+                at = x.at < 0 ? -1 : x.at + (int)gridDim.x;
+            }
         }
     }
     tc_fence_before();
@@ -636,12 +648,13 @@ __global__ void __launch_bounds__(256) weights_join(const __grid_constant__ TcWe
     const bool had = a.w.in && pos < q.x.fresh;
     const float old = had ? a.w.in[at] : 0.f;
     float s = 0.f;
-    const int n = q.runs * a.w.Hkv;
-    if (q.first + n * q.tiles <= a.items)
-        for (int i = 0; i < n; ++i) {
-            const float* p = a.partial + ((int64_t)q.first + i * q.tiles + tile) * 512 + tid;
-            s += p[0] + p[256];
-        }
+    const int s0 = first_block(q.x, 256 * tile, 31 - __clz(a.w.G)) / a.run;      // (runs before it pass the tile over)
+    if (q.first + q.runs * a.w.Hkv * q.tiles <= a.items)
+        for (int h = 0; h < a.w.Hkv; ++h)
+            for (int i = h * q.runs + s0; i < (h + 1) * q.runs; ++i) {
+                const float* p = a.partial + ((int64_t)q.first + i * q.tiles + tile) * 512 + tid;
+                s += p[0] + p[256];
+            }
     if (slot < 0 || slot >= a.w.num_slots) {
         s = 0.f;
         atomicOr(a.w.err, 1u);
