@@ -44,6 +44,7 @@ struct EvictArgs {
     int64_t scores_ld, ld, evicted_ld;
     uint32_t* err;
     int page, lg_page;                   // lg_page < 0: not a power of two
+    int lanes;                           // lanes of a warp that share a page, where it is a power of two; else 1
     int sinks, recent;
     int lim;                             // positions of a row: the shorter of ld and scores_ld
     bool in_place;                       // some output is its input
@@ -65,6 +66,7 @@ __global__ void __launch_bounds__(T, 1) evict_kernel(const __grid_constant__ Evi
     __shared__ uint32_t hist[kCopies * kCopyStride];       // counts of the digits, a copy for every eighth lane
     __shared__ uint32_t counts[2][256];                    // this CTA's, from digit 255 down
     __shared__ __align__(16) uint32_t total[256];          // the cluster's
+    __shared__ uint3 choice;                               // a digit, pages above it, pages at it
     __shared__ uint2 warp_counts[kWarps], cta_counts;      // (pages that surely stay, pages at the lowest kept score)
     cg::cluster_group cl = cg::this_cluster();
     const int C = (int)cl.num_blocks(), c = (int)cl.block_rank();
@@ -116,11 +118,18 @@ __global__ void __launch_bounds__(T, 1) evict_kernel(const __grid_constant__ Evi
 #pragma unroll
         for (int e = 0; e < kEach; ++e) {
             const int t = tid + e * T;
-            if (t >= nt) continue;
-            if (P == 1)
-                share[t] = order_of(x[e]);
-            else
-                atomicMax(&share[page_of(t)], order_of(x[e]));
+            uint32_t y = t < nt ? order_of(x[e]) : 0;
+            if (P == 1) {
+                if (t < nt) share[t] = y;
+                continue;
+            }
+            // (pages start at multiples of P from t = 0 on: lanes of one page, side by side, agree first)
+            bool one = true;
+            for (int o = 1; o < a.lanes; o <<= 1) {
+                y = max(y, __shfl_xor_sync(0xffffffffu, y, o));
+                one = (lane & (2 * o - 1)) == 0;
+            }
+            if (one && t < nt) atomicMax(&share[page_of(t)], y);
         }
         __syncthreads();
         // lowest score that stays, and how many of those at it
@@ -163,30 +172,29 @@ __global__ void __launch_bounds__(T, 1) evict_kernel(const __grid_constant__ Evi
                     }
                 }
                 __syncthreads();
-                // every warp: the digit with fewer than k pages above it and at least k
-                // from it on; lane l has digits 255 - 8 l .. 248 - 8 l
-                const uint4 u0 = reinterpret_cast<const uint4*>(total)[2 * lane], u1 = reinterpret_cast<const uint4*>(total)[2 * lane + 1];
-                const uint32_t v[8] = {u0.x, u0.y, u0.z, u0.w, u1.x, u1.y, u1.z, u1.w};
-                const uint32_t sum = ((v[0] + v[1]) + (v[2] + v[3])) + ((v[4] + v[5]) + (v[6] + v[7]));
-                uint32_t upto = sum;
+                // the digit with fewer than k pages above it and at least k from it on:
+                // lane l has digits 255 - 8 l .. 248 - 8 l
+                if (warp == 0) {
+                    const uint4 u0 = reinterpret_cast<const uint4*>(total)[2 * lane], u1 = reinterpret_cast<const uint4*>(total)[2 * lane + 1];
+                    const uint32_t v[8] = {u0.x, u0.y, u0.z, u0.w, u1.x, u1.y, u1.z, u1.w};
+                    const uint32_t sum = ((v[0] + v[1]) + (v[2] + v[3])) + ((v[4] + v[5]) + (v[6] + v[7]));
+                    uint32_t upto = sum;
 #pragma unroll
-                for (int o = 1; o < 32; o <<= 1) {
-                    const uint32_t y = __shfl_up_sync(0xffffffffu, upto, o);
-                    if (lane >= o) upto += y;
-                }
-                const int l = __ffs(__ballot_sync(0xffffffffu, upto >= (uint32_t)k)) - 1;
-                uint32_t above = upto - sum, digit = 0, size = 0;
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    if (size == 0 && above + v[i] >= (uint32_t)k) {
-                        digit = 255 - 8 * lane - i;
-                        size = v[i];
+                    for (int o = 1; o < 32; o <<= 1) {
+                        const uint32_t y = __shfl_up_sync(0xffffffffu, upto, o);
+                        if (lane >= o) upto += y;
                     }
-                    if (size == 0) above += v[i];
+                    uint32_t before = upto - sum;
+                    if (before < (uint32_t)k && upto >= (uint32_t)k) {
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            if (before < (uint32_t)k && before + v[i] >= (uint32_t)k) choice = make_uint3(255 - 8 * lane - i, before, v[i]);
+                            before += v[i];
+                        }
+                    }
                 }
-                above = __shfl_sync(0xffffffffu, above, l);
-                digit = __shfl_sync(0xffffffffu, digit, l);
-                size = __shfl_sync(0xffffffffu, size, l);
+                __syncthreads();
+                const uint32_t digit = choice.x, above = choice.y, size = choice.z;
                 k -= (int)above;
                 found |= digit << shift;
                 mask |= 255u << shift;
@@ -613,6 +621,7 @@ int sgl_kv_evict(const sgl_evict_params* params, const float* scores, int64_t sc
     a.lg_page = (P & (P - 1)) == 0 ? 31 - __builtin_clz(P) : -1;
     a.sinks = std::min<int32_t>(params->sinks, INT32_MAX / 2);
     a.recent = std::min<int32_t>(params->recent, INT32_MAX / 2);
+    a.lanes = a.lg_page >= 0 ? std::min(P, 32) : 1;
     a.lim = (int)lim;
     a.in_place = scores == scores_out || req_to_token == table_out || (positions && positions == positions_out);
     // Rows of up to 2048 positions: a CTA of 256 threads; longer ones: 1024 threads
