@@ -906,11 +906,15 @@ def sgl_attn_weights_workspace_bytes(params, window=0):
 
 
 def _table_rows(t, what, batch, dev, dtype):
-    """A contiguous tensor with a row for each of `batch` requests: (address, row length)."""
-    p = _flat(t, what, dev, dtype)
-    if t.dim() != 2 or t.shape[0] < batch:
-        raise ValueError("%s must have a row per request" % what)
-    return p, t.shape[1]
+    """A contiguous tensor [>= batch, any]: (address, row length)."""
+    try:
+        rows, cols = t.shape
+        if rows >= batch and t.dtype is dtype and t.get_device() == dev and t.is_contiguous():
+            return t.data_ptr(), cols
+    except (AttributeError, TypeError, ValueError):
+        pass          # not a tensor, or not of two dimensions
+    _flat(t, what, dev, dtype)
+    raise ValueError("%s must have a row per request" % what)
 
 
 def sgl_attn_weights(q, lse, k_pool, req_to_token, lens, extend_lens, params, scores_in, scores_out, workspace, decay=1.0,
@@ -920,31 +924,34 @@ def sgl_attn_weights(q, lse, k_pool, req_to_token, lens, extend_lens, params, sc
     extend_lens None: a decode batch, lens its contexts; else chunks behind lens cached tokens, of which the last
     `window` rows of each request ask (0: all)."""
     T = _T or _torch()
-    kind, d, dev = params.dtype, params.head_dim, T._C._cuda_getDevice()
-    pq, sq, n, hq = _rows(q, "q", params.num_qo_heads, d, T.float32 if kind == SGL_DTYPE_F32 else T.bfloat16, None, dev)
+    kind, d, batch, dev = params.dtype, params.head_dim, params.batch, T._C._cuda_getDevice()
+    f32, i32 = T.float32, T.int32
+    pq, sq, n, hq = _rows(q, "q", params.num_qo_heads, d, f32 if kind == SGL_DTYPE_F32 else T.bfloat16, None, dev)
     if sq != hq * d:
         raise ValueError("q must be contiguous")
-    B = (params.batch,)
+    pe = None
     if extend_lens is None:
-        if n != params.batch:
+        if n != batch:
             raise ValueError("q must have a row per request")
-    elif params.batch and not (params.host_prefix_lens and params.host_extend_lens):
-        raise ValueError("params must have host_prefix_lens and host_extend_lens")
-    elif sum(params.host_extend_lens[:params.batch]) > n:
-        raise ValueError("q must hold the rows of extend_lens")
-    pt, ld = _table_rows(req_to_token, "req_to_token", params.batch, dev, T.int32)
-    po, sld = _table_rows(scores_out, "scores_out", params.batch, dev, T.float32)
-    pi = None
-    if scores_in is not None:
-        pi, ild = _table_rows(scores_in, "scores_in", params.batch, dev, T.float32)
+    else:
+        pe = _flat(extend_lens, "extend_lens", dev, i32, (batch,))
+        if batch and not (params.host_prefix_lens and params.host_extend_lens):
+            raise ValueError("params must have host_prefix_lens and host_extend_lens")
+        if batch and sum(params.host_extend_lens[:batch]) > n:
+            raise ValueError("q must hold the rows of extend_lens")
+    pt, ld = _table_rows(req_to_token, "req_to_token", batch, dev, i32)
+    po, sld = _table_rows(scores_out, "scores_out", batch, dev, f32)
+    pi = po if scores_in is scores_out else None
+    if pi is None and scores_in is not None:
+        pi, ild = _table_rows(scores_in, "scores_in", batch, dev, f32)
         if ild != sld:
             raise ValueError("scores_in and scores_out must have rows of one length")
-    st = _lib().sgl_attn_weights(pq, _flat(lse, "lse", dev, T.float32, (n, hq)),
-                                 _writable(_flat(k_pool, "k_pool", dev), k_pool, "k_pool",
-                                           params.num_slots * _row_bytes(params)),
-                                 pt, ld, _flat(lens, "lens", dev, T.int32, B),
-                                 None if extend_lens is None else _flat(extend_lens, "extend_lens", dev, T.int32, B),
-                                 ctypes.byref(params), window, pi, po, sld, decay, _flat(workspace, "workspace", dev),
+    pk = _flat(k_pool, "k_pool", dev)
+    need = params.num_slots * _row_bytes(params, kind, params.num_kv_heads * d)
+    if k_pool.nbytes < need:
+        _writable(pk, k_pool, "k_pool", need)
+    st = _lib().sgl_attn_weights(pq, _flat(lse, "lse", dev, f32, (n, hq)), pk, pt, ld, _flat(lens, "lens", dev, i32, (batch,)),
+                                 pe, ctypes.byref(params), window, pi, po, sld, decay, _flat(workspace, "workspace", dev),
                                  workspace.nbytes, _stream(stream))
     if st:
         raise SglError(st, "sgl_attn_weights")
@@ -956,26 +963,33 @@ def sgl_kv_evict(scores, req_to_token, lens, budgets, scores_out, table_out, len
     [B, L], req_to_token and positions [B, ld] into their outputs (each may be its input), lens [B] into lens_out; the
     slots that left into evicted [B, any] and their number into evicted_count [B]."""
     T = _T or _torch()
-    dev, B = T._C._cuda_getDevice(), len(lens)
-    ps, sld = _table_rows(scores, "scores", B, dev, T.float32)
-    pt, ld = _table_rows(req_to_token, "req_to_token", B, dev, T.int32)
+    dev, f32, i32 = T._C._cuda_getDevice(), T.float32, T.int32
+    if not isinstance(lens, T.Tensor):
+        raise TypeError("lens must be a CUDA tensor")
+    n = lens.shape
+    pl = _flat(lens, "lens", dev, i32)
+    if len(n) != 1:
+        raise ValueError("lens must have one dimension")
+    B = n[0]
+    ps, sld = _table_rows(scores, "scores", B, dev, f32)
+    pt, ld = _table_rows(req_to_token, "req_to_token", B, dev, i32)
+    shape = req_to_token.shape
+    pso = ps if scores_out is scores else _flat(scores_out, "scores_out", dev, f32, scores.shape)
+    pto = pt if table_out is req_to_token else _flat(table_out, "table_out", dev, i32, shape)
+    plo = pl if lens_out is lens else _flat(lens_out, "lens_out", dev, i32, n)
     pp = ppo = pe = pc = None
     eld = 0
     if (positions is None) != (positions_out is None):
         raise ValueError("positions and positions_out go together")
     if positions is not None:
-        pp = _flat(positions, "positions", dev, T.int32, req_to_token.shape)
-        ppo = _flat(positions_out, "positions_out", dev, T.int32, req_to_token.shape)
+        pp = _flat(positions, "positions", dev, i32, shape)
+        ppo = pp if positions_out is positions else _flat(positions_out, "positions_out", dev, i32, shape)
     if evicted is not None:
-        pe, eld = _table_rows(evicted, "evicted", B, dev, T.int32)
+        pe, eld = _table_rows(evicted, "evicted", B, dev, i32)
     if evicted_count is not None:
-        pc = _flat(evicted_count, "evicted_count", dev, T.int32, (B,))
+        pc = _flat(evicted_count, "evicted_count", dev, i32, n)
     p = SglEvictParams(B, page_size, sinks, recent)
-    st = _lib().sgl_kv_evict(ctypes.byref(p), ps, sld, pt, ld, pp, _flat(lens, "lens", dev, T.int32, (B,)),
-                             _flat(budgets, "budgets", dev, T.int32, (B,)),
-                             _flat(scores_out, "scores_out", dev, T.float32, scores.shape),
-                             _flat(table_out, "table_out", dev, T.int32, req_to_token.shape), ppo,
-                             _flat(lens_out, "lens_out", dev, T.int32, (B,)), pe, eld, pc,
-                             _flat(workspace, "workspace", dev), workspace.nbytes, _stream(stream))
+    st = _lib().sgl_kv_evict(ctypes.byref(p), ps, sld, pt, ld, pp, pl, _flat(budgets, "budgets", dev, i32, n), pso, pto, ppo,
+                             plo, pe, eld, pc, _flat(workspace, "workspace", dev), workspace.nbytes, _stream(stream))
     if st:
         raise SglError(st, "sgl_kv_evict")
