@@ -57,6 +57,7 @@ constexpr int kItemWarp = 14;
 constexpr int kLStages = 8;
 constexpr int kItems = 8;                // items found ahead
 constexpr int kMaxRows = 1 << 24;        // query rows of a call
+constexpr int kMaxItems = 1 << 25;
 // registers of a thread: 2 x 128 x 176 + 128 x 96 + 128 x 64 = the launch's 512 x 128
 constexpr int kSoftmaxRegs = 176, kLoadRegs = 96, kOtherRegs = 64;
 
@@ -85,12 +86,31 @@ struct TcWeightArgs {
     int items, run;                      // items of the call; query blocks of an item
 };
 
-// A request's items in the order tile, run of query blocks, KV head.
+// Query blocks pass a tile over until one has a row that sees its first position.
+__host__ __device__ __forceinline__ int64_t first_block(int64_t p0, int64_t t0, int lg) {
+    return (t0 > p0 ? (t0 - p0) << lg : 0) >> 7;
+}
+
+// A request's items, in the order run of query blocks, tile, KV head: a tile has
+// those runs that do not pass it over as a whole.
 struct Request {
     Asked x;
-    int r, first, tiles, runs, blocks;   // first item
-    int first_tile;                      // tiles of the requests before it
+    int r, tiles, runs, blocks, head;    // head: items of a KV head
+    int first, first_tile;               // items and tiles of the requests before it
 };
+// Of `tiles` tiles of 256 positions: how many have every run (they come first),
+// and the items of them all.
+__host__ __device__ __forceinline__ int64_t items_of_head(int64_t p0, int64_t tiles, int64_t runs, int run, int lg,
+                                                          int64_t* whole) {
+    int64_t n = 0, w = tiles;
+    while (w > 0 && first_block(p0, 256 * (w - 1), lg) >= run) {
+        const int64_t past = first_block(p0, 256 * (w - 1), lg) / run;
+        n += past < runs ? runs - past : 0;
+        --w;
+    }
+    *whole = w;
+    return n + w * runs;
+}
 
 // Walks the batch 32 requests at a time, a lane per request; find() returns the
 // request of an item (by_tile: of a tile).  Items must not fall from call to call.
@@ -104,7 +124,8 @@ struct Walk {
     int n_items, n_tiles, n_rows;        // of the 32
     bool filled = false;
 
-    __device__ __forceinline__ void fill(const WeightArgs& a, int run) {
+    __device__ __forceinline__ void fill(const TcWeightArgs& ta) {
+        const WeightArgs& a = ta.w;
         const int lane = threadIdx.x & 31, r = b + lane;
         len = r < a.B ? __ldg(a.lens + r) : 0;
         ext = r < a.B ? __ldg(a.ext + r) : 0;
@@ -117,8 +138,8 @@ struct Walk {
         }
         before = rows + se - e;
         n_rows = __shfl_sync(0xffffffffu, se, 31);
-        const Request q = request(a, run, len, ext, before);
-        up_items = q.tiles * q.runs * a.Hkv;
+        const Request q = request(ta, len, ext, before);
+        up_items = q.head * a.Hkv;
         up_tiles = q.tiles;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -132,26 +153,31 @@ struct Walk {
         n_tiles = __shfl_sync(0xffffffffu, up_tiles, 31);
         filled = true;
     }
-    static __device__ __forceinline__ Request request(const WeightArgs& a, int run, int len, int ext, int64_t before) {
+    static __device__ __forceinline__ Request request(const TcWeightArgs& ta, int len, int ext, int64_t before) {
+        const WeightArgs& a = ta.w;
         Request q{};
         if (len < 0 || ext < 0 || (int64_t)len + ext > a.lim || before + ext > a.n_rows) return q;
         const int ask = a.window > 0 ? min(a.window, ext) : ext;
         q.x = Asked{len + ext, ask, len + ext - ask, len, before + ext - ask};
         q.tiles = (q.x.total + 255) / 256;
         q.blocks = (ask * a.G + 127) / 128;
-        q.runs = (q.blocks + run - 1) / run;
+        q.runs = (q.blocks + ta.run - 1) / ta.run;
+        int64_t whole;
+        const int64_t head = items_of_head(q.x.p0, q.tiles, q.runs, ta.run, 31 - __clz(a.G), &whole);
+        if (head * a.Hkv > ta.items) return Request{};       // (other lengths than the host's)
+        q.head = (int)head;
         return q;
     }
-    __device__ __forceinline__ bool find(const WeightArgs& a, int run, int at, bool by_tile, Request& q) {
+    __device__ __forceinline__ bool find(const TcWeightArgs& a, int at, bool by_tile, Request& q) {
         for (;;) {
-            if (!filled) fill(a, run);
+            if (!filled) fill(a);
             const uint32_t hit = __ballot_sync(0xffffffffu, by_tile ? tiles + up_tiles > at : items + up_items > at);
             if (hit) {
                 const int l = __ffs(hit) - 1;
-                q = request(a, run, __shfl_sync(0xffffffffu, len, l), __shfl_sync(0xffffffffu, ext, l),
+                q = request(a, __shfl_sync(0xffffffffu, len, l), __shfl_sync(0xffffffffu, ext, l),
                             __shfl_sync(0xffffffffu, before, l));
                 q.r = b + l;
-                q.first = items + __shfl_sync(0xffffffffu, up_items, l) - q.tiles * q.runs * a.Hkv;
+                q.first = items + __shfl_sync(0xffffffffu, up_items, l) - q.head * a.w.Hkv;
                 q.first_tile = tiles + __shfl_sync(0xffffffffu, up_tiles, l) - q.tiles;
                 return true;
             }
@@ -160,7 +186,7 @@ struct Walk {
             rows += n_rows;
             b += 32;
             filled = false;
-            if (b >= a.B) return false;
+            if (b >= a.w.B) return false;
         }
     }
 };
@@ -172,34 +198,43 @@ struct alignas(16) Item {
     int total, rows, row, r;             // .. total, query rows of a head, first query token; request
 };
 
-// Query blocks pass a tile over until one has a row that sees its first position.
-__device__ __forceinline__ int first_block(const Asked& x, int t0, int lg) { return max(t0 - x.p0, 0) << lg >> 7; }
-
-// The next item from `at` on, `step` apart, that has query blocks; at -1: none.
-__device__ __forceinline__ Item next_item(const TcWeightArgs& a, Walk& w, int at, int step) {
+// Item `at`, or at -1 past the last.
+__device__ __forceinline__ Item item_at(const TcWeightArgs& a, Walk& w, int at) {
     Request q;
     Item it{};
+    it.at = -1;
+    if (at >= a.items || !w.find(a, at, false, q)) return it;
     const int lg = 31 - __clz(a.w.G);
-    for (;; at += step) {
-        it.at = -1;
-        if (at >= a.items || !w.find(a.w, a.run, at, false, q)) return it;
-        const int k = at - q.first, hs = k / q.tiles, tile = k - hs * q.tiles, h = hs / q.runs, s = hs - h * q.runs;
-        const int t0 = 256 * tile;
-        it.b0 = max(s * a.run, first_block(q.x, t0, lg));
-        it.b1 = min((s + 1) * a.run, q.blocks);
-        if (it.b0 >= it.b1) continue;    // (the join passes over it too)
-        it.at = at;
-        it.t0 = t0;
-        it.two = t0 + 128 < q.x.total;
-        it.h = h;
-        it.b0_1 = it.two ? max(it.b0, first_block(q.x, t0 + 128, lg)) : it.b1;
-        it.p0 = q.x.p0;
-        it.total = q.x.total;
-        it.rows = q.x.ask << lg;
-        it.row = (int)q.x.row;
-        it.r = q.r;
-        return it;
+    int64_t whole;
+    items_of_head(q.x.p0, q.tiles, q.runs, a.run, lg, &whole);
+    int k = at - q.first;
+    it.h = k / q.head;
+    k -= it.h * q.head;
+    int tile, s;                         // (of the tile, counted from its first run)
+    if (k < (int)whole * q.runs) {
+        tile = k / q.runs;
+        s = k - tile * q.runs;
+    } else {
+        k -= (int)whole * q.runs;
+        for (tile = (int)whole;; ++tile) {
+            const int past = (int)(first_block(q.x.p0, 256 * tile, lg) / a.run), n = q.runs - past;
+            s = past + k;
+            if (k < n || tile + 1 >= q.tiles) break;
+            k -= max(n, 0);
+        }
     }
+    it.at = at;
+    it.t0 = 256 * tile;
+    it.two = it.t0 + 128 < q.x.total;
+    it.b0 = max(s * a.run, (int)first_block(q.x.p0, it.t0, lg));
+    it.b1 = min((s + 1) * a.run, q.blocks);
+    it.b0_1 = it.two ? max(it.b0, (int)first_block(q.x.p0, it.t0 + 128, lg)) : it.b1;
+    it.p0 = q.x.p0;
+    it.total = q.x.total;
+    it.rows = q.x.ask << lg;
+    it.row = (int)q.x.row;
+    it.r = q.r;
+    return it;
 }
 
 // packed pairs
@@ -585,7 +620,7 @@ __global__ void __launch_bounds__(kThreads, 1) weights_tc_kernel(const __grid_co
             Walk walk;
             int at = blockIdx.x;
             for (uint32_t n = 0; at >= 0; ++n) {
-                const Item x = next_item(a, walk, at, (int)gridDim.x);
+                const Item x = item_at(a, walk, at);
                 const uint32_t i = n % kItems;
                 wait(L::IEMPTY + i, ((n / kItems) & 1u) ^ 1u);
                 if (gave_up) break;
@@ -609,20 +644,30 @@ __global__ void __launch_bounds__(kThreads, 1) weights_tc_kernel(const __grid_co
     }
 }
 
-// The partial sums of a tile's heads and runs, in order, into its scores.
-__global__ void __launch_bounds__(256) weights_join(const __grid_constant__ TcWeightArgs a) {
+// The partial sums of a tile's heads and runs, always in the same order, into its
+// scores: four threads a position, a quarter of them each.
+constexpr int kJoin = 4;
+__global__ void __launch_bounds__(256 * kJoin) weights_join(const __grid_constant__ TcWeightArgs a) {
     __shared__ Request sr;
-    __shared__ int found;
-    const int tid = threadIdx.x;
+    __shared__ int found, first, runs;   // the tile's first item of KV head 0 and its runs
+    __shared__ float part[kJoin][256];
+    const int tid = threadIdx.x & 255, g = threadIdx.x >> 8;
     grid_dep_wait();
     grid_dep_launch();
-    if (tid < 32) {
+    if (threadIdx.x < 32) {
         Walk walk;
         Request q{};
-        const bool ok = walk.find(a.w, a.run, (int)blockIdx.x, true, q);
+        const bool ok = walk.find(a, (int)blockIdx.x, true, q);
         if (tid == 0) {
+            const int lg = 31 - __clz(a.w.G), tile = (int)blockIdx.x - q.first_tile;
+            int64_t whole = 0, before;
+            if (ok) items_of_head(q.x.p0, q.tiles, q.runs, a.run, lg, &whole);
+            before = min(whole, (int64_t)tile) * q.runs;
+            for (int64_t t = whole; t < tile; ++t) before += max(q.runs - (int)(first_block(q.x.p0, 256 * t, lg) / a.run), 0);
             sr = q;
             found = ok;
+            first = q.first + (int)before;
+            runs = ok ? max(q.runs - (int)(first_block(q.x.p0, 256 * tile, lg) / a.run), 0) : 0;
         }
         if (blockIdx.x == 0) {           // lengths that the tables do not hold
             int64_t before = 0;
@@ -640,21 +685,25 @@ __global__ void __launch_bounds__(256) weights_join(const __grid_constant__ TcWe
     }
     __syncthreads();
     if (!found) return;
-    const Request q = sr;
-    const int tile = (int)blockIdx.x - q.first_tile, pos = 256 * tile + tid;
-    if (pos >= q.x.total) return;
-    const int slot = __ldg(a.w.r2t + (int64_t)q.r * a.w.ld + pos);
-    const int64_t at = (int64_t)q.r * a.w.scores_ld + pos;
-    const bool had = a.w.in && pos < q.x.fresh;
+    const int pos = 256 * ((int)blockIdx.x - sr.first_tile) + tid, total = sr.x.total, r = sr.r;
+    const bool mine = g == 0 && pos < total, had = mine && a.w.in && pos < sr.x.fresh;
+    const int64_t at = (int64_t)r * a.w.scores_ld + pos;
+    const int slot = mine ? __ldg(a.w.r2t + (int64_t)r * a.w.ld + pos) : 0;
     const float old = had ? a.w.in[at] : 0.f;
     float s = 0.f;
-    const int s0 = first_block(q.x, 256 * tile, 31 - __clz(a.w.G)) / a.run;      // (runs before it pass the tile over)
-    if (q.first + q.runs * a.w.Hkv * q.tiles <= a.items)
-        for (int h = 0; h < a.w.Hkv; ++h)
-            for (int i = h * q.runs + s0; i < (h + 1) * q.runs; ++i) {
-                const float* p = a.partial + ((int64_t)q.first + i * q.tiles + tile) * 512 + tid;
-                s += p[0] + p[256];
-            }
+    const int n = runs * a.w.Hkv, head = sr.head;
+    if (pos < total && sr.first + head * a.w.Hkv <= a.items) {
+#pragma unroll 4
+        for (int i = g; i < n; i += kJoin) {
+            const int h = i / runs;
+            const float* p = a.partial + ((int64_t)first + h * head + (i - h * runs)) * 512 + tid;
+            s += p[0] + p[256];
+        }
+    }
+    part[g][tid] = s;
+    __syncthreads();
+    if (!mine) return;
+    s = (part[0][tid] + part[1][tid]) + (part[2][tid] + part[3][tid]);
     if (slot < 0 || slot >= a.w.num_slots) {
         s = 0.f;
         atomicOr(a.w.err, 1u);
@@ -699,17 +748,21 @@ TcPlan tc_plan(const sgl_attn_params* p, int window) {
         x.tiles += tiles;
         units += tiles * blocks * p->num_kv_heads;
     }
-    // four items for each SM, of at most 16 query blocks
-    x.run = (int)std::min<int64_t>(std::max<int64_t>((units + 4 * 152 - 1) / (4 * 152), 1), 16);
+    // an item for each SM, of at most 16 query blocks
+    x.run = (int)std::min<int64_t>(std::max<int64_t>((units + 151) / 152, 1), 16);
+    const int lg = 31 - __builtin_clz((unsigned)G);
     for (int r = 0; r < p->batch; ++r) {
         size(r, tiles, blocks);
-        x.items += tiles * ((blocks + x.run - 1) / x.run) * p->num_kv_heads;
+        const int64_t e = p->host_extend_lens[r], ask = window > 0 ? std::min<int64_t>(window, e) : e;
+        int64_t whole;
+        x.items += p->num_kv_heads
+                   * items_of_head(p->host_prefix_lens[r] + e - ask, tiles, (blocks + x.run - 1) / x.run, x.run, lg, &whole);
     }
     return x;
 }
 
 int launch_weights_tc(const WeightArgs& w, int kv, int d, const TcPlan& plan, float* partial, cudaStream_t s) {
-    if (plan.items > INT32_MAX / 2 || plan.tiles > INT32_MAX / 2 || w.n_rows > kMaxRows) return -1;
+    if (plan.items > kMaxItems || plan.tiles > INT32_MAX / 64 || w.n_rows > kMaxRows) return -1;
     TcWeightArgs a{w, partial, (int)plan.items, plan.run};
     if (plan.items > 0) {
         CUtensorMap tmq{};
@@ -727,7 +780,7 @@ int launch_weights_tc(const WeightArgs& w, int kv, int d, const TcPlan& plan, fl
     pdl[0].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)plan.tiles);
-    cfg.blockDim = dim3(256);
+    cfg.blockDim = dim3(256 * kJoin);
     cfg.stream = s;
     cfg.attrs = pdl;
     cfg.numAttrs = 1;
