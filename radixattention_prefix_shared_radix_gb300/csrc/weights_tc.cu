@@ -460,7 +460,6 @@ __global__ void __launch_bounds__(kThreads, 1) weights_tc_kernel(const __grid_co
             const int p = it.t0 + 128 * t + 32 * q + lane;
             slot = -1;
             if (p < it.total) slot = __ldg(a.w.r2t + (int64_t)it.r * a.w.ld + p);
-            if (slot >= a.w.num_slots) slot = -1;    // (the join reports it)
         };
         if (more) lookup();
         uint32_t copied = 0, ends = 0;               // tiles copied; those that are their item's last, by their number's low bits
@@ -471,7 +470,7 @@ __global__ void __launch_bounds__(kThreads, 1) weights_tc_kernel(const __grid_co
                 for (int k = 0; k < 4; ++k) {
                     // four lanes copy a row's neighbouring pieces
                     const int r = 8 * k + (lane >> 2), s = __shfl_sync(0xffffffffu, slot, r);
-                    const bool ok = s >= 0;
+                    const bool ok = s >= 0 && s < a.w.num_slots;         // (the join reports others)
                     const uint8_t* src = a.w.kp + (int64_t)(ok ? s : 0) * a.w.row_bytes
                                          + (KV == 2 ? fp4_code_off(it.h, D) : it.h * L::ROW);
                     const uint32_t dst = to + r * L::STRIDE;
