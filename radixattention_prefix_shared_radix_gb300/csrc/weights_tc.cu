@@ -22,18 +22,18 @@
 // broadcast, and a warp's broadcast costs the same 512 bytes of bandwidth
 // whatever it is worth, so it is used for two positions at once.  A whole half
 // block (128 scores of a thread) goes to registers before any exponential, which
-// hands the accumulators back to the MMAs; the warpgroups have 176 registers a
+// hands the accumulators back to the MMAs; the warpgroups have 168 registers a
 // thread for it, taken from the others.  The two warpgroups' sums, 256 each, go
 // to memory; a second launch adds those of a request's heads and runs in order
 // and puts them into the scores.
 //   warps 0 .. 7    softmax: columns 64 (w / 4) on, thread = TMEM lane
-//   warps 8 .. 11   K: rows 32 (w % 4) on of both tiles, copied to shared memory
-//                   some tiles ahead, and from there, converted, to TMEM, where two
-//                   items' rows take turns
-//   warp 12         issues the MMAs (and owns TMEM)
-//   warp 13         Q blocks by TMA, and beside them the rows' log-sum-exps, which
+//   warps 8 .. 15   K: tile w / 4 - 2, rows 32 (w % 4) on, copied to shared memory an
+//                   item or two ahead, and from there, converted, to TMEM, where
+//                   two items' rows take turns
+//   warp 16         issues the MMAs (and owns TMEM)
+//   warp 17         Q blocks by TMA, and beside them the rows' log-sum-exps, which
 //                   it loads a block ahead
-//   warp 14         finds the items and puts them where the others read them
+//   warp 18         finds the items and puts them where the others read them
 // All waits are bounded: one that gives up sets bit 2 of the error word, and the
 // code runs to its end without hanging.
 
@@ -51,26 +51,26 @@ namespace {
 
 using namespace tc;
 
-constexpr int kThreads = 512;
-constexpr int kLoadWarp = 8, kMmaWarp = 12, kQueryWarp = 13;
-constexpr int kItemWarp = 14;
+constexpr int kThreads = 640;
+constexpr int kLoadWarp = 8, kMmaWarp = 16, kQueryWarp = 17, kItemWarp = 18;
+constexpr int kReaders = 18;             // warps that go through the items
 constexpr int kLStages = 8;
 constexpr int kItems = 8;                // items found ahead
 constexpr int kMaxRows = 1 << 24;        // query rows of a call
 constexpr int kMaxItems = 1 << 25;
-// registers of a thread: 2 x 128 x 176 + 128 x 96 + 128 x 64 = the launch's 512 x 128
-constexpr int kSoftmaxRegs = 176, kLoadRegs = 96, kOtherRegs = 64;
+// registers of a thread: 2 x 128 x 168 + 2 x 128 x 48 + 128 x 48 = the launch's 640 x 96
+constexpr int kSoftmaxRegs = 168, kLoadRegs = 48, kOtherRegs = 48;
 
 template <int D, int KV>
 struct Lay {
     // a pool row of one head as staged: its bytes (4-bit rows: codes, then scales) and the stride, an odd number of 16 bytes
     static constexpr int ROW = KV == 0 ? D * 2 : KV == 1 ? D : D / 2;
     static constexpr int STRIDE = KV == 2 ? D / 2 + 16 : ROW + 16;
-    static constexpr int KTILES = KV == 0 && D == 128 ? 3 : 4;   // staged tiles
+    static constexpr int KTILES = KV == 0 && D == 128 ? 1 : 2;   // staged tiles of each load warpgroup
     static constexpr int QSTAGES = KV == 0 && D == 128 ? 3 : 4;
     static constexpr int QTILE = 128 * D * 2;
     static constexpr int OFF_K = QSTAGES * QTILE;
-    static constexpr int OFF_L = OFF_K + KTILES * 128 * STRIDE;  // minus the log-sum-exps of a block's columns
+    static constexpr int OFF_L = OFF_K + 2 * KTILES * 128 * STRIDE;  // minus the log-sum-exps of a block's columns
     static constexpr int OFF_ITEM = OFF_L + kLStages * 512;
     static constexpr int OFF_BAR = OFF_ITEM + kItems * 64;
     static constexpr int OFF_TMEM = OFF_BAR + 40 * 8;
@@ -321,7 +321,7 @@ __global__ void __launch_bounds__(kThreads, 1) weights_tc_kernel(const __grid_co
     const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
     if (tid == 0) {
         for (int i = 0; i < 2; ++i) {
-            mbar_init(bar(L::AFULL + i), 4);
+            mbar_init(bar(L::AFULL + i), 8);
             mbar_init(bar(L::AEMPTY + i), 1);
         }
         mbar_init(bar(L::SFULL), 1);
@@ -332,7 +332,7 @@ __global__ void __launch_bounds__(kThreads, 1) weights_tc_kernel(const __grid_co
         }
         for (int i = 0; i < kItems; ++i) {
             mbar_init(bar(L::IFULL + i), 1);
-            mbar_init(bar(L::IEMPTY + i), 14);
+            mbar_init(bar(L::IEMPTY + i), kReaders);
         }
         mbar_init(bar(L::DONE), 1);
         mbar_fence_init();
@@ -451,76 +451,71 @@ __global__ void __launch_bounds__(kThreads, 1) weights_tc_kernel(const __grid_co
     } else if (warp < kMmaWarp) {
         // ------------------------------------------------------------ K
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(kLoadRegs));
-        const int q = warp & 3;
-        const uint32_t tl = tbase + ((uint32_t)(32 * q) << 16);
-        const uint32_t stage = sq + L::OFF_K + 32 * q * L::STRIDE;       // this warp's rows of the first staged tile
-        int t = 0, slot = -1;                        // the next tile to copy: of item `it`
+        const int q = warp & 3, t = (warp - kLoadWarp) >> 2;
+        const uint32_t tl = tbase + ((uint32_t)(32 * q) << 16) + 64 * t;
+        const uint32_t stage = sq + L::OFF_K + (t * L::KTILES * 128 + 32 * q) * L::STRIDE;       // this warp's rows of its first staged tile
+        int slot = -1;
         bool more = next();
-        auto lookup = [&] {                          // lane: the slot of its row of that tile
+        auto lookup = [&] {                          // lane: the slot of its row of the next tile to copy
             const int p = it.t0 + 128 * t + 32 * q + lane;
             slot = -1;
             if (p < it.total) slot = __ldg(a.w.r2t + (int64_t)it.r * a.w.ld + p);
         };
         if (more) lookup();
-        uint32_t copied = 0, ends = 0;               // tiles copied; those that are their item's last, by their number's low bits
-        auto copy = [&] {                            // the next tile, as one group (empty past the last)
+        uint32_t copied = 0, absent = 0;             // items copied; those without this tile, by their number's low bits
+        auto copy = [&] {                            // the next item's tile, as one group (empty without one)
             if (more) {
                 const uint32_t to = stage + (copied % L::KTILES) * 128 * L::STRIDE;
+                const bool none = t == 1 && !it.two;
+                absent = (absent & ~(1u << (copied & 31u))) | (uint32_t)none << (copied & 31u);
+                if (!none) {
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    // four lanes copy a row's neighbouring pieces
-                    const int r = 8 * k + (lane >> 2), s = __shfl_sync(0xffffffffu, slot, r);
-                    const bool ok = s >= 0 && s < a.w.num_slots;         // (the join reports others)
-                    const uint8_t* src = a.w.kp + (int64_t)(ok ? s : 0) * a.w.row_bytes
-                                         + (KV == 2 ? fp4_code_off(it.h, D) : it.h * L::ROW);
-                    const uint32_t dst = to + r * L::STRIDE;
+                    for (int k = 0; k < 4; ++k) {
+                        // four lanes copy a row's neighbouring pieces
+                        const int r = 8 * k + (lane >> 2), s = __shfl_sync(0xffffffffu, slot, r);
+                        const bool ok = s >= 0 && s < a.w.num_slots;         // (the join reports others)
+                        const uint8_t* src = a.w.kp + (int64_t)(ok ? s : 0) * a.w.row_bytes
+                                             + (KV == 2 ? fp4_code_off(it.h, D) : it.h * L::ROW);
+                        const uint32_t dst = to + r * L::STRIDE;
 #pragma unroll
-                    for (int i = 0; i < (L::ROW + 63) / 64; ++i) {
-                        const int piece = 4 * i + (lane & 3);
-                        if (16 * piece < L::ROW) cp_async16(dst + 16 * piece, src + 16 * piece, ok);
+                        for (int i = 0; i < (L::ROW + 63) / 64; ++i) {
+                            const int piece = 4 * i + (lane & 3);
+                            if (16 * piece < L::ROW) cp_async16(dst + 16 * piece, src + 16 * piece, ok);
+                        }
+                        if (KV == 2 && (lane & 3) == 0)
+                            cp_async_small<D / 16>(dst + D / 2, a.w.kp + (int64_t)(ok ? s : 0) * a.w.row_bytes
+                                                   + fp4_scale_off(it.h, a.w.Hkv, D), ok);
                     }
-                    if (KV == 2 && (lane & 3) == 0)
-                        cp_async_small<D / 16>(dst + D / 2, a.w.kp + (int64_t)(ok ? s : 0) * a.w.row_bytes
-                                               + fp4_scale_off(it.h, a.w.Hkv, D), ok);
                 }
-                const bool last = t == 1 || !it.two;
-                ends = (ends & ~(1u << (copied & 31u))) | (uint32_t)last << (copied & 31u);
                 ++copied;
-                t = last ? 0 : 1;
-                if (last) more = next();
+                more = next();
                 if (more) lookup();
             }
             cp_async_commit();
         };
 #pragma unroll 1
         for (int i = 0; i < L::KTILES; ++i) copy();
-        uint32_t n = 0, col = 0;                     // items put into TMEM; the tile's place in its item's columns
 #pragma unroll 1
-        for (uint32_t tn = 0; tn < copied; ++tn) {
+        for (uint32_t n = 0; n < copied; ++n) {
             const uint32_t ab = n & 1u;
-            if (col == 0) {
-                wait(L::AEMPTY + ab, ((n >> 1) & 1u) ^ 1u);
-                if (gave_up) break;
-                tc_fence_after();
-            }
+            wait(L::AEMPTY + ab, ((n >> 1) & 1u) ^ 1u);
+            if (gave_up) break;
+            tc_fence_after();
             cp_async_wait<L::KTILES - 1>();
             __syncwarp();
-            const uint32_t from = stage + (tn % L::KTILES) * 128 * L::STRIDE + lane * L::STRIDE;
+            if (!(absent >> (n & 31u) & 1u)) {
+                const uint32_t from = stage + (n % L::KTILES) * 128 * L::STRIDE + lane * L::STRIDE;
 #pragma unroll
-            for (int c = 0; c < D / 32; ++c) {
-                uint32_t y[16];
-                convert32<D, KV>(from, c, y);
-                tst16u_nw(tl + ab * 128 + col + 16 * c, y);
+                for (int c = 0; c < D / 32; ++c) {
+                    uint32_t y[16];
+                    convert32<D, KV>(from, c, y);
+                    tst16u_nw(tl + ab * 128 + 16 * c, y);
+                }
+                tst_wait();
             }
-            tst_wait();
             tc_fence_before();
             __syncwarp();
-            col = 64;
-            if (ends >> (tn & 31u) & 1u) {
-                if (lane == 0) mbar_arrive(bar(L::AFULL + ab));
-                ++n;
-                col = 0;
-            }
+            if (lane == 0) mbar_arrive(bar(L::AFULL + ab));
             __syncwarp();
             copy();                                  // (into the tile just read)
         }
