@@ -719,22 +719,26 @@ int sgl_attn_weights_workspace_bytes(const sgl_attn_params* params, int32_t wind
  *                row i of request r at position lens[r] + i, seeing positions
  *                up to its own; params->host_prefix_lens and host_extend_lens
  *                are host copies of the two, as in sgl_extend_attn
+ *                (at most 2^24 rows)
  *   window       chunks: the last `window` rows of each request ask (0: all)
  *   scores_in    device fp32 [B, scores_ld], or NULL: as zeros (decay unused);
  *                scores_out: likewise, may be scores_in itself and must not
  *                overlap it otherwise.  Positions past a context are neither
  *                read nor written
- *   decay        what a gathered score keeps, >= 0 and finite
+ *   decay        what a gathered score keeps, >= 0 and finite; 0: scores_in is
+ *                not read
  * The products are those of the attention call on the same pool (fp32 sums;
  * the decode form takes the query of an E4M3 or 4-bit pool as f16, elements out
  * of its range set SGL_ERR_BOUNDS for sgl_check, chunks take it as it is); the
- * weights and their sums are fp32, always added in the same order.  A slot outside the pool gives its token no weight
- * and sets bit 0 of the workspace's error word; a length outside the table sets
- * bit 1 and leaves the request's scores as they were.  A prefix that requests
- * share is read once for each of them.
+ * weights and their sums are fp32, always added in the same order.  A slot
+ * outside the pool gives its token no weight and sets bit 0 of the workspace's
+ * error word; a length outside the table (or beyond 2^26) sets bit 1 and leaves
+ * the request's scores as they were.  A prefix that requests share is read once
+ * for each of them.
  * workspace: device, 256-byte aligned, sgl_attn_weights_workspace_bytes (a
  * decode plan's serves in the decode form); calls that may overlap on the GPU
- * need one each.  Can be captured; the decode form follows lens at replay.
+ * need one each.  Can be captured; the decode form follows lens at replay, a
+ * captured chunk keeps the lengths that it was captured with.
  * ["SGLang 深度解读" "5. Attention 层": attention over req_to_token rows, whose
  * weights these are] */
 int sgl_attn_weights(const void* q, const float* lse, const void* k_pool, const int32_t* req_to_token, int64_t ld,

@@ -779,7 +779,7 @@ def _refuse(t, what, dtype, shape, dev, layout):
 
 def _positions(rope, t, n, dev):
     """The address of a rotation's positions: int32 [axes, n] (one axis: [n] or [1, n])."""
-    shape = (n,) if rope.axes == 1 and t.dim() == 1 else (rope.axes, n)
+    shape = (n,) if rope.axes == 1 and getattr(t, "ndim", 1) == 1 else (rope.axes, n)
     return _flat(t, "positions", dev, _T.int32, shape)
 
 

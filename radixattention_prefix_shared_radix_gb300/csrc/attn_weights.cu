@@ -458,7 +458,7 @@ int sgl_attn_weights(const void* q, const float* lse, const void* k_pool, const 
     if (!workspace || !aligned(workspace, sgl::kWsAlign) || ws_bytes < sgl::kWsAlign) return SGL_ERR_WORKSPACE;
     if (B == 0) return SGL_OK;
     if (!lens) return SGL_ERR_INVALID_ARG;
-    const int64_t lim = std::min<int64_t>(std::min(ld, scores_ld), INT32_MAX / 2);
+    const int64_t lim = std::min<int64_t>(std::min(ld, scores_ld), kMaxLen);
     int64_t rows = B, most = lim;
     if (extend_lens) {
         if (!params->host_extend_lens || !params->host_prefix_lens) return SGL_ERR_INVALID_ARG;

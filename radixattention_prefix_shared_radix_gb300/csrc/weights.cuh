@@ -10,6 +10,7 @@ namespace wts {
 
 using namespace sgldev;
 
+constexpr int kMaxLen = 1 << 26;         // positions of a context
 constexpr int kKvF32 = 3;                // pools by dtype, as elsewhere: 0 bf16, 1 E4M3, 2 4-bit rows
 
 struct WeightArgs {

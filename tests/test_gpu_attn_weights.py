@@ -385,6 +385,91 @@ def test_decode_in_a_graph_follows_the_lengths(kind):
     assert not scores.cpu().numpy()[np.arange(140)[None] >= (lens + 3)[:, None]].any() and tol.sum() == 0
 
 
+@pytest.mark.parametrize("kind,hkv", [("bf16", 8), ("f32", 8), ("fp8", 16), ("fp4", 32)])
+@pytest.mark.parametrize("decode", [False, True])
+def test_rows_far_into_the_pool(kind, hkv, decode):
+    """Keys more than 2^31 bytes into a pool."""
+    pre, ext = np.array([30, 0]), np.array([1, 1]) if decode else np.array([40, 5])
+    c = Cache(kind, pre + ext, hkv, hkv, 128, seed=13)
+    q = c.queries(int(ext.sum()))
+    lse = c.lse(q, pre, ext, 128 ** -0.5)
+    near = _run(c, q, lse, pre, ext, 0, None, 1.0, decode)
+    first = 2 ** 31 // (c.pool[0].numel() * c.pool.element_size()) + 5
+    far = torch.zeros(first + c.slots, *c.pool.shape[1:], dtype=c.pool.dtype, device="cuda")
+    far[first:] = c.pool.cuda()
+    table = torch.from_numpy(np.where(c.table >= 0, c.table + first, -1).astype(np.int32)).cuda()
+    c.slots += first
+    p = c.params(**({} if decode else dict(host_prefix_lens=pre, host_extend_lens=ext)))
+    ws = torch.zeros(sgl.sgl_attn_weights_workspace_bytes(p), dtype=torch.uint8, device="cuda")
+    lens = torch.from_numpy((pre + ext if decode else pre).astype(np.int32)).cuda()
+    extd = None if decode else torch.from_numpy(ext.astype(np.int32)).cuda()
+    out = torch.full(near.shape, 7.0, device="cuda")
+    sgl.sgl_attn_weights(q.cuda(), lse.cuda(), far, table, lens, extd, p, None, out, ws)
+    sgl.sgl_check(ws)
+    assert np.array_equal(out.cpu().numpy(), near)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "fp8"])
+def test_two_streams_at_once(kind):
+    """Two chunk calls side by side, each with its workspace: the bits of each alone."""
+    runs = []
+    for seed, (pre, ext) in enumerate((([900, 40], [200, 130]), ([10, 700], [300, 64]))):
+        pre, ext = np.array(pre), np.array(ext)
+        c = Cache(kind, pre + ext, 16, 4, 128, seed=seed)
+        q = c.queries(int(ext.sum()))
+        lse = c.lse(q, pre, ext, 128 ** -0.5)
+        alone = _run(c, q, lse, pre, ext, 0, None, 1.0, False)
+        p = c.params(host_prefix_lens=pre, host_extend_lens=ext)
+        ws = torch.zeros(sgl.sgl_attn_weights_workspace_bytes(p), dtype=torch.uint8, device="cuda")
+        out = torch.full(alone.shape, 7.0, device="cuda")
+        pd, ed = (torch.from_numpy(x.astype(np.int32)).cuda() for x in (pre, ext))
+        runs.append((torch.cuda.Stream(), alone, out, ws,
+                     (q.cuda(), lse.cuda(), c.pool.cuda(), torch.from_numpy(c.table).cuda(), pd, ed, p, None, out, ws)))
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for s, _, _, _, args in runs:
+            sgl.sgl_attn_weights(*args, stream=s)
+    torch.cuda.synchronize()
+    for _, alone, out, ws, _ in runs:
+        sgl.sgl_check(ws)
+        assert np.array_equal(out.cpu().numpy(), alone)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "fp4"])
+def test_a_captured_chunk_with_the_eviction_behind_it(kind):
+    """Weights of a chunk and the eviction by them in one graph, replayed without waits in between."""
+    pre, ext = np.array([300, 0, 150]), np.array([60, 200, 33])
+    c = Cache(kind, pre + ext, 8, 2, 128, ld=400, seed=14)
+    q = c.queries(int(ext.sum()))
+    lse = c.lse(q, pre, ext, 128 ** -0.5)
+    p = c.params(host_prefix_lens=pre, host_extend_lens=ext)
+    ws = torch.zeros(sgl.sgl_attn_weights_workspace_bytes(p, 16), dtype=torch.uint8, device="cuda")
+    pd, ed, n = (torch.from_numpy(x.astype(np.int32)).cuda() for x in (pre, ext, pre + ext))
+    table = torch.from_numpy(c.table).cuda()
+    scores, kept, to, lens = torch.zeros(3, 400, device="cuda"), torch.zeros(3, 400, device="cuda"), table.clone(), n.clone()
+    bud = torch.full((3,), 100, dtype=torch.int32, device="cuda")
+    qd, ld, pool = q.cuda(), lse.cuda(), c.pool.cuda()
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(s):
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=s):
+            sgl.sgl_attn_weights(qd, ld, pool, table, pd, ed, p, None, scores, ws, window=16)
+            sgl.sgl_kv_evict(scores, table, n, bud, kept, to, lens, ws, recent=16)
+    for _ in range(5):
+        graph.replay()
+    torch.cuda.synchronize()
+    sgl.sgl_check(ws)
+    sc = scores.cpu().numpy()
+    want, tol = c.expect(q, lse, pre, ext, 16, np.zeros((3, 400), dtype=np.float32), 0.0, False, 128 ** -0.5)
+    for r in range(3):
+        L = int(pre[r] + ext[r])
+        assert (np.abs(sc[r, :L] - want[r, :L]) <= tol[r, :L]).all()
+        stays = oevict.keep(sc[r, :L], 100, recent=16)
+        assert int(lens[r]) == 100 and np.array_equal(to[r, :100].cpu().numpy(), c.table[r, :L][stays])
+        assert np.array_equal(kept[r, :100].cpu().numpy(), sc[r, :L][stays])
+
+
 def test_python_arguments_are_checked():
     q = torch.zeros(4, 2, 64, dtype=torch.bfloat16, device="cuda")
     lse, sc = torch.zeros(4, 2, device="cuda"), torch.zeros(4, 8, device="cuda")
