@@ -5,6 +5,8 @@
 // call, a weight is exp(s - L): no second softmax, one product Q K^T and one
 // exponential per (row, head, position), and a sum over rows.
 
+#include <cooperative_groups.h>
+
 #include <algorithm>
 #include <cmath>
 
@@ -15,23 +17,31 @@ namespace {
 
 using namespace sgldev;
 using namespace sgl::wts;
+namespace cg = cooperative_groups;
 
 // ---------------------------------------------------------------------------
-// Chunks over fp32 pools, on CUDA cores: a CTA per (tile of 32 positions, request) takes every KV
-// head and asking row, 32 rows at a time; a thread has one position and four
-// rows of each 32.
+// Chunks over fp32 pools, on CUDA cores (exact products): a cluster of CTAs per
+// (tile of 32 positions, request) deals the KV heads among its CTAs and adds
+// their sums through distributed shared memory, in order.  A CTA takes 32 rows at
+// a time; a thread has one position and four rows of each 32.
 // ---------------------------------------------------------------------------
+constexpr int kF32Cluster = 8;
+
 template <int D>
-__global__ void __launch_bounds__(256) weights_plain(const __grid_constant__ WeightArgs a) {
+__global__ void __launch_bounds__(256) weights_chunk_f32(const __grid_constant__ WeightArgs a) {
     constexpr int RS = D + 4;            // (rows of 32 in distinct banks)
     __shared__ __align__(16) float sk[32 * RS], sq[32 * RS];
     __shared__ float sl[32];
+    __shared__ float sums[32];
     __shared__ int64_t before_s;
+    cg::cluster_group cl = cg::this_cluster();
     const int r = blockIdx.y, tid = threadIdx.x, t0 = blockIdx.x * 32;
+    const int C = gridDim.z, part = blockIdx.z;          // (the cluster lies along z)
+    grid_dep_wait();
+    grid_dep_launch();
     if (tid < 32) {
         int64_t s = 0;
-        if (a.ext)
-            for (int b = tid; b < r; b += 32) s += max(__ldg(a.ext + b), 0);
+        for (int b = tid; b < r; b += 32) s += max(__ldg(a.ext + b), 0);
         for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
         if (tid == 0) before_s = s;
     }
@@ -51,7 +61,7 @@ __global__ void __launch_bounds__(256) weights_plain(const __grid_constant__ Wei
     const int rows = x.ask * a.G;
     // (rows before the one that first sees the tile are passed over)
     const int row0 = max(t0 - x.p0, 0) * a.G & ~31;
-    for (int h = 0; h < a.Hkv; ++h) {
+    for (int h = part; h < a.Hkv; h += C) {
         __syncthreads();
         for (int c = sub; c < D / 4; c += 8) {
             float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -90,6 +100,14 @@ __global__ void __launch_bounds__(256) weights_plain(const __grid_constant__ Wei
     }
 #pragma unroll
     for (int o = 1; o < 8; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    if (C > 1) {
+        if (sub == 0) sums[tid >> 3] = sum;
+        cl.sync();
+        if (part == 0 && sub == 0)
+            for (int c = 1; c < C; ++c) sum += cl.map_shared_rank(sums, c)[tid >> 3];
+        cl.sync();
+        if (part > 0) return;
+    }
     if (sub == 0 && pos < x.total) {
         if (slot < 0) sum = 0.f;
         const int64_t at = r * a.scores_ld + pos;
@@ -513,13 +531,22 @@ int sgl_attn_weights(const void* q, const float* lse, const void* k_pool, const 
         const int e = launch_weights_tc(a, kv, d, plan, partial, s);
         return e < 0 ? SGL_ERR_UNSUPPORTED : cuda_status(static_cast<cudaError_t>(e));
     }
-    const dim3 grid((unsigned)((most + 31) / 32), (unsigned)B);
     if (B > 65535) return SGL_ERR_UNSUPPORTED;
-    if (d == 64)
-        weights_plain<64><<<grid, 256, 0, s>>>(a);
-    else
-        weights_plain<128><<<grid, 256, 0, s>>>(a);
-    return cuda_status(cudaGetLastError());
+    int C = 1;
+    while (C < kF32Cluster && 2 * C <= a.Hkv) C *= 2;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = (unsigned)C;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)((most + 31) / 32), (unsigned)B, (unsigned)C);
+    cfg.blockDim = dim3(256);
+    cfg.stream = s;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cuda_status(cudaLaunchKernelEx(&cfg, d == 64 ? weights_chunk_f32<64> : weights_chunk_f32<128>, a));
 }
 
 }  // extern "C"
