@@ -136,8 +136,12 @@ __global__ void __launch_bounds__(256) weights_chunk_f32(const __grid_constant__
 template <int D, int KV>
 struct Stream {
     static constexpr int RW = D * (KV == kKvF32 ? 32 : KV == 0 ? 16 : KV == 1 ? 8 : 4) / 8 / 16;   // a lane's words of a row
-    static constexpr int NR = KV == kKvF32 ? (D == 128 ? 1 : 2) : KV == 2 ? 8 : 32 / RW;            // rows of a lane
+    static constexpr int NR = KV == kKvF32 ? 2 : KV == 2 ? 8 : 32 / RW;                        // rows of a lane
     static constexpr int PU = 8 * NR;                                                               // positions of a warp
+    // CTAs of an SM: three where 80 registers do (bf16: three 92 us, two 102, on 64
+    // contexts of 1 to 8192 tokens), two where they spill (E4M3 58 instead of 67,
+    // 4 bits 55 instead of 97)
+    static constexpr int CTAS = KV == 0 || (KV == kKvF32 && D == 64) ? 3 : 2;
 };
 constexpr int kStreamThreads = 256;
 
@@ -164,7 +168,7 @@ __device__ __forceinline__ void mma16816_f16(float* c, uint32_t a0, uint32_t a1,
 }
 
 template <int D, int KV>
-__global__ void __launch_bounds__(kStreamThreads, 3) weights_decode(const __grid_constant__ WeightArgs a, int hw, int nsub) {
+__global__ void __launch_bounds__(kStreamThreads, Stream<D, KV>::CTAS) weights_decode(const __grid_constant__ WeightArgs a, int hw, int nsub) {
     using U = Stream<D, KV>;
     constexpr int NR = U::NR, RW = U::RW, PU = U::PU;
     constexpr bool F32 = KV == kKvF32;
@@ -313,26 +317,31 @@ __global__ void __launch_bounds__(kStreamThreads, 3) weights_decode(const __grid
             const uint32_t now = live;
             float c[F32 ? NR * 2 : NR / 2][4];
             if constexpr (F32) {
+                // (lane t keeps the products of query rows t and t + 4)
 #pragma unroll
-                for (int n = 0; n < NR; ++n) {
-                    // (lane t keeps the products of rows t and t + 4)
-                    float mine[2] = {0.f, 0.f};
-                    for (int j = 0; j < a.G; ++j) {
-                        const float4* q = reinterpret_cast<const float4*>(&sq[(warp * 8 + j) * D]);
-                        float dot = 0.f;
+                for (int n = 0; n < NR; ++n) c[n][0] = c[n][1] = 0.f;
+                for (int j = 0; j < a.G; ++j) {
+                    const float4* q = reinterpret_cast<const float4*>(&sq[(warp * 8 + j) * D]);
+                    float dot[NR];
 #pragma unroll
-                        for (int i = 0; i < RW / 4; ++i) {
-                            const float4 y = q[4 * i + t];
-                            dot = fmaf(__uint_as_float(raw[n][4 * i]), y.x, dot);
-                            dot = fmaf(__uint_as_float(raw[n][4 * i + 1]), y.y, dot);
-                            dot = fmaf(__uint_as_float(raw[n][4 * i + 2]), y.z, dot);
-                            dot = fmaf(__uint_as_float(raw[n][4 * i + 3]), y.w, dot);
+                    for (int n = 0; n < NR; ++n) dot[n] = 0.f;
+#pragma unroll
+                    for (int i = 0; i < RW / 4; ++i) {
+                        const float4 y = q[4 * i + t];
+#pragma unroll
+                        for (int n = 0; n < NR; ++n) {
+                            dot[n] = fmaf(__uint_as_float(raw[n][4 * i]), y.x, dot[n]);
+                            dot[n] = fmaf(__uint_as_float(raw[n][4 * i + 1]), y.y, dot[n]);
+                            dot[n] = fmaf(__uint_as_float(raw[n][4 * i + 2]), y.z, dot[n]);
+                            dot[n] = fmaf(__uint_as_float(raw[n][4 * i + 3]), y.w, dot[n]);
                         }
-                        dot = quad_sum(dot);
-                        if ((j & 3) == t) mine[j >> 2] = dot;
                     }
-                    c[n][0] = mine[0];
-                    c[n][1] = mine[1];
+#pragma unroll
+                    for (int n = 0; n < NR; ++n) {
+                        const float all = quad_sum(dot[n]);
+                        if (j == t) c[n][0] = all;
+                        if (j == t + 4) c[n][1] = all;
+                    }
                 }
             } else {
 #pragma unroll
@@ -414,26 +423,27 @@ int cuda_status(cudaError_t e) {
     return SGL_ERR_CUDA;
 }
 
-// [head_dim 128][dtype]: the kernel, positions of a warp
+// [head_dim 128][dtype]: the kernel, positions of a warp, CTAs of an SM
 struct DecodeKernel {
     void (*run)(WeightArgs, int, int);
-    int positions;
+    int positions, ctas;
 };
+template <int D, int KV>
+constexpr DecodeKernel decode_kernel() {
+    return {weights_decode<D, KV>, Stream<D, KV>::PU, Stream<D, KV>::CTAS};
+}
 constexpr DecodeKernel decode_kernels[2][4] = {
-    {{weights_decode<64, kKvF32>, Stream<64, kKvF32>::PU}, {weights_decode<64, 0>, Stream<64, 0>::PU},
-     {weights_decode<64, 1>, Stream<64, 1>::PU}, {weights_decode<64, 2>, Stream<64, 2>::PU}},
-    {{weights_decode<128, kKvF32>, Stream<128, kKvF32>::PU}, {weights_decode<128, 0>, Stream<128, 0>::PU},
-     {weights_decode<128, 1>, Stream<128, 1>::PU}, {weights_decode<128, 2>, Stream<128, 2>::PU}}};
+    {decode_kernel<64, kKvF32>(), decode_kernel<64, 0>(), decode_kernel<64, 1>(), decode_kernel<64, 2>()},
+    {decode_kernel<128, kKvF32>(), decode_kernel<128, 0>(), decode_kernel<128, 1>(), decode_kernel<128, 2>()}};
 
 cudaError_t launch_decode(const DecodeKernel& k, const WeightArgs& a, cudaStream_t s) {
     // a warp per KV head up to eight, else several per head
     const int hw = std::min(a.Hkv, 8), nsub = 8 / hw, tp = k.positions * nsub;
-    constexpr int kCtas = 152 * 3;
     cudaLaunchAttribute pdl[1];
     pdl[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     pdl[0].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)std::min<int64_t>(kCtas, a.B * (((int64_t)a.lim + tp - 1) / tp)));
+    cfg.gridDim = dim3((unsigned)std::min<int64_t>(152 * k.ctas, a.B * (((int64_t)a.lim + tp - 1) / tp)));
     cfg.blockDim = dim3((unsigned)(hw * nsub * 32));
     cfg.stream = s;
     cfg.attrs = pdl;
