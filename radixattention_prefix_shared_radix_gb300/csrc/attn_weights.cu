@@ -21,21 +21,27 @@ namespace cg = cooperative_groups;
 
 // ---------------------------------------------------------------------------
 // Chunks over fp32 pools, on CUDA cores (exact products): a cluster of CTAs per
-// (tile of 32 positions, request) deals the KV heads among its CTAs and adds
-// their sums through distributed shared memory, in order.  A CTA takes 32 rows at
-// a time; a thread has one position and four rows of each 32.
+// (tile of 64 positions, request) deals the KV heads among its CTAs and adds
+// their sums through distributed shared memory, in order.  A CTA takes 64 rows at
+// a time; a thread multiplies four positions by four rows, so that eight 16-byte
+// reads of shared memory, which bound it, feed 64 multiply-adds.
 // ---------------------------------------------------------------------------
-constexpr int kF32Cluster = 8;
+constexpr int kF32Cluster = 8, kF32Tile = 64;
+template <int D>
+constexpr int f32_smem() {
+    return 2 * kF32Tile * (D + 4) * 4;
+}
 
 template <int D>
 __global__ void __launch_bounds__(256) weights_chunk_f32(const __grid_constant__ WeightArgs a) {
-    constexpr int RS = D + 4;            // (rows of 32 in distinct banks)
-    __shared__ __align__(16) float sk[32 * RS], sq[32 * RS];
-    __shared__ float sl[32];
-    __shared__ float sums[32];
+    constexpr int RS = D + 4, T = kF32Tile;
+    extern __shared__ __align__(16) float sk[];          // T keys, then T query rows
+    float* const sq = sk + T * RS;
+    __shared__ float sl[T], sums[T];
+    __shared__ int32_t slots[T];
     __shared__ int64_t before_s;
     cg::cluster_group cl = cg::this_cluster();
-    const int r = blockIdx.y, tid = threadIdx.x, t0 = blockIdx.x * 32;
+    const int r = blockIdx.y, tid = threadIdx.x, t0 = blockIdx.x * T;
     const int C = gridDim.z, part = blockIdx.z;          // (the cluster lies along z)
     grid_dep_wait();
     grid_dep_launch();
@@ -47,72 +53,93 @@ __global__ void __launch_bounds__(256) weights_chunk_f32(const __grid_constant__
     }
     __syncthreads();
     const Asked x = asked(a, r, before_s, tid == 0 && t0 == 0);
-    if (t0 >= x.total) return;
-    const int pos = t0 + (tid >> 3), sub = tid & 7;
-    int64_t slot = -1;
-    if (pos < x.total) {
-        slot = __ldg(a.r2t + r * a.ld + pos);
-        if (slot < 0 || slot >= a.num_slots) {
-            if (sub == 0) atomicOr(a.err, 1u);
-            slot = -1;
+    if (t0 >= x.total) return;                           // (the whole cluster)
+    if (tid < T) {
+        int32_t slot = -1;
+        if (t0 + tid < x.total) {
+            slot = __ldg(a.r2t + r * a.ld + t0 + tid);
+            if (slot < 0 || slot >= a.num_slots) {
+                atomicOr(a.err, 1u);
+                slot = -1;
+            }
         }
+        slots[tid] = slot;
     }
-    float sum = 0.f;
+    const int py = tid >> 4, rx = tid & 15;              // positions py + 16 i, rows rx + 16 j
+    float sum[4] = {0.f, 0.f, 0.f, 0.f};
     const int rows = x.ask * a.G;
     // (rows before the one that first sees the tile are passed over)
-    const int row0 = max(t0 - x.p0, 0) * a.G & ~31;
+    const int row0 = max(t0 - x.p0, 0) * a.G & ~(T - 1);
     for (int h = part; h < a.Hkv; h += C) {
         __syncthreads();
-        for (int c = sub; c < D / 4; c += 8) {
+        for (int i = tid; i < T * (D / 4); i += 256) {
+            const int p = i / (D / 4), c = i - p * (D / 4), slot = slots[p];
             float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (slot >= 0) v = reinterpret_cast<const float4*>(a.kp + slot * a.row_bytes)[h * (D / 4) + c];
-            *reinterpret_cast<float4*>(&sk[(tid >> 3) * RS + 4 * c]) = v;
+            if (slot >= 0) v = reinterpret_cast<const float4*>(a.kp + (int64_t)slot * a.row_bytes)[h * (D / 4) + c];
+            *reinterpret_cast<float4*>(&sk[p * RS + 4 * c]) = v;
         }
-        for (int b = row0; b < rows; b += 32) {
+        for (int b = row0; b < rows; b += T) {
             __syncthreads();
-            const int mine = b + (tid >> 3);
-            const int64_t qrow = (x.row + mine / a.G) * a.Hq + h * a.G + mine % a.G;
-            for (int c = sub; c < D / 4; c += 8) {
+            for (int i = tid; i < T * (D / 4); i += 256) {
+                const int y = i / (D / 4), c = i - y * (D / 4), row = b + y;
                 float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-                if (mine < rows) v = reinterpret_cast<const float4*>(a.q)[qrow * (D / 4) + c];
-                *reinterpret_cast<float4*>(&sq[(tid >> 3) * RS + 4 * c]) = v;
+                if (row < rows)
+                    v = reinterpret_cast<const float4*>(a.q)[((x.row + row / a.G) * a.Hq + h * a.G + row % a.G) * (D / 4) + c];
+                *reinterpret_cast<float4*>(&sq[y * RS + 4 * c]) = v;
             }
-            if (sub == 0) sl[tid >> 3] = mine < rows ? minus_lse(a.lse[qrow]) : 0.f;
+            if (tid < T) {
+                const int row = b + tid;
+                sl[tid] = row < rows ? minus_lse(a.lse[(x.row + row / a.G) * a.Hq + h * a.G + row % a.G]) : 0.f;
+            }
             __syncthreads();
-            float dot[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 8
+            float dot[4][4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) dot[i][j] = 0.f;
+#pragma unroll 4
             for (int c = 0; c < D; c += 4) {
-                const float4 k = *reinterpret_cast<const float4*>(&sk[(tid >> 3) * RS + c]);
+                float4 k[4], y[4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const float4 y = *reinterpret_cast<const float4*>(&sq[(4 * i + (sub & 3) + 16 * (sub >> 2)) * RS + c]);
-                    dot[i] = fmaf(k.x, y.x, fmaf(k.y, y.y, fmaf(k.z, y.z, fmaf(k.w, y.w, dot[i]))));
+                    k[i] = *reinterpret_cast<const float4*>(&sk[(py + 16 * i) * RS + c]);
+                    y[i] = *reinterpret_cast<const float4*>(&sq[(rx + 16 * i) * RS + c]);
                 }
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        dot[i][j] = fmaf(k[i].x, y[j].x, fmaf(k[i].y, y[j].y, fmaf(k[i].z, y[j].z, fmaf(k[i].w, y[j].w, dot[i][j]))));
             }
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int row = 4 * i + (sub & 3) + 16 * (sub >> 2);
-                // a row sees positions up to its own
-                if (b + row < rows && pos <= x.p0 + (b + row) / a.G)
-                    sum += weight_of(dot[i], a.scale, sl[row]);
+            for (int j = 0; j < 4; ++j) {
+                const int row = b + rx + 16 * j, last = x.p0 + row / a.G;        // (a row sees positions up to its own)
+                const float m = sl[rx + 16 * j];
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (row < rows && t0 + py + 16 * i <= last) sum[i] += weight_of(dot[i][j], a.scale, m);
             }
         }
     }
 #pragma unroll
-    for (int o = 1; o < 8; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    if (C > 1) {
-        if (sub == 0) sums[tid >> 3] = sum;
-        cl.sync();
-        if (part == 0 && sub == 0)
-            for (int c = 1; c < C; ++c) sum += cl.map_shared_rank(sums, c)[tid >> 3];
-        cl.sync();
-        if (part > 0) return;
+    for (int i = 0; i < 4; ++i) {
+#pragma unroll
+        for (int o = 1; o < 16; o <<= 1) sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], o);
+        if (rx == 0) sums[py + 16 * i] = sum[i];
     }
-    if (sub == 0 && pos < x.total) {
-        if (slot < 0) sum = 0.f;
+    if (C > 1)
+        cl.sync();
+    else
+        __syncthreads();
+    const int pos = t0 + tid;
+    if (part == 0 && tid < T && pos < x.total) {
+        float s = sums[tid];
+        for (int c = 1; c < C; ++c) s += cl.map_shared_rank(sums, c)[tid];
+        if (slots[tid] < 0) s = 0.f;
         const int64_t at = r * a.scores_ld + pos;
-        a.out[at] = a.in && pos < x.fresh ? fmaf(a.decay, a.in[at], sum) : sum;
+        a.out[at] = a.in && pos < x.fresh ? fmaf(a.decay, a.in[at], s) : s;
     }
+    if (C > 1) cl.sync();
 }
 
 // ---------------------------------------------------------------------------
@@ -551,11 +578,15 @@ int sgl_attn_weights(const void* q, const float* lse, const void* k_pool, const 
     attr[1].val.clusterDim.x = attr[1].val.clusterDim.y = 1;
     attr[1].val.clusterDim.z = (unsigned)C;
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)((most + 31) / 32), (unsigned)B, (unsigned)C);
+    cfg.gridDim = dim3((unsigned)((most + kF32Tile - 1) / kF32Tile), (unsigned)B, (unsigned)C);
     cfg.blockDim = dim3(256);
+    cfg.dynamicSmemBytes = (size_t)(d == 64 ? f32_smem<64>() : f32_smem<128>());
     cfg.stream = s;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
+    static sgl::PerDevice ready;
+    if (const int e = ready_here(ready, [] { return large_smem(weights_chunk_f32<128>, f32_smem<128>()); }))
+        return cuda_status(static_cast<cudaError_t>(e));
     return cuda_status(cudaLaunchKernelEx(&cfg, d == 64 ? weights_chunk_f32<64> : weights_chunk_f32<128>, a));
 }
 
