@@ -24,7 +24,9 @@ namespace cg = cooperative_groups;
 // (tile of 64 positions, request) deals the KV heads among its CTAs and adds
 // their sums through distributed shared memory, in order.  A CTA takes 64 rows at
 // a time; a thread multiplies four positions by four rows, so that eight 16-byte
-// reads of shared memory, which bound it, feed 64 multiply-adds.
+// reads of shared memory, which bound it, feed 64 multiply-adds (20 TFLOP/s; one
+// position by four rows: 7).  4 x 40 to 96 tokens of 32 heads behind 500 to 2000:
+// 119 us.
 // ---------------------------------------------------------------------------
 constexpr int kF32Cluster = 8, kF32Tile = 64;
 template <int D>
@@ -158,7 +160,14 @@ __global__ void __launch_bounds__(256) weights_chunk_f32(const __grid_constant__
 // neighbouring positions; their sums meet in shared memory and are added in the
 // heads' order.  Each CTA takes an equal, contiguous run of the batch's tiles, so
 // a request's query stays in registers over its tiles.
-// Memory-bound; what counts is the bytes in flight.
+// Memory-bound; what counts is the bytes in flight, loads of the next unit being
+// issued before the exponentials of this one.  64 contexts of 1 to 8192 tokens, 8
+// heads of 128: bf16 91.7 us (6.1 TB/s, 0.90 of the measured copy; ncu: 558 of 559
+// MB read, issue slots 48%), E4M3 57.7 (5.0 TB/s), 4 bits 54.8 (3.0: four
+// conversions and four multiplications by scales for eight codes, 24 at the copy's
+// rate), 30 such over fp32 89.4 (5.6 TB/s).  One context of 180 tokens 4.1 us.
+// Before, a CTA per 32 positions with keys and queries staged through shared
+// memory took 2041 us on the bf16 batch.
 // ---------------------------------------------------------------------------
 template <int D, int KV>
 struct Stream {

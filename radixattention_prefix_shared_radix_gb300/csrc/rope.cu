@@ -16,6 +16,12 @@
 // reduction.  The nearest quarter turn is split off before the
 // conversion to fp32, so that the fp32 angle is at most an eighth of a turn.
 //
+// Several axes: a token has a position on each, a pair turns by its axis's (two
+// bits a pair among the arguments).  That is one more load a pair where the angles
+// are made, and no other work: 16384 rows of 72 heads on three axes take 92.0 us
+// (one axis 91.4).  The appends that are given positions are instances of their
+// own: with the choice at run time the 4-bit one spilled 32 bytes instead of 8.
+//
 // Work: a warp works on one token by itself -- it finds the request, position
 // and slot, puts the token's sines and cosines into its own piece of shared
 // memory, and takes units of 16 elements (two 16-byte pieces that the rotation
