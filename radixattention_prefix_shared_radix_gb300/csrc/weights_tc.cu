@@ -682,6 +682,7 @@ __global__ void __launch_bounds__(256 * kJoin) weights_join(const __grid_constan
             first = q.first + (int)before;
             runs = ok ? max(q.runs - (int)(first_block(q.x.p0, 256 * tile, lg) / a.run), 0) : 0;
         }
+        __syncwarp();
         if (blockIdx.x == 0) {           // lengths that the tables do not hold
             int64_t before = 0;
             for (int b = 0; b < a.w.B; b += 32) {

@@ -101,6 +101,28 @@ def test_long_rows(n, page, sinks, recent, in_place):
         r.check(page, sinks, recent, in_place, positions=scores == "ties")
 
 
+@pytest.mark.parametrize("page", [32, 64, 100, 999, 2048, 2 ** 28, 2 ** 30 - 1])
+@pytest.mark.parametrize("in_place", [False, True])
+def test_pages_as_long_as_rows_and_longer(page, in_place):
+    lens = [0, 1, 31, 32, 33, 64, 99, 100, 101, 999, 1000, 2000, 2048, 9000]
+    r = Rows(lens, [n // 2 for n in lens], "spread", seed=3)
+    for sinks, recent in ((0, 0), (40, 10)):
+        r.check(page, sinks, recent, in_place)
+    r = Rows(lens[:-1], [n // 3 for n in lens[:-1]], "ties", seed=4)
+    r.check(page, 0, 5, in_place)
+
+
+def test_empty_tables_and_batches():
+    f, t = torch.zeros(2, 0, device="cuda"), torch.zeros(2, 0, dtype=torch.int32, device="cuda")
+    n = torch.zeros(2, dtype=torch.int32, device="cuda")
+    ws = torch.zeros(256, dtype=torch.uint8, device="cuda")
+    sgl.sgl_kv_evict(f, t, n, n, f, t, torch.full_like(n, 5), ws)
+    sgl.sgl_check(ws)
+    e = n[:0]
+    sgl.sgl_kv_evict(f[:0], t[:0], e, e, f[:0], t[:0], e, ws)
+    sgl.sgl_check(ws)
+
+
 def test_the_longest_rows():
     """786432 pages are the most."""
     n = 786432

@@ -227,6 +227,36 @@ def test_append_at(kind, hq, hkv, d, rot, off, pairs, axes, decode):
 
 
 @gpu
+def test_append_at_in_a_graph_follows_lengths_and_positions():
+    B, hkv, d, slots, ld = 3, 2, 128, 64, 16
+    r, freq, axis, amp = _axes(d, d, (16, 24, 24))
+    params = sgl.make_params(sgl.SGL_DTYPE_BF16, B, 2, hkv, d, slots)
+    table = torch.randperm(slots)[:B * ld].view(B, ld).to(torch.int32).cuda()
+    k, v = (torch.randn(B, hkv, d, device="cuda").bfloat16() for _ in "kv")
+    kp, vp = (torch.zeros(slots, hkv, d, dtype=torch.bfloat16, device="cuda") for _ in "kv")
+    lens = torch.tensor([1, 5, 9], dtype=torch.int32, device="cuda")
+    pos = torch.randint(0, 5000, (3, B), dtype=torch.int32, device="cuda")
+    ws = torch.zeros(256, dtype=torch.uint8, device="cuda")
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(s):
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=s):
+            sgl.sgl_kv_append_at(r, params, None, k, v, kp, vp, table, lens, None, pos, None, ws)
+    del r
+    for _ in range(3):
+        kp.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        to = table.cpu().numpy()[np.arange(B), lens.cpu().numpy() - 1]
+        _check(kp[to], k, pos.cpu().numpy().astype(np.int64), d, 0, False, freq, axis, amp)
+        assert int(kp.flatten(1).any(1).sum()) == B
+        lens += 1
+        pos += 77
+    sgl.sgl_check(ws)
+
+
+@gpu
 def test_python_arguments_are_checked():
     r = sgl.sgl_rope_create(64, axes=(10, 11, 11))
     q = torch.zeros(4, 2, 64, dtype=torch.bfloat16, device="cuda")
