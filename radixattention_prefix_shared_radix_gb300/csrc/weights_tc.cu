@@ -409,7 +409,8 @@ __global__ void __launch_bounds__(kThreads, 1) weights_tc_kernel(const __grid_co
                 // stands at it or behind
                 const int from = 128 * b + 64 * wg;
                 const int lo = ((it.t0 + row - it.p0) << lg) - from, hi = min(it.rows - from, 64);
-                const bool all = __all_sync(0xffffffffu, lo + (both ? 128 << lg : 0) <= 0) && hi == 64;
+                // (all of them for all positions of both tiles; what stands past the context is not read)
+                const bool all = (min(it.t0 + 255, it.total - 1) - it.p0) << lg <= from && hi == 64;
                 float v0[64], v1[64];
                 wait(L::SFULL, qn & 1u);
                 if (gave_up) break;
@@ -660,7 +661,7 @@ __global__ void __launch_bounds__(kThreads, 1) weights_tc_kernel(const __grid_co
 // The partial sums of a tile's heads and runs, always in the same order, into its
 // scores: four threads a position, a quarter of them each.
 constexpr int kJoin = 4;
-__global__ void __launch_bounds__(256 * kJoin) weights_join(const __grid_constant__ TcWeightArgs a) {
+__global__ void __launch_bounds__(256 * kJoin, 2) weights_join(const __grid_constant__ TcWeightArgs a) {
     __shared__ Request sr;
     __shared__ int found, first, runs;   // the tile's first item of KV head 0 and its runs
     __shared__ float part[kJoin][256];
