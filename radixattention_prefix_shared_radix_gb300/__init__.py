@@ -707,9 +707,9 @@ def sgl_fp4_row_bytes(num_kv_heads, head_dim):
 
 
 class Rope:
-    """Owns an sgl_rope_table handle; head_dim, rot_dim and the number of axes as given."""
+    """Owns an sgl_rope_table handle; head_dim, rot_dim and the number of axes as given (0: none were)."""
 
-    def __init__(self, handle, head_dim, rot_dim, axes=1):
+    def __init__(self, handle, head_dim, rot_dim, axes=0):
         self.handle = handle
         self.head_dim = head_dim
         self.rot_dim = rot_dim
@@ -779,7 +779,8 @@ def _refuse(t, what, dtype, shape, dev, layout):
 
 def _positions(rope, t, n, dev):
     """The address of a rotation's positions: int32 [axes, n] (one axis: [n] or [1, n])."""
-    shape = (n,) if rope.axes == 1 and getattr(t, "ndim", 1) == 1 else (rope.axes, n)
+    axes = rope.axes or 1
+    shape = (n,) if axes == 1 and getattr(t, "ndim", 1) == 1 else (axes, n)
     return _flat(t, "positions", dev, _T.int32, shape)
 
 
@@ -813,14 +814,18 @@ def sgl_rope(rope, q, k, positions, q_out=None, k_out=None, stream=None):
         pko, sko = pk, sk
         if k_out is not None:
             pko, sko, _, _ = _rows(k_out, "k_out", hk, d, dt, n, dev)
-    st = _lib().sgl_rope(rope.handle, kind, pq, sq, hq, pk, sk, hk, _positions(rope, positions, n, dev), n,
-                         pqo, sqo, pko, sko, _stream(stream))
+    pp = _positions(rope, positions, n, dev) if rope.axes else _flat(positions, "positions", dev, T.int32, (n,))
+    st = _lib().sgl_rope(rope.handle, kind, pq, sq, hq, pk, sk, hk, pp, n, pqo, sqo, pko, sko, _stream(stream))
     if st:
         raise SglError(st, "sgl_rope")
 
 
-def _append(where, rope, params, q, k_new, v_new, k_pool, v_pool, req_to_token, lens, extend_lens, positions, q_out,
-            workspace, stream):
+def sgl_kv_append(rope, params, q, k_new, v_new, k_pool, v_pool, req_to_token, lens, extend_lens, q_out, workspace,
+                  stream=None, positions=None):
+    """New keys and values [N, Hkv, d] into the paged pools, keys and queries rotated on the way (rope None: not
+    rotated; q and q_out None: keys and values only).  extend_lens given: N = the sum of extend_lens (or more, in a
+    padded batch) rows ordered by request, row i of request r at position lens[r] + i; None: row r is request r's
+    newest token, at position lens[r] - 1.  positions: as sgl_kv_append_at takes them."""
     T = _T or _torch()
     kind, hkv, d, dev = params.dtype, params.num_kv_heads, params.head_dim, T._C._cuda_getDevice()
     dt = T.float32 if kind == SGL_DTYPE_F32 else T.bfloat16
@@ -841,24 +846,19 @@ def _append(where, rope, params, q, k_new, v_new, k_pool, v_pool, req_to_token, 
     if k_pool.nbytes < need or v_pool.nbytes < need:
         _writable(pkp, k_pool, "k_pool", need)
         _writable(pvp, v_pool, "v_pool", need)
-    at = () if positions is None else (_positions(rope, positions, n, dev),)
-    st = getattr(_lib(), where)(None if rope is None else rope.handle, ctypes.byref(params), pq, sq, pk, sk, pv, sv,
-                                pkp, pvp, _flat(req_to_token, "req_to_token", dev, T.int32), rows[1],
-                                _flat(lens, "lens", dev, T.int32, B),
-                                None if extend_lens is None else _flat(extend_lens, "extend_lens", dev, T.int32, B),
-                                *at, n, pqo, sqo, _flat(workspace, "workspace", dev), workspace.nbytes, _stream(stream))
+    i32 = T.int32
+    handle = None if rope is None else rope.handle
+    pt, pl = _flat(req_to_token, "req_to_token", dev, i32), _flat(lens, "lens", dev, i32, B)
+    pe = None if extend_lens is None else _flat(extend_lens, "extend_lens", dev, i32, B)
+    pw = _flat(workspace, "workspace", dev)
+    if positions is None:
+        st = _lib().sgl_kv_append(handle, ctypes.byref(params), pq, sq, pk, sk, pv, sv, pkp, pvp, pt, rows[1], pl, pe, n, pqo,
+                                  sqo, pw, workspace.nbytes, _stream(stream))
+    else:
+        st = _lib().sgl_kv_append_at(handle, ctypes.byref(params), pq, sq, pk, sk, pv, sv, pkp, pvp, pt, rows[1], pl, pe,
+                                     _positions(rope, positions, n, dev), n, pqo, sqo, pw, workspace.nbytes, _stream(stream))
     if st:
-        raise SglError(st, where)
-
-
-def sgl_kv_append(rope, params, q, k_new, v_new, k_pool, v_pool, req_to_token, lens, extend_lens, q_out, workspace,
-                  stream=None):
-    """New keys and values [N, Hkv, d] into the paged pools, keys and queries rotated on the way (rope None: not
-    rotated; q and q_out None: keys and values only).  extend_lens given: N = the sum of extend_lens (or more, in a
-    padded batch) rows ordered by request, row i of request r at position lens[r] + i; None: row r is request r's
-    newest token, at position lens[r] - 1."""
-    _append("sgl_kv_append", rope, params, q, k_new, v_new, k_pool, v_pool, req_to_token, lens, extend_lens, None, q_out,
-            workspace, stream)
+        raise SglError(st, "sgl_kv_append" if positions is None else "sgl_kv_append_at")
 
 
 def sgl_kv_append_at(rope, params, q, k_new, v_new, k_pool, v_pool, req_to_token, lens, extend_lens, positions, q_out,
@@ -867,8 +867,8 @@ def sgl_kv_append_at(rope, params, q, k_new, v_new, k_pool, v_pool, req_to_token
     position is neither rotated nor stored."""
     if rope is None or positions is None:
         raise TypeError("rope and positions must be given")
-    _append("sgl_kv_append_at", rope, params, q, k_new, v_new, k_pool, v_pool, req_to_token, lens, extend_lens, positions,
-            q_out, workspace, stream)
+    sgl_kv_append(rope, params, q, k_new, v_new, k_pool, v_pool, req_to_token, lens, extend_lens, q_out, workspace, stream,
+                  positions)
 
 
 def sgl_mla_kv_append(rope, params, q, kv_new, kv_pool, req_to_token, lens, extend_lens, q_out, workspace, stream=None):
