@@ -719,7 +719,7 @@ int sgl_attn_weights_workspace_bytes(const sgl_attn_params* params, int32_t wind
  *                row i of request r at position lens[r] + i, seeing positions
  *                up to its own; params->host_prefix_lens and host_extend_lens
  *                are host copies of the two, as in sgl_extend_attn
- *                (at most 2^24 rows)
+ *                (at most 2^24 rows; over fp32 pools, 65535 requests)
  *   window       chunks: the last `window` rows of each request ask (0: all)
  *   scores_in    device fp32 [B, scores_ld], or NULL: as zeros (decay unused);
  *                scores_out: likewise, may be scores_in itself and must not
@@ -777,7 +777,8 @@ typedef struct {
  * overlap an input otherwise; entries of outputs past lens[r] stay as they
  * were.  Slots are moved, not looked at.  A length outside [0, ld] or
  * scores_ld sets bit 1 and counts as the nearest end.  The cached keys stay
- * where they are and as they were rotated.
+ * where they are and as they were rotated.  Rows (the shorter of ld and
+ * scores_ld) of more than 786432 pages, or of 2^30 positions: SGL_ERR_UNSUPPORTED.
  * workspace: device, 256-byte aligned, its first 256 bytes (the error word;
  * calls may share it).  Can be captured.
  * ["SGLang 深度拆解" §2.3: the cache keeps what its budget allows; there whole
