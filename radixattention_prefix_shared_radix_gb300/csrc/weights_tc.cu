@@ -54,7 +54,7 @@
 // for a second set of scores beside two sets of keys.
 // Windows (one block an item) are bound by the keys' way through shared memory and
 // conversion, about 3800 cycles an item: 16 x 32 rows over 1500 to 4000 tokens in 4
-// bits 34.0 us, in E4M3 34.3, in bf16 43.6.
+// bits 32.5 us, in E4M3 34.3, in bf16 43.6.
 
 #include <algorithm>
 
@@ -106,7 +106,9 @@ struct TcWeightArgs {
 };
 
 // Query blocks pass a tile over until one has a row that sees its first position.
-__host__ __device__ __forceinline__ int64_t first_block(int64_t p0, int64_t t0, int lg) {
+// (Int: 32 bits hold it for contexts of kMaxLen; 64 for lengths not yet checked.)
+template <class Int>
+__host__ __device__ __forceinline__ Int first_block(Int p0, Int t0, int lg) {
     return (t0 > p0 ? (t0 - p0) << lg : 0) >> 7;
 }
 
@@ -114,21 +116,23 @@ __host__ __device__ __forceinline__ int64_t first_block(int64_t p0, int64_t t0, 
 // those runs that do not pass it over as a whole.
 struct Request {
     Asked x;
-    int r, tiles, runs, blocks, head;    // head: items of a KV head
+    int r, tiles, runs, blocks;
+    int head, whole;                     // items of a KV head; tiles that have every run
     int first, first_tile;               // items and tiles of the requests before it
 };
 // Of `tiles` tiles of 256 positions: how many have every run (they come first),
 // and the items of them all.
-__host__ __device__ __forceinline__ int64_t items_of_head(int64_t p0, int64_t tiles, int64_t runs, int run, int lg,
-                                                          int64_t* whole) {
-    int64_t n = 0, w = tiles;
-    while (w > 0 && first_block(p0, 256 * (w - 1), lg) >= run) {
-        const int64_t past = first_block(p0, 256 * (w - 1), lg) / run;
+template <class Int>
+__host__ __device__ __forceinline__ int64_t items_of_head(Int p0, Int tiles, Int runs, Int run, int lg, Int* whole) {
+    int64_t n = 0;
+    Int w = tiles;
+    for (; w > 0; --w) {
+        const Int past = first_block<Int>(p0, 256 * (w - 1), lg) / run;
+        if (past == 0) break;
         n += past < runs ? runs - past : 0;
-        --w;
     }
     *whole = w;
-    return n + w * runs;
+    return n + (int64_t)w * runs;
 }
 
 // Walks the batch 32 requests at a time, a lane per request; find() returns the
@@ -181,8 +185,7 @@ struct Walk {
         q.tiles = (q.x.total + 255) / 256;
         q.blocks = (ask * a.G + 127) / 128;
         q.runs = (q.blocks + ta.run - 1) / ta.run;
-        int64_t whole;
-        const int64_t head = items_of_head(q.x.p0, q.tiles, q.runs, ta.run, 31 - __clz(a.G), &whole);
+        const int64_t head = items_of_head<int>(q.x.p0, q.tiles, q.runs, ta.run, 31 - __clz(a.G), &q.whole);
         if (head * a.Hkv > ta.items) return Request{};       // (other lengths than the host's)
         q.head = (int)head;
         return q;
@@ -217,44 +220,66 @@ struct alignas(16) Item {
     int total, rows, row, r;             // .. total, query rows of a head, first query token; request
 };
 
-// Item `at`, or at -1 past the last.
-__device__ __forceinline__ Item item_at(const TcWeightArgs& a, Walk& w, int at) {
+// Finds items, of rising numbers, by one warp; the request is kept from one to
+// the next.
+struct Finder {
+    Walk walk;
     Request q;
-    Item it{};
-    it.at = -1;
-    if (at >= a.items || !w.find(a, at, false, q)) return it;
-    const int lg = 31 - __clz(a.w.G);
-    int64_t whole;
-    items_of_head(q.x.p0, q.tiles, q.runs, a.run, lg, &whole);
-    int k = at - q.first;
-    it.h = k / q.head;
-    k -= it.h * q.head;
-    int tile, s;                         // (of the tile, counted from its first run)
-    if (k < (int)whole * q.runs) {
-        tile = k / q.runs;
-        s = k - tile * q.runs;
-    } else {
-        k -= (int)whole * q.runs;
-        for (tile = (int)whole;; ++tile) {
-            const int past = (int)(first_block(q.x.p0, 256 * tile, lg) / a.run), n = q.runs - past;
-            s = past + k;
-            if (k < n || tile + 1 >= q.tiles) break;
-            k -= max(n, 0);
+    int end = 0;                         // one past the request's last item
+
+    // item `at`, or at -1 past the last
+    __device__ __forceinline__ Item item(const TcWeightArgs& a, int at) {
+        Item it{};
+        it.at = -1;
+        if (at >= a.items) return it;
+        if (at >= end) {
+            if (!walk.find(a, at, false, q)) return it;
+            end = q.first + q.head * a.w.Hkv;
         }
+        const int lane = threadIdx.x & 31, lg = 31 - __clz(a.w.G);
+        int k = at - q.first;
+        it.h = k / q.head;
+        k -= it.h * q.head;
+        int tile, s;
+        if (k < q.whole * q.runs) {
+            tile = k / q.runs;
+            s = k - tile * q.runs;
+        } else {
+            // the other tiles, 32 at a time
+            k -= q.whole * q.runs;
+            for (int b = q.whole;; b += 32) {
+                const int past = first_block<int>(q.x.p0, 256 * (b + lane), lg) / a.run;
+                const int n = b + lane < q.tiles ? max(q.runs - past, 0) : 0;
+                int upto = n;
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const int y = __shfl_up_sync(0xffffffffu, upto, o);
+                    if (lane >= o) upto += y;
+                }
+                const uint32_t hit = __ballot_sync(0xffffffffu, upto > k);
+                if (hit || b + 32 >= q.tiles) {      // (one of them holds it)
+                    const int l = hit ? __ffs(hit) - 1 : 0;
+                    tile = b + l;
+                    s = __shfl_sync(0xffffffffu, past + k - (upto - n), l);
+                    break;
+                }
+                k -= __shfl_sync(0xffffffffu, upto, 31);
+            }
+        }
+        it.at = at;
+        it.t0 = 256 * tile;
+        it.two = it.t0 + 128 < q.x.total;
+        it.b0 = max(s * a.run, first_block<int>(q.x.p0, it.t0, lg));
+        it.b1 = min((s + 1) * a.run, q.blocks);
+        it.b0_1 = it.two ? max(it.b0, first_block<int>(q.x.p0, it.t0 + 128, lg)) : it.b1;
+        it.p0 = q.x.p0;
+        it.total = q.x.total;
+        it.rows = q.x.ask << lg;
+        it.row = (int)q.x.row;
+        it.r = q.r;
+        return it;
     }
-    it.at = at;
-    it.t0 = 256 * tile;
-    it.two = it.t0 + 128 < q.x.total;
-    it.b0 = max(s * a.run, (int)first_block(q.x.p0, it.t0, lg));
-    it.b1 = min((s + 1) * a.run, q.blocks);
-    it.b0_1 = it.two ? max(it.b0, (int)first_block(q.x.p0, it.t0 + 128, lg)) : it.b1;
-    it.p0 = q.x.p0;
-    it.total = q.x.total;
-    it.rows = q.x.ask << lg;
-    it.row = (int)q.x.row;
-    it.r = q.r;
-    return it;
-}
+};
 
 // packed pairs
 __device__ __forceinline__ uint64_t pack2(float x, float y) {
@@ -631,10 +656,10 @@ __global__ void __launch_bounds__(kThreads, 1) weights_tc_kernel(const __grid_co
                 mbar_wait(bar(L::QFULL + i % L::QSTAGES), (i / L::QSTAGES) & 1u);
         } else if (warp == kItemWarp) {
             // -------------------------------------------------------- items
-            Walk walk;
+            Finder finder;
             int at = blockIdx.x;
             for (uint32_t n = 0; at >= 0; ++n) {
-                const Item x = item_at(a, walk, at);
+                const Item x = finder.item(a, at);
                 const uint32_t i = n % kItems;
                 wait(L::IEMPTY + i, ((n / kItems) & 1u) ^ 1u);
                 if (gave_up) break;
@@ -673,15 +698,19 @@ __global__ void __launch_bounds__(256 * kJoin, 2) weights_join(const __grid_cons
         Request q{};
         const bool ok = walk.find(a, (int)blockIdx.x, true, q);
         if (tid == 0) {
-            const int lg = 31 - __clz(a.w.G), tile = (int)blockIdx.x - q.first_tile;
-            int64_t whole = 0, before;
-            if (ok) items_of_head(q.x.p0, q.tiles, q.runs, a.run, lg, &whole);
-            before = min(whole, (int64_t)tile) * q.runs;
-            for (int64_t t = whole; t < tile; ++t) before += max(q.runs - (int)(first_block(q.x.p0, 256 * t, lg) / a.run), 0);
             sr = q;
             found = ok;
-            first = q.first + (int)before;
-            runs = ok ? max(q.runs - (int)(first_block(q.x.p0, 256 * tile, lg) / a.run), 0) : 0;
+        }
+        // items of the tiles before this one, 32 tiles at a time
+        const int lg = 31 - __clz(a.w.G), tile = (int)blockIdx.x - q.first_tile;
+        int before = 0;
+        for (int t = q.whole + tid; ok && t < tile; t += 32)
+            before += max(q.runs - first_block<int>(q.x.p0, 256 * t, lg) / a.run, 0);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) before += __shfl_xor_sync(0xffffffffu, before, o);
+        if (tid == 0) {
+            first = q.first + before + min(q.whole, tile) * q.runs;
+            runs = ok ? max(q.runs - first_block<int>(q.x.p0, 256 * tile, lg) / a.run, 0) : 0;
         }
         __syncwarp();
         if (blockIdx.x == 0) {           // lengths that the tables do not hold
@@ -770,8 +799,8 @@ TcPlan tc_plan(const sgl_attn_params* p, int window) {
         size(r, tiles, blocks);
         const int64_t e = p->host_extend_lens[r], ask = window > 0 ? std::min<int64_t>(window, e) : e;
         int64_t whole;
-        x.items += p->num_kv_heads
-                   * items_of_head(p->host_prefix_lens[r] + e - ask, tiles, (blocks + x.run - 1) / x.run, x.run, lg, &whole);
+        x.items += p->num_kv_heads * items_of_head<int64_t>(p->host_prefix_lens[r] + e - ask, tiles,
+                                                            (blocks + x.run - 1) / x.run, x.run, lg, &whole);
     }
     return x;
 }

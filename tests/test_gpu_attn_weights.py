@@ -193,6 +193,32 @@ def test_long_chunks(kind, hq, hkv, d):
     _check(c, pre, ext, 100, decay=0.0)
 
 
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+@pytest.mark.parametrize("hq,hkv,n", [(2, 2, 11000), (8, 1, 9100)])
+def test_long_prompts_from_the_start(kind, hq, hkv, n):
+    """More than 32 tiles that only some runs of query blocks see.  Against float64 on the GPU; a score sums n hq weights
+    in fp32, off by 2^-24 of itself for each of them at most, the weights themselves by less than 2^-13 (a product's sum of
+    magnitudes is below 2^5 here: 2^5 (64 + 12) 2^-24, and 2^-21)."""
+    c = Cache(kind, [n, 300], hq, hkv, 64, seed=n)
+    pre, ext = np.array([0, 100]), np.array([n, 200])
+    q = c.queries(n + 200)
+    want, lse, at = np.zeros((2, n)), torch.zeros(n + 200, hq, dtype=torch.float64, device="cuda"), 0
+    for r in range(2):
+        L, e = int(pre[r] + ext[r]), int(ext[r])
+        k, x = torch.from_numpy(c.keys(r, L)).cuda(), q[at:at + e].double().cuda()
+        hidden = torch.arange(L, device="cuda")[None] > int(pre[r]) + torch.arange(e, device="cuda")[:, None]
+        for h in range(hq):
+            w = (x[:, h] @ k[:, h * hkv // hq].T / 8).masked_fill_(hidden, -torch.inf)
+            lse[at:at + e, h] = torch.logsumexp(w, 1).float().double()
+            want[r, :L] += w.sub_(lse[at:at + e, h, None]).exp_().sum(0).cpu().numpy()
+        at += e
+    got = _run(c, q, lse.float().cpu(), pre, ext, 0, None, 1.0, False)
+    for r in range(2):
+        L = int(pre[r] + ext[r])
+        err = np.abs(got[r, :L] - want[r, :L])
+        assert (err <= want[r, :L] * ((int(ext[r]) * hq + 8) * 2.0 ** -24 + 2.0 ** -13) + 1e-30).all(), err.max()
+
+
 @pytest.mark.parametrize("kind", list(KINDS))
 def test_chunks_of_many_requests(kind):
     rng = np.random.default_rng(4)
