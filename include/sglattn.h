@@ -696,8 +696,10 @@ int sgl_mla_kv_append(const sgl_rope_table* rope, const sgl_mla_params* params, 
 /* ======================================================================== */
 
 /* Device workspace that sgl_attn_weights needs (bytes, a multiple of 256): in
- * the decode form (no host_extend_lens in params) 256; else by the lengths in
- * params->host_prefix_lens / host_extend_lens and by `window`. */
+ * the decode form (no host_extend_lens in params) and over fp32 pools 256; else
+ * by the lengths in params->host_prefix_lens / host_extend_lens and by `window`,
+ * no more than 2 KB for every 256 positions of a request and KV head, and 160 MB
+ * besides.  SGL_ERR_UNSUPPORTED for lengths that the call refuses. */
 int sgl_attn_weights_workspace_bytes(const sgl_attn_params* params, int32_t window, size_t* bytes);
 
 /* The attention weights that each cached token gets from a call's queries,
@@ -719,7 +721,10 @@ int sgl_attn_weights_workspace_bytes(const sgl_attn_params* params, int32_t wind
  *                row i of request r at position lens[r] + i, seeing positions
  *                up to its own; params->host_prefix_lens and host_extend_lens
  *                are host copies of the two, as in sgl_extend_attn
- *                (at most 2^24 rows; over fp32 pools, 65535 requests)
+ *                (contexts of at most 2^26 tokens; over fp32 pools 65535
+ *                requests, else 2^24 rows, and 2^32 positions x KV heads over
+ *                all requests, each counted up to a multiple of 256:
+ *                SGL_ERR_UNSUPPORTED beyond)
  *   window       chunks: the last `window` rows of each request ask (0: all)
  *   scores_in    device fp32 [B, scores_ld], or NULL: as zeros (decay unused);
  *                scores_out: likewise, may be scores_in itself and must not

@@ -487,6 +487,16 @@ cudaError_t launch_decode(const DecodeKernel& k, const WeightArgs& a, cudaStream
     return cudaLaunchKernelEx(&cfg, k.run, a, hw, nsub);
 }
 
+// What a chunk call needs (host lengths that are not negative), or
+// SGL_ERR_UNSUPPORTED: the same for the call and for the size of its workspace.
+int chunk_plan(const sgl_attn_params* p, int window, TcPlan* plan) {
+    if (p->dtype != SGL_DTYPE_F32) return tc_plan(p, window, plan);
+    if (p->batch > 65535) return SGL_ERR_UNSUPPORTED;
+    for (int32_t r = 0; r < p->batch; ++r)
+        if ((int64_t)p->host_prefix_lens[r] + p->host_extend_lens[r] > kMaxLen) return SGL_ERR_UNSUPPORTED;
+    return SGL_OK;
+}
+
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
 }  // namespace
@@ -506,8 +516,13 @@ int sgl_attn_weights_workspace_bytes(const sgl_attn_params* params, int32_t wind
         for (int32_t r = 0; r < params->batch; ++r)
             if (params->host_prefix_lens[r] < 0 || params->host_extend_lens[r] < 0) return SGL_ERR_INVALID_ARG;
     }
-    *bytes = sgl::kWsAlign;
-    if (params->host_extend_lens && params->dtype != SGL_DTYPE_F32) *bytes += (size_t)tc_plan(params, window).items * 2048;
+    size_t n = sgl::kWsAlign;
+    if (params->host_extend_lens) {
+        TcPlan plan{};
+        if (const int e = chunk_plan(params, window, &plan)) return e;
+        n += (size_t)plan.items * 2048;
+    }
+    *bytes = n;
     return SGL_OK;
 }
 
@@ -524,16 +539,17 @@ int sgl_attn_weights(const void* q, const float* lse, const void* k_pool, const 
     if (!lens) return SGL_ERR_INVALID_ARG;
     const int64_t lim = std::min<int64_t>(std::min(ld, scores_ld), kMaxLen);
     int64_t rows = B, most = lim;
+    TcPlan plan{};
     if (extend_lens) {
         if (!params->host_extend_lens || !params->host_prefix_lens) return SGL_ERR_INVALID_ARG;
         rows = most = 0;
         for (int32_t r = 0; r < B; ++r) {
             const int64_t p = params->host_prefix_lens[r], e = params->host_extend_lens[r];
             if (p < 0 || e < 0 || p + e > std::min(ld, scores_ld)) return SGL_ERR_INVALID_ARG;
-            if (p + e > lim) return SGL_ERR_UNSUPPORTED;
             rows += e;
             most = std::max(most, p + e);
         }
+        if (const int e = chunk_plan(params, window, &plan)) return e;
     }
     if (most == 0) return SGL_OK;
     if (!k_pool || !req_to_token || !scores_out || (rows > 0 && (!q || !lse))) return SGL_ERR_INVALID_ARG;
@@ -570,14 +586,11 @@ int sgl_attn_weights(const void* q, const float* lse, const void* k_pool, const 
         return cuda_status(launch_decode(*kernel, a, s));
     }
     if (kind != SGL_DTYPE_F32) {
-        const TcPlan plan = tc_plan(params, window);
         if (ws_bytes < sgl::kWsAlign + (size_t)plan.items * 2048) return SGL_ERR_WORKSPACE;
         auto* partial = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + sgl::kWsAlign);
         const int kv = kind == SGL_DTYPE_BF16 ? 0 : kind == SGL_DTYPE_BF16_FP8KV ? 1 : 2;
-        const int e = launch_weights_tc(a, kv, d, plan, partial, s);
-        return e < 0 ? SGL_ERR_UNSUPPORTED : cuda_status(static_cast<cudaError_t>(e));
+        return cuda_status(static_cast<cudaError_t>(launch_weights_tc(a, kv, d, plan, partial, s)));
     }
-    if (B > 65535) return SGL_ERR_UNSUPPORTED;
     int C = 1;
     while (C < kF32Cluster && 2 * C <= a.Hkv) C *= 2;
     cudaLaunchAttribute attr[2];

@@ -68,8 +68,8 @@ struct TcPlan {
     int64_t items, tiles;                // work items; tiles of 256 positions
     int run;                             // query blocks of an item
 };
-TcPlan tc_plan(const sgl_attn_params* params, int window);
-// 0, a cudaError_t, or -1: beyond what the kernels count
+int tc_plan(const sgl_attn_params* params, int window, TcPlan* plan);
+// 0 or a cudaError_t
 int launch_weights_tc(const WeightArgs& args, int kv, int head_dim, const TcPlan& plan, float* partial, cudaStream_t s);
 
 }  // namespace wts

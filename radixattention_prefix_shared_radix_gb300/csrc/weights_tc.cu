@@ -76,7 +76,10 @@ constexpr int kReaders = 18;             // warps that go through the items
 constexpr int kLStages = 8;
 constexpr int kItems = 8;                // items found ahead
 constexpr int kMaxRows = 1 << 24;        // query rows of a call
-constexpr int kMaxItems = 1 << 25;
+constexpr int kMaxTiles = 1 << 24;       // tiles x KV heads of a call
+constexpr int kMaxItems = 1 << 25;       // (what tc_plan makes of these stays below it)
+constexpr int kSumBlocks = 16;           // query blocks that a thread sums before it puts them away
+constexpr int kItemsPerSm = 512;
 // registers of a thread: 2 x 128 x 168 + 2 x 128 x 48 + 128 x 48 = the launch's 640 x 96
 constexpr int kSoftmaxRegs = 168, kLoadRegs = 48, kOtherRegs = 48;
 
@@ -427,71 +430,82 @@ __global__ void __launch_bounds__(kThreads, 1) weights_tc_kernel(const __grid_co
         const uint64_t scale2 = pack2(a.w.scale, a.w.scale), log2e2 = pack2(kLog2e, kLog2e);
         uint32_t qn = 0;
         while (next()) {
-            float sum0 = 0.f, sum1 = 0.f;
-            for (int b = it.b0; b < it.b1; ++b, ++qn) {
-                const bool both = b >= it.b0_1;
-                // of this warpgroup's columns, those that a position is seen by: of rows that ask, from the first that
-                // stands at it or behind
-                const int from = 128 * b + 64 * wg;
-                const int lo = ((it.t0 + row - it.p0) << lg) - from, hi = min(it.rows - from, 64);
-                // (all of them for all positions of both tiles; what stands past the context is not read)
-                const bool all = (min(it.t0 + 255, it.total - 1) - it.p0) << lg <= from && hi == 64;
-                float v0[64], v1[64];
-                wait(L::SFULL, qn & 1u);
-                if (gave_up) break;
-                tc_fence_after();
-                tld64_nw(ts, v0);
-                if (both) tld64_nw(ts + 128, v1);
-                tld_wait();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(bar(L::SEMPTY));
-                const uint32_t lp = sl + qn % kLStages * 512 + 256 * wg;
-                uint64_t acc0 = 0, acc1 = 0;
-                // weights of two columns of a position, added to acc
-                auto add = [&](float s0, float s1, uint64_t m, uint64_t& acc, int c, int first, auto masked) {
-                    float x0, x1;
-                    unpack2(mul2(fma2(pack2(s0, s1), scale2, m), log2e2), x0, x1);
-                    x0 = ex2_ftz(x0);
-                    x1 = ex2_ftz(x1);
-                    if constexpr (decltype(masked)::value) {
-                        x0 = c >= first && c < hi ? x0 : 0.f;
-                        x1 = c + 1 >= first && c + 1 < hi ? x1 : 0.f;
-                    }
-                    acc = add2(pack2(x0, x1), acc);
-                };
-                auto terms = [&](auto masked, auto two) {
-#pragma unroll
-                    for (int j = 0; j < 16; ++j) {
-                        uint32_t w[4];
-                        lds128(lp + 16 * j, w);
-                        const uint64_t m0 = pack2(__uint_as_float(w[0]), __uint_as_float(w[1]));
-                        const uint64_t m1 = pack2(__uint_as_float(w[2]), __uint_as_float(w[3]));
-                        add(v0[4 * j], v0[4 * j + 1], m0, acc0, 4 * j, lo, masked);
-                        add(v0[4 * j + 2], v0[4 * j + 3], m1, acc0, 4 * j + 2, lo, masked);
-                        if constexpr (decltype(two)::value) {
-                            add(v1[4 * j], v1[4 * j + 1], m0, acc1, 4 * j, lo + (128 << lg), masked);
-                            add(v1[4 * j + 2], v1[4 * j + 3], m1, acc1, 4 * j + 2, lo + (128 << lg), masked);
+            float* const out = a.partial + (int64_t)it.at * 512 + 256 * wg + row;
+            for (int run0 = it.b0; run0 < it.b1; run0 += kSumBlocks) {
+                float sum0 = 0.f, sum1 = 0.f;
+                const int run1 = min(run0 + kSumBlocks, it.b1);
+                for (int b = run0; b < run1; ++b, ++qn) {
+                    const bool both = b >= it.b0_1;
+                    // of this warpgroup's columns, those that a position is seen by: of rows that ask, from the first that
+                    // stands at it or behind
+                    const int from = 128 * b + 64 * wg;
+                    const int lo = ((it.t0 + row - it.p0) << lg) - from, hi = min(it.rows - from, 64);
+                    // (all of them for all positions of both tiles; what stands past the context is not read)
+                    const bool all = (min(it.t0 + 255, it.total - 1) - it.p0) << lg <= from && hi == 64;
+                    float v0[64], v1[64];
+                    wait(L::SFULL, qn & 1u);
+                    if (gave_up) break;
+                    tc_fence_after();
+                    tld64_nw(ts, v0);
+                    if (both) tld64_nw(ts + 128, v1);
+                    tld_wait();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bar(L::SEMPTY));
+                    const uint32_t lp = sl + qn % kLStages * 512 + 256 * wg;
+                    uint64_t acc0 = 0, acc1 = 0;
+                    // weights of two columns of a position, added to acc
+                    auto add = [&](float s0, float s1, uint64_t m, uint64_t& acc, int c, int first, auto masked) {
+                        float x0, x1;
+                        unpack2(mul2(fma2(pack2(s0, s1), scale2, m), log2e2), x0, x1);
+                        x0 = ex2_ftz(x0);
+                        x1 = ex2_ftz(x1);
+                        if constexpr (decltype(masked)::value) {
+                            x0 = c >= first && c < hi ? x0 : 0.f;
+                            x1 = c + 1 >= first && c + 1 < hi ? x1 : 0.f;
                         }
-                    }
-                };
-                if (!both)
-                    terms(std::true_type{}, std::false_type{});
-                else if (all)
-                    terms(std::false_type{}, std::true_type{});
-                else
-                    terms(std::true_type{}, std::true_type{});
-                // (a block's sum by itself: long chains round more)
-                float x, y;
-                unpack2(acc0, x, y);
-                sum0 += x + y;
-                unpack2(acc1, x, y);
-                sum1 += x + y;
+                        acc = add2(pack2(x0, x1), acc);
+                    };
+                    auto terms = [&](auto masked, auto two) {
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) {
+                            uint32_t w[4];
+                            lds128(lp + 16 * j, w);
+                            const uint64_t m0 = pack2(__uint_as_float(w[0]), __uint_as_float(w[1]));
+                            const uint64_t m1 = pack2(__uint_as_float(w[2]), __uint_as_float(w[3]));
+                            add(v0[4 * j], v0[4 * j + 1], m0, acc0, 4 * j, lo, masked);
+                            add(v0[4 * j + 2], v0[4 * j + 3], m1, acc0, 4 * j + 2, lo, masked);
+                            if constexpr (decltype(two)::value) {
+                                add(v1[4 * j], v1[4 * j + 1], m0, acc1, 4 * j, lo + (128 << lg), masked);
+                                add(v1[4 * j + 2], v1[4 * j + 3], m1, acc1, 4 * j + 2, lo + (128 << lg), masked);
+                            }
+                        }
+                    };
+                    if (!both)
+                        terms(std::true_type{}, std::false_type{});
+                    else if (all)
+                        terms(std::false_type{}, std::true_type{});
+                    else
+                        terms(std::true_type{}, std::true_type{});
+                    // (a block's sum by itself: long chains round more)
+                    float x, y;
+                    unpack2(acc0, x, y);
+                    sum0 += x + y;
+                    unpack2(acc1, x, y);
+                    sum1 += x + y;
+                }
+                if (gave_up) break;
+                // (and so are those of 16 blocks: a long run's are added up in memory,
+                // by this thread alone and so always in the same order)
+                if (run0 == it.b0) {
+                    out[0] = sum0;
+                    out[128] = sum1;
+                } else {
+                    atomicAdd(out, sum0);
+                    atomicAdd(out + 128, sum1);
+                }
             }
             if (gave_up) break;
-            float* out = a.partial + (int64_t)it.at * 512 + 256 * wg + row;
-            out[0] = sum0;
-            out[128] = sum1;
         }
     } else if (warp < kMmaWarp) {
         // ------------------------------------------------------------ K
@@ -777,8 +791,8 @@ cudaError_t run(const TcWeightArgs& a, const CUtensorMap& tmq, int ctas, cudaStr
 }  // namespace
 
 // The call's items, tiles and query blocks of an item, from the host's lengths
-// (valid ones, at most kMaxRows query rows).
-TcPlan tc_plan(const sgl_attn_params* p, int window) {
+// (valid ones); SGL_ERR_UNSUPPORTED beyond what the kernels count.
+int tc_plan(const sgl_attn_params* p, int window, TcPlan* plan) {
     const int G = p->num_qo_heads / p->num_kv_heads;
     auto size = [&](int r, int64_t& tiles, int64_t& blocks) {
         const int64_t e = p->host_extend_lens[r], ask = window > 0 ? std::min<int64_t>(window, e) : e;
@@ -786,14 +800,25 @@ TcPlan tc_plan(const sgl_attn_params* p, int window) {
         blocks = (ask * G + 127) / 128;
     };
     TcPlan x{0, 0, 1};
-    int64_t units = 0, tiles, blocks;
+    int64_t rows = 0, units = 0, most = 1, tiles, blocks;
     for (int r = 0; r < p->batch; ++r) {
+        rows += p->host_extend_lens[r];
+        if ((int64_t)p->host_prefix_lens[r] + p->host_extend_lens[r] > kMaxLen || rows > kMaxRows) return SGL_ERR_UNSUPPORTED;
         size(r, tiles, blocks);
         x.tiles += tiles;
         units += tiles * blocks * p->num_kv_heads;
+        most = std::max(most, blocks);
+        if (x.tiles * p->num_kv_heads > kMaxTiles) return SGL_ERR_UNSUPPORTED;
     }
-    // an item for each SM, of at most 16 query blocks
-    x.run = (int)std::min<int64_t>(std::max<int64_t>((units + 151) / 152, 1), 16);
+    // An item for each SM, of at most 16 query blocks while an SM has up to 512
+    // items, beyond that as many as keep it at 512: an item's sums take 2 KB of
+    // workspace however long its run is, so that what a call needs grows with its
+    // positions (2 KB for 256 of them and a KV head, at least) and not with rows x
+    // positions (a prompt of 131072 tokens, 64/8 heads: 84 MB; runs of 16 took 2.1 GB).
+    constexpr int64_t kSms = 152;
+    x.run = (int)std::min(std::max<int64_t>(std::clamp<int64_t>((units + kSms - 1) / kSms, 1, kSumBlocks),
+                                            (units + kItemsPerSm * kSms - 1) / (kItemsPerSm * kSms)),
+                          std::max<int64_t>(most, kSumBlocks));
     const int lg = 31 - __builtin_clz((unsigned)G);
     for (int r = 0; r < p->batch; ++r) {
         size(r, tiles, blocks);
@@ -802,11 +827,12 @@ TcPlan tc_plan(const sgl_attn_params* p, int window) {
         x.items += p->num_kv_heads * items_of_head<int64_t>(p->host_prefix_lens[r] + e - ask, tiles,
                                                             (blocks + x.run - 1) / x.run, x.run, lg, &whole);
     }
-    return x;
+    if (x.items > kMaxItems) return SGL_ERR_UNSUPPORTED;
+    *plan = x;
+    return SGL_OK;
 }
 
 int launch_weights_tc(const WeightArgs& w, int kv, int d, const TcPlan& plan, float* partial, cudaStream_t s) {
-    if (plan.items > kMaxItems || plan.tiles > INT32_MAX / 64 || w.n_rows > kMaxRows) return -1;
     TcWeightArgs a{w, partial, (int)plan.items, plan.run};
     if (plan.items > 0) {
         CUtensorMap tmq{};

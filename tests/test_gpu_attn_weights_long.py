@@ -1,0 +1,57 @@
+"""Attention weights of long chunks against float64 at sampled positions: log-sum-exps are any, so that a position's score
+is a sum over the rows that see it and no other position is needed for it."""
+
+import numpy as np
+import pytest
+import torch
+
+import radixattention_prefix_shared_radix_gb300 as sgl
+from tests.test_gpu_attn_weights import Cache, _run
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    from radixattention_prefix_shared_radix_gb300 import build
+    build.build()
+
+
+def _want(c, q, lse, pre, ext, at, r, adds):
+    """float64 scores of request r's positions `at`, and a bound: that of oracle/evict.py for each weight, and `adds`
+    additions in sequence."""
+    first = int(sum(ext[:r]))
+    x, l = q[first:first + ext[r]].cuda(), lse[first:first + ext[r]].cuda().double()
+    k = torch.from_numpy(c.keys(r, int(pre[r] + ext[r]))[at]).cuda()
+    at = torch.from_numpy(at).cuda()
+    seen = at[None] <= int(pre[r]) + torch.arange(int(ext[r]), device="cuda")[:, None]
+    sm = c.d ** -0.5
+    want, off = (torch.zeros(len(at), dtype=torch.float64, device="cuda") for _ in "ab")
+    for h in range(c.hq):
+        kh, xh = k[:, h * c.hkv // c.hq], x[:, h].double()
+        s = sm * xh @ kh.T - l[:, h, None]
+        size = sm * xh.abs() @ kh.abs().T
+        w = s.exp().masked_fill_(~seen, 0.0)
+        want += w.sum(0)
+        off += (w * ((size * (c.d + 12) + s.abs()) * 2.0 ** -24 + 2.0 ** -21)).sum(0)
+    return want.cpu().numpy(), (off + want * adds * 2.0 ** -24).cpu().numpy()
+
+
+@pytest.mark.parametrize("kind,d", [("bf16", 128), ("fp8", 64), ("fp4", 128)])
+def test_runs_of_more_than_sixteen_query_blocks(kind, d):
+    """64 query heads over 8 KV heads and 27000 tokens: runs of 18 blocks, whose sums a thread adds up in memory.  In
+    sequence: 32 columns and 2 of a block, 16 blocks, 2 parts of a run, 94 runs of 8 heads by four threads, 3.  (A run
+    that were lost or added twice would be a part in a hundred or more.)"""
+    pre, ext = np.array([0, 900]), np.array([27000, 300])
+    c = Cache(kind, pre + ext, 64, 8, d, seed=d)
+    q = c.queries(int(ext.sum()))
+    lse = 6 + torch.randn(len(q), 64, generator=torch.Generator().manual_seed(1))
+    got = _run(c, q, lse, pre, ext, 0, None, 1.0, False)
+    rng = np.random.default_rng(2)
+    for r, n in enumerate(pre + ext):
+        edges = np.concatenate([[0, 1, 127, 128, 255, 256, n - 130, n - 129, n - 128, n - 2, n - 1]])
+        at = np.unique(np.concatenate([edges, rng.integers(0, n, 80)]))
+        want, tol = _want(c, q, lse, pre, ext, at, r, 34 + 16 + 2 + 94 * 2 + 3)
+        err = np.abs(got[r, at] - want)
+        assert (err <= tol).all(), ((err / tol).max(), at[err > tol][:4])
+    assert np.array_equal(_run(c, q, lse, pre, ext, 0, None, 1.0, False), got)     # (in the same order again)
