@@ -472,14 +472,14 @@ constexpr DecodeKernel decode_kernels[2][4] = {
     {decode_kernel<64, kKvF32>(), decode_kernel<64, 0>(), decode_kernel<64, 1>(), decode_kernel<64, 2>()},
     {decode_kernel<128, kKvF32>(), decode_kernel<128, 0>(), decode_kernel<128, 1>(), decode_kernel<128, 2>()}};
 
-cudaError_t launch_decode(const DecodeKernel& k, const WeightArgs& a, cudaStream_t s) {
+cudaError_t launch_decode(const DecodeKernel& k, const WeightArgs& a, int sms, cudaStream_t s) {
     // a warp per KV head up to eight, else several per head
     const int hw = std::min(a.Hkv, 8), nsub = 8 / hw, tp = k.positions * nsub;
     cudaLaunchAttribute pdl[1];
     pdl[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     pdl[0].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)std::min<int64_t>(152 * k.ctas, a.B * (((int64_t)a.lim + tp - 1) / tp)));
+    cfg.gridDim = dim3((unsigned)std::min<int64_t>(sms * k.ctas, a.B * (((int64_t)a.lim + tp - 1) / tp)));
     cfg.blockDim = dim3((unsigned)(hw * nsub * 32));
     cfg.stream = s;
     cfg.attrs = pdl;
@@ -583,7 +583,7 @@ int sgl_attn_weights(const void* q, const float* lse, const void* k_pool, const 
     auto s = reinterpret_cast<cudaStream_t>(stream);
     if (!extend_lens) {
         const auto* kernel = &decode_kernels[d == 128][kind];
-        return cuda_status(launch_decode(*kernel, a, s));
+        return cuda_status(launch_decode(*kernel, a, target_sms(params), s));
     }
     if (kind != SGL_DTYPE_F32) {
         if (ws_bytes < sgl::kWsAlign + (size_t)plan.items * 2048) return SGL_ERR_WORKSPACE;

@@ -2,6 +2,8 @@
 // share: their arguments, what a request asks, and a weight.
 #pragma once
 
+#include <algorithm>
+
 #include "device_common.cuh"
 #include "fp4.cuh"
 
@@ -67,7 +69,10 @@ __device__ __forceinline__ float weight_of(float product, float scale, float m) 
 struct TcPlan {
     int64_t items, tiles;                // work items; tiles of 256 positions
     int run;                             // query blocks of an item
+    int sms;                             // SMs to fill
 };
+// params->num_sms, or the device's SMs (bounded, so that products with it stay small)
+inline int target_sms(const sgl_attn_params* p) { return std::min(query_num_sms(p->num_sms), 4096); }
 int tc_plan(const sgl_attn_params* params, int window, TcPlan* plan);
 // 0 or a cudaError_t
 int launch_weights_tc(const WeightArgs& args, int kv, int head_dim, const TcPlan& plan, float* partial, cudaStream_t s);

@@ -799,7 +799,7 @@ int tc_plan(const sgl_attn_params* p, int window, TcPlan* plan) {
         tiles = (p->host_prefix_lens[r] + e + 255) / 256;
         blocks = (ask * G + 127) / 128;
     };
-    TcPlan x{0, 0, 1};
+    TcPlan x{0, 0, 1, target_sms(p)};
     int64_t rows = 0, units = 0, most = 1, tiles, blocks;
     for (int r = 0; r < p->batch; ++r) {
         rows += p->host_extend_lens[r];
@@ -815,9 +815,9 @@ int tc_plan(const sgl_attn_params* p, int window, TcPlan* plan) {
     // workspace however long its run is, so that what a call needs grows with its
     // positions (2 KB for 256 of them and a KV head, at least) and not with rows x
     // positions (a prompt of 131072 tokens, 64/8 heads: 84 MB; runs of 16 took 2.1 GB).
-    constexpr int64_t kSms = 152;
-    x.run = (int)std::min(std::max<int64_t>(std::clamp<int64_t>((units + kSms - 1) / kSms, 1, kSumBlocks),
-                                            (units + kItemsPerSm * kSms - 1) / (kItemsPerSm * kSms)),
+    const int64_t sms = x.sms;
+    x.run = (int)std::min(std::max<int64_t>(std::clamp<int64_t>((units + sms - 1) / sms, 1, kSumBlocks),
+                                            (units + kItemsPerSm * sms - 1) / (kItemsPerSm * sms)),
                           std::max<int64_t>(most, kSumBlocks));
     const int lg = 31 - __builtin_clz((unsigned)G);
     for (int r = 0; r < p->batch; ++r) {
@@ -837,7 +837,7 @@ int launch_weights_tc(const WeightArgs& w, int kv, int d, const TcPlan& plan, fl
     if (plan.items > 0) {
         CUtensorMap tmq{};
         if (const int e = encode_query_map(w.q, w.n_rows, w.Hq, d, w.G, 128 / w.G, &tmq)) return e;
-        const int ctas = (int)std::min<int64_t>(152, plan.items);
+        const int ctas = (int)std::min<int64_t>(plan.sms, plan.items);
         cudaError_t e;
         if (d == 64)
             e = kv == 0 ? run<64, 0>(a, tmq, ctas, s) : kv == 1 ? run<64, 1>(a, tmq, ctas, s) : run<64, 2>(a, tmq, ctas, s);

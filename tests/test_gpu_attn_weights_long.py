@@ -6,7 +6,7 @@ import pytest
 import torch
 
 import radixattention_prefix_shared_radix_gb300 as sgl
-from tests.test_gpu_attn_weights import Cache, _run
+from tests.test_gpu_attn_weights import Cache, KINDS, _check, _run
 
 pytestmark = pytest.mark.gpu
 
@@ -55,3 +55,14 @@ def test_runs_of_more_than_sixteen_query_blocks(kind, d):
         err = np.abs(got[r, at] - want)
         assert (err <= tol).all(), ((err / tol).max(), at[err > tol][:4])
     assert np.array_equal(_run(c, q, lse, pre, ext, 0, None, 1.0, False), got)     # (in the same order again)
+
+
+@pytest.mark.parametrize("kind", list(KINDS))
+@pytest.mark.parametrize("num_sms", [1, 5, 400])
+def test_work_cut_for_other_numbers_of_sms(kind, num_sms):
+    pre, ext = np.array([0, 300, 40]), np.array([290, 70, 0])
+    c = Cache(kind, pre + ext, 32, 8, 64, seed=5)
+    _check(c, pre, ext, num_sms=num_sms)
+    lens = np.array([300, 0, 1, 1000, 65])
+    has = (lens > 0).astype(np.int64)
+    _check(Cache(kind, lens, 8, 8, 64, seed=6), lens - has, has, decode=True, num_sms=num_sms)

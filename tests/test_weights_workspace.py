@@ -33,7 +33,7 @@ def _both(p, window=0):
 @pytest.mark.parametrize("hq,hkv", [(64, 8), (32, 8), (8, 8), (8, 1)])
 @pytest.mark.parametrize("dtype", [sgl.SGL_DTYPE_BF16, sgl.SGL_DTYPE_BF16_FP8KV, sgl.SGL_DTYPE_BF16_FP4KV])
 def test_it_grows_with_positions_alone(pre, ext, hq, hkv, dtype):
-    """2 KB for 256 positions of a request and KV head, and 160 MB besides, however many rows ask."""
+    """2 KB for 256 positions of a request and KV head, and 160 MB (1 MiB an SM) besides, however many rows ask."""
     for window in (0, 4096):
         st, n, _ = _both(_params(pre, ext, hq, hkv, dtype), window)
         tiles = sum(-(-(a + b) // 256) for a, b in zip(pre, ext))
@@ -70,3 +70,16 @@ def test_limits_over_fp32_pools():
     assert st == -3 and call == -3
     st, _, call = _both(_params([1 << 26], [1], dtype=f32))
     assert st == -3 and call == -3
+
+
+def test_work_is_cut_for_the_sms_asked_for():
+    """num_sms as in the attention calls' planning; 0 and 152 are one on the device that the kernels are for."""
+    def items(pre, ext, n):          # of a KV head
+        return (sgl.sgl_attn_weights_workspace_bytes(_params([pre], [ext], num_sms=n)) - 256) / 2048 / 8
+    # 13 query blocks for each of two tiles: 208 of all heads, two an SM of 152, 13 an SM of 16
+    assert [items(300, 200, n) for n in (0, 152, 16, 1)] == [14, 14, 2, 2]
+    # 57 blocks for each of five tiles, four runs of 15 (152 SMs) or of 16; rows see the last three from block 13, 29
+    # and 45 on: runs 0, 1 and 3 of 15, or 0, 1 and 2 of 16
+    assert [items(300, 900, n) for n in (0, 152, 16, 1)] == [16, 16, 17, 17]
+    long = {n: sgl.sgl_attn_weights_workspace_bytes(_params([0], [1 << 20], num_sms=n)) for n in (8, 152, 2 ** 31 - 1)}
+    assert long[8] <= 256 + 2048 * 8 * 4096 + (8 << 20) and long[8] < long[152] < long[2 ** 31 - 1] < 1 << 33
