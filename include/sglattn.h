@@ -738,14 +738,16 @@ int sgl_attn_weights_workspace_bytes(const sgl_attn_params* params, int32_t wind
  * weights and their sums are fp32, always added in the same order.  A slot
  * outside the pool gives its token no weight and sets bit 0 of the workspace's
  * error word; a length outside the table (or beyond 2^26) sets bit 1 and leaves
- * the request's scores as they were.  A prefix that requests share is read once
+ * the request's scores as they were.  So do device lengths of a chunk call for
+ * which the work that the host copies planned has no room (those of requests
+ * behind such a one may stay as they were too).  A prefix that requests share is read once
  * for each of them.  params->num_sms (at most 4096 count) is the number of SMs
  * that the work is cut for, for the call as for the size of its workspace; with
  * another one the sums of a chunk may be formed in another order.
  * workspace: device, 256-byte aligned, sgl_attn_weights_workspace_bytes (a
  * decode plan's serves in the decode form); calls that may overlap on the GPU
  * need one each.  Can be captured; the decode form follows lens at replay, a
- * captured chunk keeps the lengths that it was captured with.
+ * captured chunk the lengths that fit into what it was captured with.
  * ["SGLang 深度解读" "5. Attention 层": attention over req_to_token rows, whose
  * weights these are] */
 int sgl_attn_weights(const void* q, const float* lse, const void* k_pool, const int32_t* req_to_token, int64_t ld,

@@ -55,6 +55,10 @@ __global__ void __launch_bounds__(256) weights_chunk_f32(const __grid_constant__
     }
     __syncthreads();
     const Asked x = asked(a, r, before_s, tid == 0 && t0 == 0);
+    if (x.total > (int)gridDim.x * T) {                  // (longer than the host's longest: its scores stay as they were)
+        if (tid == 0 && t0 == 0) atomicOr(a.err, 2u);
+        return;
+    }
     if (t0 >= x.total) return;                           // (the whole cluster)
     if (tid < T) {
         int32_t slot = -1;

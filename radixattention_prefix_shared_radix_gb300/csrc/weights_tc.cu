@@ -140,12 +140,15 @@ __host__ __device__ __forceinline__ int64_t items_of_head(Int p0, Int tiles, Int
 
 // Walks the batch 32 requests at a time, a lane per request; find() returns the
 // request of an item (by_tile: of a tile).  Items must not fall from call to call.
+// (Lengths may be other ones than the host planned for: sums of the items past
+// the planned ones stop at kPast, so that they cannot wrap.)
+constexpr int kPast = 1 << 29;
 struct Walk {
     int b = 0;                           // first request of the 32
     int64_t rows = 0;                    // query rows before them
     int items = 0, tiles = 0;            // items and tiles before them
     // this lane's request: its lengths; items and tiles up to and with it; rows before it
-    int len, ext, up_items, up_tiles;
+    int len, ext, total, up_items, up_tiles;
     int64_t before;
     int n_items, n_tiles, n_rows;        // of the 32
     bool filled = false;
@@ -165,6 +168,7 @@ struct Walk {
         before = rows + se - e;
         n_rows = __shfl_sync(0xffffffffu, se, 31);
         const Request q = request(ta, len, ext, before);
+        total = q.x.total;
         up_items = q.head * a.Hkv;
         up_tiles = q.tiles;
 #pragma unroll
@@ -206,7 +210,7 @@ struct Walk {
                 q.first_tile = tiles + __shfl_sync(0xffffffffu, up_tiles, l) - q.tiles;
                 return true;
             }
-            items += n_items;
+            items = min(items + n_items, kPast);
             tiles += n_tiles;
             rows += n_rows;
             b += 32;
@@ -214,7 +218,22 @@ struct Walk {
             if (b >= a.w.B) return false;
         }
     }
+    // whether the tables hold all lengths, and what was planned all their items and tiles
+    static __device__ __forceinline__ bool fits(const TcWeightArgs& a, int64_t planned_tiles) {
+        Walk w;
+        int64_t items = 0, tiles = 0;
+        bool bad = false;
+        for (; w.b < a.w.B; w.b += 32) {
+            w.fill(a);
+            bad |= (w.len | w.ext) != 0 && w.total == 0;
+            items += w.n_items;
+            tiles += w.n_tiles;
+            w.rows += w.n_rows;
+        }
+        return !__any_sync(0xffffffffu, bad) && items <= a.items && tiles <= planned_tiles;
+    }
 };
+static_assert((int64_t)kPast + 32 * (int64_t)kMaxItems <= INT32_MAX, "items of 32 requests, and of those before them");
 
 // An item as its warps see it (64 bytes of shared memory).
 struct alignas(16) Item {
@@ -727,30 +746,21 @@ __global__ void __launch_bounds__(256 * kJoin, 2) weights_join(const __grid_cons
             runs = ok ? max(q.runs - first_block<int>(q.x.p0, 256 * tile, lg) / a.run, 0) : 0;
         }
         __syncwarp();
-        if (blockIdx.x == 0) {           // lengths that the tables do not hold
-            int64_t before = 0;
-            for (int b = 0; b < a.w.B; b += 32) {
-                const int r = b + tid, e = r < a.w.B ? min(max(__ldg(a.w.ext + r), 0), kMaxRows) : 0;
-                int64_t s = e;
-                for (int o = 1; o < 32; o <<= 1) {
-                    const int64_t y = __shfl_up_sync(0xffffffffu, s, o);
-                    if (tid >= o) s += y;
-                }
-                if (r < a.w.B) asked(a.w, r, before + s - e, true);
-                before += __shfl_sync(0xffffffffu, s, 31);
-            }
-        }
+    } else if (threadIdx.x < 64 && blockIdx.x == 0) {
+        if (!Walk::fits(a, gridDim.x) && threadIdx.x == 32) atomicOr(a.w.err, 2u);
     }
     __syncthreads();
     if (!found) return;
+    const int n = runs * a.w.Hkv, head = sr.head;
+    // (a request that what was planned has no room for: its scores stay as they were)
+    if (sr.first + head * a.w.Hkv > a.items || sr.first_tile + sr.tiles > (int)gridDim.x) return;
     const int pos = 256 * ((int)blockIdx.x - sr.first_tile) + tid, total = sr.x.total, r = sr.r;
     const bool mine = g == 0 && pos < total, had = mine && a.w.in && pos < sr.x.fresh;
     const int64_t at = (int64_t)r * a.w.scores_ld + pos;
     const int slot = mine ? __ldg(a.w.r2t + (int64_t)r * a.w.ld + pos) : 0;
     const float old = had ? a.w.in[at] : 0.f;
     float s = 0.f;
-    const int n = runs * a.w.Hkv, head = sr.head;
-    if (pos < total && sr.first + head * a.w.Hkv <= a.items) {
+    if (pos < total) {
 #pragma unroll 4
         for (int i = g; i < n; i += kJoin) {
             const int h = i / runs;
