@@ -72,10 +72,13 @@ __global__ void __launch_bounds__(256) weights_chunk_f32(const __grid_constant__
         slots[tid] = slot;
     }
     const int py = tid >> 4, rx = tid & 15;              // positions py + 16 i, rows rx + 16 j
-    float sum[4] = {0.f, 0.f, 0.f, 0.f};
-    const int rows = x.ask * a.G;
+    // (the sums of eight blocks, 32 weights, are added with what each addition
+    // rounds off kept: a position's rows may be many thousand blocks)
+    float sum[4] = {0.f, 0.f, 0.f, 0.f}, off[4] = {0.f, 0.f, 0.f, 0.f}, now[4] = {0.f, 0.f, 0.f, 0.f};
+    const int lg = 31 - __clz(a.G);
+    const int rows = x.ask << lg;
     // (rows before the one that first sees the tile are passed over)
-    const int row0 = max(t0 - x.p0, 0) * a.G & ~(T - 1);
+    const int row0 = max(t0 - x.p0, 0) << lg & ~(T - 1);
     for (int h = part; h < a.Hkv; h += C) {
         __syncthreads();
         for (int i = tid; i < T * (D / 4); i += 256) {
@@ -90,12 +93,12 @@ __global__ void __launch_bounds__(256) weights_chunk_f32(const __grid_constant__
                 const int y = i / (D / 4), c = i - y * (D / 4), row = b + y;
                 float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
                 if (row < rows)
-                    v = reinterpret_cast<const float4*>(a.q)[((x.row + row / a.G) * a.Hq + h * a.G + row % a.G) * (D / 4) + c];
+                    v = reinterpret_cast<const float4*>(a.q)[((x.row + (row >> lg)) * a.Hq + (h << lg) + (row & (a.G - 1))) * (D / 4) + c];
                 *reinterpret_cast<float4*>(&sq[y * RS + 4 * c]) = v;
             }
             if (tid < T) {
                 const int row = b + tid;
-                sl[tid] = row < rows ? minus_lse(a.lse[(x.row + row / a.G) * a.Hq + h * a.G + row % a.G]) : 0.f;
+                sl[tid] = row < rows ? minus_lse(a.lse[(x.row + (row >> lg)) * a.Hq + (h << lg) + (row & (a.G - 1))]) : 0.f;
             }
             __syncthreads();
             float dot[4][4];
@@ -119,16 +122,26 @@ __global__ void __launch_bounds__(256) weights_chunk_f32(const __grid_constant__
             }
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                const int row = b + rx + 16 * j, last = x.p0 + row / a.G;        // (a row sees positions up to its own)
+                const int row = b + rx + 16 * j, last = x.p0 + (row >> lg);        // (a row sees positions up to its own)
                 const float m = sl[rx + 16 * j];
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
-                    if (row < rows && t0 + py + 16 * i <= last) sum[i] += weight_of(dot[i][j], a.scale, m);
+                    if (row < rows && t0 + py + 16 * i <= last) now[i] += weight_of(dot[i][j], a.scale, m);
+            }
+            if ((b & (7 * T)) == 7 * T || b + T >= rows) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float s = sum[i] + now[i], y = s - sum[i];
+                    off[i] += (sum[i] - (s - y)) + (now[i] - y);
+                    sum[i] = s;
+                    now[i] = 0.f;
+                }
             }
         }
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
+        if (off[i] == off[i]) sum[i] += off[i];          // (an infinite sum stays one)
 #pragma unroll
         for (int o = 1; o < 16; o <<= 1) sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], o);
         if (rx == 0) sums[py + 16 * i] = sum[i];

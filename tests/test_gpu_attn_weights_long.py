@@ -66,3 +66,21 @@ def test_work_cut_for_other_numbers_of_sms(kind, num_sms):
     lens = np.array([300, 0, 1, 1000, 65])
     has = (lens > 0).astype(np.int64)
     _check(Cache(kind, lens, 8, 8, 64, seed=6), lens - has, has, decode=True, num_sms=num_sms)
+
+
+@pytest.mark.parametrize("kind", list(KINDS))
+@pytest.mark.parametrize("lse", [3.3, 5.1, 7.7])
+def test_thousands_of_equal_weights(kind, lse):
+    """Keys of zeros: 9216 tokens of 8 heads give a position up to 73728 equal weights, whose roundings would all go one
+    way in a long chain of additions (4608 in a row: 5e-5 at 5.1).  A weight is off by 2^-24 of its exponent twice and
+    by 2^-21; in sequence fp32 pools add 32 weights, 4 lanes and 8 CTAs with three roundings more, the others 34 of a block,
+    16 blocks, 36 runs by four threads and 3."""
+    n = 9216
+    c = Cache(kind, [n], 8, 1, 64, seed=1, spread=0.0)
+    q = c.queries(n)
+    l = torch.full((n, 8), lse)
+    got = _run(c, q, l, np.array([0]), np.array([n]), 0, None, 1.0, False)[0]
+    want = 8 * np.arange(n, 0, -1) * np.exp(-np.float64(np.float32(lse)))
+    adds = 32 + 4 + 8 + 3 if kind == "f32" else 34 + 16 + 9 + 3
+    err = np.abs(got / want - 1)
+    assert err.max() <= lse * 2.0 ** -23 + 2.0 ** -21 + adds * 2.0 ** -24, err.max()
