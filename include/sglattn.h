@@ -712,7 +712,9 @@ int sgl_attn_weights_workspace_bytes(const sgl_attn_params* params, int32_t wind
  * but the new tokens' (chunks); those begin at 0.
  *   q, lse       device [N, Hq, d] and fp32 [N, Hq]: the queries of an attention
  *                call and the log-sum-exp that it gave (a row at -inf adds
- *                nothing)
+ *                nothing, whatever its query holds; over pools other than fp32,
+ *                a key that is infinite or NaN makes its own token's score NaN
+ *                wherever a chunk's row at -inf stands at the token or behind)
  *   k_pool       as in the attention call (a 4-bit or E4M3 pool's k_scale from
  *                params; v_scale is not used but checked)
  *   lens, extend_lens  device int32 [B].  extend_lens NULL (decode): row r is

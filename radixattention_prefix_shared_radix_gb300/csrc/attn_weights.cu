@@ -98,7 +98,7 @@ __global__ void __launch_bounds__(256) weights_chunk_f32(const __grid_constant__
             }
             if (tid < T) {
                 const int row = b + tid;
-                sl[tid] = row < rows ? minus_lse(a.lse[(x.row + (row >> lg)) * a.Hq + (h << lg) + (row & (a.G - 1))]) : 0.f;
+                sl[tid] = row < rows ? a.lse[(x.row + (row >> lg)) * a.Hq + (h << lg) + (row & (a.G - 1))] : -INFINITY;
             }
             __syncthreads();
             float dot[4][4];
@@ -123,10 +123,10 @@ __global__ void __launch_bounds__(256) weights_chunk_f32(const __grid_constant__
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 const int row = b + rx + 16 * j, last = x.p0 + (row >> lg);        // (a row sees positions up to its own)
-                const float m = sl[rx + 16 * j];
+                const float l = sl[rx + 16 * j];         // (-infinity: no row, or one that adds nothing)
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
-                    if (row < rows && t0 + py + 16 * i <= last) now[i] += weight_of(dot[i][j], a.scale, m);
+                    if (l != -INFINITY && t0 + py + 16 * i <= last) now[i] += weight_of(dot[i][j], a.scale, -l);
             }
             if ((b & (7 * T)) == 7 * T || b + T >= rows) {
 #pragma unroll
@@ -321,7 +321,7 @@ __global__ void __launch_bounds__(kStreamThreads, Stream<D, KV>::CTAS) weights_d
     // the query rows of KV head h: B fragments (row g of eight) of the same
     // pieces that the keys come in, and the log-sum-exps of columns 2 t, 2 t + 1
     uint32_t qf[F32 ? 1 : QW];
-    float l0, l1;
+    float l0, l1;                                    // (-infinity: no row, or one that adds nothing)
     auto load_query = [&](int r2, int h) {
         const int64_t row = (int64_t)r2 * a.Hq + h * a.G;
         if constexpr (F32) {
@@ -329,8 +329,8 @@ __global__ void __launch_bounds__(kStreamThreads, Stream<D, KV>::CTAS) weights_d
             for (int i = lane; i < a.G * (D / 4); i += 32)
                 reinterpret_cast<float4*>(&sq[warp * 8 * D])[i] = __ldg(reinterpret_cast<const float4*>(a.q) + row * (D / 4) + i);
             __syncwarp();
-            l0 = t < a.G ? minus_lse(__ldg(a.lse + row + t)) : 0.f;
-            l1 = t + 4 < a.G ? minus_lse(__ldg(a.lse + row + t + 4)) : 0.f;
+            l0 = t < a.G ? __ldg(a.lse + row + t) : -INFINITY;
+            l1 = t + 4 < a.G ? __ldg(a.lse + row + t + 4) : -INFINITY;
         } else {
             const uint4* q = reinterpret_cast<const uint4*>(static_cast<const bf16*>(a.q) + (row + min(g, a.G - 1)) * D);
             uint32_t bad = 0;
@@ -342,9 +342,9 @@ __global__ void __launch_bounds__(kStreamThreads, Stream<D, KV>::CTAS) weights_d
 #pragma unroll
                 for (int j = 0; j < 4; ++j) qf[4 * i + j] = KV == 0 ? w[j] : bf16x2_to_f16x2_chk(w[j], bad);
             }
-            if (bad && g < a.G) atomicOr(a.err, kErrQRange);
-            l0 = 2 * t < a.G ? minus_lse(__ldg(a.lse + row + 2 * t)) : 0.f;
-            l1 = 2 * t + 1 < a.G ? minus_lse(__ldg(a.lse + row + 2 * t + 1)) : 0.f;
+            if (bad && g < a.G && __ldg(a.lse + row + g) != -INFINITY) atomicOr(a.err, kErrQRange);
+            l0 = 2 * t < a.G ? __ldg(a.lse + row + 2 * t) : -INFINITY;
+            l1 = 2 * t + 1 < a.G ? __ldg(a.lse + row + 2 * t + 1) : -INFINITY;
         }
     };
     load_slots(r, tile, len);
@@ -439,12 +439,12 @@ __global__ void __launch_bounds__(kStreamThreads, Stream<D, KV>::CTAS) weights_d
                 load_keys(h + hw, tile, len);
             else if (at + 1 < end)
                 load_keys(wh, tile2, len2);
-            // (columns that are no query rows may hold 0 times an infinity)
-            const bool v0 = F32 ? t < a.G : 2 * t < a.G, v1 = F32 ? t + 4 < a.G : 2 * t + 1 < a.G;
+            // (columns that add nothing may hold infinities and NaN)
+            const bool v0 = l0 != -INFINITY, v1 = l1 != -INFINITY;
 #pragma unroll
             for (int n = 0; n < NR; ++n) {
                 const float x0 = F32 ? c[n][0] : c[n / 2][2 * (n & 1)], x1 = F32 ? c[n][1] : c[n / 2][2 * (n & 1) + 1];
-                const float w0 = weight_of(x0, a.scale, l0), w1 = weight_of(x1, a.scale, l1);
+                const float w0 = weight_of(x0, a.scale, -l0), w1 = weight_of(x1, a.scale, -l1);
                 if (now >> n & 1u) sum[n] += (v0 ? w0 : 0.f) + (v1 ? w1 : 0.f);
             }
         }

@@ -56,7 +56,8 @@ __device__ __forceinline__ Asked asked(const WeightArgs& a, int r, int64_t befor
 }
 
 // What a row adds to its products' scale before the exponential: minus its
-// log-sum-exp, and -infinity for a row that saw nothing (it adds no weight).
+// log-sum-exp, and -infinity for a row that saw nothing (which is passed over
+// besides: its products may be infinite or NaN).
 __device__ __forceinline__ float minus_lse(float l) { return l == -INFINITY ? l : -l; }
 // exp(s + m): the difference first, rounded once, then to base 2 (in base 2
 // from the start the log-sum-exp itself would be rounded, by up to 2^-20)

@@ -93,7 +93,8 @@ struct Lay {
     static constexpr int QTILE = 128 * D * 2;
     static constexpr int OFF_K = QSTAGES * QTILE;
     static constexpr int OFF_L = OFF_K + 2 * KTILES * 128 * STRIDE;  // minus the log-sum-exps of a block's columns
-    static constexpr int OFF_ITEM = OFF_L + kLStages * 512;
+    static constexpr int OFF_NONE = OFF_L + kLStages * 512;      // those of rows that add nothing: whether there are any; bits
+    static constexpr int OFF_ITEM = OFF_NONE + kLStages * 32;
     static constexpr int OFF_BAR = OFF_ITEM + kItems * 64;
     static constexpr int OFF_TMEM = OFF_BAR + 40 * 8;
     static constexpr int END = OFF_TMEM + 16;
@@ -607,9 +608,24 @@ __global__ void __launch_bounds__(kThreads, 1) weights_tc_kernel(const __grid_co
             uint32_t n = 0, st = 0, qpar = 0, sn = 0;
             for (; next(); ++n) {
                 const uint32_t ta = tbase + (n & 1u) * 128;
-                wait(L::AFULL + (n & 1u), (n >> 1) & 1u);
                 for (int b = it.b0; b < it.b1; ++b, ++sn) {
                     wait(L::QFULL + st, qpar);
+                    if (ld_shared_s32(sq + L::OFF_NONE + sn % kLStages * 32) && !gave_up) {
+                        // Rows at -infinity add nothing, whatever they hold: zeros take their
+                        // place (0 times the scale and -infinity give no weight).  Here, where
+                        // keys are waited for, and not in the terms: to pass their columns over
+                        // there cost 2 to 7% of every call.
+                        for (int c = lane; c < 128; c += 32) {
+                            const uint32_t none = ld_shared_s32(sq + L::OFF_NONE + sn % kLStages * 32 + 16 + 4 * (c & 3));
+                            if (!(none >> (c >> 2) & 1u)) continue;
+                            for (int x = 0; x < D / 64; ++x)
+                                for (int j = 0; j < 128; j += 16)    // (whole rows: the swizzle stays within them)
+                                    st_shared_v4(sq + st * L::QTILE + x * kQRegion + c * 128 + j, 0, 0, 0, 0);
+                        }
+                        fence_proxy_async_smem();
+                        __syncwarp();
+                    }
+                    if (b == it.b0) wait(L::AFULL + (n & 1u), (n >> 1) & 1u);
                     wait(L::SEMPTY, (sn & 1u) ^ 1u);
                     if (gave_up) break;
                     tc_fence_after();
@@ -651,7 +667,7 @@ __global__ void __launch_bounds__(kThreads, 1) weights_tc_kernel(const __grid_co
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const int rho = 128 * b + 4 * lane + i;
-                    nx[i] = -INFINITY;
+                    nx[i] = INFINITY;                // (no row: masked)
                     if (rho < it.rows)
                         nx[i] = __ldg(a.w.lse + ((int64_t)it.row + (rho >> lg)) * a.w.Hq + (it.h << lg) + (rho & (a.w.G - 1)));
                 }
@@ -681,6 +697,16 @@ __global__ void __launch_bounds__(kThreads, 1) weights_tc_kernel(const __grid_co
                 static_assert(kLStages >= L::QSTAGES + 2, "log-sum-exp stages");
                 st_shared_v4(sl + qn % kLStages * 512 + 16 * lane, __float_as_uint(minus_lse(y[0])),
                              __float_as_uint(minus_lse(y[1])), __float_as_uint(minus_lse(y[2])), __float_as_uint(minus_lse(y[3])));
+                // (bit `lane` of word i: column 4 lane + i)
+                const uint32_t np = sq + L::OFF_NONE + qn % kLStages * 32;
+                const int some = __any_sync(0xffffffffu, fminf(fminf(y[0], y[1]), fminf(y[2], y[3])) == -INFINITY);
+                if (some) {
+                    uint32_t none[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) none[i] = __ballot_sync(0xffffffffu, y[i] == -INFINITY);
+                    if (lane == 0) st_shared_v4(np + 16, none[0], none[1], none[2], none[3]);
+                }
+                if (lane == 0) st_shared_s32(np, some);
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar(L::QFULL + st));
             }
