@@ -674,7 +674,8 @@ int sgl_kv_append(const sgl_rope_table* rope, const sgl_attn_params* params, con
  * For tokens with positions on several axes, and for requests whose rows no
  * longer count their tokens (sgl_kv_evict).  Where a row is stored is still
  * found by lens and extend_lens.  A row at a negative position (on any axis)
- * is left out: neither rotated nor stored.  rope must be given. */
+ * is left out: neither rotated nor stored, nor is its slot or length reported
+ * (rows that pad a batch).  rope must be given. */
 int sgl_kv_append_at(const sgl_rope_table* rope, const sgl_attn_params* params, const void* q, int64_t q_stride,
                      const void* k_new, int64_t k_stride, const void* v_new, int64_t v_stride, void* k_pool,
                      void* v_pool, const int32_t* req_to_token, int64_t ld, const int32_t* lens,

@@ -363,29 +363,33 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 9 : 6) rope_kernel(
     fetch(id0);
     // position and slot: -1 where there is nothing to do
     int pos = -1, slot = -1;
+    [[maybe_unused]] uint32_t wrong = 0;      // what there is to report of the row
     if constexpr (POOL != kPoolNone) {
         int r = (int)n, i = 0;
         if (!a.ext || find_request(a.ext, a.B, (int)n, lane, &r, &i)) {
             const int64_t p = a.ext ? (int64_t)__ldg(a.lens + r) + i : (int64_t)__ldg(a.lens + r) - 1;
             // no context (decode): nothing to append; past the table: an error
             if (p >= a.ld || (p < 0 && a.ext)) {
-                if (lane == 0 && id0 == 0) atomicOr(a.err, 2u);
+                wrong = 2u;
             } else if (p >= 0) {
                 pos = (int)p;
                 slot = __ldg(a.r2t + (int64_t)r * a.ld + p);
                 if (slot < 0 || slot >= a.num_slots) {
-                    if (lane == 0 && id0 == 0) atomicOr(a.err, 1u);
+                    wrong = 1u;
                     slot = -1;
                 }
             }
         }
     }
-    if (AT && (POOL == kPoolNone || pos >= 0)) {
+    if constexpr (AT) {
         // (the further axes' are read again below, from L1)
-        pos = __ldg(a.positions + n);
+        int given = __ldg(a.positions + n);
         for (int x = 1; x < a.axes; ++x)
-            if (__ldg(a.positions + x * a.n_rows + n) < 0) pos = -1;
+            if (__ldg(a.positions + x * a.n_rows + n) < 0) given = -1;
+        if (given < 0) wrong = 0;             // (a row that is left out)
+        if (POOL == kPoolNone || pos >= 0) pos = given;
     }
+    if (POOL != kPoolNone && wrong && lane == 0 && id0 == 0) atomicOr(a.err, wrong);
     if (pos < 0) return;
     const int half = a.rot >> 1;
     for (int j = lane; j < half; j += 32) {
