@@ -826,6 +826,8 @@ def sgl_kv_append(rope, params, q, k_new, v_new, k_pool, v_pool, req_to_token, l
     rotated; q and q_out None: keys and values only).  extend_lens given: N = the sum of extend_lens (or more, in a
     padded batch) rows ordered by request, row i of request r at position lens[r] + i; None: row r is request r's
     newest token, at position lens[r] - 1.  positions: as sgl_kv_append_at takes them."""
+    if rope is None and positions is not None:
+        raise TypeError("positions need a rope")
     T = _T or _torch()
     kind, hkv, d, dev = params.dtype, params.num_kv_heads, params.head_dim, T._C._cuda_getDevice()
     dt = T.float32 if kind == SGL_DTYPE_F32 else T.bfloat16
