@@ -54,8 +54,10 @@ __global__ void __launch_bounds__(256) weights_chunk_f32(const __grid_constant__
         if (tid == 0) before_s = s;
     }
     __syncthreads();
-    const Asked x = asked(a, r, before_s, tid == 0 && t0 == 0);
-    if (x.total > (int)gridDim.x * T) {                  // (longer than the host's longest: its scores stay as they were)
+    const int len = __ldg(a.lens + r), ext = __ldg(a.ext + r);
+    const Asked x = asked(a, len, ext, before_s);
+    // (lengths that the tables do not hold, or longer than the host's longest: its scores stay as they were)
+    if ((x.total == 0 && (len | ext) != 0) || x.total > (int)gridDim.x * T) {
         if (tid == 0 && t0 == 0) atomicOr(a.err, 2u);
         return;
     }

@@ -336,14 +336,9 @@ __global__ void __launch_bounds__(1024, 1) evict_long_kernel(const __grid_consta
     __shared__ uint3 choice;                               // the digit, pages above it, pages at it
     __shared__ uint2 warp_counts[kWarps], cta_counts;      // (pages that surely stay, pages at the lowest kept score)
     cg::cluster_group cl = cg::this_cluster();
-    const int C = (int)cl.num_blocks(), c = (int)cl.block_rank();
+    constexpr int C = kMaxCluster;                         // (fewer CTAs: evict_kernel)
+    const int c = (int)cl.block_rank();
     const int r = blockIdx.x / C, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    auto sync_all = [&] {
-        if (C > 1)
-            cl.sync();
-        else
-            __syncthreads();
-    };
     grid_dep_wait();
     grid_dep_launch();
     int n = a.lens[r];                       // (lens_out may be lens)
@@ -422,17 +417,12 @@ __global__ void __launch_bounds__(1024, 1) evict_long_kernel(const __grid_consta
                         hist[i * kCopyStride + 255 - tid] = 0;
                     }
                 }
-                if (C > 1) {
-                    if (tid < 256) counts[pass & 1][tid] = v;
-                    cl.sync();
-                    if (tid < 256) {
-                        v = 0;
-#pragma unroll
-                        for (int b = 0; b < kMaxCluster; ++b)
-                            if (b < C) v += cl.map_shared_rank(counts[pass & 1], b)[tid];
-                    }
-                }
+                if (tid < 256) counts[pass & 1][tid] = v;
+                cl.sync();
                 if (tid < 256) {
+                    v = 0;
+#pragma unroll
+                    for (int b = 0; b < C; ++b) v += cl.map_shared_rank(counts[pass & 1], b)[tid];
                     upto = v;
 #pragma unroll
                     for (int o = 1; o < 32; o <<= 1) {
@@ -485,17 +475,15 @@ __global__ void __launch_bounds__(1024, 1) evict_long_kernel(const __grid_consta
         }
         if (tid == 31) cta_counts = w;
         uint32_t surely = __shfl_sync(0xffffffffu, w.x - own.x, warp), equals = __shfl_sync(0xffffffffu, w.y - own.y, warp);
-        if (C > 1) {
-            cl.sync();
-            uint2 o = lane < c ? *cl.map_shared_rank(&cta_counts, lane) : make_uint2(0, 0);
+        cl.sync();
+        uint2 o = lane < c ? *cl.map_shared_rank(&cta_counts, lane) : make_uint2(0, 0);
 #pragma unroll
-            for (int i = 8; i > 0; i >>= 1) {        // (the CTAs before this one: at most 15)
-                o.x += __shfl_xor_sync(0xffffffffu, o.x, i);
-                o.y += __shfl_xor_sync(0xffffffffu, o.y, i);
-            }
-            surely += __shfl_sync(0xffffffffu, o.x, 0);
-            equals += __shfl_sync(0xffffffffu, o.y, 0);
+        for (int i = 8; i > 0; i >>= 1) {            // (the CTAs before this one: at most 15)
+            o.x += __shfl_xor_sync(0xffffffffu, o.x, i);
+            o.y += __shfl_xor_sync(0xffffffffu, o.y, i);
         }
+        surely += __shfl_sync(0xffffffffu, o.x, 0);
+        equals += __shfl_sync(0xffffffffu, o.y, 0);
         const uint32_t below = (1u << lane) - 1u;
         for (int i = r0; i < r1; i += 32) {
             const bool s = sure(i + lane), e = equal(i + lane);
@@ -507,7 +495,7 @@ __global__ void __launch_bounds__(1024, 1) evict_long_kernel(const __grid_consta
             surely += __popc(bs);
             equals += __popc(be);
         }
-        sync_all();
+        cl.sync();
     }
     const int left = some ? n - (first - head - more) * P : n;
     if (c == 0 && tid == 0) {
@@ -526,20 +514,14 @@ __global__ void __launch_bounds__(1024, 1) evict_long_kernel(const __grid_consta
             const int64_t p = q0 + e * kThreads;
             to[e] = (int)p;
             if (some && p < n) {
-                const int page = page_of((int)p);
-                int place;
-                if (C == 1) {
-                    place = (int)share[page];
-                } else {
-                    const int owner = (int)((page * inv) >> 40);
-                    place = (int)cl.map_shared_rank(share, owner)[page - owner * S];
-                }
+                const int page = page_of((int)p), owner = (int)((page * inv) >> 40);
+                const int place = (int)cl.map_shared_rank(share, owner)[page - owner * S];
                 const int rest = (int)p - page * P;
                 // (a page that leaves: its place among those, from the end of the ints on)
                 to[e] = place >= 0 ? place * P + rest : ~((page - ~place) * P + rest);
             }
         }
-        if (some && a.in_place) sync_all();
+        if (some && a.in_place) cl.sync();
 #pragma unroll
         for (int e = 0; e < kEach; ++e) {
             const int64_t p = q0 + e * kThreads;
@@ -558,7 +540,7 @@ __global__ void __launch_bounds__(1024, 1) evict_long_kernel(const __grid_consta
             }
         }
     }
-    if (C > 1 && some) cl.sync();      // (others may still read this CTA's share)
+    if (some) cl.sync();               // (others may still read this CTA's share)
 }
 
 int cuda_status(cudaError_t e) {

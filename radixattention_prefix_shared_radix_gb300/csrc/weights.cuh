@@ -29,30 +29,17 @@ struct WeightArgs {
     float scale, decay;                  // scale: of a product
 };
 
-// What request r asks: rows [row, row + ask) of the queries, row i of which sees
-// positions 0 .. p0 + i; its scores [0, total), those from `fresh` on beginning
-// at 0.  ask 0: nothing to do (or lengths that the tables do not hold).
+// What request r asks of a chunk call: rows [row, row + ask) of the queries, row i
+// of which sees positions 0 .. p0 + i; its scores [0, total), those from `fresh` on
+// beginning at 0.  total 0: nothing to do (or lengths that the tables do not hold).
 struct Asked {
     int total, ask, p0, fresh;
     int64_t row;
 };
-__device__ __forceinline__ Asked asked(const WeightArgs& a, int r, int64_t before, bool flag) {
-    Asked x{0, 0, 0, 0, 0};
-    const int len = __ldg(a.lens + r);
-    if (!a.ext) {
-        if (len < 0 || len > a.lim) {
-            if (flag) atomicOr(a.err, 2u);
-            return x;
-        }
-        return Asked{len, len > 0 ? 1 : 0, len - 1, len - 1, r};
-    }
-    const int e = __ldg(a.ext + r);
-    if (len < 0 || e < 0 || (int64_t)len + e > a.lim || before + e > a.n_rows) {
-        if (flag) atomicOr(a.err, 2u);
-        return x;
-    }
-    const int ask = a.window > 0 ? min(a.window, e) : e;
-    return Asked{len + e, ask, len + e - ask, len, before + e - ask};
+__device__ __forceinline__ Asked asked(const WeightArgs& a, int len, int ext, int64_t before) {
+    if (len < 0 || ext < 0 || (int64_t)len + ext > a.lim || before + ext > a.n_rows) return Asked{0, 0, 0, 0, 0};
+    const int ask = a.window > 0 ? min(a.window, ext) : ext;
+    return Asked{len + ext, ask, len + ext - ask, len, before + ext - ask};
 }
 
 // What a row adds to its products' scale before the exponential: minus its

@@ -187,11 +187,9 @@ struct Walk {
     static __device__ __forceinline__ Request request(const TcWeightArgs& ta, int len, int ext, int64_t before) {
         const WeightArgs& a = ta.w;
         Request q{};
-        if (len < 0 || ext < 0 || (int64_t)len + ext > a.lim || before + ext > a.n_rows) return q;
-        const int ask = a.window > 0 ? min(a.window, ext) : ext;
-        q.x = Asked{len + ext, ask, len + ext - ask, len, before + ext - ask};
+        q.x = asked(a, len, ext, before);
         q.tiles = (q.x.total + 255) / 256;
-        q.blocks = (ask * a.G + 127) / 128;
+        q.blocks = (q.x.ask * a.G + 127) / 128;
         q.runs = (q.blocks + ta.run - 1) / ta.run;
         const int64_t head = items_of_head<int>(q.x.p0, q.tiles, q.runs, ta.run, 31 - __clz(a.G), &q.whole);
         if (head * a.Hkv > ta.items) return Request{};       // (other lengths than the host's)
