@@ -18,13 +18,20 @@
 // order, eight a thread, with one exchange of the CTAs' totals, and every value
 // goes to its place.  Places only get smaller and every read comes before the
 // exchange, so a row may be moved onto itself.
-// What bounds it is the chain of rounds, not bytes: 0.4 us each with 256 threads,
-// 0.7 with 1024, 1.6 across 16 CTAs.  48 rows of 100 to 2000 tokens that lose one
-// each take 7.2 us, 64 of 1024 to 8192 cut to a quarter 11.1, 4 of 131072 in pages
-// of 16 18.1 (the bytes' times at the copy's rate: 0.2, 0.8, 1.3).  Rounds that
+// What bounds it is a chain of dependent steps, not bytes.  Calls that keep all
+// (launch, reads, stores in order), then what calls that keep only what must stay
+// take more (numbers, stores in other places), then the rounds: 64 rows of 2048
+// cut to a quarter 2.3 + 1.9 + 2.8 us, 64 of 8192 3.5 + 3.6 + 4.8, 4 of 100000 to
+// 131072 in pages of 16 3.5 + 6.7 + 9.2 (barriers of 16 CTAs in both), 4 of 500000
+// 12 + 29 + 12 (places looked up in other CTAs' shares, a barrier for every 65536
+// positions); the bytes' times at the copy's rate: 0.3, 1.3, 1.3, 5.  Rounds that
 // went through one set of counters, read by every warp with bank conflicts, took
-// 1.7 us; rows read again for the moves, and places looked up across the cluster,
-// cost another 2 to 4.
+// 1.7 us each; rows read again for the moves, and places looked up across the
+// cluster, cost another 2 to 4.
+// The launch goes by the tables' width, as the host does not see the lengths: 48
+// rows of 100 to 2000 tokens take 6.5 us in tables of their width and 76 in tables
+// of 131072 (48 clusters of 16 CTAs, an SM each); scores of 2048 over such a table
+// 6.5 again.
 //
 // ["SGLang 深度拆解" §2.3: the cache keeps what its budget allows]
 
