@@ -784,7 +784,7 @@ typedef struct {
  *                r, in order, in its first evicted_count[r] entries (device
  *                int32 [B], or NULL).  Slots past evicted_ld are counted, not
  *                written, and set bit 1 of the error word.  The caller frees
- *                those that no other row and no tree node holds
+ *                those that no other row and no tree node holds (below)
  * Each output may be its input itself (the rows change in place) and must not
  * overlap an input otherwise; entries of outputs past lens[r] stay as they
  * were.  Slots are moved, not looked at.  A length outside [0, ld] or
@@ -798,6 +798,22 @@ typedef struct {
  * scores_ld 2000 or 2048 over any table, 76 with ld and scores_ld 131072).
  * workspace: device, 256-byte aligned, its first 256 bytes (the error word;
  * calls may share it).  Can be captured.
+ *
+ * Rows from sgl_build_batch, thinned out:
+ *   - over a tree with pages of more than one slot, page_size must be the
+ *     tree's: sgl_tree_free returns the whole page of every slot that it is
+ *     given, and sgl_batch_append takes the slot after a row's last one, which
+ *     in a row closed up by single tokens may be another token's;
+ *   - the slots of the prompt's full pages (the row's first len / P * P entries
+ *     as sgl_build_batch wrote it) are tree nodes'.  They are not freed when they
+ *     leave the row: the nodes keep them while the request holds last_nodes, and
+ *     as cache from then on.  The rest of the row, and what sgl_batch_append
+ *     adds, is the request's: its evicted pages go to sgl_tree_free at once;
+ *   - sgl_batch_append takes the thinned rows and lengths (groups NULL: those of
+ *     before no longer hold), sgl_groups_from_table gives their groups;
+ *   - at the request's end: sgl_tree_unlock of its last_nodes and sgl_tree_free
+ *     of its own slots that are left.  sgl_tree_cache_finished and
+ *     sgl_tree_finish are for rows that are still their sequences.
  * ["SGLang 深度拆解" §2.3: the cache keeps what its budget allows; there whole
  * sequences by last use, here a sequence's tokens by attention] */
 int sgl_kv_evict(const sgl_evict_params* params, const float* scores, int64_t scores_ld, const int32_t* req_to_token,
