@@ -58,6 +58,28 @@ def test_runs_of_more_than_sixteen_query_blocks(kind, d):
 
 
 @pytest.mark.parametrize("kind", list(KINDS))
+@pytest.mark.parametrize("hq,hkv,n", [(2, 2, 11000), (8, 1, 9100), (16, 4, 9473)])
+def test_no_item_of_a_long_prompt_is_lost(kind, hq, hkv, n):
+    """Log-sum-exps of one size for early and late rows: the last run of query blocks is more than a hundredth of the
+    first positions' scores, a full one more, and the bound (weights good to 2^-12, additions in sequence: 34 of a block,
+    16 blocks, or 32 weights in fp32, then four threads over the runs of all heads) far below."""
+    pre, ext = np.array([0, 700]), np.array([n, 200])
+    c = Cache(kind, pre + ext, hq, hkv, 64, seed=n)
+    q = c.queries(int(ext.sum()))
+    lse = 5 + 0.5 * torch.randn(len(q), hq, generator=torch.Generator().manual_seed(n))
+    got = _run(c, q, lse, pre, ext, 0, None, 1.0, False)
+    rng = np.random.default_rng(n)
+    for r, L in enumerate(pre + ext):
+        at = np.unique(np.concatenate([np.arange(4), [127, 128, 255, 256, L - 1], 256 * rng.integers(0, L // 256, 12),
+                                       rng.integers(0, L, 60)]))
+        runs = -(-int(ext[r]) * hq // hkv // 128 // 4)
+        want, tol = _want(c, q, lse, pre, ext, at, r, 34 + 16 + runs * hkv // 4 + 8)
+        err = np.abs(got[r, at] - want)
+        assert (err <= tol).all(), ((err / tol).max(), at[err > tol][:4])
+        assert (tol[at < 4] < 2.0 ** -11 * want[at < 4]).all()
+
+
+@pytest.mark.parametrize("kind", list(KINDS))
 @pytest.mark.parametrize("num_sms", [1, 5, 400])
 def test_work_cut_for_other_numbers_of_sms(kind, num_sms):
     pre, ext = np.array([0, 300, 40]), np.array([290, 70, 0])
