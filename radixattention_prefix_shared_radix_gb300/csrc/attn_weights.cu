@@ -321,9 +321,9 @@ __global__ void __launch_bounds__(kStreamThreads, Stream<D, KV>::CTAS) weights_d
         }
     };
     // the query rows of KV head h: B fragments (row g of eight) of the same
-    // pieces that the keys come in, and the log-sum-exps of columns 2 t, 2 t + 1
+    // pieces that the keys come in, and minus the log-sum-exps of columns 2 t, 2 t + 1
     uint32_t qf[F32 ? 1 : QW];
-    float l0, l1;                                    // (-infinity: no row, or one that adds nothing)
+    float l0, l1;                                    // (infinity: no row, or one that adds nothing)
     auto load_query = [&](int r2, int h) {
         const int64_t row = (int64_t)r2 * a.Hq + h * a.G;
         if constexpr (F32) {
@@ -331,8 +331,8 @@ __global__ void __launch_bounds__(kStreamThreads, Stream<D, KV>::CTAS) weights_d
             for (int i = lane; i < a.G * (D / 4); i += 32)
                 reinterpret_cast<float4*>(&sq[warp * 8 * D])[i] = __ldg(reinterpret_cast<const float4*>(a.q) + row * (D / 4) + i);
             __syncwarp();
-            l0 = t < a.G ? __ldg(a.lse + row + t) : -INFINITY;
-            l1 = t + 4 < a.G ? __ldg(a.lse + row + t + 4) : -INFINITY;
+            l0 = t < a.G ? -__ldg(a.lse + row + t) : INFINITY;
+            l1 = t + 4 < a.G ? -__ldg(a.lse + row + t + 4) : INFINITY;
         } else {
             const uint4* q = reinterpret_cast<const uint4*>(static_cast<const bf16*>(a.q) + (row + min(g, a.G - 1)) * D);
             uint32_t bad = 0;
@@ -345,8 +345,8 @@ __global__ void __launch_bounds__(kStreamThreads, Stream<D, KV>::CTAS) weights_d
                 for (int j = 0; j < 4; ++j) qf[4 * i + j] = KV == 0 ? w[j] : bf16x2_to_f16x2_chk(w[j], bad);
             }
             if (bad && g < a.G && __ldg(a.lse + row + g) != -INFINITY) atomicOr(a.err, kErrQRange);
-            l0 = 2 * t < a.G ? __ldg(a.lse + row + 2 * t) : -INFINITY;
-            l1 = 2 * t + 1 < a.G ? __ldg(a.lse + row + 2 * t + 1) : -INFINITY;
+            l0 = 2 * t < a.G ? -__ldg(a.lse + row + 2 * t) : INFINITY;
+            l1 = 2 * t + 1 < a.G ? -__ldg(a.lse + row + 2 * t + 1) : INFINITY;
         }
     };
     load_slots(r, tile, len);
@@ -442,11 +442,11 @@ __global__ void __launch_bounds__(kStreamThreads, Stream<D, KV>::CTAS) weights_d
             else if (at + 1 < end)
                 load_keys(wh, tile2, len2);
             // (columns that add nothing may hold infinities and NaN)
-            const bool v0 = l0 != -INFINITY, v1 = l1 != -INFINITY;
+            const bool v0 = l0 != INFINITY, v1 = l1 != INFINITY;
 #pragma unroll
             for (int n = 0; n < NR; ++n) {
                 const float x0 = F32 ? c[n][0] : c[n / 2][2 * (n & 1)], x1 = F32 ? c[n][1] : c[n / 2][2 * (n & 1) + 1];
-                const float w0 = weight_of(x0, a.scale, -l0), w1 = weight_of(x1, a.scale, -l1);
+                const float w0 = weight_of(x0, a.scale, l0), w1 = weight_of(x1, a.scale, l1);
                 if (now >> n & 1u) sum[n] += (v0 ? w0 : 0.f) + (v1 ? w1 : 0.f);
             }
         }
