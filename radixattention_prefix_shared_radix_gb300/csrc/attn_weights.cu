@@ -24,9 +24,10 @@ namespace cg = cooperative_groups;
 // (tile of 64 positions, request) deals the KV heads among its CTAs and adds
 // their sums through distributed shared memory, in order.  A CTA takes 64 rows at
 // a time; a thread multiplies four positions by four rows, so that eight 16-byte
-// reads of shared memory, which bound it, feed 64 multiply-adds (20 TFLOP/s; one
-// position by four rows: 7).  4 x 40 to 96 tokens of 32 heads behind 500 to 2000:
-// 119 us.
+// reads of shared memory, which bound it, feed 64 multiply-adds (4 x 40 to 96
+// tokens of 32 heads behind 500 to 2000 139 us, 26 TFLOP/s; 2 x 1000 tokens of 64
+// heads behind up to 500 1.44 ms, 17 TFLOP/s; one position by four rows took three
+// times as long).
 // ---------------------------------------------------------------------------
 constexpr int kF32Cluster = 8, kF32Tile = 64;
 template <int D>
@@ -181,10 +182,12 @@ __global__ void __launch_bounds__(256) weights_chunk_f32(const __grid_constant__
 // a request's query stays in registers over its tiles.
 // Memory-bound; what counts is the bytes in flight, loads of the next unit being
 // issued before the exponentials of this one.  64 contexts of 1 to 8192 tokens, 8
-// heads of 128: bf16 91.7 us (6.1 TB/s, 0.90 of the measured copy; ncu: 558 of 559
-// MB read, issue slots 48%), E4M3 57.7 (5.0 TB/s), 4 bits 54.8 (3.0: four
-// conversions and four multiplications by scales for eight codes, 24 at the copy's
-// rate), 30 such over fp32 89.4 (5.6 TB/s).  One context of 180 tokens 4.1 us.
+// heads of 128: bf16 91.5 us (6.1 TB/s, 0.90 of the measured copy; ncu: 558 of 559
+// MB read, issue slots 48%), 30 such over fp32 88.7 (5.6 TB/s).  E4M3 55.2 us (5.1
+// TB/s; ncu: DRAM 56%, issue slots 38%) and 4 bits 51.7 (3.1; DRAM 35%, issue slots
+// 50%) have no unit full: 16 warps an SM, each with one unit's loads ahead, wait for
+// those (E4M3 30% of their cycles, 4 bits 20%), for each other and for their own chains.  One context
+// of 180 tokens 4.1 us.
 // Before, a CTA per 32 positions with keys and queries staged through shared
 // memory took 2041 us on the bf16 batch.
 // ---------------------------------------------------------------------------

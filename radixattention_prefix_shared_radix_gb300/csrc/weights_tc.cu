@@ -37,8 +37,9 @@
 // All waits are bounded: one that gives up sets bit 2 of the error word, and the
 // code runs to its end without hanging.
 //
-// 8 x 512 new tokens behind 4096, 64 heads of 128: 234 us with the join, 1250
-// TFLOP/s, 0.65 of the measured peak (152 us).  A block of 128 rows by 256
+// 8 x 512 new tokens behind 4096, 64 heads of 128: 236 us with the join in calls
+// back to back, 1240 TFLOP/s, 0.64 of the measured peak (152 us); 247 a call among
+// others.  A block of 128 rows by 256
 // positions is 1024 cycles of MMAs and 1024 of exponentials (32 a cycle and SM);
 // it takes about 1900 (clock stamps of a softmax warp): 1350 of exponentials and
 // what goes with them, then, for all warps at once, 170 until the next scores are
@@ -50,11 +51,15 @@
 // with work numbered, so that 152 CTAs get equal shares, 235.  Without the
 // product by log2 e (the log-sum-exp rounded in base 2) it takes 227, and loses
 // bits of every weight.  Blocks of N = 64, which would let the warpgroups run out
-// of step, cost 0.8 of the time of N = 128.  What remains is that no TMEM is left
-// for a second set of scores beside two sets of keys.
-// Windows (one block an item) are bound by the keys' way through shared memory and
-// conversion, about 3800 cycles an item: 16 x 32 rows over 1500 to 4000 tokens in 4
-// bits 32.5 us, in E4M3 34.3, in bf16 43.6.
+// of step, cost 0.8 of the time of N = 128.  What remains at d = 128 is that two
+// sets of keys and one of scores fill TMEM; at d = 64 (221 us; 122 for its
+// exponentials) the keys take half as much, and 128 columns lie idle.
+// Windows (one block an item): 16 x 32 rows over 1500 to 4000 tokens in 4 bits 33.0
+// us, in E4M3 32.2, in bf16 44.2, about 3800 cycles an item.  An item's chain of
+// copy, conversion, product, exponentials and sums has no second block to hide
+// behind, and every item fetches its block of queries anew; conversion is not what
+// bounds it (bf16, which needs none, takes longest, with one staged tile for each
+// load warpgroup and twice the bytes; a second load warpgroup gave 0.3 us).
 
 #include <algorithm>
 
