@@ -699,8 +699,9 @@ int sgl_mla_kv_append(const sgl_rope_table* rope, const sgl_mla_params* params, 
 /* Device workspace that sgl_attn_weights needs (bytes, a multiple of 256): in
  * the decode form (no host_extend_lens in params) and over fp32 pools 256; else
  * by the lengths in params->host_prefix_lens / host_extend_lens and by `window`,
- * no more than 2 KB for every 256 positions of a request and KV head, and
- * 1 MiB for each SM (params->num_sms) besides.  SGL_ERR_UNSUPPORTED for lengths that the call refuses. */
+ * no more than 2 KB for every 256 positions of a request and KV head, and 1 MiB
+ * for each SM (params->num_sms) besides.  SGL_ERR_UNSUPPORTED for lengths that
+ * the call refuses. */
 int sgl_attn_weights_workspace_bytes(const sgl_attn_params* params, int32_t window, size_t* bytes);
 
 /* The attention weights that each cached token gets from a call's queries,
@@ -743,10 +744,10 @@ int sgl_attn_weights_workspace_bytes(const sgl_attn_params* params, int32_t wind
  * error word; a length outside the table (or beyond 2^26) sets bit 1 and leaves
  * the request's scores as they were.  So do device lengths of a chunk call for
  * which the work that the host copies planned has no room (those of requests
- * behind such a one may stay as they were too).  A prefix that requests share is read once
- * for each of them.  params->num_sms (at most 4096 count) is the number of SMs
- * that the work is cut for, for the call as for the size of its workspace; with
- * another one the sums of a chunk may be formed in another order.
+ * behind such a one may stay as they were too).  A prefix that requests share is
+ * read once for each of them.  params->num_sms (at most 4096 count) is the number
+ * of SMs that the work is cut for, for the call as for the size of its workspace;
+ * with another one the sums of a chunk may be formed in another order.
  * workspace: device, 256-byte aligned, sgl_attn_weights_workspace_bytes (a
  * decode plan's serves in the decode form); calls that may overlap on the GPU
  * need one each.  Can be captured; the decode form follows lens at replay, a

@@ -74,3 +74,26 @@ def test_keys_under_excluded_rows(kind, decode):
             assert np.isnan(got[0, p])
             got[0, p] = clean[0, p]
     assert np.array_equal(got, clean)
+
+
+@pytest.mark.parametrize("kind", list(KINDS))
+@pytest.mark.parametrize("num_sms", [0, 1, 3])
+def test_excluded_rows_all_over_long_runs(kind, num_sms):
+    """A third of the rows, in runs of up to sixteen query blocks one after the other on few SMs, and blocks of nothing
+    else."""
+    pre, ext = np.array([700, 0, 33]), np.array([400, 290, 1])
+    c = Cache(kind, pre + ext, 16, 2, 64, seed=4)
+    q = c.queries(int(ext.sum()))
+    lse = 5 + torch.randn(len(q), 16, generator=torch.Generator().manual_seed(5))
+    out = torch.rand(len(q), 16, generator=torch.Generator().manual_seed(6)) < 0.3
+    out[64:128] = True
+    out[690] = True
+    lse[out] = -np.inf
+    q[out] = 0
+    want = _run(c, q, lse, pre, ext, 0, None, 1.0, False, num_sms=num_sms)
+    ref, tol = c.expect(q, lse, pre, ext, 0, np.zeros(want.shape, dtype=np.float32), 0.0, False, 0.125)
+    live = np.arange(want.shape[1])[None] < (pre + ext)[:, None]
+    assert (np.abs(want - ref) <= tol)[live].all() and not want[2, :34].any()
+    x = q.clone()
+    x[out] = float("nan")
+    assert np.array_equal(_run(c, x, lse, pre, ext, 0, None, 1.0, False, num_sms=num_sms), want)
