@@ -186,8 +186,8 @@ __global__ void __launch_bounds__(256) weights_chunk_f32(const __grid_constant__
 // MB read, issue slots 48%), 30 such over fp32 88.7 (5.6 TB/s).  E4M3 55.2 us (5.1
 // TB/s; ncu: DRAM 56%, issue slots 38%) and 4 bits 51.7 (3.1; DRAM 35%, issue slots
 // 50%) have no unit full: 16 warps an SM, each with one unit's loads ahead, wait for
-// those (E4M3 30% of their cycles, 4 bits 20%), for each other and for their own chains.  One context
-// of 180 tokens 4.1 us.
+// those (E4M3 30% of their cycles, 4 bits 20%), for each other and for their own
+// chains.  One context of 180 tokens 4.1 us.
 // Before, a CTA per 32 positions with keys and queries staged through shared
 // memory took 2041 us on the bf16 batch.
 // ---------------------------------------------------------------------------

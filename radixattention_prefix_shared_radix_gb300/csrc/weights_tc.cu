@@ -854,6 +854,8 @@ int tc_plan(const sgl_attn_params* p, int window, TcPlan* plan) {
     // workspace however long its run is, so that what a call needs grows with its
     // positions (2 KB for 256 of them and a KV head, at least) and not with rows x
     // positions (a prompt of 131072 tokens, 64/8 heads: 84 MB; runs of 16 took 2.1 GB).
+    // The longest run that rows allow, 2^20 blocks, takes a second, and a wait gives
+    // up after six.
     const int64_t sms = x.sms;
     x.run = (int)std::min(std::max<int64_t>(std::clamp<int64_t>((units + sms - 1) / sms, 1, kSumBlocks),
                                             (units + kItemsPerSm * sms - 1) / (kItemsPerSm * sms)),

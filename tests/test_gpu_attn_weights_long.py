@@ -57,6 +57,22 @@ def test_runs_of_more_than_sixteen_query_blocks(kind, d):
     assert np.array_equal(_run(c, q, lse, pre, ext, 0, None, 1.0, False), got)     # (in the same order again)
 
 
+@pytest.mark.parametrize("num_sms,run", [(8, 350), (2, 1398)])
+def test_runs_of_hundreds_of_query_blocks(num_sms, run):
+    """The same work cut for few SMs: 1688 blocks of 106 tiles and 8 heads, 512 items an SM.  In sequence as above, with
+    the parts of a longer run and fewer runs."""
+    n = 27000
+    c = Cache("fp8", [n], 64, 8, 64, seed=3)
+    q = c.queries(n)
+    lse = 6 + torch.randn(n, 64, generator=torch.Generator().manual_seed(1))
+    assert run == -(-106 * 1688 * 8 // (512 * num_sms))
+    got = _run(c, q, lse, np.array([0]), np.array([n]), 0, None, 1.0, False, num_sms=num_sms)
+    at = np.unique(np.concatenate([[0, 1, 127, 128, 255, 256, n - 129, n - 1], np.random.default_rng(2).integers(0, n, 80)]))
+    want, tol = _want(c, q, lse, [0], [n], at, 0, 34 + 16 + -(-run // 16) + -(-1688 // run) * 2 + 3)
+    err = np.abs(got[0, at] - want)
+    assert (err <= tol).all(), ((err / tol).max(), at[err > tol][:4])
+
+
 @pytest.mark.parametrize("kind", list(KINDS))
 @pytest.mark.parametrize("hq,hkv,n", [(2, 2, 11000), (8, 1, 9100), (16, 4, 9473)])
 def test_no_item_of_a_long_prompt_is_lost(kind, hq, hkv, n):
